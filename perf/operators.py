@@ -398,8 +398,9 @@ def exact(case, seed):
     for b in range(0, k, 128):
         x = st["x"][:, b:b + 128].double()
         scale = x.abs().amax(1, keepdim=True) / 448
-        # the codes are of x times 448 / max, a number of 32 bits by definition: it decides ties
-        v = x * (1 / torch.where(scale > 0, scale, torch.ones_like(scale))).float().double()
+        # the codes are of x times 448 / max, factor and product numbers of 32 bits by definition:
+        # they decide the ties
+        v = (x * (1 / torch.where(scale > 0, scale, torch.ones_like(scale))).float().double()).float().double()
         # e4m3: three bits behind the point of a binade, no binade below 2^-6
         step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
         a[:, b:b + 128] = torch.round(v / step) * step * scale
