@@ -1,6 +1,8 @@
 // The C ABI (include/dit.h): argument validation, workspace layout, the launch
 // sequence of a dual-stream block, a single-stream block and the whole step, and the
 // host runtime pieces (launch accounting, per-launch timing, TMA descriptor encoding).
+#include <math.h>
+
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
@@ -39,7 +41,9 @@ const char* kernel_class_name(int cls) {
       "adaln",          "gemm_qkv_rmsnorm_rope", "gemm_fused_qkv_mlp",  "gemm_gated_residual",
       "gemm_swiglu",    "gemm_plain",            "attention",           "modulation_gemv",
       "rope_table",     "pack_mlp_in",           "gemm_dual_out_proj",  "gemm_dual_mlp_out",
-      "gemm_single_out_proj", "quantize_act"};
+      "gemm_single_out_proj", "quantize_act",    "text_rope_table",     "qk_norm_rope",
+      "text_attention", "text_attention_join",   "quantize_blocks_fp8", "linear_fp8_blocks",
+      "linear_fp8_join"};
   return (cls >= 0 && cls < kClsCount) ? names[cls] : "?";
 }
 
@@ -885,7 +889,7 @@ dit_status dit_sync_status(void* ws, dit_stream_t stream, uint32_t* where_out) {
   if (h.word != 0) {
     DIT_CUDA(cudaMemsetAsync(ws, 0, 8, st));
     DIT_CUDA(cudaStreamSynchronize(st));
-    return DIT_ERR_TIMEOUT;
+    return (h.word & ~(uint32_t)kStatusBadEntry) ? DIT_ERR_TIMEOUT : DIT_ERR_INVALID_ARG;
   }
   return DIT_OK;
 }
@@ -952,6 +956,222 @@ dit_status dit_attention(int batch, int heads, int n, const void* q_dev, const v
   if (ws_bytes < sizeof(DeviceStatus)) return DIT_ERR_WORKSPACE;
   return cuda_status(launch_attention(batch, heads, n, (const bf16*)q_dev, (const bf16*)k_dev, (const bf16*)v_dev,
                                       (bf16*)out_dev, ld_out, status_of(ws), (cudaStream_t)stream));
+}
+
+// ---- text-side operations -----------------------------------------------------------
+
+}  // extern "C"
+
+namespace dit {
+namespace {
+
+constexpr int kMaxTextRows = 1 << 26, kMaxAttnRows = 1 << 28, kMaxSeqs = 16384, kMaxLen = 1 << 24;
+constexpr long long kMaxLd = 1 << 24;
+
+inline bool finite_pos(double v) { return v > 0.0 && v <= 1.7e308; }
+
+// Whether two strided matrices [rows, width] of bf16 share an element.  Disjoint address
+// ranges do not; with equal strides, neither do disjoint column ranges.
+bool strided_overlap(const void* a, long long lda, long long rows_a, long long width_a, const void* b, long long ldb,
+                     long long rows_b, long long width_b) {
+  if (rows_a <= 0 || rows_b <= 0) return false;
+  const long long pa = (long long)((uintptr_t)a / 2), pb = (long long)((uintptr_t)b / 2);
+  const long long ea = pa + (rows_a - 1) * lda + width_a, eb = pb + (rows_b - 1) * ldb + width_b;
+  if (ea <= pb || eb <= pa) return false;
+  if (lda != ldb) return true;
+  long long d = (pb - pa) % lda;  // b's first column as a column of a's rows
+  if (d < 0) d += lda;
+  return !(d >= width_a && d + width_b <= lda);
+}
+
+dit_status check_text_attn(const dit_text_attn* a) {
+  if (!a) return DIT_ERR_INVALID_ARG;
+  if (a->head_dim != 64 && a->head_dim != 128) return DIT_ERR_UNSUPPORTED;
+  if (a->heads_q < 1 || a->heads_q > 1024 || a->heads_k < 1 || a->heads_q % a->heads_k != 0 ||
+      a->heads_q / a->heads_k > 64)
+    return DIT_ERR_INVALID_ARG;
+  if (a->seqs < 0 || a->seqs > kMaxSeqs || a->rows_q < 0 || a->rows_q > kMaxAttnRows || a->rows_k < 0 ||
+      a->rows_k > kMaxAttnRows || a->max_q < 0 || a->max_q > kMaxLen || a->max_k < 0 || a->max_k > kMaxLen)
+    return DIT_ERR_INVALID_ARG;
+  if (!finite_pos(a->scale) || a->scale > 3.0e38f) return DIT_ERR_INVALID_ARG;
+  return DIT_OK;
+}
+
+TextAttnArgs text_attn_sizes(const dit_text_attn& a) {
+  TextAttnArgs t;
+  memset(&t, 0, sizeof(t));
+  t.seqs = a.seqs; t.heads_q = a.heads_q; t.heads_k = a.heads_k; t.head_dim = a.head_dim;
+  t.rows_q = a.rows_q; t.rows_k = a.rows_k; t.causal = a.causal != 0; t.scale = a.scale;
+  t.max_q = a.max_q < a.rows_q ? a.max_q : a.rows_q;
+  t.max_k = a.max_k < a.rows_k ? a.max_k : a.rows_k;
+  return t;
+}
+
+inline bool linear_fp8_sizes_ok(int rows, int n_out, int k) {
+  return rows >= 1 && rows <= kMaxTokens && n_out >= 1 && n_out <= kMaxTokens && n_out % 8 == 0 && k >= 1 &&
+         k <= kMaxTokens && k % 16 == 0;
+}
+
+}  // namespace
+}  // namespace dit
+
+extern "C" {
+
+dit_status dit_text_rope_table(const dit_text_rope* rope, const int32_t* pos_dev, int n, float* table_dev,
+                               dit_stream_t stream) {
+  if (!rope || n < 0 || n > kMaxLen) return DIT_ERR_INVALID_ARG;
+  const dit_text_rope& c = *rope;
+  if (c.rot_dim < 2 || c.rot_dim > 256 || c.rot_dim % 2 != 0) return DIT_ERR_UNSUPPORTED;
+  if (!(c.theta > 1.0 && c.theta <= 1e12) || !finite_pos(c.magnitude) || c.magnitude > 1e30)
+    return DIT_ERR_INVALID_ARG;
+  double theta = c.theta;
+  switch (c.scaling) {
+    case DIT_ROPE_SCALE_NONE: break;
+    case DIT_ROPE_SCALE_NTK:
+      if (c.rot_dim < 4) return DIT_ERR_UNSUPPORTED;
+      if (!(c.factor >= 1.0 && c.factor <= 1e6)) return DIT_ERR_INVALID_ARG;
+      theta *= pow(c.factor, (double)c.rot_dim / (c.rot_dim - 2));
+      break;
+    case DIT_ROPE_SCALE_BY_PARTS:
+      if (!(c.low >= 0.0 && c.high > c.low && c.high <= 1e12) || c.original_len < 1) return DIT_ERR_INVALID_ARG;
+      [[fallthrough]];
+    case DIT_ROPE_SCALE_LINEAR:
+      if (!(c.factor >= 1.0 && c.factor <= 1e6)) return DIT_ERR_INVALID_ARG;
+      break;
+    default: return DIT_ERR_INVALID_ARG;
+  }
+  if (n == 0) return DIT_OK;
+  if ((reinterpret_cast<uintptr_t>(pos_dev) & 3u) || !aligned16(table_dev)) return DIT_ERR_INVALID_ARG;
+  constexpr double kTwoPi = 6.283185307179586476925;
+  TextRopeArgs a;
+  a.half = c.rot_dim / 2;
+  a.magnitude = (float)c.magnitude;
+  a.pos = pos_dev;
+  a.n = n;
+  a.table = table_dev;
+  for (int j = 0; j < a.half; ++j) {
+    double w = pow(theta, -2.0 * j / c.rot_dim);
+    if (c.scaling == DIT_ROPE_SCALE_LINEAR) w /= c.factor;
+    if (c.scaling == DIT_ROPE_SCALE_BY_PARTS) {
+      double g = (w * c.original_len / kTwoPi - c.low) / (c.high - c.low);
+      g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
+      w = g * w + (1.0 - g) * w / c.factor;
+    }
+    // w <= 1, so a position turns by less than 1/4: the fixed point stays below 2^62
+    a.freq[j] = (uint64_t)llrint(ldexp(w / kTwoPi, 64));
+  }
+  return cuda_status(launch_text_rope(a, (cudaStream_t)stream));
+}
+
+dit_status dit_qk_norm_rope(int rows, int heads_q, int heads_k, int head_dim, int rot_dim, dit_rope_layout layout,
+                            const void* q_dev, long long ldq, const void* k_dev, long long ldk, const void* q_norm,
+                            const void* k_norm, float eps, const float* table_dev, int table_rows,
+                            const int32_t* table_row_dev, void* q_out_dev, long long ldq_out, void* k_out_dev,
+                            long long ldk_out, void* ws, size_t ws_bytes, dit_stream_t stream) {
+  if (head_dim != 64 && head_dim != 128) return DIT_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0) return DIT_ERR_UNSUPPORTED;
+  if (rows < 0 || rows > kMaxTextRows || heads_q < 1 || heads_q > 1024 || heads_k < 0 || heads_k > 1024)
+    return DIT_ERR_INVALID_ARG;
+  if (layout != DIT_ROPE_INTERLEAVED && layout != DIT_ROPE_HALF) return DIT_ERR_INVALID_ARG;
+  if (!(eps >= 0.f && eps <= 3.0e38f) || (heads_k > 0 && (q_norm == nullptr) != (k_norm == nullptr)))
+    return DIT_ERR_INVALID_ARG;
+  const long long wq = (long long)heads_q * head_dim, wk = (long long)heads_k * head_dim;
+  auto bad_ld = [](long long ld, long long w) { return ld < w || ld > kMaxLd || ld % 8 != 0; };
+  if (bad_ld(ldq, wq) || bad_ld(ldq_out, wq) || (heads_k > 0 && (bad_ld(ldk, wk) || bad_ld(ldk_out, wk))))
+    return DIT_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (table_rows < 0 || (!table_row_dev && rows > table_rows))) return DIT_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return DIT_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(DeviceStatus)) return DIT_ERR_WORKSPACE;
+  if (rows == 0) return DIT_OK;
+  if (!aligned16(q_dev) || !aligned16(q_out_dev) || (q_norm && !aligned16(q_norm)) ||
+      (heads_k > 0 && (!aligned16(k_dev) || !aligned16(k_out_dev) || (k_norm && !aligned16(k_norm)))))
+    return DIT_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!aligned16(table_dev) || (reinterpret_cast<uintptr_t>(table_row_dev) & 3u))) return DIT_ERR_INVALID_ARG;
+  auto clash = [&](const void* in, long long ld_in, long long w_in, const void* out, long long ld_out, long long w_out) {
+    return strided_overlap(in, ld_in, rows, w_in, out, ld_out, rows, w_out);
+  };
+  // a head is read and written by the same warp: exactly in place is the one overlap allowed
+  if (!(q_out_dev == q_dev && ldq_out == ldq) && clash(q_dev, ldq, wq, q_out_dev, ldq_out, wq)) return DIT_ERR_INVALID_ARG;
+  if (heads_k > 0) {
+    if (!(k_out_dev == k_dev && ldk_out == ldk) && clash(k_dev, ldk, wk, k_out_dev, ldk_out, wk))
+      return DIT_ERR_INVALID_ARG;
+    if (clash(q_dev, ldq, wq, k_out_dev, ldk_out, wk) || clash(k_dev, ldk, wk, q_out_dev, ldq_out, wq) ||
+        clash(q_out_dev, ldq_out, wq, k_out_dev, ldk_out, wk))
+      return DIT_ERR_INVALID_ARG;
+  }
+  QKNormRopeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.rows = rows; a.heads_q = heads_q; a.heads_k = heads_k; a.head_dim = head_dim; a.rot_dim = rot_dim;
+  a.layout = layout; a.q = (const bf16*)q_dev; a.k = (const bf16*)k_dev; a.q_norm = (const bf16*)q_norm;
+  a.k_norm = (const bf16*)k_norm; a.ldq = ldq; a.ldk = ldk; a.ldq_out = ldq_out; a.ldk_out = ldk_out; a.eps = eps;
+  a.table = table_dev; a.table_rows = table_rows; a.table_row = table_row_dev; a.q_out = (bf16*)q_out_dev;
+  a.k_out = (bf16*)k_out_dev; a.status = status_of(ws);
+  return cuda_status(launch_qk_norm_rope(a, (cudaStream_t)stream));
+}
+
+dit_status dit_text_attention_workspace(const dit_text_attn* a, size_t* bytes) {
+  DIT_TRY(check_text_attn(a));
+  if (!bytes) return DIT_ERR_INVALID_ARG;
+  *bytes = sizeof(DeviceStatus) + text_attention_parts_bytes(text_attn_sizes(*a));
+  return DIT_OK;
+}
+
+dit_status dit_text_attention(const dit_text_attn* a, const int32_t* q_off, const int32_t* q_len,
+                              const int32_t* k_off, const int32_t* k_len, const void* q_dev, long long ldq,
+                              const void* k_dev, long long ldk, const void* v_dev, long long ldv, void* out_dev,
+                              long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream) {
+  DIT_TRY(check_text_attn(a));
+  const long long wq = (long long)a->heads_q * a->head_dim, wk = (long long)a->heads_k * a->head_dim;
+  auto bad_ld = [](long long ld, long long w) { return ld < w || ld > kMaxLd || ld % 8 != 0; };
+  if (bad_ld(ldq, wq) || bad_ld(ldk, wk) || bad_ld(ldv, wk) || bad_ld(ldo, wq)) return DIT_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return DIT_ERR_INVALID_ARG;
+  TextAttnArgs t = text_attn_sizes(*a);
+  if (ws_bytes < sizeof(DeviceStatus) + text_attention_parts_bytes(t)) return DIT_ERR_WORKSPACE;
+  if (a->seqs == 0 || a->rows_q == 0 || a->max_q == 0) return DIT_OK;
+  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (!q_off || !k_off || !aligned4(q_off) || !aligned4(k_off) || !aligned4(q_len) || !aligned4(k_len))
+    return DIT_ERR_INVALID_ARG;
+  if (!aligned16(q_dev) || !aligned16(out_dev) || (a->rows_k > 0 && (!aligned16(k_dev) || !aligned16(v_dev))))
+    return DIT_ERR_INVALID_ARG;
+  if (strided_overlap(q_dev, ldq, a->rows_q, wq, out_dev, ldo, a->rows_q, wq) ||
+      strided_overlap(k_dev, ldk, a->rows_k, wk, out_dev, ldo, a->rows_q, wq) ||
+      strided_overlap(v_dev, ldv, a->rows_k, wk, out_dev, ldo, a->rows_q, wq))
+    return DIT_ERR_INVALID_ARG;
+  t.q_off = q_off; t.q_len = q_len; t.k_off = k_off; t.k_len = k_len;
+  t.q = (const bf16*)q_dev; t.k = (const bf16*)k_dev; t.v = (const bf16*)v_dev; t.out = (bf16*)out_dev;
+  t.ldq = ldq; t.ldk = ldk; t.ldv = ldv; t.ldo = ldo;
+  t.status = status_of(ws);
+  t.parts = reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)));
+  return cuda_status(launch_text_attention(t, (cudaStream_t)stream));
+}
+
+dit_status dit_quantize_blocks_fp8(const void* x_dev, long long ld, int rows, int cols, int block_rows, void* q_dev,
+                                   float* scale_dev, dit_stream_t stream) {
+  if (rows < 1 || rows > kMaxTokens || cols < 16 || cols > kMaxTokens || cols % 16 != 0 || ld < cols || ld > kMaxLd ||
+      ld % 8 != 0 || (block_rows != 1 && block_rows != 128))
+    return DIT_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(q_dev) || !aligned16(scale_dev)) return DIT_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize_blocks((const bf16*)x_dev, ld, rows, cols, block_rows, (uint8_t*)q_dev, scale_dev,
+                                            (cudaStream_t)stream));
+}
+
+dit_status dit_linear_fp8_blocks_workspace(int rows, int n_out, int k, size_t* bytes) {
+  if (!linear_fp8_sizes_ok(rows, n_out, k) || !bytes) return DIT_ERR_INVALID_ARG;
+  *bytes = sizeof(DeviceStatus) + linear_fp8_parts_bytes(rows, n_out, k);
+  return DIT_OK;
+}
+
+dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev, const float* a_scale_dev,
+                                 const void* w_q_dev, const float* w_scale_dev, void* out_dev, int ld_out, void* ws,
+                                 size_t ws_bytes, dit_stream_t stream) {
+  if (!linear_fp8_sizes_ok(rows, n_out, k) || ld_out < n_out || ld_out % 8 != 0) return DIT_ERR_INVALID_ARG;
+  if (!aligned16(a_q_dev) || !aligned16(a_scale_dev) || !aligned16(w_q_dev) || !aligned16(w_scale_dev) ||
+      !aligned16(out_dev) || !aligned16(ws))
+    return DIT_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(DeviceStatus) + linear_fp8_parts_bytes(rows, n_out, k)) return DIT_ERR_WORKSPACE;
+  LinearFp8Args a{rows, n_out, k, (const uint8_t*)a_q_dev, (const uint8_t*)w_q_dev, a_scale_dev, w_scale_dev,
+                  (bf16*)out_dev, ld_out, status_of(ws), reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)))};
+  return cuda_status(launch_linear_fp8(a, (cudaStream_t)stream));
 }
 
 unsigned long long dit_launch_count(void) { return g_launches.load(); }

@@ -16,9 +16,11 @@ typedef __nv_bfloat16 bf16;
 // ---------------------------------------------------------------------------------
 // Device status word (first bytes of every workspace).  Kernels never trap: a wait
 // that runs past its limit sets a bit here, the kernel unwinds, and the host reports
-// DIT_ERR_TIMEOUT from dit_sync_status().
+// DIT_ERR_TIMEOUT from dit_sync_status().  A kernel that meets an entry out of range in a
+// device array of lengths or positions skips it and sets kStatusBadEntry
+// (DIT_ERR_INVALID_ARG).
 // ---------------------------------------------------------------------------------
-enum : uint32_t { kStatusTimeout = 1u, kStatusBadLaunch = 2u };
+enum : uint32_t { kStatusTimeout = 1u, kStatusBadLaunch = 2u, kStatusBadEntry = 4u };
 
 struct DeviceStatus {
   uint32_t word;     // OR of kStatus* bits

@@ -26,7 +26,14 @@ enum KernelClass : int {
   kClsGemmDualMlpOut = 11, // dual-stream MLP-out + gated residual
   kClsGemmSingleOut = 12,  // single-stream out-projection over [attn | act] + gated residual
   kClsQuantAct = 13,       // per-row e4m3 quantisation of an out-projection's input
-  kClsCount = 14
+  kClsTextRope = 14,       // rotary table of 1-D positions
+  kClsQKNormRope = 15,     // per-head RMSNorm + rotation of queries and keys
+  kClsTextAttention = 16,  // grouped-head attention over packed sequences
+  kClsTextJoin = 17,       // joining its key splits
+  kClsQuantBlocks = 18,    // e4m3 quantisation with a scale per block
+  kClsLinearFp8Blocks = 19,  // e4m3 product with block scales
+  kClsLinearFp8Join = 20,  // joining its depth splits
+  kClsCount = 21
 };
 
 const char* kernel_class_name(int cls);
@@ -185,5 +192,66 @@ cudaError_t launch_gemm(const GemmProblemHost* probs, int nprob, int batch, floa
 // ---------------------------------------------------------------------------------
 cudaError_t launch_attention(int batch, int heads, int n, const bf16* q, const bf16* k, const bf16* v, bf16* out,
                              int ld_out, DeviceStatus* status, cudaStream_t s);
+
+// ---------------------------------------------------------------------------------
+// Text-side operations
+// ---------------------------------------------------------------------------------
+constexpr uint32_t kSiteTextLengths = 0x501, kSiteTextRow = 0x601;
+
+// An entry of a device array is out of range: record it (the first site wins) and skip it.
+__device__ __forceinline__ void report_bad_entry(DeviceStatus* status, uint32_t site) {
+  if (atomicOr(&status->word, kStatusBadEntry) == 0u) atomicExch(&status->where, site);
+}
+
+// freq: turns per position of each pair as 64-bit fixed point (2^64 = one turn).
+struct TextRopeArgs {
+  uint64_t freq[128];
+  int half;
+  float magnitude;
+  const int32_t* pos;
+  int n;
+  float* table;
+};
+cudaError_t launch_text_rope(const TextRopeArgs& a, cudaStream_t s);
+
+struct QKNormRopeArgs {
+  int rows, heads_q, heads_k, head_dim, rot_dim, layout;
+  const bf16 *q, *k, *q_norm, *k_norm;
+  long long ldq, ldk, ldq_out, ldk_out;
+  float eps;
+  const float* table;
+  int table_rows;
+  const int32_t* table_row;
+  bf16 *q_out, *k_out;
+  DeviceStatus* status;
+};
+cudaError_t launch_qk_norm_rope(const QKNormRopeArgs& a, cudaStream_t s);
+
+struct TextAttnArgs {
+  int seqs, heads_q, heads_k, head_dim, rows_q, rows_k, max_q, max_k, causal;
+  float scale;
+  const int32_t *q_off, *q_len, *k_off, *k_len;
+  const bf16 *q, *k, *v;
+  bf16* out;
+  long long ldq, ldk, ldv, ldo;
+  DeviceStatus* status;
+  float* parts;  // workspace of the key splits
+};
+size_t text_attention_parts_bytes(const TextAttnArgs& a);
+cudaError_t launch_text_attention(const TextAttnArgs& a, cudaStream_t s);
+
+cudaError_t launch_quantize_blocks(const bf16* x, long long ld, int rows, int cols, int block_rows, uint8_t* q,
+                                   float* scale, cudaStream_t s);
+struct LinearFp8Args {
+  int rows, n, k;
+  const uint8_t *a, *w;
+  const float *a_scale, *w_scale;
+  bf16* out;
+  int ld_out;
+  DeviceStatus* status;
+  float* parts;  // workspace of the depth splits
+};
+size_t linear_fp8_parts_bytes(int rows, int n, int k);
+cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
 
 }  // namespace dit

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(PKG, "libdit.so")
 
 DIT_OK, DIT_ERR_INVALID_ARG, DIT_ERR_UNSUPPORTED, DIT_ERR_WORKSPACE, DIT_ERR_CUDA, DIT_ERR_TIMEOUT = range(6)
 DIT_EPI_STORE, DIT_EPI_GATED_RESIDUAL, DIT_EPI_SWIGLU = range(3)
+DIT_ROPE_INTERLEAVED, DIT_ROPE_HALF = range(2)
+DIT_ROPE_SCALE_NONE, DIT_ROPE_SCALE_LINEAR, DIT_ROPE_SCALE_NTK, DIT_ROPE_SCALE_BY_PARTS = range(4)
 
 
 class DitError(RuntimeError):
@@ -73,6 +75,16 @@ class dit_weights(C.Structure):
                 ("dual_fp8", C.POINTER(dit_dual_fp8))]
 
 
+class dit_text_rope(C.Structure):
+    _fields_ = [("rot_dim", C.c_int), ("theta", C.c_double), ("scaling", C.c_int), ("factor", C.c_double),
+                ("low", C.c_double), ("high", C.c_double), ("original_len", C.c_int), ("magnitude", C.c_double)]
+
+
+class dit_text_attn(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("seqs", "heads_q", "heads_k", "head_dim", "rows_q", "rows_k", "max_q", "max_k",
+                                       "causal")] + [("scale", C.c_float)]
+
+
 _P = C.c_void_p
 _I = C.c_int
 _SZ = C.c_size_t
@@ -105,6 +117,15 @@ _SIGS = {
     "dit_graph_launch": (_I, [_P, _P]),
     "dit_graph_destroy": (_I, [_P]),
     "dit_selftest_wait_timeout": (_I, [_P, _SZ, C.c_uint, _P]),
+    "dit_text_rope_table": (_I, [C.POINTER(dit_text_rope), _P, _I, _P, _P]),
+    "dit_qk_norm_rope": (_I, [_I, _I, _I, _I, _I, _I, _P, _LL, _P, _LL, _P, _P, _F, _P, _I, _P, _P, _LL, _P, _LL, _P,
+                              _SZ, _P]),
+    "dit_text_attention_workspace": (_I, [C.POINTER(dit_text_attn), C.POINTER(_SZ)]),
+    "dit_text_attention": (_I, [C.POINTER(dit_text_attn), _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _SZ,
+                                _P]),
+    "dit_quantize_blocks_fp8": (_I, [_P, _LL, _I, _I, _I, _P, _P, _P]),
+    "dit_linear_fp8_blocks_workspace": (_I, [_I, _I, _I, C.POINTER(_SZ)]),
+    "dit_linear_fp8_blocks": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "dit_launch_count": (C.c_ulonglong, []),
     "dit_timing_begin": (_I, [_I]),
     "dit_timing_select": (_I, [C.c_uint]),
@@ -169,6 +190,18 @@ def make_shape(batch, n_txt, n_img, n_ref=0) -> dit_shape:
     s = dit_shape()
     s.batch, s.n_txt, s.n_img, s.n_ref = batch, n_txt, n_img, n_ref
     return s
+
+
+def make_text_rope(rot_dim, theta=10000.0, scaling=DIT_ROPE_SCALE_NONE, factor=1.0, low=1.0, high=4.0, original_len=1,
+                   magnitude=1.0) -> dit_text_rope:
+    return dit_text_rope(rot_dim, theta, scaling, factor, low, high, original_len, magnitude)
+
+
+def make_text_attn(seqs, heads_q, heads_k, head_dim, rows_q, rows_k, max_q, max_k, causal=True,
+                   scale=None) -> dit_text_attn:
+    """Sizes of a dit_text_attention call; `scale` None means 1 / sqrt(head_dim)."""
+    return dit_text_attn(seqs, heads_q, heads_k, head_dim, rows_q, rows_k, max_q, max_k, 1 if causal else 0,
+                         head_dim ** -0.5 if scale is None else scale)
 
 
 # ---------------------------------------------------------------------------------- calls
@@ -275,10 +308,11 @@ def dit_graph_destroy(graph: int):
 
 
 def dit_sync_status(ws, stream=None):
-    """Returns (status, where).  Does not raise on DIT_ERR_TIMEOUT."""
+    """Returns (status, where).  Does not raise on DIT_ERR_TIMEOUT or DIT_ERR_INVALID_ARG (an
+    entry out of range in a device array), only on a CUDA error."""
     where = C.c_uint32(0)
     st = lib().dit_sync_status(_ptr(ws), _stream(stream), C.byref(where))
-    if st not in (DIT_OK, DIT_ERR_TIMEOUT):
+    if st not in (DIT_OK, DIT_ERR_TIMEOUT) and not (st == DIT_ERR_INVALID_ARG and where.value):
         _check("dit_sync_status", st)
     return st, where.value
 
@@ -299,6 +333,51 @@ def dit_linear(batch, rows, n_out, k, a_dev, w_dev, out_dev, ld_out, epi, gate_d
 def dit_attention(batch, heads, n, q_dev, k_dev, v_dev, out_dev, ld_out, ws, ws_bytes, stream=None):
     _check("dit_attention", lib().dit_attention(batch, heads, n, _ptr(q_dev), _ptr(k_dev), _ptr(v_dev), _ptr(out_dev),
                                                  ld_out, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dit_text_rope_table(rope: dit_text_rope, pos_dev, n: int, table_dev, stream=None):
+    _check("dit_text_rope_table", lib().dit_text_rope_table(C.byref(rope), _ptr(pos_dev), n, _ptr(table_dev),
+                                                            _stream(stream)))
+
+
+def dit_qk_norm_rope(rows, heads_q, heads_k, head_dim, rot_dim, layout, q_dev, ldq, k_dev, ldk, q_norm, k_norm, eps,
+                     table_dev, table_rows, table_row_dev, q_out_dev, ldq_out, k_out_dev, ldk_out, ws, ws_bytes,
+                     stream=None):
+    _check("dit_qk_norm_rope", lib().dit_qk_norm_rope(
+        rows, heads_q, heads_k, head_dim, rot_dim, layout, _ptr(q_dev), ldq, _ptr(k_dev), ldk, _ptr(q_norm),
+        _ptr(k_norm), eps, _ptr(table_dev), table_rows, _ptr(table_row_dev), _ptr(q_out_dev), ldq_out,
+        _ptr(k_out_dev), ldk_out, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dit_text_attention_workspace(a: dit_text_attn) -> int:
+    n = _SZ(0)
+    _check("dit_text_attention_workspace", lib().dit_text_attention_workspace(C.byref(a), C.byref(n)))
+    return n.value
+
+
+def dit_text_attention(a: dit_text_attn, q_off, q_len, k_off, k_len, q_dev, ldq, k_dev, ldk, v_dev, ldv, out_dev, ldo,
+                       ws, ws_bytes, stream=None):
+    _check("dit_text_attention", lib().dit_text_attention(
+        C.byref(a), _ptr(q_off), _ptr(q_len), _ptr(k_off), _ptr(k_len), _ptr(q_dev), ldq, _ptr(k_dev), ldk,
+        _ptr(v_dev), ldv, _ptr(out_dev), ldo, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dit_quantize_blocks_fp8(x_dev, ld, rows, cols, block_rows, q_dev, scale_dev, stream=None):
+    _check("dit_quantize_blocks_fp8", lib().dit_quantize_blocks_fp8(_ptr(x_dev), ld, rows, cols, block_rows,
+                                                                     _ptr(q_dev), _ptr(scale_dev), _stream(stream)))
+
+
+def dit_linear_fp8_blocks_workspace(rows, n_out, k) -> int:
+    n = _SZ(0)
+    _check("dit_linear_fp8_blocks_workspace", lib().dit_linear_fp8_blocks_workspace(rows, n_out, k, C.byref(n)))
+    return n.value
+
+
+def dit_linear_fp8_blocks(rows, n_out, k, a_q_dev, a_scale_dev, w_q_dev, w_scale_dev, out_dev, ld_out, ws, ws_bytes,
+                          stream=None):
+    _check("dit_linear_fp8_blocks", lib().dit_linear_fp8_blocks(
+        rows, n_out, k, _ptr(a_q_dev), _ptr(a_scale_dev), _ptr(w_q_dev), _ptr(w_scale_dev), _ptr(out_dev), ld_out,
+        _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def dit_modulation_static(w: dit_weights, sigma_dev, batch: int, mod_dev, stream=None):

@@ -276,9 +276,11 @@ dit_status dit_step_host(const dit_weights* w, const dit_shape* shape, const voi
                          dit_stream_t stream);
 
 /* Synchronise `stream`, read and clear the workspace's device status word.  Returns
- * DIT_ERR_TIMEOUT if a kernel gave up on a wait since the last call, else DIT_OK
- * (or DIT_ERR_CUDA if the stream reports an error).  *where_out (may be NULL) receives
- * the id of the first wait that gave up. */
+ * DIT_ERR_TIMEOUT if a kernel gave up on a wait since the last call, else
+ * DIT_ERR_INVALID_ARG if a kernel met a length, start or position out of range in a device
+ * array (text-side operations), else DIT_OK (or DIT_ERR_CUDA if the stream reports an
+ * error).  *where_out (may be NULL) receives the id of the first wait that gave up, or of the
+ * check that failed. */
 dit_status dit_sync_status(void* ws, dit_stream_t stream, uint32_t* where_out);
 
 /* ---- CUDA graphs of a step (fixed shape and buffers) ------------------------------ */
@@ -345,6 +347,148 @@ dit_status dit_linear(int batch, int rows, int n_out, int k, const void* a_dev, 
  * workspace of >= 256 bytes (only its status word is used). */
 dit_status dit_attention(int batch, int heads, int n, const void* q_dev, const void* k_dev, const void* v_dev,
                          void* out_dev, int ld_out, void* ws, size_t ws_bytes, dit_stream_t stream);
+
+/* ---- Text-side operations (the text encoder in front of the step) -------------------- */
+
+/* The step reads text features [n_txt, txt_dim] that a language model produces.  These
+ * operations are what such a model's layers are made of, beside the step's own components:
+ * 1-D rotary tables, per-head norms with the rotation, causal grouped-head attention over
+ * packed sequences, and e4m3 products with a scale per block of 128.  None of them is
+ * described on the pages; each states its formula.  All are forward only.
+ *
+ * Lengths, starts and positions are DEVICE int32 arrays, so a captured graph can be replayed
+ * with other lengths.  The host cannot see them: the kernels check each one, and an entry
+ * that is out of range is skipped (what it would have written stays as it was) and recorded
+ * in the workspace status word, which dit_sync_status then reports as
+ * DIT_ERR_INVALID_ARG with the site id 0x501 (attention) or 0x601 (rotation). */
+
+/* Which values of a head turn together: adjacent pairs (2j, 2j + 1), or the halves
+ * (j, j + rot_dim / 2) of the head's first rot_dim values. */
+typedef enum { DIT_ROPE_INTERLEAVED = 0, DIT_ROPE_HALF = 1 } dit_rope_layout;
+
+/* How a rotation is stretched to contexts longer than the trained one.  With
+ * w_j = theta^(-2j / rot_dim), j < rot_dim / 2, and f = factor:
+ *   NONE      w_j
+ *   LINEAR    w_j / f
+ *   NTK       (theta * f^(rot_dim / (rot_dim - 2)))^(-2j / rot_dim)
+ *   BY_PARTS  g w_j + (1 - g) w_j / f, g = clamp((t - low) / (high - low), 0, 1), where
+ *             t = w_j original_len / (2 pi) is the number of turns over the trained length:
+ *             fast pairs stay, slow ones are interpolated */
+typedef enum {
+  DIT_ROPE_SCALE_NONE = 0,
+  DIT_ROPE_SCALE_LINEAR = 1,
+  DIT_ROPE_SCALE_NTK = 2,
+  DIT_ROPE_SCALE_BY_PARTS = 3
+} dit_rope_scaling;
+
+/* rot_dim: even, 2 .. 256 (NTK: >= 4).  theta in (1, 1e12].  factor in [1, 1e6] and, for
+ * BY_PARTS, 0 <= low < high and original_len >= 1; they are ignored where unused.
+ * magnitude: cosines and sines are multiplied by it (1 for none), finite, > 0. */
+typedef struct {
+  int rot_dim;
+  double theta;
+  dit_rope_scaling scaling;
+  double factor, low, high;
+  int original_len;
+  double magnitude;
+} dit_text_rope;
+
+/* Rotary table of n positions: table_dev[(i * rot_dim / 2 + j) * 2 + {0, 1}] =
+ * magnitude * {cos, sin}(p_i w'_j), w' from dit_text_rope.  pos_dev [n] int32 device, any
+ * values (negative ones turn backwards), or NULL for 0 .. n - 1; table_dev
+ * [n, rot_dim / 2, 2] fp32 device.  The angle is reduced in 64-bit fixed-point turns: for
+ * |p| <= 2^24 an entry is within 4 * 2^-24 * magnitude of the real number.
+ * 0 <= n <= 2^24. */
+dit_status dit_text_rope_table(const dit_text_rope* rope, const int32_t* pos_dev, int n, float* table_dev,
+                               dit_stream_t stream);
+
+/* RMSNorm of every query and key head, and its rotation, in one pass.  For each row r and
+ * each head x [head_dim] of q_dev (heads_q of them) and k_dev (heads_k):
+ *   y = x / sqrt(mean(x^2) + eps) * w          (q_norm for queries, k_norm for keys)
+ *   (y_a, y_b) <- (y_a c - y_b s, y_b c + y_a s) for the rot_dim / 2 pairs of `layout`,
+ *   c, s = table_dev[t, pair], t = table_row_dev[r], or r where table_row_dev is NULL;
+ * values from rot_dim on stay y.  fp32 arithmetic, one rounding to bf16 at the end.
+ * q_norm and k_norm [head_dim] bf16: both NULL for the rotation alone (no norm), else both
+ * given.  Head h of row r is at q_dev + r * ldq + h * head_dim, the outputs likewise with
+ * ldq_out, ldk_out.  The outputs may be the inputs themselves (same pointer and stride);
+ * any other overlap is DIT_ERR_INVALID_ARG.  heads_k may be 0 (k pointers ignored).
+ * table_dev [table_rows, rot_dim / 2, 2] fp32.  A row whose index lies outside
+ * [0, table_rows) is left as it was and recorded (see above); without table_row_dev,
+ * rows <= table_rows.
+ * head_dim 64 or 128, rot_dim % 8 == 0, 0 <= rot_dim <= head_dim (0: no rotation, table_dev
+ * NULL); ld* % 8 == 0 and >= heads * head_dim, <= 2^24; 0 <= rows <= 2^26, heads_q and
+ * heads_k <= 1024, heads_q >= 1; eps >= 0 and finite.  ws: any workspace of >= 256 bytes
+ * (only its status word is used). */
+dit_status dit_qk_norm_rope(int rows, int heads_q, int heads_k, int head_dim, int rot_dim, dit_rope_layout layout,
+                            const void* q_dev, long long ldq, const void* k_dev, long long ldk, const void* q_norm,
+                            const void* k_norm, float eps, const float* table_dev, int table_rows,
+                            const int32_t* table_row_dev, void* q_out_dev, long long ldq_out, void* k_out_dev,
+                            long long ldk_out, void* ws, size_t ws_bytes, dit_stream_t stream);
+
+/* Sizes of one dit_text_attention call.  heads_q % heads_k == 0, heads_q / heads_k <= 64,
+ * head_dim 64 or 128; 0 <= seqs <= 16384; rows_q and rows_k (rows of the whole buffers)
+ * 0 .. 2^28; max_q and max_k: upper bounds of the sequences' lengths, 0 .. 2^24, which choose
+ * how the work is split; scale > 0 and finite (the usual one is 1 / sqrt(head_dim)). */
+typedef struct {
+  int seqs, heads_q, heads_k, head_dim;
+  int rows_q, rows_k, max_q, max_k;
+  int causal;
+  float scale;
+} dit_text_attn;
+
+/* Bytes of workspace that dit_text_attention needs for these sizes (at least the 256 of the
+ * status word; more where the keys of few rows are split over the GPU). */
+dit_status dit_text_attention_workspace(const dit_text_attn* a, size_t* bytes);
+
+/* Attention with grouped heads over packed or padded sequences.  Sequence s has the query
+ * rows [q_off[s], q_off[s] + nq) and the key rows [k_off[s], k_off[s] + nk), where
+ * nq = q_len[s], or q_off[s + 1] - q_off[s] where q_len is NULL (nk likewise).  For each of
+ * its queries i < nq and heads h < heads_q, with the keys and values of head
+ * h / (heads_q / heads_k):
+ *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j   over the visible keys j < nk,
+ * all of them, or with `causal` those with j <= i + nk - nq (the last query sees the last
+ * key: nq = nk is a whole prompt, nq = 1 a new token over a cache that holds its key).
+ * A query that sees no key (nk == 0, or causal with nk < nq) gets zeros.
+ * q_dev + row * ldq + h * head_dim, k and v likewise with heads_k, out_dev + row * ldo +
+ * h * head_dim; all bf16.  Rows of out_dev that belong to no sequence are not written, rows
+ * behind a sequence's keys not used, whatever they hold.  A visible value that is infinite
+ * or NaN reaches the queries that see it, and no others.
+ * Sequences may share key rows; query rows of two sequences must not overlap.
+ * Scores, statistics and sums in fp32; the probabilities are rounded to bf16 for the product
+ * with V.  The order of sums depends only on the sizes and lengths: equal calls give equal bits.
+ * q_off and k_off [seqs + 1] (the last entry is read only without lengths), q_len and k_len
+ * [seqs] int32 device.  ld* % 8 == 0, >= heads * head_dim, <= 2^24.  out_dev must not overlap
+ * the elements of q_dev, k_dev or v_dev (columns of one buffer may interleave). */
+dit_status dit_text_attention(const dit_text_attn* a, const int32_t* q_off, const int32_t* q_len,
+                              const int32_t* k_off, const int32_t* k_len, const void* q_dev, long long ldq,
+                              const void* k_dev, long long ldk, const void* v_dev, long long ldv, void* out_dev,
+                              long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream);
+
+/* e4m3 copy of a bf16 matrix with one fp32 scale per block of block_rows x 128 values:
+ * block_rows 1 for activations (a scale per row and 128 columns), 128 for weights.
+ *   m = max(max|x| over the block, 448 * 2^-118),  scale = m / 448,
+ *   q = e4m3(x * (448 / m)),  each operation rounded to fp32, the last to nearest even.
+ * x_dev [rows, cols] with row stride ld; q_dev [rows, cols] bytes, contiguous; scale_dev
+ * [ceil(rows / block_rows), ceil(cols / 128)].  The last blocks of a row or column may be
+ * short.  A NaN becomes the NaN code of its place; an infinity makes its block's products NaN.
+ * cols % 16 == 0, ld % 8 == 0, ld >= cols, 1 <= rows, cols <= 2^20. */
+dit_status dit_quantize_blocks_fp8(const void* x_dev, long long ld, int rows, int cols, int block_rows, void* q_dev,
+                                   float* scale_dev, dit_stream_t stream);
+
+/* Bytes of workspace that dit_linear_fp8_blocks needs (at least the 256 of the status word;
+ * more where the depth of a product with few rows is split over the GPU). */
+dit_status dit_linear_fp8_blocks_workspace(int rows, int n_out, int k, size_t* bytes);
+
+/* Linear layer on e4m3 operands with block scales:
+ *   out[r, c] = sum_b a_scale[r, b] w_scale[c / 128, b] sum_{i in block b} a_q[r, i] w_q[c, i],
+ * blocks of 128 along k, every sum in fp32, one rounding to bf16.  a_q [rows, k] and a_scale
+ * [rows, ceil(k / 128)] from dit_quantize_blocks_fp8 with block_rows 1, w_q [n_out, k] and
+ * w_scale [ceil(n_out / 128), ceil(k / 128)] with block_rows 128; out_dev [rows, ld_out]
+ * written at columns [0, n_out).  k % 16 == 0, n_out % 8 == 0, ld_out % 8 == 0,
+ * ld_out >= n_out; 1 <= rows, n_out, k <= 2^20, else DIT_ERR_INVALID_ARG. */
+dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev, const float* a_scale_dev,
+                                 const void* w_q_dev, const float* w_scale_dev, void* out_dev, int ld_out, void* ws,
+                                 size_t ws_bytes, dit_stream_t stream);
 
 /* ---- Allocation-free variant -------------------------------------------------------- */
 
