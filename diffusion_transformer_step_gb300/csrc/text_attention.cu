@@ -1,9 +1,53 @@
-// Attention with grouped heads over packed or padded sequences, causal or not.
+// Attention with grouped heads over packed or padded sequences, causal or not: whole prompts,
+// their last parts over a cache, single new tokens.
+//
+// The query heads that share a key head are rows of one tile: row r of a 128-row tile is query
+// token r / G and head r % G of the group (G = heads_q / heads_k), so a key tile is read once for
+// the whole group and a short sequence still fills its tile.  TQ = 128 / G tokens per tile, two
+// tiles (2 TQ tokens) per CTA.
+//
+// text_attention_kernel, one CTA per (pair of query tiles, key head, key split), 320 threads, is
+// the two-tile pipeline of the joint attention: warp 0 loads (Q through a 4-D tensor map whose
+// box is G heads x TQ tokens), warp 1 issues S_t = Q_t K^T and O_t += P_t V on tcgen05 with P
+// read from Tensor Memory, warps 2-5 and 6-9 run one tile's softmax each, one thread per row,
+// with the lazy running maximum.  What is different here:
+//   - Masks.  Row r sees the keys below its own limit (causal: token + 1 + nk - nq), compared per
+//     thread, only in the key blocks that a warp's rows do not see whole.  A tile runs only as
+//     many key blocks as its last token sees.  A row that sees nothing keeps m = -inf, l = 0 and
+//     writes zeros.
+//   - Keys past the sequence's end are other sequences' or unwritten memory.  Their scores are
+//     replaced, not added to; their V rows, which a zero probability would not silence if they
+//     hold NaN, are zeroed in shared memory before the last block's MMA.
+//   - V rows that a causal row must not see but its tile needs can hold NaN as well.  A row whose
+//     output is not finite looks at the (under 256) keys behind its limit that its tile took in,
+//     and if one of them is to blame computes itself again, alone.
+//   - Work order.  Tiles are dealt out longest first over all sequences (tile index within its
+//     sequence, descending), so the last wave holds the short ones.  For up to 64 sequences each
+//     CTA finds its tile itself: with n_s tiles in sequence s, C(v) = sum max(0, n_s - v) tiles
+//     have an index >= v, and a search over v takes a few warp sums.  For more, a one-CTA kernel
+//     lists the tiles first.
+//   - Key splits.  Where tiles x key heads leave SMs idle, the keys of a tile are cut into equal
+//     runs of blocks whose unnormalised outputs, maxima and sums go to the workspace, and
+//     text_attention_join_kernel adds them up in split order.
+#include <math.h>
+
+#include <atomic>
+
 #include "runtime.h"
+#include "tc_attention.cuh"
 
 namespace dit {
 
 namespace {
+
+constexpr int kThreads = 320;
+constexpr int kKeys = 128;                     // keys per block
+constexpr uint32_t kHalfBytes = 128 * 64 * 2;  // 64 dims of a 128-row tile
+constexpr uint32_t kTmemCols = 512;
+constexpr float kPsumLimit = 4096.0f;  // row sum of P that sends a key block down the slow path
+constexpr int kInlineSeqs = 64;        // up to here a CTA finds its tile itself
+constexpr int kSMs = 152;
+constexpr int kLevels = 1024;          // tile-index levels of the listing kernel
 
 struct Span {
   int q0, nq, k0, nk;
@@ -24,62 +68,698 @@ __device__ __forceinline__ Span load_span(const TextAttnArgs& a, int s) {
   return r;
 }
 
-// One warp per (query row of a sequence, query head): the running maximum and sum of the
-// softmax over one pass of the keys, each lane holding head_dim / 32 values.
+struct Plan {
+  int group, tq, tp;   // heads per key head, tokens per tile and per pair
+  int tiles, levels;   // bounds of the pairs over all sequences, and of one sequence's
+  int splits;
+  bool list;
+};
+
+Plan make_plan(const TextAttnArgs& a) {
+  Plan p;
+  p.group = a.heads_q / a.heads_k;
+  p.tq = 128 / p.group;
+  p.tp = 2 * p.tq;
+  p.levels = (a.max_q + p.tp - 1) / p.tp;
+  const long long packed = (long long)a.rows_q / p.tp + a.seqs, padded = (long long)a.seqs * p.levels;
+  p.tiles = (int)(packed < padded ? packed : padded);
+  p.list = a.seqs > kInlineSeqs;
+  // Splits only fill SMs that would stay idle, and leave each part four key blocks: a part costs
+  // a fixed ~3 us (launch, first loads, join) against ~1.3 us per block.
+  const long long items = (long long)p.tiles * a.heads_k;
+  const int blocks = (a.max_k + kKeys - 1) / kKeys;
+  p.splits = 1;
+  if (items > 0 && items < kSMs) {
+    int s = (int)(kSMs / items);
+    if (s > blocks / 4) s = blocks / 4;
+    if (s > 32) s = 32;
+    p.splits = s < 1 ? 1 : s;
+  }
+  return p;
+}
+
+// Workspace: the tile list, then per tile its first output row and token count, then the splits'
+// (max, sum) and unnormalised outputs, 256 rows per (tile, key head, split).
+struct Parts {
+  size_t list, desc, ml, o, total;
+};
+inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+Parts parts_layout(const Plan& p, int heads_k, int head_dim) {
+  Parts l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at = up256(at + bytes);
+    return r;
+  };
+  const size_t items = p.splits > 1 ? (size_t)p.tiles * heads_k * p.splits : 0;
+  l.list = take(p.list ? (size_t)p.tiles * 8 : 0);
+  l.desc = take(p.splits > 1 ? (size_t)p.tiles * 8 : 0);
+  l.ml = take(items * 256 * 8);
+  l.o = take(items * 256 * (size_t)head_dim * 4);
+  l.total = at;
+  return l;
+}
+
+struct alignas(64) TextAttnParams {
+  CUtensorMap q_map, k_map, v_map;
+  TextAttnArgs a;
+  int group, tq, levels, tiles, splits;
+  float scale_log2;
+  const int2* list;
+  int2* desc;
+  float2* ml;
+  float* o;
+};
+
+enum : uint32_t { kSiteQ = 0x511, kSiteFree, kSiteReady, kSitePFull, kSiteSFull, kSiteODone, kSiteFixed, kSiteFix };
+
 template <int D>
-__global__ void text_attention_simple_kernel(const TextAttnArgs a) {
-  constexpr int V = D / 32;
+struct Smem {
+  static constexpr uint32_t kTile = (D / 64) * kHalfBytes;  // a 128-row tile of Q, K or V
+  static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBar = 6 * kTile;
+  static constexpr size_t kBytes = 1024 + kBar + 256;
+};
+
+// The t-th pair of tiles, longest first (whole warp; span and tile index broadcast).
+__device__ __forceinline__ bool find_tile(const TextAttnArgs& a, int tp, int levels, int tiles, int t, int lane,
+                                          Span& sp, int& index) {
+  Span s[2];
+  int n[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int id = lane + 32 * i;
+    s[i] = Span{0, 0, 0, 0, true};
+    if (id < a.seqs) s[i] = load_span(a, id);
+    n[i] = (s[i].nq + tp - 1) / tp;
+    if (!s[i].ok && blockIdx.x == 0) report_bad_entry(a.status, kSiteTextLengths);
+  }
+  auto count = [&](int v) { return __reduce_add_sync(0xffffffffu, max(0, n[0] - v) + max(0, n[1] - v)); };
+  const int all = count(0);
+  // more tiles than the buffers' rows allow: query rows of several sequences overlap
+  if (all > tiles && blockIdx.x == 0 && lane == 0) report_bad_entry(a.status, kSiteTextLengths);
+  if (all <= t) return false;
+  int lo = 0, hi = levels;  // count(lo) > t >= count(hi)
+  while (hi - lo > 1) {
+    const int v = (lo + hi) >> 1;
+    if (count(v) > t) lo = v;
+    else hi = v;
+  }
+  index = lo;
+  int r = t - count(lo + 1);  // the r-th sequence with more than `lo` tiles
+  const uint32_t b0 = __ballot_sync(0xffffffffu, n[0] > lo), b1 = __ballot_sync(0xffffffffu, n[1] > lo);
+  const int second = r >= __popc(b0);
+  const uint32_t b = second ? b1 : b0;
+  if (second) r -= __popc(b0);
+  const bool me = ((b >> lane) & 1u) && __popc(b & ((1u << lane) - 1u)) == r;
+  const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+  sp.q0 = __shfl_sync(0xffffffffu, second ? s[1].q0 : s[0].q0, src);
+  sp.nq = __shfl_sync(0xffffffffu, second ? s[1].nq : s[0].nq, src);
+  sp.k0 = __shfl_sync(0xffffffffu, second ? s[1].k0 : s[0].k0, src);
+  sp.nk = __shfl_sync(0xffffffffu, second ? s[1].nk : s[0].nk, src);
+  return true;
+}
+
+// Lists the pairs of tiles (sequence, index), longest first up to kLevels steps: a histogram of
+// the tiles' levels, its running sum from the top, then every tile to the next place of its
+// level.  Unused places get sequence -1.
+__global__ void __launch_bounds__(1024) text_attention_list_kernel(const TextAttnArgs a, int tp, int levels, int tiles,
+                                                                   int2* list) {
+  __shared__ int at[kLevels];
+  __shared__ int total, warp_sum[32];
   grid_dependency_wait();
   allow_dependents();
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int h = blockIdx.y, s = blockIdx.z;
-  const Span sp = load_span(a, s);
-  if (!sp.ok) {
-    if (threadIdx.x == 0) report_bad_entry(a.status, kSiteTextLengths);
-    return;
+  const int t = threadIdx.x;
+  at[t] = 0;
+  __syncthreads();
+  const int shift = levels <= kLevels ? 0 : 32 - __clz((levels - 1) / kLevels);
+  for (int s = t; s < a.seqs; s += 1024) {
+    const Span sp = load_span(a, s);
+    if (!sp.ok) report_bad_entry(a.status, kSiteTextLengths);
+    const int n = (sp.nq + tp - 1) / tp;
+    for (int i = 0; i < n; ++i) atomicAdd(&at[i >> shift], 1);
   }
-  if (i >= sp.nq) return;
-  const int hk = h / (a.heads_q / a.heads_k);
-  const bf16* qp = a.q + (long long)(sp.q0 + i) * a.ldq + h * D + lane * V;
-  float q[V], o[V];
+  __syncthreads();
+  // thread t: the tiles of the levels above level kLevels - 1 - t
+  const int mine = at[kLevels - 1 - t];
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if ((t & 31) >= o) sum += v;
+  }
+  if ((t & 31) == 31) warp_sum[t >> 5] = sum;
+  __syncthreads();
+  for (int w = 0; w < (t >> 5); ++w) sum += warp_sum[w];
+  at[kLevels - 1 - t] = sum - mine;
+  if (t == kLevels - 1) total = sum;
+  __syncthreads();
+  if (t == 0 && total > tiles) report_bad_entry(a.status, kSiteTextLengths);
+  for (int s = t; s < a.seqs; s += 1024) {
+    const int n = (load_span(a, s).nq + tp - 1) / tp;
+    for (int i = 0; i < n; ++i) {
+      const int p = atomicAdd(&at[i >> shift], 1);
+      if (p < tiles) list[p] = make_int2(s, i);
+    }
+  }
+  for (int p = total + t; p < tiles; p += 1024) list[p] = make_int2(-1, 0);
+}
+
+// ---- tensor-core work ------------------------------------------------------------------
+
+template <int D>
+struct Descs {
+  uint64_t q[2][D / 16], k[2][D / 16], v[2][8];
+};
+
+template <int D>
+__device__ __forceinline__ void make_descs(uint8_t* smem, Descs<D>& d) {
+  using L = Smem<D>;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+      d.q[t][kk] = make_sdesc_sw128(smem_u32(smem + L::kQ + t * L::kTile) + off, 16, 1024);
+      d.k[t][kk] = make_sdesc_sw128(smem_u32(smem + L::kK + t * L::kTile) + off, 16, 1024);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      d.v[t][kk] = make_sdesc_sw128(smem_u32(smem + L::kV + t * L::kTile) + kk * 2048, kHalfBytes, 1024);
+  }
+}
+
+template <int ST>
+__device__ __forceinline__ void issue_qk(const Descs<128>& d, uint32_t tmem, int t, uint32_t idesc, uint64_t* bar) {
+  umma8_ss(tmem + (uint32_t)(t * 256), d.q[t], d.k[ST], idesc);
+  umma_commit(bar);
+}
+template <int ST>
+__device__ __forceinline__ void issue_qk(const Descs<64>& d, uint32_t tmem, int t, uint32_t idesc, uint64_t* bar) {
+  umma4_ss(tmem + (uint32_t)(t * 256), d.q[t], d.k[ST], idesc);
+  umma_commit(bar);
+}
+
+struct Bars {
+  uint64_t *q_full, *ready, *slot_free, *s_full, *p_full, *o_done, *fixed, *drain;
+};
+
+// Key block j of the issuer (ring stage ST = j & 1), n[t] blocks for tile t:
+//   O0 += P0 V_j, S0 = Q0 K_{j+1}^T, O1 += P1 V_j, S1 = Q1 K_{j+1}^T.
+template <int D, int ST>
+__device__ __forceinline__ bool mma_block(const Descs<D>& d, uint32_t tmem, int j, int n0, int n1, bool fix,
+                                          uint32_t idesc_qk, uint32_t idesc_pv, const Bars& bar, const WaitCtx& wc) {
+  if (!mbar_wait(&bar.ready[ST], (uint32_t)(j >> 1) & 1u, wc, kSiteReady)) return false;
+  if (fix && j + 1 == max(n0, n1) && !mbar_wait(bar.fixed, 0, wc, kSiteFixed)) return false;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int n = t ? n1 : n0;
+    if (j < n) {
+      if (!mbar_wait(&bar.p_full[t], (uint32_t)j & 1u, wc, kSitePFull)) return false;
+      tc_fence_after();
+      umma8_ts(tmem + (uint32_t)(t * 256 + 128), tmem + (uint32_t)(t * 256), d.v[ST], idesc_pv, j > 0 ? 1u : 0u);
+      if (j + 1 < n) issue_qk<ST ^ 1>(d, tmem, t, idesc_qk, &bar.s_full[t]);
+      else umma_commit(&bar.o_done[t]);
+    }
+  }
+  return true;
+}
+
+// One row alone, by a whole warp: keys [j0, j1) of the sequence.  Lane l holds dims
+// [l D/32, (l + 1) D/32).  m in log2 units.
+template <int D>
+__device__ __noinline__ void attend_row(const TextAttnArgs& a, const bf16* qp, const bf16* kp, const bf16* vp, int n,
+                                        float c, int lane, float& m, float& l, float (&o)[D / 32]) {
+  constexpr int V = D / 32;
+  float q[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    q[e] = __bfloat162float(qp[e]) * a.scale;
+    q[e] = __bfloat162float(qp[lane * V + e]);
     o[e] = 0.f;
   }
-  const int end = a.causal ? min(sp.nk, i + sp.nk - sp.nq + 1) : sp.nk;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < end; ++j) {
-    const bf16* kp = a.k + (long long)(sp.k0 + j) * a.ldk + hk * D + lane * V;
-    const bf16* vp = a.v + (long long)(sp.k0 + j) * a.ldv + hk * D + lane * V;
+  m = -INFINITY;
+  l = 0.f;
+  for (int j = 0; j < n; ++j) {
     float x = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) x += q[e] * __bfloat162float(kp[e]);
+    for (int e = 0; e < V; ++e) x += q[e] * __bfloat162float(kp[(long long)j * a.ldk + lane * V + e]);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+    x *= c;
     const float mn = fmaxf(m, x);
-    const float al = __expf(m - mn), p = __expf(x - mn);
+    const float mr = mn == -INFINITY ? 0.f : mn;
+    const float al = ex2_approx(m - mr), p = ex2_approx(x - mr);
     m = mn;
     l = l * al + p;
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = o[e] * al + p * __bfloat162float(vp[e]);
+    for (int e = 0; e < V; ++e) o[e] = o[e] * al + p * __bfloat162float(vp[(long long)j * a.ldv + lane * V + e]);
   }
-  bf16* op = a.out + (long long)(sp.q0 + i) * a.ldo + h * D + lane * V;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __grid_constant__ TextAttnParams P) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  const Bars bar{bars + 0, bars + 1, bars + 3, bars + 5, bars + 7, bars + 9, bars + 11, bars + 12};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* item = reinterpret_cast<int*>(tmem_slot + 2);  // q0, nq, k0, nk, first token; nq < 0: nothing to do
+
+  const TextAttnArgs& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = P.group, TQ = P.tq, TP = 2 * TQ;
+  const int hk = blockIdx.x % a.heads_k;
+  const int rest = blockIdx.x / a.heads_k;
+  const int split = rest % P.splits, t_rank = rest / P.splits;
+
+  if (threadIdx.x == 32) {
+    mbar_init(bar.q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.ready[i], 1);
+      mbar_init(&bar.slot_free[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.o_done[i], 1);
+    }
+    mbar_init(bar.fixed, 1);
+    mbar_init(bar.drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&P.q_map);
+    tma_prefetch_desc(&P.k_map);
+    tma_prefetch_desc(&P.v_map);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();  // lengths, Q, K, V and the output belong to earlier kernels of the stream
+  allow_dependents();
+  if (warp == 0) {
+    Span sp{0, -1, 0, 0, true};
+    int index = 0;
+    bool found;
+    if (P.list) {
+      const int2 e = P.list[t_rank];
+      found = e.x >= 0;
+      if (found) sp = load_span(a, e.x);
+      index = e.y;
+    } else {
+      found = find_tile(a, TP, P.levels, P.tiles, t_rank, lane, sp, index);
+    }
+    if (lane == 0) {
+      item[0] = sp.q0;
+      item[1] = found ? sp.nq : -1;
+      item[2] = sp.k0;
+      item[3] = sp.nk;
+      item[4] = index * TP;
+      if (P.splits > 1 && hk == 0 && split == 0)
+        P.desc[t_rank] = found ? make_int2(sp.q0 + index * TP, min(TP, sp.nq - index * TP)) : make_int2(0, 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{a.status, abort_flag, kWaitLimitNs};
+  const int q0 = item[0], nq = item[1], k0 = item[2], nk = item[3], tok0 = item[4];
+  const int shift = nk - nq;  // causal: token i sees keys j <= i + shift
+
+  // key blocks of each tile, and this split's run [b0, b0 + n[t]) of them
+  int n0 = 0, n1 = 0, b0 = 0;
+  if (nq >= 0) {
+    auto blocks = [&](int first) {
+      if (first >= nq) return 0;
+      const int last = min(first + TQ, nq) - 1;
+      const int end = a.causal ? min(nk, last + shift + 1) : nk;
+      return end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    };
+    n0 = blocks(tok0);
+    n1 = blocks(tok0 + TQ);
+    if (P.splits > 1) {
+      const int nb = max(n0, n1);
+      b0 = (int)((long long)nb * split / P.splits);
+      const int b1 = (int)((long long)nb * (split + 1) / P.splits);
+      n0 = max(0, min(n0, b1) - b0);
+      n1 = max(0, min(n1, b1) - b0);
+    }
+  }
+  const int nmax = max(n0, n1);
+  // rows of the last block's V past the sequence's keys must read as zeros
+  const bool fix = nmax > 0 && (b0 + nmax) * kKeys > nk;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    // Ring slot j & 1 carries V_j and K_{j+1}; slot j >= 1 is loaded once the scores of block
+    // j - 1 of the longer tile are complete, which ends every read of V_{j-2} and K_{j-1}.
+    bool ok = true;
+    if (lane == 0 && nmax > 0) {
+      int issued = 0;
+      const uint32_t qbytes = (uint32_t)(G * TQ) * 128u * (D / 64);
+      mbar_arrive_expect_tx(bar.q_full, (uint32_t)((n0 > 0) + (n1 > 0)) * qbytes + L::kTile);
+      for (int t = 0; t < 2; ++t)
+        if ((t ? n1 : n0) > 0)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(smem + L::kQ + t * L::kTile + h * kHalfBytes, &P.q_map, bar.q_full, h * 64, 0, hk,
+                        q0 + tok0 + t * TQ);
+      for (int h = 0; h < D / 64; ++h)
+        tma_load_3d(smem + L::kK + h * kHalfBytes, &P.k_map, bar.q_full, h * 64, hk, k0 + b0 * kKeys);
+      for (int j = 0; j < nmax; ++j) {
+        const int b = j & 1;
+        if (j >= 1 && !mbar_wait_sleep(&bar.slot_free[b], (uint32_t)((j - 1) >> 1) & 1u, wc, kSiteFree)) {
+          ok = false;
+          break;
+        }
+        const bool more = j + 1 < nmax;
+        mbar_arrive_expect_tx(&bar.ready[b], more ? 2 * L::kTile : L::kTile);
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_3d(smem + L::kV + b * L::kTile + h * kHalfBytes, &P.v_map, &bar.ready[b], h * 64, hk,
+                      k0 + (b0 + j) * kKeys);
+        if (more)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(smem + L::kK + (b ^ 1) * L::kTile + h * kHalfBytes, &P.k_map, &bar.ready[b], h * 64, hk,
+                        k0 + (b0 + j + 1) * kKeys);
+        issued = j + 1;
+      }
+      if (!ok) {
+        // Unwinding: let copies in flight land (bounded) before the block exits.
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try(bar.q_full, 0) && global_timer_ns() - t0 < 100000000ull) {
+        }
+        for (int j = (issued > 2 ? issued - 2 : 0); j < issued; ++j)
+          while (!mbar_try(&bar.ready[j & 1], (uint32_t)(j >> 1) & 1u) && global_timer_ns() - t0 < 200000000ull) {
+          }
+      }
+    }
+    __syncwarp();
+    if (fix) {
+      const int j = nmax - 1;
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) ok = mbar_wait_sleep(&bar.ready[j & 1], (uint32_t)(j >> 1) & 1u, wc, kSiteFix);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        const int valid = nk - (b0 + j) * kKeys;  // 1 .. 127: rows are 128 contiguous bytes each
+        for (int h = 0; h < D / 64; ++h) {
+          uint4* v = reinterpret_cast<uint4*>(smem + L::kV + (j & 1) * L::kTile + h * kHalfBytes);
+          for (int i = valid * 8 + lane; i < kKeys * 8; i += 32) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.fixed);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && nmax > 0) {
+      const uint32_t idesc_qk = make_idesc_bf16(128, kKeys, false);
+      const uint32_t idesc_pv = make_idesc_bf16(128, D, true);
+      Descs<D> d;
+      make_descs<D>(smem, d);
+      bool ok = mbar_wait(bar.q_full, 0, wc, kSiteQ);
+      if (ok) {
+        tc_fence_after();
+        if (n0 > 0) issue_qk<0>(d, tmem, 0, idesc_qk, &bar.s_full[0]);
+        if (n1 > 0) issue_qk<0>(d, tmem, 1, idesc_qk, &bar.s_full[1]);
+      }
+      for (int j = 0; j < nmax && ok; j += 2) {
+        ok = mma_block<D, 0>(d, tmem, j, n0, n1, fix, idesc_qk, idesc_pv, bar, wc);
+        if (ok && j + 1 < nmax) ok = mma_block<D, 1>(d, tmem, j + 1, n0, n1, fix, idesc_qk, idesc_pv, bar, wc);
+      }
+      umma_commit(bar.drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try(bar.drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
+      }
+    }
+  } else if (nq >= 0) {
+    // ------------------------------------------------------------ softmax / output
+    const int tile = (warp - 2) >> 2;  // warps 2-5 -> tile 0, warps 6-9 -> tile 1
+    const int qq = warp & 3;           // TMEM lane quarter of this warp
+    const int row = qq * 32 + lane;
+    const int n = tile ? n1 : n0;
+    const bool releaser = tile == (n1 >= n0 ? 1 : 0) && qq == 2 && lane == 0;
+    const uint32_t tS = tmem + (uint32_t)(tile * 256) + ((uint32_t)(qq * 32) << 16);
+    const uint32_t tO = tS + 128;
+    const float c = P.scale_log2;
+    const int token = row / G, g = row - token * G;
+    const int qi = tok0 + tile * TQ + token;
+    const bool active = token < TQ && qi < nq;
+    // keys this row sees; rows that are not stored need no mask
+    const int limit = !active ? 0x3fffffff : (a.causal ? min(nk, qi + shift + 1) : nk);
+    float m_run = active ? -INFINITY : 0.f, l_run = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = mbar_wait(&bar.s_full[tile], (uint32_t)j & 1u, wc, kSiteSFull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (releaser) mbar_arrive(&bar.slot_free[(j + 1) & 1]);
+      tc_fence_after();
+      const int kv_valid = limit - (b0 + j) * kKeys;
+      const bool whole = __all_sync(0xffffffffu, kv_valid >= kKeys);
+      // Fast path against the running maximum; the slow path finds the block's maximum first.
+      // A row that has seen no key yet has no maximum and must take the slow one.
+      uint32_t pk[64];
+      float psum = 0.f, unused = -INFINITY, alpha = 1.0f;
+      bool slow = j == 0 || (active && m_run == -INFINITY);
+      if (!__all_sync(0xffffffffu, slow)) {
+        const float mneg = m_run == -INFINITY ? 0.f : -m_run;
+        if (whole) softmax_row<false, false>(tS, kv_valid, c, mneg, unused, psum, pk);
+        else softmax_row<true, false>(tS, kv_valid, c, mneg, unused, psum, pk);
+        slow = slow || (active && psum > kPsumLimit);
+      }
+      if (__any_sync(0xffffffffu, slow)) {
+        float mx = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < V; ++e) op[e] = __float2bfloat16(o[e] * inv);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t r[32];
+          tmem_load32(tS + q * 32, r);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (whole || q * 32 + i < kv_valid) mx = fmaxf(mx, __uint_as_float(r[i]));
+        }
+        const float m_cand = fmaxf(m_run, mx * c);
+        bool resc = false;
+        if (active && m_cand > m_run) {
+          alpha = ex2_approx(m_run - m_cand);
+          m_run = m_cand;
+          resc = true;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t r[32];
+            tmem_load32(tO + cc * 32, r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_store32(tO + cc * 32, r);
+          }
+        }
+        const float mneg = m_run == -INFINITY ? 0.f : -m_run;
+        if (whole) softmax_row<false, false>(tS, kv_valid, c, mneg, unused, psum, pk);
+        else softmax_row<true, false>(tS, kv_valid, c, mneg, unused, psum, pk);
+      }
+      l_run = l_run * alpha + psum;
+      tmem_store32(tS, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+      tmem_store32(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+      tmem_store_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[tile]);
+    }
+    if (ok && n > 0) {
+      ok = mbar_wait_sleep(&bar.o_done[tile], 0, wc, kSiteODone);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok) {
+      const bool none = n == 0 || l_run == 0.f;  // no key seen: zeros
+      const float inv_l = none ? 0.f : 1.0f / l_run;
+      const long long part = ((long long)t_rank * a.heads_k + hk) * P.splits + split;
+      const int prow = (tile * TQ + token) * G + g;
+      bf16* out = a.out + (long long)(q0 + qi) * a.ldo + (hk * G + g) * D;
+      float* po = P.splits > 1 ? P.o + (part * 256 + prow) * D : nullptr;
+      bool bad = false;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t r[32];
+        if (n > 0) tmem_load32(tO + cc * 32, r);
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          f[i] = none ? 0.f : __uint_as_float(r[i]);
+          bad |= !(fabsf(f[i]) <= 3.4028235e38f);
+        }
+        if (active) {
+          if (po) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(po + cc * 32)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<uint4*>(out + cc * 32)[i] =
+                  make_uint4(pack_bf16x2(f[8 * i] * inv_l, f[8 * i + 1] * inv_l),
+                             pack_bf16x2(f[8 * i + 2] * inv_l, f[8 * i + 3] * inv_l),
+                             pack_bf16x2(f[8 * i + 4] * inv_l, f[8 * i + 5] * inv_l),
+                             pack_bf16x2(f[8 * i + 6] * inv_l, f[8 * i + 7] * inv_l));
+          }
+        }
+      }
+      if (active && po) P.ml[part * 256 + prow] = none ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
+      // Rows that are not finite: was it a value that they must not see?
+      const int taken = min(nk, (b0 + n) * kKeys);
+      uint32_t todo = __ballot_sync(0xffffffffu, bad && active && limit < taken);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int r_lim = __shfl_sync(0xffffffffu, limit, src), r_qi = __shfl_sync(0xffffffffu, qi, src);
+        const int r_g = __shfl_sync(0xffffffffu, g, src), r_prow = __shfl_sync(0xffffffffu, prow, src);
+        constexpr int V = D / 32;
+        const bf16* vp = a.v + (long long)k0 * a.ldv + hk * D;
+        bool blame = false;
+        for (int j = max(r_lim, b0 * kKeys); j < taken; ++j)
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            blame |= !(fabsf(__bfloat162float(vp[(long long)j * a.ldv + lane * V + e])) <= 3.4028235e38f);
+        if (!__any_sync(0xffffffffu, blame)) continue;
+        const int j0 = b0 * kKeys;
+        float m, l, o[V];
+        attend_row<D>(a, a.q + (long long)(q0 + r_qi) * a.ldq + (hk * G + r_g) * D,
+                      a.k + (long long)(k0 + j0) * a.ldk + hk * D, vp + (long long)j0 * a.ldv, max(0, r_lim - j0), c,
+                      lane, m, l, o);
+        if (P.splits > 1) {
+          float* dst = P.o + (part * 256 + r_prow) * D;
+#pragma unroll
+          for (int e = 0; e < V; ++e) dst[lane * V + e] = o[e];
+          if (lane == 0) P.ml[part * 256 + r_prow] = make_float2(m, l);
+        } else {
+          bf16* dst = a.out + (long long)(q0 + r_qi) * a.ldo + (hk * G + r_g) * D;
+#pragma unroll
+          for (int e = 0; e < V; ++e) dst[lane * V + e] = __float2bfloat16(l == 0.f ? 0.f : o[e] / l);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Adds the splits of every row of a pair of tiles up, in split order: one CTA per (pair, key
+// head), one warp per row at a time.
+template <int D>
+__global__ void __launch_bounds__(256) text_attention_join_kernel(const __grid_constant__ TextAttnParams P) {
+  constexpr int V = D / 32;
+  grid_dependency_wait();
+  allow_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hk = blockIdx.x % P.a.heads_k, t = blockIdx.x / P.a.heads_k;
+  const int2 d = P.desc[t];
+  const int G = P.group;
+  for (int r = warp; r < d.y * G; r += 8) {
+    const long long at = (long long)blockIdx.x * P.splits * 256 + r;
+    float m = -INFINITY;
+    for (int s = 0; s < P.splits; ++s) m = fmaxf(m, P.ml[at + s * 256].x);
+    const float mr = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+    for (int s = 0; s < P.splits; ++s) {
+      const float2 ml = P.ml[at + s * 256];
+      if (ml.y == 0.f) continue;  // this run held no key that the row sees
+      const float w = ex2_approx(ml.x - mr);
+      l += w * ml.y;
+      const float* po = P.o + (at + s * 256) * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] += w * po[e];
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    bf16* out = P.a.out + (long long)(d.x + r / G) * P.a.ldo + (hk * G + r % G) * D + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = __float2bfloat16(o[e] * inv);
+  }
+}
+
+std::atomic<bool> g_attr_set[32];  // (device, head_dim): the shared-memory attribute is raised
+
+template <int D>
+cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
+  TextAttnParams P;
+  memset(&P, 0, sizeof(P));
+  const uint64_t G = p.group, Hk = a.heads_k;
+  // rows_k == 0: the maps are never used; they only have to be valid
+  const bf16* k = a.rows_k > 0 ? a.k : a.q;
+  const bf16* v = a.rows_k > 0 ? a.v : a.q;
+  const uint64_t qd[4] = {D, G, Hk, (uint64_t)a.rows_q}, qs[3] = {D * 2, G * D * 2, (uint64_t)a.ldq * 2};
+  const uint32_t qb[4] = {64, (uint32_t)G, 1, (uint32_t)p.tq};
+  const uint64_t rk = a.rows_k > 0 ? a.rows_k : 1;
+  const uint64_t kd[3] = {D, Hk, rk}, ks[2] = {D * 2, (uint64_t)a.ldk * 2}, vs[2] = {D * 2, (uint64_t)a.ldv * 2};
+  const uint32_t kb[3] = {64, 1, kKeys};
+  if (!encode_tmap_bf16(&P.q_map, a.q, 4, qd, qs, qb)) return cudaErrorInvalidValue;
+  if (!encode_tmap_bf16(&P.k_map, k, 3, kd, ks, kb)) return cudaErrorInvalidValue;
+  if (!encode_tmap_bf16(&P.v_map, v, 3, kd, vs, kb)) return cudaErrorInvalidValue;
+  P.a = a;
+  P.group = p.group;
+  P.tq = p.tq;
+  P.levels = p.levels;
+  P.tiles = p.tiles;
+  P.splits = p.splits;
+  P.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
+  const Parts l = parts_layout(p, a.heads_k, D);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.parts);
+  int2* list = reinterpret_cast<int2*>(ws + l.list);
+  P.list = p.list ? list : nullptr;
+  P.desc = reinterpret_cast<int2*>(ws + l.desc);
+  P.ml = reinterpret_cast<float2*>(ws + l.ml);
+  P.o = reinterpret_cast<float*>(ws + l.o);
+  const size_t smem = Smem<D>::kBytes;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int slot = dev * 2 + (D == 64);
+  if (dev >= 16 || !g_attr_set[slot].load(std::memory_order_acquire)) {
+    cudaError_t e =
+        cudaFuncSetAttribute(text_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 16) g_attr_set[slot].store(true, std::memory_order_release);
+  }
+  if (p.list) {
+    LaunchScope scope(kClsTextAttention, s);
+    cudaError_t e =
+        launch_k(text_attention_list_kernel, dim3(1), dim3(1024), 0, s, a, p.tq * 2, p.levels, p.tiles, list);
+    if (e != cudaSuccess) return e;
+  }
+  const long long grid = (long long)p.tiles * a.heads_k * p.splits;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  {
+    LaunchScope scope(kClsTextAttention, s);
+    cudaError_t e = launch_k(text_attention_kernel<D>, dim3((unsigned)grid), dim3(kThreads), smem, s, P);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.splits > 1) {
+    LaunchScope scope(kClsTextJoin, s);
+    return launch_k(text_attention_join_kernel<D>, dim3((unsigned)(p.tiles * a.heads_k)), dim3(256), 0, s, P);
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-size_t text_attention_parts_bytes(const TextAttnArgs&) { return 0; }
+size_t text_attention_parts_bytes(const TextAttnArgs& a) {
+  if (a.seqs == 0 || a.rows_q == 0 || a.max_q == 0) return 0;
+  return parts_layout(make_plan(a), a.heads_k, a.head_dim).total;
+}
 
 cudaError_t launch_text_attention(const TextAttnArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.max_q + 7) / 8), (unsigned)a.heads_q, (unsigned)a.seqs);
-  LaunchScope scope(kClsTextAttention, s);
-  if (a.head_dim == 64) return launch_k(text_attention_simple_kernel<64>, grid, dim3(256), 0, s, a);
-  return launch_k(text_attention_simple_kernel<128>, grid, dim3(256), 0, s, a);
+  const Plan p = make_plan(a);
+  return a.head_dim == 64 ? launch<64>(a, p, s) : launch<128>(a, p, s);
 }
 
 }  // namespace dit
