@@ -42,8 +42,7 @@ const char* kernel_class_name(int cls) {
       "gemm_swiglu",    "gemm_plain",            "attention",           "modulation_gemv",
       "rope_table",     "pack_mlp_in",           "gemm_dual_out_proj",  "gemm_dual_mlp_out",
       "gemm_single_out_proj", "quantize_act",    "text_rope_table",     "qk_norm_rope",
-      "text_attention", "text_attention_join",   "quantize_blocks_fp8", "linear_fp8_blocks",
-      "linear_fp8_join"};
+      "text_attention", "text_attention_join",   "quantize_blocks_fp8", "linear_fp8_blocks"};
   return (cls >= 0 && cls < kClsCount) ? names[cls] : "?";
 }
 
@@ -1157,7 +1156,7 @@ dit_status dit_quantize_blocks_fp8(const void* x_dev, long long ld, int rows, in
 
 dit_status dit_linear_fp8_blocks_workspace(int rows, int n_out, int k, size_t* bytes) {
   if (!linear_fp8_sizes_ok(rows, n_out, k) || !bytes) return DIT_ERR_INVALID_ARG;
-  *bytes = sizeof(DeviceStatus) + linear_fp8_parts_bytes(rows, n_out, k);
+  *bytes = sizeof(DeviceStatus);
   return DIT_OK;
 }
 
@@ -1168,9 +1167,9 @@ dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev
   if (!aligned16(a_q_dev) || !aligned16(a_scale_dev) || !aligned16(w_q_dev) || !aligned16(w_scale_dev) ||
       !aligned16(out_dev) || !aligned16(ws))
     return DIT_ERR_INVALID_ARG;
-  if (ws_bytes < sizeof(DeviceStatus) + linear_fp8_parts_bytes(rows, n_out, k)) return DIT_ERR_WORKSPACE;
+  if (ws_bytes < sizeof(DeviceStatus)) return DIT_ERR_WORKSPACE;
   LinearFp8Args a{rows, n_out, k, (const uint8_t*)a_q_dev, (const uint8_t*)w_q_dev, a_scale_dev, w_scale_dev,
-                  (bf16*)out_dev, ld_out, status_of(ws), reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)))};
+                  (bf16*)out_dev, ld_out, status_of(ws)};
   return cuda_status(launch_linear_fp8(a, (cudaStream_t)stream));
 }
 

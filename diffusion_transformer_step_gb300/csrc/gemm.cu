@@ -46,6 +46,7 @@
 //             >= 3H: SWIGLU into the concat buffer (single-stream fused projection).
 #include <atomic>
 
+#include "cta_pair.cuh"
 #include "runtime.h"
 
 namespace dit {
@@ -112,61 +113,6 @@ __device__ __forceinline__ TileInfo decode_tile(const GemmParams& P, int t) {
 // Wait sites, reported through DeviceStatus::where.
 enum : uint32_t { kSiteEmpty = 0x101, kSiteFull = 0x102, kSiteAccEmpty = 0x103, kSiteAccFull = 0x104 };
 
-__device__ __forceinline__ uint32_t cta_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t caddr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
-}
-__device__ __forceinline__ void tma3_2sm(void* dst, const CUtensorMap* m, uint32_t mbar_cluster, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
-          "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(mbar_cluster), "r"(x), "r"(y), "r"(z) : "memory");
-}
-__device__ __forceinline__ void tma2_2sm(void* dst, const CUtensorMap* m, uint32_t mbar_cluster, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
-          "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(mbar_cluster), "r"(x), "r"(y) : "memory");
-}
-// Bring a weight tile into L2 ahead of its shared-memory load (no completion to wait for).
-__device__ __forceinline__ void pf_l2(const CUtensorMap* m, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
-               "r"(x), "r"(y) : "memory");
-}
-// Advance a shared-memory descriptor by `units` x 16 bytes: the start-address field is
-// the low 14 bits, and no shared-memory address reaches 2^18 bytes, so the add never
-// carries out of the field.
-__device__ __forceinline__ uint64_t desc_advance(uint64_t d, uint32_t units) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(d));
-  lo += units;
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void umma2(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
-}
-__device__ __forceinline__ void umma2_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
-}
-// Instruction descriptor of kind::f8f6f4 with e4m3 A and B (format code 0) and fp32 D.
-__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
 // Packed fp32x2 arithmetic (one instruction for two lanes of a row).
 __device__ __forceinline__ float2 f2(float a, float b) { return make_float2(a, b); }
 __device__ __forceinline__ float2 acc2(const uint32_t (&v)[32], int i) {
@@ -197,11 +143,6 @@ __device__ __forceinline__ void dequant32(uint32_t (&v)[32], const Dequant& dq, 
     v[4 * i + 2] = __float_as_uint(b.x);
     v[4 * i + 3] = __float_as_uint(b.y);
   }
-}
-
-__device__ __forceinline__ void commit_both(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-               "h"((uint16_t)3) : "memory");
 }
 
 __device__ __forceinline__ void store_row32(bf16* dst, const float* f) {

@@ -1,6 +1,22 @@
-// e4m3 operands with one fp32 scale per block of 128: quantisation and the product.
+// e4m3 operands with one fp32 scale per block of 128: quantisation and the product
+//   out[r, c] = sum_b sa[r, b] sw[c / 128, b] (a_b . w_b).
+//
+// The scales are any fp32 numbers, so the tensor cores sum one block of 128 depths at a time into
+// Tensor Memory and the threads that own an accumulator row fold it into fp32 registers:
+// acc += part * (sa sw), one packed fp32x2 FMA per two columns.  A block's MMAs run while the
+// block before it is folded.
+//
+//   linear_fp8_wide_kernel   many rows: CTA pairs, 256 x BN tiles, the operands' ring of the bf16
+//                            product (128-byte rows hold one block of depth).
+//   linear_fp8_few_kernel    up to 128 rows, where reading the weights bounds the time: the weights'
+//                            rows take the MMA's 128-row side and the few activation rows its column
+//                            side, the depth split over a cluster whose CTAs add their parts
+//                            through distributed shared memory, in rank order.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
+#include "cta_pair.cuh"
 #include "runtime.h"
 
 namespace dit {
@@ -8,84 +24,622 @@ namespace dit {
 namespace {
 
 constexpr float kAmaxFloor = 448.0f * 0x1p-118f;  // keeps 448 / max finite
+constexpr int kSMs = 152;
 
-// One CTA of 128 threads per block of block_rows x 128 values: thread t takes column t.
-__global__ void quantize_blocks_kernel(const bf16* x, long long ld, int rows, int cols, int block_rows, uint8_t* q,
-                                       float* scale) {
-  grid_dependency_wait();
-  allow_dependents();
-  const int cb = blockIdx.x, rb = blockIdx.y + blockIdx.z * 65535;
-  const int r0 = rb * block_rows;
-  if (r0 >= rows) return;
-  const int c = cb * 128 + threadIdx.x, r1 = min(rows, r0 + block_rows);
-  float amax = 0.f;
-  if (c < cols)
-    for (int r = r0; r < r1; ++r) amax = fmaxf(amax, fabsf(__bfloat162float(x[r * ld + c])));
-  __shared__ float red[4];
+// ---- quantisation ------------------------------------------------------------------------
+
+__device__ __forceinline__ float absmax8(const uint4& u, float m) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-  __syncthreads();
-  amax = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), kAmaxFloor);
-  const float inv = 448.0f / amax;
-  if (c < cols)
-    for (int r = r0; r < r1; ++r)
-      q[(long long)r * cols + c] =
-          (uint8_t)__nv_cvt_float_to_fp8(__bfloat162float(x[r * ld + c]) * inv, __NV_SATFINITE, __NV_E4M3);
-  if (threadIdx.x == 0) scale[(long long)rb * gridDim.x + cb] = amax / 448.0f;
-}
-
-__device__ __forceinline__ float e4m3(uint8_t b) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
-}
-
-// 16 x 16 outputs per CTA, one per thread, the operands of 32 depths staged as fp32.
-__global__ void linear_fp8_simple_kernel(const LinearFp8Args p) {
-  __shared__ float sa[16][33], sw[16][33];
-  grid_dependency_wait();
-  allow_dependents();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int r0 = blockIdx.y * 16, c0 = blockIdx.x * 16;
-  const int kb_n = (p.k + 127) / 128;
-  float acc = 0.f;
-  for (int k0 = 0; k0 < p.k; k0 += 128) {
-    float part = 0.f;
-    for (int k1 = k0; k1 < min(p.k, k0 + 128); k1 += 32) {
-      for (int e = threadIdx.x; e < 512; e += 256) {
-        const int r = e >> 5, kk = e & 31;
-        sa[r][kk] = (r0 + r < p.rows && k1 + kk < p.k) ? e4m3(p.a[(long long)(r0 + r) * p.k + k1 + kk]) : 0.f;
-        sw[r][kk] = (c0 + r < p.n && k1 + kk < p.k) ? e4m3(p.w[(long long)(c0 + r) * p.k + k1 + kk]) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int kk = 0; kk < 32; ++kk) part += sa[ty][kk] * sw[tx][kk];
-      __syncthreads();
-    }
-    if (r0 + ty < p.rows && c0 + tx < p.n)
-      acc += part * (p.a_scale[(long long)(r0 + ty) * kb_n + k0 / 128] *
-                     p.w_scale[(long long)((c0 + tx) / 128) * kb_n + k0 / 128]);
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack_bf16x2(w[j]);
+    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
   }
-  if (r0 + ty < p.rows && c0 + tx < p.n)
-    p.out[(long long)(r0 + ty) * p.ld_out + c0 + tx] = __float2bfloat16(acc);
+  return m;
+}
+
+__device__ __forceinline__ uint2 codes8(const uint4& u, float inv) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack_bf16x2(w[j]);
+    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f.x * inv, f.y * inv), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+
+// A scale per row and 128 columns: eight threads of 16 values each per block, so a row's read
+// and write are whole 16-byte accesses of neighbouring threads.  blockDim = (8 x blocks of one
+// row, up to 256; rows).
+__global__ void __launch_bounds__(256) quantize_row_blocks_kernel(const bf16* __restrict__ x, long long ld, int rows,
+                                                                  int cols, uint8_t* __restrict__ q,
+                                                                  float* __restrict__ scale) {
+  grid_dependency_wait();
+  allow_dependents();
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 16;
+  const bool ok = row < rows && c < cols;
+  uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (ok) {
+    const uint4* p = reinterpret_cast<const uint4*>(x + row * ld + c);
+    u[0] = p[0];
+    u[1] = p[1];
+  }
+  float m = absmax8(u[1], absmax8(u[0], kAmaxFloor));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!ok) return;
+  const float inv = 448.0f / m;
+  const uint2 lo = codes8(u[0], inv), hi = codes8(u[1], inv);
+  *reinterpret_cast<uint4*>(q + (long long)row * cols + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  if (c % 128 == 0) scale[(long long)row * ((cols + 127) / 128) + c / 128] = m / 448.0f;
+}
+
+// A scale per 128 x 128 block: one CTA each, the block held in registers.
+__global__ void __launch_bounds__(256) quantize_square_blocks_kernel(const bf16* __restrict__ x, long long ld, int rows,
+                                                                     int cols, uint8_t* __restrict__ q,
+                                                                     float* __restrict__ scale) {
+  grid_dependency_wait();
+  allow_dependents();
+  const int c = blockIdx.y * 128 + (threadIdx.x & 15) * 8, r0 = blockIdx.x * 128 + (threadIdx.x >> 4);
+  uint4 u[8];
+  float m = kAmaxFloor;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    u[i] = make_uint4(0, 0, 0, 0);
+    if (r0 + 16 * i < rows && c < cols) u[i] = *reinterpret_cast<const uint4*>(x + (r0 + 16 * i) * ld + c);
+    m = absmax8(u[i], m);
+  }
+  __shared__ float red[8];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
+  const float inv = 448.0f / m;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (r0 + 16 * i < rows && c < cols)
+      *reinterpret_cast<uint2*>(q + (long long)(r0 + 16 * i) * cols + c) = codes8(u[i], inv);
+  if (threadIdx.x == 0) scale[(long long)blockIdx.x * gridDim.y + blockIdx.y] = m / 448.0f;
+}
+
+// ---- product, many rows ------------------------------------------------------------------
+
+enum : uint32_t { kSiteEmpty = 0x701, kSiteFull, kSiteAccEmpty, kSiteAccFull };
+
+struct alignas(64) Params {
+  CUtensorMap a_map, w_map;
+  LinearFp8Args a;
+  int kblocks, m_tiles, tiles;
+};
+
+constexpr int kThreads = 320;
+
+template <int BN>
+struct Wide {
+  static constexpr uint32_t kA = 128 * 128, kW = BN / 2 * 128, kStage = kA + kW;
+  static constexpr int kStages = BN == 256 ? 7 : 9;
+  static constexpr int kBufs = 512 / BN;  // accumulators in Tensor Memory
+  static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256;
+};
+
+// Warps as in the bf16 product: 0 loads, 1 issues (leader CTA), 2-9 fold and store, two per row
+// quarter with BN / 2 columns each.  Per block of depth there is one commit, on the
+// accumulator; the stage it frees is handed back by a folding thread of each CTA, because an
+// issuing thread is held about one MMA per commit.
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_fp8_wide_kernel(const __grid_constant__ Params P) {
+  using L = Wide<BN>;
+  constexpr int kCols = BN / 2;  // columns of a folding warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sW = smem + L::kStages * L::kA;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;
+  uint64_t* acc_empty = acc_full + L::kBufs;
+  uint64_t* drain = acc_empty + L::kBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < L::kBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 16);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&P.a_map);
+    tma_prefetch_desc(&P.w_map);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated in both
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{P.a.status, abort_flag, kWaitLimitNs};
+  grid_dependency_wait();
+  allow_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int t = pair; t < P.tiles && ok; t += npairs) {
+        const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
+        const int arow = mt * 256 + (int)rank * 128, wrow = nt * BN + (int)rank * (BN / 2);
+        for (int kb = 0; kb < P.kblocks; ++kb) {
+          if (!mbar_wait_sleep(&empty[stage], phase ^ 1u, wc, kSiteEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = map_to_rank(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
+          tma2_2sm(sA + stage * L::kA, &P.a_map, fb, kb * 128, arow);
+          tma2_2sm(sW + stage * L::kW, &P.w_map, fb, kb * 128, wrow);
+          ++issued;
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        // Unwinding: let copies in flight land (bounded) before the pair exits.
+        const long long outstanding = issued < L::kStages ? issued : L::kStages;
+        for (long long i = 0; i < outstanding; ++i) {
+          if (stage == 0) {
+            stage = L::kStages;
+            phase ^= 1u;
+          }
+          --stage;
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_try(&full[stage], phase) && global_timer_ns() - t0 < 100000000ull) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = make_idesc_e4m3(256, BN);
+      const uint64_t a0 = make_sdesc_sw128(smem_u32(sA), 16, 1024), w0 = make_sdesc_sw128(smem_u32(sW), 16, 1024);
+      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+      bool ok = true;
+      for (int t = pair; t < P.tiles && ok; t += npairs) {
+        for (int kb = 0; kb < P.kblocks; ++kb) {
+          if (!mbar_wait(&acc_empty[buf], buf_phase ^ 1u, wc, kSiteAccEmpty) ||
+              !mbar_wait(&full[stage], phase, wc, kSiteFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = desc_advance(a0, stage * (L::kA >> 4)), wd = desc_advance(w0, stage * (L::kW >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma2_f8(tmem + buf * BN, desc_advance(ad, kk * 2), desc_advance(wd, kk * 2), idesc, kk ? 1u : 0u);
+          commit_both(&acc_full[buf]);
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == L::kBufs) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+                   : "memory");
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try(drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
+      }
+    }
+  } else {
+    const int q = warp & 3, eh = (warp - 2) >> 2;
+    const bool releaser = warp == 2 && lane == 0;
+    const uint32_t acc_empty0 = map_to_rank(smem_u32(&acc_empty[0]), 0);
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(eh * kCols);
+    uint32_t stage = 0, buf = 0, buf_phase = 0;
+    bool ok = true;
+    for (int t = pair; t < P.tiles && ok; t += npairs) {
+      const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
+      const int row = mt * 256 + (int)rank * 128 + q * 32 + lane;
+      const int col = nt * BN + eh * kCols;
+      const bool row_ok = row < P.a.rows;
+      // rows and column blocks past the end: any scale of the matrix does, nothing is stored
+      const float* sa = P.a.a_scale + (long long)min(row, P.a.rows - 1) * P.kblocks;
+      const float* sw = P.a.w_scale + (long long)(min(col, P.a.n - 1) / 128) * P.kblocks;
+      float2 acc[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      float s_next = __ldg(sa) * __ldg(sw);
+      for (int kb = 0; kb < P.kblocks; ++kb) {
+        const float2 s2 = make_float2(s_next, s_next);
+        const int kn = min(kb + 1, P.kblocks - 1);
+        s_next = __ldg(sa + kn) * __ldg(sw + kn);
+        ok = mbar_wait(&acc_full[buf], buf_phase, wc, kSiteAccFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (releaser) mbar_arrive(&empty[stage]);  // the block's MMAs have read the stage
+        tc_fence_after();
+        const uint32_t tb = trow + buf * BN;
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t v[32];
+          tmem_load32(tb + c * 32, v);
+          if (c + 1 == kCols / 32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(acc_empty0 + buf * 8);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[c * 16 + i] =
+                __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[c * 16 + i]);
+        }
+        if (++stage == L::kStages) stage = 0;
+        if (++buf == L::kBufs) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      if (ok && row_ok) {
+        bf16* out = P.a.out + (long long)row * P.a.ld_out + col;
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i)
+          if (col + i * 8 < P.a.n)
+            reinterpret_cast<uint4*>(out)[i] =
+                make_uint4(pack_bf16x2(acc[4 * i].x, acc[4 * i].y), pack_bf16x2(acc[4 * i + 1].x, acc[4 * i + 1].y),
+                           pack_bf16x2(acc[4 * i + 2].x, acc[4 * i + 2].y),
+                           pack_bf16x2(acc[4 * i + 3].x, acc[4 * i + 3].y));
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync_all();  // no MMA, load or remote arrive of the pair is still in flight
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ---- product, few rows -------------------------------------------------------------------
+
+constexpr int kFewThreads = 192;
+
+template <int T>  // activation rows, rounded up: 16, 32, 64 or 128
+struct Few {
+  static constexpr uint32_t kW = 128 * 128, kA = T * 128, kStage = kW + kA;
+  static constexpr int kStages = T <= 32 ? 5 : 6;  // two CTAs per SM up to 32 rows
+  static constexpr int kBufs = 4;                  // accumulators in Tensor Memory
+  static constexpr uint32_t kTmem = kBufs * T;     // 64 .. 512 columns
+  static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256 + 4 * T * 4;
+  static_assert((size_t)kStages * kStage >= (size_t)T * 128 * 4, "the parts reuse the ring");
+};
+
+__device__ __forceinline__ void umma1_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// One cluster per 128 output columns (one row block of w_scale); rank r of S takes the depth
+// blocks [K r / S, K (r + 1) / S).  Warp 0 loads, warp 1 issues, warps 2-5 fold: thread = one
+// output column, registers = the activation rows.
+template <int T>
+__global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __grid_constant__ Params P, int S) {
+  using L = Few<T>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sW = smem;
+  uint8_t* sA = smem + L::kStages * L::kW;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;
+  uint64_t* acc_empty = acc_full + L::kBufs;
+  uint64_t* drain = acc_empty + L::kBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % S, nb = blockIdx.x / S;
+  const int kb0 = (int)((long long)P.kblocks * rank / S), kb1 = (int)((long long)P.kblocks * (rank + 1) / S);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < L::kBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&P.a_map);
+    tma_prefetch_desc(&P.w_map);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{P.a.status, abort_flag, kWaitLimitNs};
+  grid_dependency_wait();
+  allow_dependents();
+
+  float2 acc[T / 2];
+#pragma unroll
+  for (int i = 0; i < T / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+  const int n = kb1 - kb0;
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      bool ok = true;
+      for (int i = 0; i < n; ++i) {
+        const int s = i % L::kStages;
+        if (!mbar_wait_sleep(&empty[s], ((uint32_t)(i / L::kStages) & 1u) ^ 1u, wc, kSiteEmpty)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&full[s], L::kStage);
+        tma_load_2d(sW + s * L::kW, &P.w_map, &full[s], (kb0 + i) * 128, nb * 128);
+        tma_load_2d(sA + s * L::kA, &P.a_map, &full[s], (kb0 + i) * 128, 0);
+        issued = i + 1;
+      }
+      if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        for (int i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
+          while (!mbar_try(&full[i % L::kStages], (uint32_t)(i / L::kStages) & 1u) &&
+                 global_timer_ns() - t0 < 200000000ull) {
+          }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc_e4m3(128, T);
+      const uint64_t w0 = make_sdesc_sw128(smem_u32(sW), 16, 1024), a0 = make_sdesc_sw128(smem_u32(sA), 16, 1024);
+      for (int i = 0; i < n; ++i) {
+        const int s = i % L::kStages, b = i % L::kBufs;
+        if (!mbar_wait(&acc_empty[b], ((uint32_t)(i / L::kBufs) & 1u) ^ 1u, wc, kSiteAccEmpty) ||
+            !mbar_wait(&full[s], (uint32_t)(i / L::kStages) & 1u, wc, kSiteFull))
+          break;
+        tc_fence_after();
+        const uint64_t wd = desc_advance(w0, s * (L::kW >> 4)), ad = desc_advance(a0, s * (L::kA >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma1_f8(tmem + b * T, desc_advance(wd, kk * 2), desc_advance(ad, kk * 2), idesc, kk ? 1u : 0u);
+        umma_commit(&acc_full[b]);
+      }
+      umma_commit(drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try(drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+    const float* sw = P.a.w_scale + (long long)nb * P.kblocks + kb0;
+    // Each warp keeps a block's factors sa sw, one per activation row, in shared memory; every
+    // thread needs all of them.  Lane l fetches rows l, l + 32, ... one block ahead.
+    float* factors = reinterpret_cast<float*>(smem + L::kStages * L::kStage + 256) + q * T;
+    constexpr int kMine = T < 32 ? 1 : T / 32;
+    const float* sa[kMine];
+    float mine[kMine];
+#pragma unroll
+    for (int e = 0; e < kMine; ++e) {
+      sa[e] = P.a.a_scale + (long long)min(lane + 32 * e, P.a.rows - 1) * P.kblocks + kb0;
+      mine[e] = n > 0 ? __ldg(sa[e]) * __ldg(sw) : 0.f;
+    }
+    for (int i = 0; i < n; ++i) {
+      const int b = i % L::kBufs;
+#pragma unroll
+      for (int e = 0; e < kMine; ++e)
+        if (lane + 32 * e < T) factors[lane + 32 * e] = mine[e];
+      __syncwarp();
+      const int next = min(i + 1, n - 1);
+      const float ws = __ldg(sw + next);
+#pragma unroll
+      for (int e = 0; e < kMine; ++e) mine[e] = __ldg(sa[e] + next) * ws;
+      bool ok = mbar_wait(&acc_full[b], (uint32_t)(i / L::kBufs) & 1u, wc, kSiteAccFull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (warp == 2 && lane == 0) mbar_arrive(&empty[i % L::kStages]);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < T / 16; ++c) {
+        uint32_t v[16];
+        tmem_load16(trow + b * T + c * 16, v);
+        if (c + 1 == T / 16) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = c * 16 + 2 * e;
+          acc[r / 2] = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                                  *reinterpret_cast<const float2*>(factors + r), acc[r / 2]);
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  const int c = nb * 128 + (warp & 3) * 32 + lane;  // this folding thread's output column
+  if (S == 1) {
+    if (warp >= 2 && c < P.a.n) {
+#pragma unroll
+      for (int r = 0; r < T; ++r)
+        if (r < P.a.rows) P.a.out[(long long)r * P.a.ld_out + c] = __float2bfloat16(r & 1 ? acc[r / 2].y : acc[r / 2].x);
+    }
+    tc_fence_before();
+    __syncthreads();
+  } else {
+    // Every rank leaves its part [row][column] in its own shared memory (the ring has been read),
+    // then adds every S-th row over all ranks.
+    float* part = reinterpret_cast<float*>(smem);
+    tc_fence_before();
+    __syncthreads();
+    if (warp >= 2) {
+#pragma unroll
+      for (int r = 0; r < T; ++r)
+        if (r < P.a.rows) part[r * 128 + (warp & 3) * 32 + lane] = r & 1 ? acc[r / 2].y : acc[r / 2].x;
+    }
+    cluster_sync_all();
+    if (warp >= 2 && c < P.a.n) {
+      for (int r = rank; r < P.a.rows; r += S) {
+        const uint32_t at = smem_u32(part + r * 128 + (warp & 3) * 32 + lane);
+        float sum = 0.f;
+        for (int k = 0; k < S; ++k) sum += ld_cluster_f32(map_to_rank(at, k));
+        P.a.out[(long long)r * P.a.ld_out + c] = __float2bfloat16(sum);
+      }
+    }
+    cluster_sync_all();  // no rank leaves while another reads its part
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmem);
+  }
+}
+
+template <typename F>
+cudaError_t raise_smem(F* kernel, size_t bytes, int id) {
+  static std::atomic<bool> done[16 * 8];  // (device, kernel)
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 16 && done[dev * 8 + id].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 16) done[dev * 8 + id].store(true, std::memory_order_release);
+  return e;
+}
+
+bool encode(Params& P, const LinearFp8Args& a, uint32_t a_box, uint32_t w_box) {
+  memset(&P, 0, sizeof(P));
+  P.a = a;
+  P.kblocks = (a.k + 127) / 128;
+  const uint64_t ad[2] = {(uint64_t)a.k, (uint64_t)a.rows}, wd[2] = {(uint64_t)a.k, (uint64_t)a.n};
+  const uint64_t st[1] = {(uint64_t)a.k};
+  const uint32_t ab[2] = {128, a_box}, wb[2] = {128, w_box};
+  return encode_tmap_u8(&P.a_map, a.a, 2, ad, st, ab) && encode_tmap_u8(&P.w_map, a.w, 2, wd, st, wb);
+}
+
+template <int BN>
+cudaError_t launch_wide(const LinearFp8Args& a, cudaStream_t s) {
+  Params P;
+  if (!encode(P, a, 128, BN / 2)) return cudaErrorInvalidValue;
+  P.m_tiles = (a.rows + 255) / 256;
+  P.tiles = P.m_tiles * ((a.n + BN - 1) / BN);
+  const cudaError_t e = raise_smem(linear_fp8_wide_kernel<BN>, Wide<BN>::kBytes, BN == 256 ? 0 : 1);
+  if (e != cudaSuccess) return e;
+  const int most = sm_count() / 2, pairs = P.tiles < most ? P.tiles : most;
+  LaunchScope scope(kClsLinearFp8Blocks, s);
+  return launch_k(linear_fp8_wide_kernel<BN>, dim3(2 * pairs), dim3(kThreads), Wide<BN>::kBytes, s, P);
+}
+
+template <int T>
+cudaError_t launch_few(const LinearFp8Args& a, cudaStream_t s) {
+  Params P;
+  if (!encode(P, a, T, 128)) return cudaErrorInvalidValue;
+  const cudaError_t e = raise_smem(linear_fp8_few_kernel<T>, Few<T>::kBytes, T == 16 ? 2 : T == 32 ? 3 : T == 64 ? 4 : 5);
+  if (e != cudaSuccess) return e;
+  // Split the depth while the CTAs still run at once (two per SM up to 32 rows).
+  const int blocks = (a.n + 127) / 128, room = kSMs * (T <= 32 ? 2 : 1);
+  int S = 1;
+  while (S < 8 && blocks * S * 2 <= room && P.kblocks >= S * 2) S *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks * S));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = Few<T>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  LaunchScope scope(kClsLinearFp8Blocks, s);
+  return cudaLaunchKernelEx(&cfg, linear_fp8_few_kernel<T>, P, S);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_blocks(const bf16* x, long long ld, int rows, int cols, int block_rows, uint8_t* q,
                                    float* scale, cudaStream_t s) {
-  const int rb = (rows + block_rows - 1) / block_rows;
-  const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)(rb < 65535 ? rb : 65535), (unsigned)((rb + 65534) / 65535));
+  const int cb = (cols + 127) / 128;
   LaunchScope scope(kClsQuantBlocks, s);
-  return launch_k(quantize_blocks_kernel, grid, dim3(128), 0, s, x, ld, rows, cols, block_rows, q, scale);
+  if (block_rows == 128)
+    return launch_k(quantize_square_blocks_kernel, dim3((unsigned)((rows + 127) / 128), (unsigned)cb), dim3(256), 0, s, x,
+                    ld, rows, cols, q, scale);
+  int tx = 8;
+  while (tx < cb * 8 && tx < 256) tx *= 2;
+  const int ty = 256 / tx;
+  return launch_k(quantize_row_blocks_kernel, dim3((unsigned)((rows + ty - 1) / ty), (unsigned)((cb * 8 + tx - 1) / tx)),
+                  dim3(tx, ty), 0, s, x, ld, rows, cols, q, scale);
 }
 
-size_t linear_fp8_parts_bytes(int, int, int) { return 0; }
-
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.n + 15) / 16), (unsigned)((a.rows + 15) / 16));
-  if (grid.y > 65535) return cudaErrorInvalidValue;
-  LaunchScope scope(kClsLinearFp8Blocks, s);
-  return launch_k(linear_fp8_simple_kernel, grid, dim3(256), 0, s, a);
+  if (a.rows <= 16) return launch_few<16>(a, s);
+  if (a.rows <= 32) return launch_few<32>(a, s);
+  if (a.rows <= 64) return launch_few<64>(a, s);
+  if (a.rows <= 128) return launch_few<128>(a, s);
+  // 256 or 128 columns per tile, whichever needs less time over its waves of CTA pairs.
+  const long long m = (a.rows + 255) / 256, pairs = kSMs / 2;
+  const long long w256 = (m * ((a.n + 255) / 256) + pairs - 1) / pairs, w128 = (m * ((a.n + 127) / 128) + pairs - 1) / pairs;
+  return w256 * 2 <= w128 ? launch_wide<256>(a, s) : launch_wide<128>(a, s);
 }
 
 }  // namespace dit

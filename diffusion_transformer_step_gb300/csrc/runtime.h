@@ -32,8 +32,7 @@ enum KernelClass : int {
   kClsTextJoin = 17,       // joining its key splits
   kClsQuantBlocks = 18,    // e4m3 quantisation with a scale per block
   kClsLinearFp8Blocks = 19,  // e4m3 product with block scales
-  kClsLinearFp8Join = 20,  // joining its depth splits
-  kClsCount = 21
+  kClsCount = 20
 };
 
 const char* kernel_class_name(int cls);
@@ -249,9 +248,7 @@ struct LinearFp8Args {
   bf16* out;
   int ld_out;
   DeviceStatus* status;
-  float* parts;  // workspace of the depth splits
 };
-size_t linear_fp8_parts_bytes(int rows, int n, int k);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
 
 }  // namespace dit

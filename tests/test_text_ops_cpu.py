@@ -129,7 +129,7 @@ def test_linear_fp8_blocks_refusals(dit, change, st):
 def test_kernel_classes_have_names(dit):
     names = [dit.dit_kernel_class_name(i) for i in range(32)]
     for n in ("text_rope_table", "qk_norm_rope", "text_attention", "text_attention_join", "quantize_blocks_fp8",
-              "linear_fp8_blocks", "linear_fp8_join"):
+              "linear_fp8_blocks"):
         assert names.count(n) == 1
 
 
