@@ -8,7 +8,7 @@
 //
 //   linear_fp8_wide_kernel   many rows: CTA pairs, 256 x BN tiles, the operands' ring of the bf16
 //                            product (128-byte rows hold one block of depth).
-//   linear_fp8_few_kernel    up to 128 rows, where reading the weights bounds the time: the weights'
+//   linear_fp8_few_kernel    up to 64 rows, where reading the weights bounds the time: the weights'
 //                            rows take the MMA's 128-row side and the few activation rows its column
 //                            side, the depth split over a cluster whose CTAs add their parts
 //                            through distributed shared memory, in rank order.
@@ -111,35 +111,77 @@ __global__ void __launch_bounds__(256) quantize_square_blocks_kernel(const bf16*
 enum : uint32_t { kSiteEmpty = 0x701, kSiteFull, kSiteAccEmpty, kSiteAccFull };
 
 struct alignas(64) Params {
-  CUtensorMap a_map, w_map;
+  CUtensorMap a_map, w_map, out_map;
   LinearFp8Args a;
   int kblocks, m_tiles, tiles;
 };
 
-constexpr int kThreads = 320;
+// Arrival at the leader's barrier that publishes no memory: the accumulator's reads are complete
+// (tcgen05.wait::ld) and ordered by tcgen05.fence.  With release semantics at cluster scope each of the
+// sixteen arrivals per block waited ~600 cycles for a memory barrier.
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
 
-template <int BN>
+// A box of the output from shared memory (128-byte swizzle), and the wait until every box of this
+// thread has been read out of it.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// One block of depth: D = A W^T over four K = 32 MMAs, descriptors 32 bytes apart, in one statement.
+__device__ __forceinline__ void umma2_f8x4(uint32_t d, uint64_t a, uint64_t w, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a1, a2, a3, w1, w2, w3;\n\t"
+      "setp.ne.b32 pf, %4, %4;\n\tsetp.eq.b32 pt, %4, %4;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 w1, %2, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 w2, %2, 4;\n\t"
+      "add.s64 a3, %1, 6;\n\tadd.s64 w3, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, pf;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, w1, %3, pt;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, w2, %3, pt;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, w3, %3, pt;\n\t}" ::"r"(d),
+      "l"(a), "l"(w), "r"(idesc), "r"(0)
+      : "memory");
+}
+
+// A stage and an accumulator always come back to the same issuer (both counts are even), whose
+// parity waits are thereby never more than one phase behind.
+constexpr int kIssuers = 2;
+
+
 struct Wide {
+  static constexpr int BN = 128;
   static constexpr uint32_t kA = 128 * 128, kW = BN / 2 * 128, kStage = kA + kW;
-  static constexpr int kStages = BN == 256 ? 7 : 9;
+  static constexpr int kStages = 8;
   static constexpr int kBufs = 512 / BN;  // accumulators in Tensor Memory
-  static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256;
+  // folding warps: one per 32 rows and 64 columns, so that accumulators leave room in the registers
+  static constexpr int kWarps = BN / 16, kThreads = 128 + kWarps * 32;
+  // behind the ring: 2 KB per folding warp, 16 rows x 64 columns of output on their way to TMA stores
+  static constexpr uint32_t kOut = kStages * kStage, kBar = kOut + kWarps * 2048;
+  static constexpr size_t kBytes = 1024 + kBar + 256;
+  static_assert(kStages % kIssuers == 0 && kBufs % kIssuers == 0, "see kIssuers");
 };
 
-// Warps as in the bf16 product: 0 loads, 1 issues (leader CTA), 2-9 fold and store, two per row
-// quarter with BN / 2 columns each.  Per block of depth there is one commit, on the
-// accumulator; the stage it frees is handed back by a folding thread of each CTA, because an
-// issuing thread is held about one MMA per commit.
-template <int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// Warp 0 loads, warps 1 and 2 issue (leader CTA) every second block of depth each, the others from
+// warp 4 fold and store, BN / 64 per row quarter with 64 columns each.  An issuing thread needs
+// ~500 cycles per block for its waits, MMAs and commit, as long as the MMAs themselves, so there are
+// two.  Per block there is one commit, on the accumulator; the stage it frees is handed back by a
+// folding thread of each CTA.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     linear_fp8_wide_kernel(const __grid_constant__ Params P) {
-  using L = Wide<BN>;
-  constexpr int kCols = BN / 2;  // columns of a folding warp
+  using L = Wide;
+  constexpr int BN = L::BN;
+  constexpr int kCols = 64;  // columns of a folding warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sW = smem + L::kStages * L::kA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* empty = full + L::kStages;
   uint64_t* acc_full = empty + L::kStages;
   uint64_t* acc_empty = acc_full + L::kBufs;
@@ -157,13 +199,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < L::kBufs; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 16);
+      mbar_init(&acc_empty[i], 2 * L::kWarps);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, kIssuers);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.a_map);
     tma_prefetch_desc(&P.w_map);
+    tma_prefetch_desc(&P.out_map);
   }
   __syncwarp();
   if (warp == 1) {
@@ -179,107 +222,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   allow_dependents();
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (int t = pair; t < P.tiles && ok; t += npairs) {
-        const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
-        const int arow = mt * 256 + (int)rank * 128, wrow = nt * BN + (int)rank * (BN / 2);
-        for (int kb = 0; kb < P.kblocks; ++kb) {
-          if (!mbar_wait_sleep(&empty[stage], phase ^ 1u, wc, kSiteEmpty)) {
-            ok = false;
-            break;
-          }
+  if (warp < 4) {
+    if (warp == 0) {
+      if (lane == 0) {
+        uint32_t stage = 0, phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        for (int t = pair; t < P.tiles && ok; t += npairs) {
+          const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
+          const int arow = mt * 256 + (int)rank * 128, wrow = nt * BN + (int)rank * (BN / 2);
+          for (int kb = 0; kb < P.kblocks; ++kb) {
+            if (!mbar_wait_sleep(&empty[stage], phase ^ 1u, wc, kSiteEmpty)) {
+              ok = false;
+              break;
+            }
+           
           const uint32_t fb = map_to_rank(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
-          tma2_2sm(sA + stage * L::kA, &P.a_map, fb, kb * 128, arow);
-          tma2_2sm(sW + stage * L::kW, &P.w_map, fb, kb * 128, wrow);
-          ++issued;
-          if (++stage == L::kStages) {
-            stage = 0;
-            phase ^= 1u;
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
+            tma2_2sm(sA + stage * L::kA, &P.a_map, fb, kb * 128, arow);
+            tma2_2sm(sW + stage * L::kW, &P.w_map, fb, kb * 128, wrow);
+            ++issued;
+            if (++stage == L::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        if (!ok && rank == 0) {
+          // Unwinding: let copies in flight land (bounded) before the pair exits.
+          const long long outstanding = issued < L::kStages ? issued : L::kStages;
+          for (long long i = 0; i < outstanding; ++i) {
+            if (stage == 0) {
+              stage = L::kStages;
+              phase ^= 1u;
+            }
+            --stage;
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try(&full[stage], phase) && global_timer_ns() - t0 < 100000000ull) {
+            }
           }
         }
       }
-      if (!ok && rank == 0) {
-        // Unwinding: let copies in flight land (bounded) before the pair exits.
-        const long long outstanding = issued < L::kStages ? issued : L::kStages;
-        for (long long i = 0; i < outstanding; ++i) {
-          if (stage == 0) {
-            stage = L::kStages;
-            phase ^= 1u;
-          }
-          --stage;
-          const uint64_t t0 = global_timer_ns();
-          while (!mbar_try(&full[stage], phase) && global_timer_ns() - t0 < 100000000ull) {
-          }
-        }
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = make_idesc_e4m3(256, BN);
-      const uint64_t a0 = make_sdesc_sw128(smem_u32(sA), 16, 1024), w0 = make_sdesc_sw128(smem_u32(sW), 16, 1024);
-      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
-      bool ok = true;
-      for (int t = pair; t < P.tiles && ok; t += npairs) {
-        for (int kb = 0; kb < P.kblocks; ++kb) {
-          if (!mbar_wait(&acc_empty[buf], buf_phase ^ 1u, wc, kSiteAccEmpty) ||
-              !mbar_wait(&full[stage], phase, wc, kSiteFull)) {
-            ok = false;
+    } else if (warp <= kIssuers) {
+      if (lane == 0 && rank == 0) {
+        const uint32_t idesc = make_idesc_e4m3(256, BN);
+        const uint64_t a0 = make_sdesc_sw128(smem_u32(sA), 16, 1024), w0 = make_sdesc_sw128(smem_u32(sW), 16, 1024);
+        // Blocks of depth over all of this pair's tiles, every kIssuers-th.
+        const uint32_t blocks = (uint32_t)((P.tiles - pair + npairs - 1) / npairs) * (uint32_t)P.kblocks;
+        for (uint32_t i = warp - 1; i < blocks; i += kIssuers) {
+          const uint32_t stage = i % L::kStages, buf = i % L::kBufs;
+          if (!mbar_wait(&acc_empty[buf], ((i / L::kBufs) & 1u) ^ 1u, wc, kSiteAccEmpty) ||
+              !mbar_wait(&full[stage], (i / L::kStages) & 1u, wc, kSiteFull))
             break;
-          }
+
           tc_fence_after();
-          const uint64_t ad = desc_advance(a0, stage * (L::kA >> 4)), wd = desc_advance(w0, stage * (L::kW >> 4));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma2_f8(tmem + buf * BN, desc_advance(ad, kk * 2), desc_advance(wd, kk * 2), idesc, kk ? 1u : 0u);
-          commit_both(&acc_full[buf]);
-          if (++stage == L::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (++buf == L::kBufs) {
-            buf = 0;
-            buf_phase ^= 1u;
-          }
+          umma2_f8x4(tmem + buf * BN, desc_advance(a0, stage * (L::kA >> 4)), desc_advance(w0, stage * (L::kW >> 4)),
+                     idesc);
+         commit_both(&acc_full[buf]);
         }
-      }
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
-                   : "memory");
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try(drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+                     : "memory");
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try(drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
+        }
       }
     }
   } else {
-    const int q = warp & 3, eh = (warp - 2) >> 2;
-    const bool releaser = warp == 2 && lane == 0;
+    const int q = warp & 3, eh = (warp - 4) >> 2;
+    const bool releaser = warp == 4 && lane == 0;
     const uint32_t acc_empty0 = map_to_rank(smem_u32(&acc_empty[0]), 0);
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(eh * kCols);
+    uint8_t* staged = smem + L::kOut + (warp - 4) * 2048;
     uint32_t stage = 0, buf = 0, buf_phase = 0;
     bool ok = true;
     for (int t = pair; t < P.tiles && ok; t += npairs) {
       const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
       const int row = mt * 256 + (int)rank * 128 + q * 32 + lane;
       const int col = nt * BN + eh * kCols;
-      const bool row_ok = row < P.a.rows;
       // rows and column blocks past the end: any scale of the matrix does, nothing is stored
       const float* sa = P.a.a_scale + (long long)min(row, P.a.rows - 1) * P.kblocks;
       const float* sw = P.a.w_scale + (long long)(min(col, P.a.n - 1) / 128) * P.kblocks;
       float2 acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      float s_next = __ldg(sa) * __ldg(sw);
+      // scales of this block and the next; the one after is in flight while this one is folded
+      const int last = P.kblocks - 1;
+      float sa0 = __ldg(sa), sw0 = __ldg(sw), sa1 = __ldg(sa + min(1, last)), sw1 = __ldg(sw + min(1, last));
       for (int kb = 0; kb < P.kblocks; ++kb) {
-        const float2 s2 = make_float2(s_next, s_next);
-        const int kn = min(kb + 1, P.kblocks - 1);
-        s_next = __ldg(sa + kn) * __ldg(sw + kn);
-        ok = mbar_wait(&acc_full[buf], buf_phase, wc, kSiteAccFull);
+        const float s = sa0 * sw0;
+        const float2 s2 = make_float2(s, s);
+        sa0 = sa1;
+        sw0 = sw1;
+        sa1 = __ldg(sa + min(kb + 2, last));
+        sw1 = __ldg(sw + min(kb + 2, last));
+        ok = mbar_wait_inline(&acc_full[buf], buf_phase, wc, kSiteAccFull);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (releaser) mbar_arrive(&empty[stage]);  // the block's MMAs have read the stage
+                if (releaser) mbar_arrive(&empty[stage]);  // the block's MMAs have read the stage
         tc_fence_after();
         const uint32_t tb = trow + buf * BN;
 #pragma unroll
@@ -289,7 +328,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (c + 1 == kCols / 32) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(acc_empty0 + buf * 8);
+            if (lane == 0) arrive_cluster_relaxed(acc_empty0 + buf * 8);
+            
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -302,17 +342,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           buf_phase ^= 1u;
         }
       }
-      if (ok && row_ok) {
-        bf16* out = P.a.out + (long long)row * P.a.ld_out + col;
+      if (!ok) break;
+      // 16 rows at a time through this warp's staging rows (128-byte swizzle) to a TMA store, which
+      // clips rows and columns past the matrix.
 #pragma unroll
-        for (int i = 0; i < kCols / 8; ++i)
-          if (col + i * 8 < P.a.n)
-            reinterpret_cast<uint4*>(out)[i] =
-                make_uint4(pack_bf16x2(acc[4 * i].x, acc[4 * i].y), pack_bf16x2(acc[4 * i + 1].x, acc[4 * i + 1].y),
-                           pack_bf16x2(acc[4 * i + 2].x, acc[4 * i + 2].y),
-                           pack_bf16x2(acc[4 * i + 3].x, acc[4 * i + 3].y));
+      for (int h = 0; h < 2; ++h) {
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+        if ((lane >> 4) == h) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2* f = acc + i * 4;
+            *reinterpret_cast<uint4*>(staged + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                           pack_bf16x2(f[3].x, f[3].y));
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0 && col < P.a.n && row + h * 16 < P.a.rows) tma_store_2d(&P.out_map, staged, col, row + h * 16);
       }
     }
+    if (lane == 0) tma_store_wait_read();
   }
 
   tc_fence_before();
@@ -327,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 constexpr int kFewThreads = 192;
 
-template <int T>  // activation rows, rounded up: 16, 32, 64 or 128
+template <int T>  // activation rows, rounded up: 16, 32 or 64
 struct Few {
   static constexpr uint32_t kW = 128 * 128, kA = T * 128, kStage = kW + kA;
   static constexpr int kStages = T <= 32 ? 5 : 6;  // two CTAs per SM up to 32 rows
@@ -541,8 +592,11 @@ __global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __gri
     if (warp >= 2 && c < P.a.n) {
       for (int r = rank; r < P.a.rows; r += S) {
         const uint32_t at = smem_u32(part + r * 128 + (warp & 3) * 32 + lane);
-        float sum = 0.f;
-        for (int k = 0; k < S; ++k) sum += ld_cluster_f32(map_to_rank(at, k));
+        float v[8], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < S ? ld_cluster_f32(map_to_rank(at, k)) : 0.f;  // all on their way
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += v[k];
         P.a.out[(long long)r * P.a.ld_out + c] = __float2bfloat16(sum);
       }
     }
@@ -575,24 +629,26 @@ bool encode(Params& P, const LinearFp8Args& a, uint32_t a_box, uint32_t w_box) {
   return encode_tmap_u8(&P.a_map, a.a, 2, ad, st, ab) && encode_tmap_u8(&P.w_map, a.w, 2, wd, st, wb);
 }
 
-template <int BN>
 cudaError_t launch_wide(const LinearFp8Args& a, cudaStream_t s) {
   Params P;
-  if (!encode(P, a, 128, BN / 2)) return cudaErrorInvalidValue;
+  if (!encode(P, a, 128, Wide::BN / 2)) return cudaErrorInvalidValue;
+  const uint64_t od[2] = {(uint64_t)a.n, (uint64_t)a.rows}, ost[1] = {(uint64_t)a.ld_out * 2};
+  const uint32_t obox[2] = {64, 16};
+  if (!encode_tmap_bf16(&P.out_map, a.out, 2, od, ost, obox)) return cudaErrorInvalidValue;
   P.m_tiles = (a.rows + 255) / 256;
-  P.tiles = P.m_tiles * ((a.n + BN - 1) / BN);
-  const cudaError_t e = raise_smem(linear_fp8_wide_kernel<BN>, Wide<BN>::kBytes, BN == 256 ? 0 : 1);
+  P.tiles = P.m_tiles * ((a.n + Wide::BN - 1) / Wide::BN);
+  const cudaError_t e = raise_smem(linear_fp8_wide_kernel, Wide::kBytes, 0);
   if (e != cudaSuccess) return e;
   const int most = sm_count() / 2, pairs = P.tiles < most ? P.tiles : most;
   LaunchScope scope(kClsLinearFp8Blocks, s);
-  return launch_k(linear_fp8_wide_kernel<BN>, dim3(2 * pairs), dim3(kThreads), Wide<BN>::kBytes, s, P);
+  return launch_k(linear_fp8_wide_kernel, dim3(2 * pairs), dim3(Wide::kThreads), Wide::kBytes, s, P);
 }
 
 template <int T>
 cudaError_t launch_few(const LinearFp8Args& a, cudaStream_t s) {
   Params P;
   if (!encode(P, a, T, 128)) return cudaErrorInvalidValue;
-  const cudaError_t e = raise_smem(linear_fp8_few_kernel<T>, Few<T>::kBytes, T == 16 ? 2 : T == 32 ? 3 : T == 64 ? 4 : 5);
+  const cudaError_t e = raise_smem(linear_fp8_few_kernel<T>, Few<T>::kBytes, T == 16 ? 1 : T == 32 ? 2 : 3);
   if (e != cudaSuccess) return e;
   // Split the depth while the CTAs still run at once (two per SM up to 32 rows).
   const int blocks = (a.n + 127) / 128, room = kSMs * (T <= 32 ? 2 : 1);
@@ -635,11 +691,7 @@ cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {
   if (a.rows <= 16) return launch_few<16>(a, s);
   if (a.rows <= 32) return launch_few<32>(a, s);
   if (a.rows <= 64) return launch_few<64>(a, s);
-  if (a.rows <= 128) return launch_few<128>(a, s);
-  // 256 or 128 columns per tile, whichever needs less time over its waves of CTA pairs.
-  const long long m = (a.rows + 255) / 256, pairs = kSMs / 2;
-  const long long w256 = (m * ((a.n + 255) / 256) + pairs - 1) / pairs, w128 = (m * ((a.n + 127) / 128) + pairs - 1) / pairs;
-  return w256 * 2 <= w128 ? launch_wide<256>(a, s) : launch_wide<128>(a, s);
+  return launch_wide(a, s);
 }
 
 }  // namespace dit
