@@ -1,5 +1,7 @@
 // Rotary positions of a text model: the table of 1-D positions, and the pass that norms
 // every query and key head and turns it.
+#include <math.h>
+
 #include "runtime.h"
 
 namespace dit {
@@ -10,43 +12,86 @@ namespace {
 // turns per position as a 64-bit fixed-point fraction F_j (2^64 = one turn), the fraction of
 // p turns is the low word of p * F_j, an exact reduction in one 64-bit integer product, where
 // fp64 angles cost fp64 arithmetic that this GPU has little of.  The nearest quarter turn is
-// split off as an integer, and the rest, at most 1/8 turn, is exact to 2^-25 relative in fp32.
-__global__ void text_rope_kernel(const __grid_constant__ TextRopeArgs a) {
-  grid_dependency_wait();
-  allow_dependents();
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (long long)a.n * a.half) return;
-  const int row = (int)(i / a.half);
-  const int j = (int)(i - (long long)row * a.half);
-  const int p = a.pos ? a.pos[row] : row;
-  const uint64_t u = (uint64_t)(int64_t)p * a.freq[j];  // p F mod 2^64: negative p turns backwards
-  const uint64_t quarter = (u + (1ull << 61)) >> 62;
-  const int64_t rest = (int64_t)(u - (quarter << 62));  // [-2^61, 2^61): -1/8 .. 1/8 turn
-  float s, c;
-  sincospif((float)rest * 0x1p-63f, &s, &c);  // 2^63 = half a turn
+// split off as an integer; 32 bits of the rest, at most 1/8 turn, fix the angle to 4e-10, and Taylor
+// series of sine and cosine to y^9 and y^10 are within 2e-9 there (|y| <= pi / 4).
+//
+// Bound by the table's write and, nearly as much, by the ~40 instructions of a pair.  A thread
+// turns two neighbouring pairs (one 16-byte store) of kRows rows: it reads their frequencies, which
+// lie in the kernel's parameters and there cost a replay per lane, once.
+
+__device__ __forceinline__ float2 turn(int p, uint64_t freq, float magnitude) {
+  // p F mod 2^64 (negative p turns backwards), plus 1/8 turn: the top two bits are the nearest quarter
+  const uint64_t u = (uint64_t)(int64_t)p * freq + (1ull << 61);
+  const uint32_t quarter = (uint32_t)(u >> 62);
+  const int rest = (int)((uint32_t)(u >> 30) ^ 0x80000000u);  // 2^31 = 1/8 turn
+  const float x = (float)rest * 0x1p-33f;                      // in half turns: -1/4 .. 1/4
+  constexpr double kPi = 3.14159265358979323846, kPi2 = kPi * kPi;
+  const float z = x * x;
+  // sin(pi x) = x (pi - pi^3 z / 3! + ...), cos(pi x) = 1 - pi^2 z / 2! + ...
+  float s = (float)(kPi * kPi2 * kPi2 * kPi2 * kPi2 / 362880.0);
+  s = fmaf(s, z, (float)(-kPi * kPi2 * kPi2 * kPi2 / 5040.0));
+  s = fmaf(s, z, (float)(kPi * kPi2 * kPi2 / 120.0));
+  s = fmaf(s, z, (float)(-kPi * kPi2 / 6.0));
+  s = fmaf(s, z, (float)kPi) * x;
+  float c = (float)(-kPi2 * kPi2 * kPi2 * kPi2 * kPi2 / 3628800.0);
+  c = fmaf(c, z, (float)(kPi2 * kPi2 * kPi2 * kPi2 / 40320.0));
+  c = fmaf(c, z, (float)(-kPi2 * kPi2 * kPi2 / 720.0));
+  c = fmaf(c, z, (float)(kPi2 * kPi2 / 24.0));
+  c = fmaf(c, z, (float)(-kPi2 / 2.0));
+  c = fmaf(c, z, 1.0f);
   // turn (c, s) by quarter * 90 degrees
   const float co = (quarter & 1) ? -s : c, si = (quarter & 1) ? c : s;
-  const float m = (quarter & 2) ? -a.magnitude : a.magnitude;
-  reinterpret_cast<float2*>(a.table)[i] = make_float2(co * m, si * m);
+  const float m = (quarter & 2) ? -magnitude : magnitude;
+  return make_float2(co * m, si * m);
 }
 
-// One warp per (row, head).  Lane l holds head_dim / 32 adjacent values.
-template <int D>
-__global__ void qk_norm_rope_kernel(const QKNormRopeArgs a) {
-  constexpr int V = D / 32;
+template <int kRows>
+__global__ void __launch_bounds__(256) text_rope_kernel(const __grid_constant__ TextRopeArgs a) {
   grid_dependency_wait();
   allow_dependents();
-  const int heads = a.heads_q + a.heads_k;
+  const int j = threadIdx.x * 2;  // this thread's first pair
+  const int r0 = (blockIdx.x * blockDim.y + threadIdx.y) * kRows;
+  if (j >= a.half) return;
+  const bool two = j + 1 < a.half;
+  const uint64_t f0 = a.freq[j], f1 = a.freq[two ? j + 1 : j];
+  int p[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) p[i] = a.pos ? __ldg(a.pos + min(r0 + i, a.n - 1)) : r0 + i;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = r0 + i;
+    if (r >= a.n) break;
+    const float2 x = turn(p[i], f0, a.magnitude), y = turn(p[i], f1, a.magnitude);
+    float* dst = a.table + ((long long)r * a.half + j) * 2;
+    if ((a.half & 1) == 0) {  // rows of whole 16-byte pieces
+      *reinterpret_cast<float4*>(dst) = make_float4(x.x, x.y, y.x, y.y);
+    } else {
+      *reinterpret_cast<float2*>(dst) = x;
+      if (two) *reinterpret_cast<float2*>(dst + 2) = y;
+    }
+  }
+}
+
+// Norm and rotation: bound by reading and writing the heads.  A lane holds 8 adjacent values (one
+// 16-byte access), so a warp takes 2 heads of 128 or 4 of 64 at once, and kUnroll such groups
+// of one row, whose cosines and sines it reads once.  Every value of a pair is
+// y = x c + other s with the sign in s; `other` is the neighbour in the lane's own vector, or the
+// value half of rot_dim away, which lies in another lane of the head: rot_dim / 2 is a multiple of
+// 4, so of the vector's two halves each has its partner in one lane, in the same or the other half.
+// 10007 rows of 40 heads of 64, 48 of them turned: 21 us, 4.9 TB/s; two groups in 42 registers (six
+// blocks per SM) hide the chain index -> table -> store best (one group 25 us, four 24).
+constexpr int kUnroll = 2;
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(256, 6) qk_norm_rope_kernel(const QKNormRopeArgs a, int chunks) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;  // lanes per head, heads at once
+  grid_dependency_wait();
+  allow_dependents();
+  const int lane = threadIdx.x & 31, l = lane % kLanes, d0 = l * 8;
   const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (item >= (long long)a.rows * heads) return;
-  const int row = (int)(item / heads);
-  const int h = (int)(item - (long long)row * heads);
-  const bool is_q = h < a.heads_q;
-  const int hh = is_q ? h : h - a.heads_q;
-  const bf16* src = is_q ? a.q + row * a.ldq + hh * D : a.k + row * a.ldk + hh * D;
-  bf16* dst = is_q ? a.q_out + row * a.ldq_out + hh * D : a.k_out + row * a.ldk_out + hh * D;
-  const bf16* w = is_q ? a.q_norm : a.k_norm;
+  const int row = (int)(item / chunks);
+  if (row >= a.rows) return;
+  const int head0 = (int)(item - (long long)row * chunks) * (kHeads * kUnroll) + lane / kLanes;
   int t = row;
   if (a.rot_dim > 0 && a.table_row) {
     t = a.table_row[row];
@@ -55,66 +100,140 @@ __global__ void qk_norm_rope_kernel(const QKNormRopeArgs a) {
       return;
     }
   }
-  float x[V];
-  float ss = 0.f;
+  const int heads = a.heads_q + a.heads_k;
+  uint4 u[kUnroll];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    x[i] = __bfloat162float(src[lane * V + i]);
-    ss += x[i] * x[i];
-  }
-  if (w) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = x[i] * rs * __bfloat162float(w[lane * V + i]);
-  }
-  const int half = a.rot_dim / 2;
-  const float* tab = a.table + (long long)t * a.rot_dim;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int d = lane * V + i;
-    if (a.layout == 0) {
-      const float other = x[i ^ 1];
-      if (d < a.rot_dim) {
-        const float c = tab[(d >> 1) * 2], s = tab[(d >> 1) * 2 + 1];
-        const float y = (d & 1) ? x[i] * c + other * s : x[i] * c - other * s;
-        dst[d] = __float2bfloat16(y);
-      } else {
-        dst[d] = __float2bfloat16(x[i]);
-      }
+  for (int i = 0; i < kUnroll; ++i) {
+    const int h = head0 + i * kHeads;
+    if (h < heads) {
+      const bf16* src = h < a.heads_q ? a.q + row * a.ldq + h * D : a.k + row * a.ldk + (h - a.heads_q) * D;
+      u[i] = *reinterpret_cast<const uint4*>(src + d0);
     } else {
-      // the partner's lane: half is a multiple of 4, so slot i of another lane
-      const int pd = d < half ? d + half : (d < a.rot_dim ? d - half : d);
-      const float other = __shfl_sync(0xffffffffu, x[i], pd / V);
-      if (d < a.rot_dim) {
-        const int p = d < half ? d : d - half;
-        const float c = tab[p * 2], s = tab[p * 2 + 1];
-        dst[d] = __float2bfloat16(d < half ? x[i] * c - other * s : x[i] * c + other * s);
-      } else {
-        dst[d] = __float2bfloat16(x[i]);
-      }
+      u[i] = make_uint4(0, 0, 0, 0);
     }
   }
+  const bool turns = d0 < a.rot_dim;  // rot_dim is a multiple of 8: the vector turns or does not
+  const int half = a.rot_dim / 2;
+  float c[8], s[8];
+  int lane_lo = lane, lane_hi = lane;  // partners of the vector's halves
+  bool crossed = false;                // ... which are the other halves of theirs
+  if (turns) {
+    const float* tab = a.table + (long long)t * a.rot_dim;
+    if (kHalf) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int d = d0 + 4 * g, p = d < half ? d : d - half;
+        const float4 x = __ldg(reinterpret_cast<const float4*>(tab + 2 * p));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(tab + 2 * p + 4));
+        const float sign = d < half ? -1.f : 1.f;
+        c[4 * g] = x.x, c[4 * g + 1] = x.z, c[4 * g + 2] = y.x, c[4 * g + 3] = y.z;
+        s[4 * g] = sign * x.y, s[4 * g + 1] = sign * x.w, s[4 * g + 2] = sign * y.y, s[4 * g + 3] = sign * y.w;
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(tab + d0 + 4 * g));
+        c[4 * g] = c[4 * g + 1] = x.x, c[4 * g + 2] = c[4 * g + 3] = x.z;
+        s[4 * g] = -x.y, s[4 * g + 1] = x.y, s[4 * g + 2] = -x.w, s[4 * g + 3] = x.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
+  }
+  if (kHalf) {
+    crossed = (half & 7) != 0;
+    const int lo = d0 < half ? d0 + half : d0 - half, hi = d0 + 4 < half ? d0 + 4 + half : d0 + 4 - half;
+    if (turns) {
+      lane_lo = lane - l + lo / 8;
+      lane_hi = lane - l + hi / 8;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const int h = head0 + i * kHeads;
+    const uint32_t w4[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_bf16x2(w4[e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+    const bool is_q = h < a.heads_q;
+    if (a.q_norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+      // groups past the last head have no k_norm to read when there are no key heads
+      const uint4 wu = __ldg(reinterpret_cast<const uint4*>((is_q || h >= heads ? a.q_norm : a.k_norm) + d0));
+      const uint32_t ww[4] = {wu.x, wu.y, wu.z, wu.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack_bf16x2(ww[e]);
+        x[2 * e] *= rs * f.x;
+        x[2 * e + 1] *= rs * f.y;
+      }
+    }
+    float y[8];
+    if (kHalf) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // what the partners hold in the same and in the other half of their vectors
+        const float lo_same = __shfl_sync(0xffffffffu, x[e], lane_lo), lo_other = __shfl_sync(0xffffffffu, x[e + 4], lane_lo);
+        const float hi_same = __shfl_sync(0xffffffffu, x[e + 4], lane_hi), hi_other = __shfl_sync(0xffffffffu, x[e], lane_hi);
+        o[e] = crossed ? lo_other : lo_same;
+        o[e + 4] = crossed ? hi_other : hi_same;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = turns ? x[e] * c[e] + o[e] * s[e] : x[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = turns ? x[e] * c[e] + x[e ^ 1] * s[e] : x[e];
+    }
+    if (h < heads) {
+      bf16* dst = is_q ? a.q_out + row * a.ldq_out + h * D : a.k_out + row * a.ldk_out + (h - a.heads_q) * D;
+      *reinterpret_cast<uint4*>(dst + d0) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                       pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_qk(const QKNormRopeArgs& a, cudaStream_t s) {
+  const int per_warp = 32 / (D / 8) * kUnroll, chunks = (a.heads_q + a.heads_k + per_warp - 1) / per_warp;
+  const long long grid = ((long long)a.rows * chunks + 7) / 8;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  LaunchScope scope(kClsQKNormRope, s);
+  if (a.layout) return launch_k(qk_norm_rope_kernel<D, true>, dim3((unsigned)grid), dim3(256), 0, s, a, chunks);
+  return launch_k(qk_norm_rope_kernel<D, false>, dim3((unsigned)grid), dim3(256), 0, s, a, chunks);
 }
 
 }  // namespace
 
 cudaError_t launch_text_rope(const TextRopeArgs& a, cudaStream_t s) {
-  const long long total = (long long)a.n * a.half;
-  if (total == 0) return cudaSuccess;
+  if (a.n == 0) return cudaSuccess;
+  int tx = 1;  // threads along a row, two pairs each
+  while (tx * 2 < a.half) tx *= 2;
+  const int ty = 256 / tx;
   LaunchScope scope(kClsTextRope, s);
-  return launch_k(text_rope_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s, a);
+  auto run = [&](auto kernel, int rows) {
+    return launch_k(kernel, dim3((unsigned)((a.n + rows * ty - 1) / (rows * ty))), dim3(tx, ty), 0, s, a);
+  };
+  // 16 rows per thread where that leaves four blocks per SM (131072 x 64 pairs: 64 us with one row
+  // per thread, 14.1 with 8), else one, for the shortest path through a small table (512 rows: 1.7 us).
+  if (a.n / (16 * ty) >= 4 * 152) return run(text_rope_kernel<16>, 16);
+  if (a.n / (4 * ty) >= 4 * 152) return run(text_rope_kernel<4>, 4);
+  return run(text_rope_kernel<1>, 1);
 }
 
 cudaError_t launch_qk_norm_rope(const QKNormRopeArgs& a, cudaStream_t s) {
-  const long long items = (long long)a.rows * (a.heads_q + a.heads_k);
-  if (items == 0) return cudaSuccess;
-  const long long grid = (items + 7) / 8;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  LaunchScope scope(kClsQKNormRope, s);
-  if (a.head_dim == 64) return launch_k(qk_norm_rope_kernel<64>, dim3((unsigned)grid), dim3(256), 0, s, a);
-  return launch_k(qk_norm_rope_kernel<128>, dim3((unsigned)grid), dim3(256), 0, s, a);
+  if (a.rows == 0) return cudaSuccess;
+  return a.head_dim == 64 ? launch_qk<64>(a, s) : launch_qk<128>(a, s);
 }
 
 }  // namespace dit
