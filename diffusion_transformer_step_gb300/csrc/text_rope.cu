@@ -72,22 +72,27 @@ __global__ void __launch_bounds__(256) text_rope_kernel(const __grid_constant__ 
   }
 }
 
-// Norm and rotation: bound by reading and writing the heads.  A lane holds 8 adjacent values (one
-// 16-byte access), so a warp takes 2 heads of 128 or 4 of 64 at once, and kUnroll such groups
-// of one row, whose cosines and sines it reads once.  Every value of a pair is
-// y = x c + other s with the sign in s; `other` is the neighbour in the lane's own vector, or the
-// value half of rot_dim away, which lies in another lane of the head: rot_dim / 2 is a multiple of
-// 4, so of the vector's two halves each has its partner in one lane, in the same or the other half.
-// 10007 rows of 40 heads of 64, 48 of them turned: 21 us, 4.9 TB/s; two groups in 42 registers (six
-// blocks per SM) hide the chain index -> table -> store best (one group 25 us, four 24).
+// Norm and rotation: bound by reading and writing the heads.  A lane holds 8 values of a head that turn
+// among themselves, so a warp takes 2 heads of 128 or 4 of 64 at once, and kUnroll such groups of
+// one row, whose cosines and sines it reads once.  Adjacent pairs: 8 neighbours, one 16-byte access.
+// Halves: 4 values and their 4 partners rot_dim / 2 further on, two 8-byte accesses (rot_dim / 2 is
+// a multiple of 4); partners in other lanes, fetched by shuffles, took 71 us where this takes 49 (heads of 128).
+// The lanes behind the turned ones hold 8 neighbours each.
+// 10007 rows of 40 heads of 64, 48 values of each turned: 21 us, 4.9 TB/s; two groups and six blocks
+// per SM hide the chain index -> table -> store best (one group 25 us, four 24).
 constexpr int kUnroll = 2;
+
+__device__ __forceinline__ void unpack4(const uint2& u, float* x) {
+  const float2 f = unpack_bf16x2(u.x), g = unpack_bf16x2(u.y);
+  x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
+}
 
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(256, 6) qk_norm_rope_kernel(const QKNormRopeArgs a, int chunks) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;  // lanes per head, heads at once
   grid_dependency_wait();
   allow_dependents();
-  const int lane = threadIdx.x & 31, l = lane % kLanes, d0 = l * 8;
+  const int lane = threadIdx.x & 31, l = lane % kLanes;
   const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int row = (int)(item / chunks);
   if (row >= a.rows) return;
@@ -100,67 +105,41 @@ __global__ void __launch_bounds__(256, 6) qk_norm_rope_kernel(const QKNormRopeAr
       return;
     }
   }
-  const int heads = a.heads_q + a.heads_k;
-  uint4 u[kUnroll];
+  const int heads = a.heads_q + a.heads_k, half = a.rot_dim / 2;
+  // where this lane's two groups of 4 values lie, and whether they turn
+  const bool turns = 8 * l < a.rot_dim;
+  const int d0 = kHalf && turns ? 4 * l : 8 * l, d1 = kHalf && turns ? d0 + half : d0 + 4;
+  uint2 u[kUnroll][2];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const int h = head0 + i * kHeads;
+    u[i][0] = u[i][1] = make_uint2(0, 0);
     if (h < heads) {
       const bf16* src = h < a.heads_q ? a.q + row * a.ldq + h * D : a.k + row * a.ldk + (h - a.heads_q) * D;
-      u[i] = *reinterpret_cast<const uint4*>(src + d0);
-    } else {
-      u[i] = make_uint4(0, 0, 0, 0);
+      if (kHalf) {
+        u[i][0] = *reinterpret_cast<const uint2*>(src + d0);
+        u[i][1] = *reinterpret_cast<const uint2*>(src + d1);
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + d0);
+        u[i][0] = make_uint2(v.x, v.y);
+        u[i][1] = make_uint2(v.z, v.w);
+      }
     }
   }
-  const bool turns = d0 < a.rot_dim;  // rot_dim is a multiple of 8: the vector turns or does not
-  const int half = a.rot_dim / 2;
-  float c[8], s[8];
-  int lane_lo = lane, lane_hi = lane;  // partners of the vector's halves
-  bool crossed = false;                // ... which are the other halves of theirs
+  // cosines and sines of the lane's four pairs: (x_e, x_{e+4}), or (x_{2e}, x_{2e+1})
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (turns) {
-    const float* tab = a.table + (long long)t * a.rot_dim;
-    if (kHalf) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int d = d0 + 4 * g, p = d < half ? d : d - half;
-        const float4 x = __ldg(reinterpret_cast<const float4*>(tab + 2 * p));
-        const float4 y = __ldg(reinterpret_cast<const float4*>(tab + 2 * p + 4));
-        const float sign = d < half ? -1.f : 1.f;
-        c[4 * g] = x.x, c[4 * g + 1] = x.z, c[4 * g + 2] = y.x, c[4 * g + 3] = y.z;
-        s[4 * g] = sign * x.y, s[4 * g + 1] = sign * x.w, s[4 * g + 2] = sign * y.y, s[4 * g + 3] = sign * y.w;
-      }
-    } else {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(tab + d0 + 4 * g));
-        c[4 * g] = c[4 * g + 1] = x.x, c[4 * g + 2] = c[4 * g + 3] = x.z;
-        s[4 * g] = -x.y, s[4 * g + 1] = x.y, s[4 * g + 2] = -x.w, s[4 * g + 3] = x.w;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
-  }
-  if (kHalf) {
-    crossed = (half & 7) != 0;
-    const int lo = d0 < half ? d0 + half : d0 - half, hi = d0 + 4 < half ? d0 + 4 + half : d0 + 4 - half;
-    if (turns) {
-      lane_lo = lane - l + lo / 8;
-      lane_hi = lane - l + hi / 8;
-    }
+    const float4* tab = reinterpret_cast<const float4*>(a.table + (long long)t * a.rot_dim + 8 * l);
+    const float4 x = __ldg(tab), y = __ldg(tab + 1);
+    c[0] = x.x, s[0] = x.y, c[1] = x.z, s[1] = x.w, c[2] = y.x, s[2] = y.y, c[3] = y.z, s[3] = y.w;
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const int h = head0 + i * kHeads;
-    const uint32_t w4[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_bf16x2(w4[e]);
-      x[2 * e] = f.x;
-      x[2 * e + 1] = f.y;
-    }
     const bool is_q = h < a.heads_q;
+    float x[8];
+    unpack4(u[i][0], x);
+    unpack4(u[i][1], x + 4);
     if (a.q_norm) {
       float ss = 0.f;
 #pragma unroll
@@ -169,36 +148,30 @@ __global__ void __launch_bounds__(256, 6) qk_norm_rope_kernel(const QKNormRopeAr
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
       // groups past the last head have no k_norm to read when there are no key heads
-      const uint4 wu = __ldg(reinterpret_cast<const uint4*>((is_q || h >= heads ? a.q_norm : a.k_norm) + d0));
-      const uint32_t ww[4] = {wu.x, wu.y, wu.z, wu.w};
+      const bf16* w = is_q || h >= heads ? a.q_norm : a.k_norm;
+      float f[8];
+      unpack4(__ldg(reinterpret_cast<const uint2*>(w + d0)), f);
+      unpack4(__ldg(reinterpret_cast<const uint2*>(w + d1)), f + 4);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack_bf16x2(ww[e]);
-        x[2 * e] *= rs * f.x;
-        x[2 * e + 1] *= rs * f.y;
-      }
+      for (int e = 0; e < 8; ++e) x[e] *= rs * f[e];
     }
     float y[8];
-    if (kHalf) {
-      float o[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // what the partners hold in the same and in the other half of their vectors
-        const float lo_same = __shfl_sync(0xffffffffu, x[e], lane_lo), lo_other = __shfl_sync(0xffffffffu, x[e + 4], lane_lo);
-        const float hi_same = __shfl_sync(0xffffffffu, x[e + 4], lane_hi), hi_other = __shfl_sync(0xffffffffu, x[e], lane_hi);
-        o[e] = crossed ? lo_other : lo_same;
-        o[e + 4] = crossed ? hi_other : hi_same;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = turns ? x[e] * c[e] + o[e] * s[e] : x[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = turns ? x[e] * c[e] + x[e ^ 1] * s[e] : x[e];
+    for (int e = 0; e < 4; ++e) {
+      const int p = kHalf ? e : 2 * e, q = kHalf ? e + 4 : 2 * e + 1;
+      y[p] = turns ? x[p] * c[e] - x[q] * s[e] : x[p];
+      y[q] = turns ? x[q] * c[e] + x[p] * s[e] : x[q];
     }
     if (h < heads) {
       bf16* dst = is_q ? a.q_out + row * a.ldq_out + h * D : a.k_out + row * a.ldk_out + (h - a.heads_q) * D;
-      *reinterpret_cast<uint4*>(dst + d0) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                       pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+      const uint2 lo = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      const uint2 hi = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+      if (kHalf) {
+        *reinterpret_cast<uint2*>(dst + d0) = lo;
+        *reinterpret_cast<uint2*>(dst + d1) = hi;
+      } else {
+        *reinterpret_cast<uint4*>(dst + d0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
   }
 }
