@@ -124,7 +124,7 @@ Parts parts_layout(const Plan& p, int heads_k, int head_dim) {
 struct alignas(64) TextAttnParams {
   CUtensorMap q_map, k_map, v_map;
   TextAttnArgs a;
-  int group, tq, levels, tiles, splits;
+  int group, tq, levels, tiles, splits, items;
   float scale_log2;
   const int2* list;
   int2* desc;
@@ -132,18 +132,28 @@ struct alignas(64) TextAttnParams {
   float* o;
 };
 
-enum : uint32_t { kSiteQ = 0x511, kSiteFree, kSiteReady, kSitePFull, kSiteSFull, kSiteODone, kSiteFixed, kSiteFix };
+enum : uint32_t {
+  kSiteQ = 0x511, kSiteFree, kSiteReady, kSitePFull, kSiteSFull, kSiteODone, kSiteFixed, kSiteFix, kSiteItem, kSiteItemFree
+};
 
 template <int D>
 struct Smem {
   static constexpr uint32_t kTile = (D / 64) * kHalfBytes;  // a 128-row tile of Q, K or V
   static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBar = 6 * kTile;
-  static constexpr size_t kBytes = 1024 + kBar + 256;
+  static constexpr size_t kBytes = 1024 + kBar + 384;
+};
+
+// One work item of a CTA, as the loading warp found it.
+struct Item {
+  int q0, nq, k0, nk, tok0;  // the sequence's rows, and the pair's first token
+  int n0, n1, b0;            // key blocks of each tile, and the first of them (of this split)
+  int hk, split, rank;       // key head, key split, place of the pair in the work order
+  int stop;                  // no more items
 };
 
 // The t-th pair of tiles, longest first (whole warp; span and tile index broadcast).
 __device__ __forceinline__ bool find_tile(const TextAttnArgs& a, int tp, int levels, int tiles, int t, int lane,
-                                          Span& sp, int& index) {
+                                          bool report, Span& sp, int& index) {
   Span s[2];
   int n[2];
 #pragma unroll
@@ -152,12 +162,12 @@ __device__ __forceinline__ bool find_tile(const TextAttnArgs& a, int tp, int lev
     s[i] = Span{0, 0, 0, 0, true};
     if (id < a.seqs) s[i] = load_span(a, id);
     n[i] = (s[i].nq + tp - 1) / tp;
-    if (!s[i].ok && blockIdx.x == 0) report_bad_entry(a.status, kSiteTextLengths);
+    if (!s[i].ok && report) report_bad_entry(a.status, kSiteTextLengths);
   }
   auto count = [&](int v) { return __reduce_add_sync(0xffffffffu, max(0, n[0] - v) + max(0, n[1] - v)); };
   const int all = count(0);
   // more tiles than the buffers' rows allow: query rows of several sequences overlap
-  if (all > tiles && blockIdx.x == 0 && lane == 0) report_bad_entry(a.status, kSiteTextLengths);
+  if (all > tiles && report && lane == 0) report_bad_entry(a.status, kSiteTextLengths);
   if (all <= t) return false;
   int lo = 0, hi = levels;  // count(lo) > t >= count(hi)
   while (hi - lo > 1) {
@@ -261,21 +271,28 @@ __device__ __forceinline__ void issue_qk(const Descs<64>& d, uint32_t tmem, int 
 }
 
 struct Bars {
-  uint64_t *q_full, *ready, *slot_free, *s_full, *p_full, *o_done, *fixed, *drain;
+  uint64_t *q_full, *ready, *slot_free, *s_full, *p_full, *o_done, *fixed, *drain, *item_full, *item_free;
+};
+
+// How often a role has waited on each of two barriers: the parity of its next wait.
+struct Turns {
+  uint32_t n[2] = {0, 0};
+  __device__ __forceinline__ uint32_t next(int i) { return (i ? n[1]++ : n[0]++) & 1u; }
 };
 
 // Key block j of the issuer (ring stage ST = j & 1), n[t] blocks for tile t:
 //   O0 += P0 V_j, S0 = Q0 K_{j+1}^T, O1 += P1 V_j, S1 = Q1 K_{j+1}^T.
 template <int D, int ST>
 __device__ __forceinline__ bool mma_block(const Descs<D>& d, uint32_t tmem, int j, int n0, int n1, bool fix,
-                                          uint32_t idesc_qk, uint32_t idesc_pv, const Bars& bar, const WaitCtx& wc) {
-  if (!mbar_wait(&bar.ready[ST], (uint32_t)(j >> 1) & 1u, wc, kSiteReady)) return false;
-  if (fix && j + 1 == max(n0, n1) && !mbar_wait(bar.fixed, 0, wc, kSiteFixed)) return false;
+                                          uint32_t idesc_qk, uint32_t idesc_pv, const Bars& bar, const WaitCtx& wc,
+                                          Turns& t_ready, Turns& t_p, uint32_t& t_fixed) {
+  if (!mbar_wait(&bar.ready[ST], t_ready.next(ST), wc, kSiteReady)) return false;
+  if (fix && j + 1 == max(n0, n1) && !mbar_wait(bar.fixed, t_fixed++ & 1u, wc, kSiteFixed)) return false;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int n = t ? n1 : n0;
     if (j < n) {
-      if (!mbar_wait(&bar.p_full[t], (uint32_t)j & 1u, wc, kSitePFull)) return false;
+      if (!mbar_wait(&bar.p_full[t], t_p.next(t), wc, kSitePFull)) return false;
       tc_fence_after();
       umma8_ts(tmem + (uint32_t)(t * 256 + 128), tmem + (uint32_t)(t * 256), d.v[ST], idesc_pv, j > 0 ? 1u : 0u);
       if (j + 1 < n) issue_qk<ST ^ 1>(d, tmem, t, idesc_qk, &bar.s_full[t]);
@@ -322,17 +339,14 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  const Bars bar{bars + 0, bars + 1, bars + 3, bars + 5, bars + 7, bars + 9, bars + 11, bars + 12};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+  const Bars bar{bars + 0, bars + 1, bars + 3, bars + 5, bars + 7, bars + 9, bars + 11, bars + 12, bars + 13, bars + 15};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* item = reinterpret_cast<int*>(tmem_slot + 2);  // q0, nq, k0, nk, first token; nq < 0: nothing to do
+  Item* items = reinterpret_cast<Item*>(bars + 18);  // two: the current one and the next
 
   const TextAttnArgs& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = P.group, TQ = P.tq, TP = 2 * TQ;
-  const int hk = blockIdx.x % a.heads_k;
-  const int rest = blockIdx.x / a.heads_k;
-  const int split = rest % P.splits, t_rank = rest / P.splits;
 
   if (threadIdx.x == 32) {
     mbar_init(bar.q_full, 1);
@@ -342,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_done[i], 1);
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_free[i], 9);  // the issuer and eight softmax warps
     }
     mbar_init(bar.fixed, 1);
     mbar_init(bar.drain, 1);
@@ -358,114 +374,143 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  grid_dependency_wait();  // lengths, Q, K, V and the output belong to earlier kernels of the stream
-  allow_dependents();
-  if (warp == 0) {
-    Span sp{0, -1, 0, 0, true};
-    int index = 0;
-    bool found;
-    if (P.list) {
-      const int2 e = P.list[t_rank];
-      found = e.x >= 0;
-      if (found) sp = load_span(a, e.x);
-      index = e.y;
-    } else {
-      found = find_tile(a, TP, P.levels, P.tiles, t_rank, lane, sp, index);
-    }
-    if (lane == 0) {
-      item[0] = sp.q0;
-      item[1] = found ? sp.nq : -1;
-      item[2] = sp.k0;
-      item[3] = sp.nk;
-      item[4] = index * TP;
-      if (P.splits > 1 && hk == 0 && split == 0)
-        P.desc[t_rank] = found ? make_int2(sp.q0 + index * TP, min(TP, sp.nq - index * TP)) : make_int2(0, 0);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{a.status, abort_flag, kWaitLimitNs};
-  const int q0 = item[0], nq = item[1], k0 = item[2], nk = item[3], tok0 = item[4];
-  const int shift = nk - nq;  // causal: token i sees keys j <= i + shift
-
-  // key blocks of each tile, and this split's run [b0, b0 + n[t]) of them
-  int n0 = 0, n1 = 0, b0 = 0;
-  if (nq >= 0) {
-    auto blocks = [&](int first) {
-      if (first >= nq) return 0;
-      const int last = min(first + TQ, nq) - 1;
-      const int end = a.causal ? min(nk, last + shift + 1) : nk;
-      return end > 0 ? (end + kKeys - 1) / kKeys : 0;
-    };
-    n0 = blocks(tok0);
-    n1 = blocks(tok0 + TQ);
-    if (P.splits > 1) {
-      const int nb = max(n0, n1);
-      b0 = (int)((long long)nb * split / P.splits);
-      const int b1 = (int)((long long)nb * (split + 1) / P.splits);
-      n0 = max(0, min(n0, b1) - b0);
-      n1 = max(0, min(n1, b1) - b0);
-    }
-  }
-  const int nmax = max(n0, n1);
-  // rows of the last block's V past the sequence's keys must read as zeros
-  const bool fix = nmax > 0 && (b0 + nmax) * kKeys > nk;
+  grid_dependency_wait();  // lengths, Q, K, V and the output belong to earlier kernels of the stream
+  allow_dependents();
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ work items and TMA producer
     // Ring slot j & 1 carries V_j and K_{j+1}; slot j >= 1 is loaded once the scores of block
-    // j - 1 of the longer tile are complete, which ends every read of V_{j-2} and K_{j-1}.
+    // j - 1 of the longer tile are complete, which ends every read of V_{j-2} and K_{j-1}.  The next
+    // item's Q and K_0 follow when the last scores are complete (every QK is done), its V_0 and K_1 when the
+    // last O of both tiles is: while the softmax warps finish one item, the next one's loads and scores are under way.
+    Turns t_free, t_item, t_o, t_ready;
+    uint32_t live = 0;     // items with key blocks so far
+    int pn = 0, pn0 = 0, pn1 = 0;  // the last such item's blocks
     bool ok = true;
-    if (lane == 0 && nmax > 0) {
-      int issued = 0;
-      const uint32_t qbytes = (uint32_t)(G * TQ) * 128u * (D / 64);
-      mbar_arrive_expect_tx(bar.q_full, (uint32_t)((n0 > 0) + (n1 > 0)) * qbytes + L::kTile);
-      for (int t = 0; t < 2; ++t)
-        if ((t ? n1 : n0) > 0)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(smem + L::kQ + t * L::kTile + h * kHalfBytes, &P.q_map, bar.q_full, h * 64, 0, hk,
-                        q0 + tok0 + t * TQ);
-      for (int h = 0; h < D / 64; ++h)
-        tma_load_3d(smem + L::kK + h * kHalfBytes, &P.k_map, bar.q_full, h * 64, hk, k0 + b0 * kKeys);
-      for (int j = 0; j < nmax; ++j) {
-        const int b = j & 1;
-        if (j >= 1 && !mbar_wait_sleep(&bar.slot_free[b], (uint32_t)((j - 1) >> 1) & 1u, wc, kSiteFree)) {
-          ok = false;
-          break;
+    for (int k = 0; ok; ++k) {
+      // items are dealt out in turns that go back and forth: long ones first, equal shares
+      const int turn = k * (int)gridDim.x;
+      const int id = turn + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+      const bool stop = turn >= P.items;
+      Span sp{0, -1, 0, 0, true};
+      int index = 0, hk = 0, split = 0, rank = 0;
+      bool found = false;
+      if (!stop && id < P.items) {
+        hk = id % a.heads_k;
+        split = (id / a.heads_k) % P.splits;
+        rank = id / a.heads_k / P.splits;
+        if (P.list) {
+          const int2 e = P.list[rank];
+          found = e.x >= 0;
+          if (found) sp = load_span(a, e.x);
+          index = e.y;
+        } else {
+          found = find_tile(a, TP, P.levels, P.tiles, rank, lane, k == 0 && blockIdx.x == 0, sp, index);
         }
-        const bool more = j + 1 < nmax;
-        mbar_arrive_expect_tx(&bar.ready[b], more ? 2 * L::kTile : L::kTile);
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_3d(smem + L::kV + b * L::kTile + h * kHalfBytes, &P.v_map, &bar.ready[b], h * 64, hk,
-                      k0 + (b0 + j) * kKeys);
-        if (more)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(smem + L::kK + (b ^ 1) * L::kTile + h * kHalfBytes, &P.k_map, &bar.ready[b], h * 64, hk,
-                        k0 + (b0 + j + 1) * kKeys);
-        issued = j + 1;
+        if (P.splits > 1 && hk == 0 && split == 0 && lane == 0)
+          P.desc[rank] = found ? make_int2(sp.q0 + index * TP, min(TP, sp.nq - index * TP)) : make_int2(0, 0);
       }
-      if (!ok) {
-        // Unwinding: let copies in flight land (bounded) before the block exits.
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try(bar.q_full, 0) && global_timer_ns() - t0 < 100000000ull) {
+      if (!stop && !found) continue;
+      Item it{sp.q0, sp.nq, sp.k0, sp.nk, index * TP, 0, 0, 0, hk, split, rank, stop};
+      if (found) {
+        // key blocks of each tile, and this split's run [b0, b0 + n) of them
+        const int shift = it.nk - it.nq;
+        auto blocks = [&](int first) {
+          if (first >= it.nq) return 0;
+          const int last = min(first + TQ, it.nq) - 1;
+          const int end = a.causal ? min(it.nk, last + shift + 1) : it.nk;
+          return end > 0 ? (end + kKeys - 1) / kKeys : 0;
+        };
+        it.n0 = blocks(it.tok0);
+        it.n1 = blocks(it.tok0 + TQ);
+        if (P.splits > 1) {
+          const int nb = max(it.n0, it.n1);
+          it.b0 = (int)((long long)nb * split / P.splits);
+          const int b1 = (int)((long long)nb * (split + 1) / P.splits);
+          it.n0 = max(0, min(it.n0, b1) - it.b0);
+          it.n1 = max(0, min(it.n1, b1) - it.b0);
         }
-        for (int j = (issued > 2 ? issued - 2 : 0); j < issued; ++j)
-          while (!mbar_try(&bar.ready[j & 1], (uint32_t)(j >> 1) & 1u) && global_timer_ns() - t0 < 200000000ull) {
+      }
+      const int slot = (int)((t_item.n[0] + t_item.n[1]) & 1u);
+      ok = mbar_wait_sleep(&bar.item_free[slot], t_item.next(slot) ^ 1u, wc, kSiteItemFree);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        items[slot] = it;
+        mbar_arrive(&bar.item_full[slot]);
+      }
+      __syncwarp();
+      if (stop) break;
+      const int nmax = max(it.n0, it.n1);
+      if (nmax == 0) continue;
+      const int krow = it.k0 + it.b0 * kKeys;
+      if (lane == 0) {
+        int issued = 0;
+        if (live > 0) ok = mbar_wait_sleep(&bar.slot_free[pn & 1], t_free.next(pn & 1), wc, kSiteFree);
+        if (ok) {
+          const uint32_t qbytes = (uint32_t)(G * TQ) * 128u * (D / 64);
+          mbar_arrive_expect_tx(bar.q_full, (uint32_t)((it.n0 > 0) + (it.n1 > 0)) * qbytes + L::kTile);
+          for (int t = 0; t < 2; ++t)
+            if ((t ? it.n1 : it.n0) > 0)
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_4d(smem + L::kQ + t * L::kTile + h * kHalfBytes, &P.q_map, bar.q_full, h * 64, 0, it.hk,
+                            it.q0 + it.tok0 + t * TQ);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(smem + L::kK + h * kHalfBytes, &P.k_map, bar.q_full, h * 64, it.hk, krow);
+          ++live;
+          if (pn0 > 0) ok = mbar_wait_sleep(&bar.o_done[0], t_o.next(0), wc, kSiteODone);
+          if (ok && pn1 > 0) ok = mbar_wait_sleep(&bar.o_done[1], t_o.next(1), wc, kSiteODone);
+        }
+        for (int j = 0; j < nmax && ok; ++j) {
+          const int b = j & 1;
+          if (j >= 1 && !mbar_wait_sleep(&bar.slot_free[b], t_free.next(b), wc, kSiteFree)) {
+            ok = false;
+            break;
           }
+          const bool more = j + 1 < nmax;
+          mbar_arrive_expect_tx(&bar.ready[b], more ? 2 * L::kTile : L::kTile);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(smem + L::kV + b * L::kTile + h * kHalfBytes, &P.v_map, &bar.ready[b], h * 64, it.hk,
+                        krow + j * kKeys);
+          if (more)
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(smem + L::kK + (b ^ 1) * L::kTile + h * kHalfBytes, &P.k_map, &bar.ready[b], h * 64, it.hk,
+                          krow + (j + 1) * kKeys);
+          issued = j + 1;
+        }
+        if (!ok) {
+          // Unwinding: let copies in flight land (bounded) before the block exits.
+          const uint64_t t0 = global_timer_ns();
+          while (live > 0 && !mbar_try(bar.q_full, (live - 1) & 1u) && global_timer_ns() - t0 < 100000000ull) {
+          }
+          for (int j = (issued > 2 ? issued - 2 : 0); j < issued; ++j)
+            while (!mbar_try(&bar.ready[j & 1], (t_ready.n[j & 1] + (uint32_t)(j >> 1)) & 1u) &&
+                   global_timer_ns() - t0 < 200000000ull) {
+            }
+        }
       }
-    }
-    __syncwarp();
-    if (fix) {
-      const int j = nmax - 1;
+      __syncwarp();
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) ok = mbar_wait_sleep(&bar.ready[j & 1], (uint32_t)(j >> 1) & 1u, wc, kSiteFix);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        const int valid = nk - (b0 + j) * kKeys;  // 1 .. 127: rows are 128 contiguous bytes each
+      if (!ok) break;
+      pn = nmax;
+      pn0 = it.n0;
+      pn1 = it.n1;
+      t_ready.n[0] += (uint32_t)(nmax + 1) >> 1;  // uses of each ring slot so far
+      t_ready.n[1] += (uint32_t)nmax >> 1;
+      if ((it.b0 + nmax) * kKeys > it.nk) {
+        // rows of the last block's V past the sequence's keys must read as zeros
+        const int j = nmax - 1, b = j & 1;
+        ok = mbar_wait_sleep(&bar.ready[b], (t_ready.n[b] - 1u) & 1u, wc, kSiteFix);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int valid = it.nk - (it.b0 + j) * kKeys;  // 1 .. 127: rows are 128 contiguous bytes each
         for (int h = 0; h < D / 64; ++h) {
-          uint4* v = reinterpret_cast<uint4*>(smem + L::kV + (j & 1) * L::kTile + h * kHalfBytes);
+          uint4* v = reinterpret_cast<uint4*>(smem + L::kV + b * L::kTile + h * kHalfBytes);
           for (int i = valid * 8 + lane; i < kKeys * 8; i += 32) v[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
@@ -475,45 +520,75 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && nmax > 0) {
+    // An item's QK may overwrite S while the softmax warps still write out the one before: P over
+    // it has been read by MMAs issued earlier.  Its first PV waits for its first P, which those
+    // warps store after they have read O.
+    if (lane == 0) {
       const uint32_t idesc_qk = make_idesc_bf16(128, kKeys, false);
       const uint32_t idesc_pv = make_idesc_bf16(128, D, true);
       Descs<D> d;
       make_descs<D>(smem, d);
-      bool ok = mbar_wait(bar.q_full, 0, wc, kSiteQ);
-      if (ok) {
-        tc_fence_after();
-        if (n0 > 0) issue_qk<0>(d, tmem, 0, idesc_qk, &bar.s_full[0]);
-        if (n1 > 0) issue_qk<0>(d, tmem, 1, idesc_qk, &bar.s_full[1]);
-      }
-      for (int j = 0; j < nmax && ok; j += 2) {
-        ok = mma_block<D, 0>(d, tmem, j, n0, n1, fix, idesc_qk, idesc_pv, bar, wc);
-        if (ok && j + 1 < nmax) ok = mma_block<D, 1>(d, tmem, j + 1, n0, n1, fix, idesc_qk, idesc_pv, bar, wc);
+      Turns t_ready, t_p;
+      uint32_t t_fixed = 0, live = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        ok = mbar_wait(&bar.item_full[k & 1], (k >> 1) & 1u, wc, kSiteItem);
+        if (!ok) break;
+        const Item& it = items[k & 1];
+        const int n0 = it.n0, n1 = it.n1, nmax = max(n0, n1);
+        const bool stop = it.stop, fix = (it.b0 + nmax) * kKeys > it.nk;
+        mbar_arrive(&bar.item_free[k & 1]);
+        if (stop) break;
+        if (nmax == 0) continue;
+        ok = mbar_wait(bar.q_full, live++ & 1u, wc, kSiteQ);
+        if (ok) {
+          tc_fence_after();
+          if (n0 > 0) issue_qk<0>(d, tmem, 0, idesc_qk, &bar.s_full[0]);
+          if (n1 > 0) issue_qk<0>(d, tmem, 1, idesc_qk, &bar.s_full[1]);
+        }
+        for (int j = 0; j < nmax && ok; j += 2) {
+          ok = mma_block<D, 0>(d, tmem, j, n0, n1, fix, idesc_qk, idesc_pv, bar, wc, t_ready, t_p, t_fixed);
+          if (ok && j + 1 < nmax)
+            ok = mma_block<D, 1>(d, tmem, j + 1, n0, n1, fix, idesc_qk, idesc_pv, bar, wc, t_ready, t_p, t_fixed);
+        }
       }
       umma_commit(bar.drain);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try(bar.drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
       }
     }
-  } else if (nq >= 0) {
+  } else {
     // ------------------------------------------------------------ softmax / output
     const int tile = (warp - 2) >> 2;  // warps 2-5 -> tile 0, warps 6-9 -> tile 1
     const int qq = warp & 3;           // TMEM lane quarter of this warp
     const int row = qq * 32 + lane;
-    const int n = tile ? n1 : n0;
-    const bool releaser = tile == (n1 >= n0 ? 1 : 0) && qq == 2 && lane == 0;
     const uint32_t tS = tmem + (uint32_t)(tile * 256) + ((uint32_t)(qq * 32) << 16);
     const uint32_t tO = tS + 128;
     const float c = P.scale_log2;
     const int token = row / G, g = row - token * G;
+    uint32_t t_s = 0, t_o = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+    ok = mbar_wait(&bar.item_full[k & 1], (k >> 1) & 1u, wc, kSiteItem);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const Item& it = items[k & 1];
+    const int q0 = it.q0, nq = it.nq, k0 = it.k0, nk = it.nk, b0 = it.b0, hk = it.hk, tok0 = it.tok0;
+    const int n = tile ? it.n1 : it.n0;
+    const bool longer = tile == (it.n1 >= it.n0 ? 1 : 0), stop = it.stop;
+    const long long part = ((long long)it.rank * a.heads_k + hk) * P.splits + it.split;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.item_free[k & 1]);
+    if (stop) break;
+    const int shift = nk - nq;  // causal: token i sees keys j <= i + shift
+    const bool releaser = longer && qq == 2 && lane == 0;
     const int qi = tok0 + tile * TQ + token;
     const bool active = token < TQ && qi < nq;
     // keys this row sees; rows that are not stored need no mask
     const int limit = !active ? 0x3fffffff : (a.causal ? min(nk, qi + shift + 1) : nk);
     float m_run = active ? -INFINITY : 0.f, l_run = 0.f;
-    bool ok = true;
     for (int j = 0; j < n; ++j) {
-      ok = mbar_wait(&bar.s_full[tile], (uint32_t)j & 1u, wc, kSiteSFull);
+      ok = mbar_wait(&bar.s_full[tile], t_s++ & 1u, wc, kSiteSFull);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (releaser) mbar_arrive(&bar.slot_free[(j + 1) & 1]);
@@ -571,14 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       if (lane == 0) mbar_arrive(&bar.p_full[tile]);
     }
     if (ok && n > 0) {
-      ok = mbar_wait_sleep(&bar.o_done[tile], 0, wc, kSiteODone);
+      ok = mbar_wait_sleep(&bar.o_done[tile], t_o++ & 1u, wc, kSiteODone);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
     if (ok) {
       const bool none = n == 0 || l_run == 0.f;  // no key seen: zeros
       const float inv_l = none ? 0.f : 1.0f / l_run;
-      const long long part = ((long long)t_rank * a.heads_k + hk) * P.splits + split;
       const int prow = (tile * TQ + token) * G + g;
       bf16* out = a.out + (long long)(q0 + qi) * a.ldo + (hk * G + g) * D;
       float* po = P.splits > 1 ? P.o + (part * 256 + prow) * D : nullptr;
@@ -642,6 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
           for (int e = 0; e < V; ++e) dst[lane * V + e] = __float2bfloat16(l == 0.f ? 0.f : o[e] / l);
         }
       }
+    }
+    tc_fence_before();  // O has been read before the next item's first P is announced
     }
   }
 
@@ -736,8 +812,10 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
         launch_k(text_attention_list_kernel, dim3(1), dim3(1024), 0, s, a, p.tq * 2, p.levels, p.tiles, list);
     if (e != cudaSuccess) return e;
   }
-  const long long grid = (long long)p.tiles * a.heads_k * p.splits;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  const long long items = (long long)p.tiles * a.heads_k * p.splits;
+  if (items > 0x7fff0000ll) return cudaErrorInvalidValue;
+  P.items = (int)items;
+  const int sms = sm_count(), grid = items < sms ? (int)items : sms;
   {
     LaunchScope scope(kClsTextAttention, s);
     cudaError_t e = launch_k(text_attention_kernel<D>, dim3((unsigned)grid), dim3(kThreads), smem, s, P);
