@@ -25,7 +25,9 @@ enum : uint32_t { kStatusTimeout = 1u, kStatusBadLaunch = 2u, kStatusBadEntry = 
 struct DeviceStatus {
   uint32_t word;     // OR of kStatus* bits
   uint32_t where;    // id of the first wait that gave up (kernel * 16 + site)
-  uint32_t pad[62];
+  uint32_t next_item;   // work counters of the text attention: zero between calls
+  uint32_t items_done;
+  uint32_t pad[60];
 };
 
 // ---------------------------------------------------------------------------------

@@ -139,7 +139,9 @@ enum : uint32_t {
 template <int D>
 struct Smem {
   static constexpr uint32_t kTile = (D / 64) * kHalfBytes;  // a 128-row tile of Q, K or V
-  static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBar = 6 * kTile;
+  static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile;
+  static constexpr uint32_t kOut = 6 * kTile;            // 32 rows x 64 dims of output per softmax warp
+  static constexpr uint32_t kBar = kOut + 8 * 4096;
   static constexpr size_t kBytes = 1024 + kBar + 384;
 };
 
@@ -393,14 +395,17 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
     int pn = 0, pn0 = 0, pn1 = 0;  // the last such item's blocks
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      // items are dealt out in turns that go back and forth: long ones first, equal shares
-      const int turn = k * (int)gridDim.x;
-      const int id = turn + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-      const bool stop = turn >= P.items;
+      // the first item by place, the others as they come, longest first
+      int id = (int)blockIdx.x;
+      if (k > 0) {
+        if (lane == 0) id = (int)(gridDim.x + atomicAdd(&a.status->next_item, 1u));
+        id = __shfl_sync(0xffffffffu, id, 0);
+      }
+      const bool stop = id >= P.items;
       Span sp{0, -1, 0, 0, true};
       int index = 0, hk = 0, split = 0, rank = 0;
       bool found = false;
-      if (!stop && id < P.items) {
+      if (!stop) {
         hk = id % a.heads_k;
         split = (id / a.heads_k) % P.splits;
         rank = id / a.heads_k / P.splits;
@@ -566,158 +571,188 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
     const uint32_t tO = tS + 128;
     const float c = P.scale_log2;
     const int token = row / G, g = row - token * G;
+    uint8_t* staged = smem + L::kOut + (warp - 2) * 4096;
     uint32_t t_s = 0, t_o = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-    ok = mbar_wait(&bar.item_full[k & 1], (k >> 1) & 1u, wc, kSiteItem);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    const Item& it = items[k & 1];
-    const int q0 = it.q0, nq = it.nq, k0 = it.k0, nk = it.nk, b0 = it.b0, hk = it.hk, tok0 = it.tok0;
-    const int n = tile ? it.n1 : it.n0;
-    const bool longer = tile == (it.n1 >= it.n0 ? 1 : 0), stop = it.stop;
-    const long long part = ((long long)it.rank * a.heads_k + hk) * P.splits + it.split;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar.item_free[k & 1]);
-    if (stop) break;
-    const int shift = nk - nq;  // causal: token i sees keys j <= i + shift
-    const bool releaser = longer && qq == 2 && lane == 0;
-    const int qi = tok0 + tile * TQ + token;
-    const bool active = token < TQ && qi < nq;
-    // keys this row sees; rows that are not stored need no mask
-    const int limit = !active ? 0x3fffffff : (a.causal ? min(nk, qi + shift + 1) : nk);
-    float m_run = active ? -INFINITY : 0.f, l_run = 0.f;
-    for (int j = 0; j < n; ++j) {
-      ok = mbar_wait(&bar.s_full[tile], t_s++ & 1u, wc, kSiteSFull);
+      ok = mbar_wait(&bar.item_full[k & 1], (k >> 1) & 1u, wc, kSiteItem);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (releaser) mbar_arrive(&bar.slot_free[(j + 1) & 1]);
-      tc_fence_after();
-      const int kv_valid = limit - (b0 + j) * kKeys;
-      const bool whole = __all_sync(0xffffffffu, kv_valid >= kKeys);
-      // Fast path against the running maximum; the slow path finds the block's maximum first.
-      // A row that has seen no key yet has no maximum and must take the slow one.
-      uint32_t pk[64];
-      float psum = 0.f, unused = -INFINITY, alpha = 1.0f;
-      bool slow = j == 0 || (active && m_run == -INFINITY);
-      if (!__all_sync(0xffffffffu, slow)) {
-        const float mneg = m_run == -INFINITY ? 0.f : -m_run;
-        if (whole) softmax_row<false, false>(tS, kv_valid, c, mneg, unused, psum, pk);
-        else softmax_row<true, false>(tS, kv_valid, c, mneg, unused, psum, pk);
-        slow = slow || (active && psum > kPsumLimit);
-      }
-      if (__any_sync(0xffffffffu, slow)) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+      // The slot stays this warp's until the end of the item: its fields are read again after the key
+      // loop, whose registers are full.
+      const volatile Item& it = items[k & 1];
+      if (it.stop) break;
+      const int n = tile ? it.n1 : it.n0;
+      const bool releaser = tile == (it.n1 >= it.n0 ? 1 : 0) && qq == 2 && lane == 0;
+      const int qi = it.tok0 + tile * TQ + token;
+      const bool active = token < TQ && qi < it.nq;
+      // keys this row sees, counted from this split's first block (causal: token i sees keys
+      // j <= i + nk - nq); rows that are not stored need no mask
+      const int limit =
+          (!active ? 0x3fffffff : (a.causal ? min(it.nk, qi + it.nk - it.nq + 1) : it.nk)) - it.b0 * kKeys;
+      float m_run = active ? -INFINITY : 0.f, l_run = 0.f;
+      for (int j = 0; j < n; ++j) {
+        ok = mbar_wait(&bar.s_full[tile], t_s++ & 1u, wc, kSiteSFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (releaser) mbar_arrive(&bar.slot_free[(j + 1) & 1]);
+        tc_fence_after();
+        const int kv_valid = limit - j * kKeys;
+        const bool whole = __all_sync(0xffffffffu, kv_valid >= kKeys);
+        // Fast path against the running maximum; the slow path finds the block's maximum first.  A
+        // row that has none yet (its first block) starts from the maximum over 32 keys: any
+        // reference does as long as the row sum of P stays within bounds.
+        uint32_t pk[64];
+        float psum = 0.f, unused = -INFINITY, alpha = 1.0f;
+        if (__any_sync(0xffffffffu, m_run == -INFINITY)) {
           uint32_t r[32];
-          tmem_load32(tS + q * 32, r);
+          tmem_load32(tS, r);
+          float mx = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (whole || q * 32 + i < kv_valid) mx = fmaxf(mx, __uint_as_float(r[i]));
+            if (whole || i < kv_valid) mx = fmaxf(mx, __uint_as_float(r[i]));
+          if (m_run == -INFINITY) m_run = mx * c;
         }
-        const float m_cand = fmaxf(m_run, mx * c);
-        bool resc = false;
-        if (active && m_cand > m_run) {
-          alpha = ex2_approx(m_run - m_cand);
-          m_run = m_cand;
-          resc = true;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
+        const float m_ref = m_run == -INFINITY ? 0.f : m_run;
+        if (whole) softmax_row<false, false>(tS, kv_valid, c, -m_ref, unused, psum, pk);
+        else softmax_row<true, false>(tS, kv_valid, c, -m_ref, unused, psum, pk);
+        const bool slow = active && (psum > kPsumLimit || m_run == -INFINITY);
+        if (__any_sync(0xffffffffu, slow)) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
             uint32_t r[32];
-            tmem_load32(tO + cc * 32, r);
+            tmem_load32(tS + q * 32, r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-            tmem_store32(tO + cc * 32, r);
+            for (int i = 0; i < 32; ++i)
+              if (whole || q * 32 + i < kv_valid) mx = fmaxf(mx, __uint_as_float(r[i]));
           }
-        }
-        const float mneg = m_run == -INFINITY ? 0.f : -m_run;
-        if (whole) softmax_row<false, false>(tS, kv_valid, c, mneg, unused, psum, pk);
-        else softmax_row<true, false>(tS, kv_valid, c, mneg, unused, psum, pk);
-      }
-      l_run = l_run * alpha + psum;
-      tmem_store32(tS, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-      tmem_store32(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
-      tmem_store_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[tile]);
-    }
-    if (ok && n > 0) {
-      ok = mbar_wait_sleep(&bar.o_done[tile], t_o++ & 1u, wc, kSiteODone);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    if (ok) {
-      const bool none = n == 0 || l_run == 0.f;  // no key seen: zeros
-      const float inv_l = none ? 0.f : 1.0f / l_run;
-      const int prow = (tile * TQ + token) * G + g;
-      bf16* out = a.out + (long long)(q0 + qi) * a.ldo + (hk * G + g) * D;
-      float* po = P.splits > 1 ? P.o + (part * 256 + prow) * D : nullptr;
-      bool bad = false;
+          const float m_cand = fmaxf(m_run, mx * c);
+          bool resc = false;
+          if (active && m_cand > m_run) {
+            alpha = ex2_approx(m_run - m_cand);
+            m_run = m_cand;
+            resc = true;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t r[32];
-        if (n > 0) tmem_load32(tO + cc * 32, r);
-        float f[32];
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t r[32];
+              tmem_load32(tO + cc * 32, r);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          f[i] = none ? 0.f : __uint_as_float(r[i]);
-          bad |= !(fabsf(f[i]) <= 3.4028235e38f);
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_store32(tO + cc * 32, r);
+            }
+          }
+          const float mneg = m_run == -INFINITY ? 0.f : -m_run;
+          if (whole) softmax_row<false, false>(tS, kv_valid, c, mneg, unused, psum, pk);
+          else softmax_row<true, false>(tS, kv_valid, c, mneg, unused, psum, pk);
         }
-        if (active) {
-          if (po) {
+        l_run = l_run * alpha + psum;
+        tmem_store32(tS, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+        tmem_store32(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+        tmem_store_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[tile]);
+      }
+      if (ok && n > 0) {
+        ok = mbar_wait_sleep(&bar.o_done[tile], t_o++ & 1u, wc, kSiteODone);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      if (ok) {
+        const bool none = n == 0 || l_run == 0.f;  // no key seen: zeros
+        const float inv_l = none ? 0.f : 1.0f / l_run;
+        const int q0 = it.q0, k0 = it.k0, nk = it.nk, b0 = it.b0, hk = it.hk;
+        const int prow = (tile * TQ + token) * G + g;
+        const long long out_at = active ? (long long)(q0 + qi) * a.ldo + (hk * G + g) * D : -1;  // this row's output
+        const long long part = ((long long)it.rank * a.heads_k + hk) * P.splits + it.split;
+        float* po = P.splits > 1 ? P.o + (part * 256 + prow) * D : nullptr;
+        // 64 dims at a time through the warp's staging rows (16-byte pieces swizzled), so that a store
+        // writes whole 128-byte pieces of four rows: straight from the registers, 16 bytes of 32 rows
+        // each, they took 2.3 us a tile.  A split's fp32 rows go out as they are.
+        bool bad = false;
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+#pragma unroll 1
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t r[32];
+            if (n > 0) tmem_load32(tO + h * 64 + cc * 32, r);
+            float f[32];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(po + cc * 32)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            for (int i = 0; i < 32; ++i) {
+              f[i] = none ? 0.f : __uint_as_float(r[i]);
+              bad |= !(fabsf(f[i]) <= 3.4028235e38f);
+            }
+            if (po) {
+              if (active) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  reinterpret_cast<float4*>(po + h * 64 + cc * 32)[i] =
+                      make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(staged + lane * 128 + (((cc * 4 + i) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16x2(f[8 * i] * inv_l, f[8 * i + 1] * inv_l),
+                               pack_bf16x2(f[8 * i + 2] * inv_l, f[8 * i + 3] * inv_l),
+                               pack_bf16x2(f[8 * i + 4] * inv_l, f[8 * i + 5] * inv_l),
+                               pack_bf16x2(f[8 * i + 6] * inv_l, f[8 * i + 7] * inv_l));
+            }
+          }
+          if (!po) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + (lane >> 3);
+              const long long at = __shfl_sync(0xffffffffu, out_at, r);
+              if (at >= 0)
+                *reinterpret_cast<uint4*>(a.out + at + h * 64 + (lane & 7) * 8) =
+                    *reinterpret_cast<const uint4*>(staged + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            }
+            __syncwarp();
+          }
+        }
+        if (active && po) P.ml[part * 256 + prow] = none ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
+        // Rows that are not finite: was it a value that they must not see?
+        const int taken = min(nk, (b0 + n) * kKeys);
+        const int seen = limit + b0 * kKeys;
+        uint32_t todo = __ballot_sync(0xffffffffu, bad && active && seen < taken);
+        while (todo) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int r_lim = __shfl_sync(0xffffffffu, seen, src), r_qi = __shfl_sync(0xffffffffu, qi, src);
+          const int r_g = __shfl_sync(0xffffffffu, g, src), r_prow = __shfl_sync(0xffffffffu, prow, src);
+          constexpr int V = D / 32;
+          const bf16* vp = a.v + (long long)k0 * a.ldv + hk * D;
+          bool blame = false;
+          for (int j = max(r_lim, b0 * kKeys); j < taken; ++j)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+              blame |= !(fabsf(__bfloat162float(vp[(long long)j * a.ldv + lane * V + e])) <= 3.4028235e38f);
+          if (!__any_sync(0xffffffffu, blame)) continue;
+          const int j0 = b0 * kKeys;
+          float m, l, o[V];
+          attend_row<D>(a, a.q + (long long)(q0 + r_qi) * a.ldq + (hk * G + r_g) * D,
+                        a.k + (long long)(k0 + j0) * a.ldk + hk * D, vp + (long long)j0 * a.ldv, max(0, r_lim - j0), c,
+                        lane, m, l, o);
+          if (P.splits > 1) {
+            float* dst = P.o + (part * 256 + r_prow) * D;
+#pragma unroll
+            for (int e = 0; e < V; ++e) dst[lane * V + e] = o[e];
+            if (lane == 0) P.ml[part * 256 + r_prow] = make_float2(m, l);
           } else {
+            bf16* dst = a.out + (long long)(q0 + r_qi) * a.ldo + (hk * G + r_g) * D;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<uint4*>(out + cc * 32)[i] =
-                  make_uint4(pack_bf16x2(f[8 * i] * inv_l, f[8 * i + 1] * inv_l),
-                             pack_bf16x2(f[8 * i + 2] * inv_l, f[8 * i + 3] * inv_l),
-                             pack_bf16x2(f[8 * i + 4] * inv_l, f[8 * i + 5] * inv_l),
-                             pack_bf16x2(f[8 * i + 6] * inv_l, f[8 * i + 7] * inv_l));
+            for (int e = 0; e < V; ++e) dst[lane * V + e] = __float2bfloat16(l == 0.f ? 0.f : o[e] / l);
           }
         }
       }
-      if (active && po) P.ml[part * 256 + prow] = none ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
-      // Rows that are not finite: was it a value that they must not see?
-      const int taken = min(nk, (b0 + n) * kKeys);
-      uint32_t todo = __ballot_sync(0xffffffffu, bad && active && limit < taken);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int r_lim = __shfl_sync(0xffffffffu, limit, src), r_qi = __shfl_sync(0xffffffffu, qi, src);
-        const int r_g = __shfl_sync(0xffffffffu, g, src), r_prow = __shfl_sync(0xffffffffu, prow, src);
-        constexpr int V = D / 32;
-        const bf16* vp = a.v + (long long)k0 * a.ldv + hk * D;
-        bool blame = false;
-        for (int j = max(r_lim, b0 * kKeys); j < taken; ++j)
-#pragma unroll
-          for (int e = 0; e < V; ++e)
-            blame |= !(fabsf(__bfloat162float(vp[(long long)j * a.ldv + lane * V + e])) <= 3.4028235e38f);
-        if (!__any_sync(0xffffffffu, blame)) continue;
-        const int j0 = b0 * kKeys;
-        float m, l, o[V];
-        attend_row<D>(a, a.q + (long long)(q0 + r_qi) * a.ldq + (hk * G + r_g) * D,
-                      a.k + (long long)(k0 + j0) * a.ldk + hk * D, vp + (long long)j0 * a.ldv, max(0, r_lim - j0), c,
-                      lane, m, l, o);
-        if (P.splits > 1) {
-          float* dst = P.o + (part * 256 + r_prow) * D;
-#pragma unroll
-          for (int e = 0; e < V; ++e) dst[lane * V + e] = o[e];
-          if (lane == 0) P.ml[part * 256 + r_prow] = make_float2(m, l);
-        } else {
-          bf16* dst = a.out + (long long)(q0 + r_qi) * a.ldo + (hk * G + r_g) * D;
-#pragma unroll
-          for (int e = 0; e < V; ++e) dst[lane * V + e] = __float2bfloat16(l == 0.f ? 0.f : o[e] / l);
-        }
-      }
-    }
-    tc_fence_before();  // O has been read before the next item's first P is announced
+      tc_fence_before();  // O has been read before the next item's first P is announced
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.item_free[k & 1]);
     }
   }
 
@@ -726,6 +761,11 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  // the last CTA leaves the counters as it found them, for the next call on this workspace
+  if (threadIdx.x == 0 && atomicAdd(&a.status->items_done, 1u) == gridDim.x - 1) {
+    a.status->next_item = 0;
+    a.status->items_done = 0;
   }
 }
 
