@@ -40,7 +40,7 @@ namespace dit {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kKeys = 128;                     // keys per block
 constexpr uint32_t kHalfBytes = 128 * 64 * 2;  // 64 dims of a 128-row tile
 constexpr uint32_t kTmemCols = 512;
@@ -122,7 +122,7 @@ Parts parts_layout(const Plan& p, int heads_k, int head_dim) {
 }
 
 struct alignas(64) TextAttnParams {
-  CUtensorMap q_map, k_map, v_map;
+  CUtensorMap q_map, k_map, v_map, o_map;  // o_map: one softmax warp's rows, where they are whole tokens
   TextAttnArgs a;
   int group, tq, levels, tiles, splits, items;
   float scale_log2;
@@ -135,6 +135,16 @@ struct alignas(64) TextAttnParams {
 enum : uint32_t {
   kSiteQ = 0x511, kSiteFree, kSiteReady, kSitePFull, kSiteSFull, kSiteODone, kSiteFixed, kSiteFix, kSiteItem, kSiteItemFree
 };
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Every store of this thread has been read out of shared memory.
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 template <int D>
 struct Smem {
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_done[i], 1);
       mbar_init(&bar.item_full[i], 1);
-      mbar_init(&bar.item_free[i], 9);  // the issuer and eight softmax warps
+      mbar_init(&bar.item_free[i], 10);  // the loader, the issuer and eight softmax warps
     }
     mbar_init(bar.fixed, 1);
     mbar_init(bar.drain, 1);
@@ -385,72 +395,24 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
   allow_dependents();
 
   if (warp == 0) {
-    // ------------------------------------------------------------ work items and TMA producer
+    // ------------------------------------------------------------ TMA producer
     // Ring slot j & 1 carries V_j and K_{j+1}; slot j >= 1 is loaded once the scores of block
     // j - 1 of the longer tile are complete, which ends every read of V_{j-2} and K_{j-1}.  The next
-    // item's Q and K_0 follow when the last scores are complete (every QK is done), its V_0 and K_1 when the
-    // last O of both tiles is: while the softmax warps finish one item, the next one's loads and scores are under way.
-    Turns t_free, t_item, t_o, t_ready;
-    uint32_t live = 0;     // items with key blocks so far
+    // item's Q and K_0 follow when the last scores are complete (every QK is done), its V_0 and K_1
+    // when the last O of both tiles is: while the softmax warps finish one item, the next one's loads
+    // and scores are under way.
+    Turns t_free, t_o, t_ready;
+    uint32_t live = 0;             // items with key blocks so far
     int pn = 0, pn0 = 0, pn1 = 0;  // the last such item's blocks
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      // the first item by place, the others as they come, longest first
-      int id = (int)blockIdx.x;
-      if (k > 0) {
-        if (lane == 0) id = (int)(gridDim.x + atomicAdd(&a.status->next_item, 1u));
-        id = __shfl_sync(0xffffffffu, id, 0);
-      }
-      const bool stop = id >= P.items;
-      Span sp{0, -1, 0, 0, true};
-      int index = 0, hk = 0, split = 0, rank = 0;
-      bool found = false;
-      if (!stop) {
-        hk = id % a.heads_k;
-        split = (id / a.heads_k) % P.splits;
-        rank = id / a.heads_k / P.splits;
-        if (P.list) {
-          const int2 e = P.list[rank];
-          found = e.x >= 0;
-          if (found) sp = load_span(a, e.x);
-          index = e.y;
-        } else {
-          found = find_tile(a, TP, P.levels, P.tiles, rank, lane, k == 0 && blockIdx.x == 0, sp, index);
-        }
-        if (P.splits > 1 && hk == 0 && split == 0 && lane == 0)
-          P.desc[rank] = found ? make_int2(sp.q0 + index * TP, min(TP, sp.nq - index * TP)) : make_int2(0, 0);
-      }
-      if (!stop && !found) continue;
-      Item it{sp.q0, sp.nq, sp.k0, sp.nk, index * TP, 0, 0, 0, hk, split, rank, stop};
-      if (found) {
-        // key blocks of each tile, and this split's run [b0, b0 + n) of them
-        const int shift = it.nk - it.nq;
-        auto blocks = [&](int first) {
-          if (first >= it.nq) return 0;
-          const int last = min(first + TQ, it.nq) - 1;
-          const int end = a.causal ? min(it.nk, last + shift + 1) : it.nk;
-          return end > 0 ? (end + kKeys - 1) / kKeys : 0;
-        };
-        it.n0 = blocks(it.tok0);
-        it.n1 = blocks(it.tok0 + TQ);
-        if (P.splits > 1) {
-          const int nb = max(it.n0, it.n1);
-          it.b0 = (int)((long long)nb * split / P.splits);
-          const int b1 = (int)((long long)nb * (split + 1) / P.splits);
-          it.n0 = max(0, min(it.n0, b1) - it.b0);
-          it.n1 = max(0, min(it.n1, b1) - it.b0);
-        }
-      }
-      const int slot = (int)((t_item.n[0] + t_item.n[1]) & 1u);
-      ok = mbar_wait_sleep(&bar.item_free[slot], t_item.next(slot) ^ 1u, wc, kSiteItemFree);
+    for (uint32_t k = 0; ok; ++k) {
+      ok = mbar_wait_sleep(&bar.item_full[k & 1], (k >> 1) & 1u, wc, kSiteItem);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane == 0) {
-        items[slot] = it;
-        mbar_arrive(&bar.item_full[slot]);
-      }
+      const Item it = items[k & 1];
       __syncwarp();
-      if (stop) break;
+      if (lane == 0) mbar_arrive(&bar.item_free[k & 1]);
+      if (it.stop) break;
       const int nmax = max(it.n0, it.n1);
       if (nmax == 0) continue;
       const int krow = it.k0 + it.b0 * kKeys;
@@ -562,6 +524,69 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       while (!mbar_try(bar.drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
       }
     }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ work items
+    // One item ahead of the others: the counter's and the lengths' latency is nobody's wait.
+    uint32_t out = 0;  // items handed on
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      // the first item by place, the others as they come, longest first
+      int id = (int)blockIdx.x;
+      if (k > 0) {
+        if (lane == 0) id = (int)(gridDim.x + atomicAdd(&a.status->next_item, 1u));
+        id = __shfl_sync(0xffffffffu, id, 0);
+      }
+      const bool stop = id >= P.items;
+      Span sp{0, -1, 0, 0, true};
+      int index = 0, hk = 0, split = 0, rank = 0;
+      bool found = false;
+      if (!stop) {
+        hk = id % a.heads_k;
+        split = (id / a.heads_k) % P.splits;
+        rank = id / a.heads_k / P.splits;
+        if (P.list) {
+          const int2 e = P.list[rank];
+          found = e.x >= 0;
+          if (found) sp = load_span(a, e.x);
+          index = e.y;
+        } else {
+          found = find_tile(a, TP, P.levels, P.tiles, rank, lane, k == 0 && blockIdx.x == 0, sp, index);
+        }
+        if (P.splits > 1 && hk == 0 && split == 0 && lane == 0)
+          P.desc[rank] = found ? make_int2(sp.q0 + index * TP, min(TP, sp.nq - index * TP)) : make_int2(0, 0);
+      }
+      if (!stop && !found) continue;
+      Item it{sp.q0, sp.nq, sp.k0, sp.nk, index * TP, 0, 0, 0, hk, split, rank, stop};
+      if (found) {
+        // key blocks of each tile, and this split's run [b0, b0 + n) of them
+        const int shift = it.nk - it.nq;
+        auto blocks = [&](int first) {
+          if (first >= it.nq) return 0;
+          const int last = min(first + TQ, it.nq) - 1;
+          const int end = a.causal ? min(it.nk, last + shift + 1) : it.nk;
+          return end > 0 ? (end + kKeys - 1) / kKeys : 0;
+        };
+        it.n0 = blocks(it.tok0);
+        it.n1 = blocks(it.tok0 + TQ);
+        if (P.splits > 1) {
+          const int nb = max(it.n0, it.n1);
+          it.b0 = (int)((long long)nb * split / P.splits);
+          const int b1 = (int)((long long)nb * (split + 1) / P.splits);
+          it.n0 = max(0, min(it.n0, b1) - it.b0);
+          it.n1 = max(0, min(it.n1, b1) - it.b0);
+        }
+      }
+      ok = mbar_wait_sleep(&bar.item_free[out & 1], ((out >> 1) & 1u) ^ 1u, wc, kSiteItemFree);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        items[out & 1] = it;
+        mbar_arrive(&bar.item_full[out & 1]);
+      }
+      __syncwarp();
+      ++out;
+      if (stop) break;
+    }
   } else {
     // ------------------------------------------------------------ softmax / output
     const int tile = (warp - 2) >> 2;  // warps 2-5 -> tile 0, warps 6-9 -> tile 1
@@ -664,15 +689,19 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       if (ok) {
         const bool none = n == 0 || l_run == 0.f;  // no key seen: zeros
         const float inv_l = none ? 0.f : 1.0f / l_run;
-        const int q0 = it.q0, k0 = it.k0, nk = it.nk, b0 = it.b0, hk = it.hk;
+        const int q0 = it.q0, k0 = it.k0, nk = it.nk, b0 = it.b0, hk = it.hk, tok0 = it.tok0;
         const int prow = (tile * TQ + token) * G + g;
         const long long out_at = active ? (long long)(q0 + qi) * a.ldo + (hk * G + g) * D : -1;  // this row's output
         const long long part = ((long long)it.rank * a.heads_k + hk) * P.splits + it.split;
         float* po = P.splits > 1 ? P.o + (part * 256 + prow) * D : nullptr;
-        // 64 dims at a time through the warp's staging rows (16-byte pieces swizzled), so that a store
-        // writes whole 128-byte pieces of four rows: straight from the registers, 16 bytes of 32 rows
-        // each, they took 2.3 us a tile.  A split's fp32 rows go out as they are.
-        bool bad = false;
+        // 64 dims at a time through the warp's staging rows (16-byte pieces swizzled): a warp that holds
+        // whole tokens of the sequence hands them to a TMA store and goes on (1.1 us a tile less than
+        // stores of 128-byte pieces of four rows each, as the others do it).  A split's fp32 rows go
+        // out as they are.
+        const bool whole_rows = P.splits == 1 && 32 % G == 0 && __all_sync(0xffffffffu, active);
+        if (lane == 0) tma_store_wait_read();  // the item before has left the staging rows
+        __syncwarp();
+        float zero = 0.f;
 #pragma unroll 1
         for (int h = 0; h < D / 64; ++h) {
 #pragma unroll 1
@@ -683,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               f[i] = none ? 0.f : __uint_as_float(r[i]);
-              bad |= !(fabsf(f[i]) <= 3.4028235e38f);
+              zero = fmaf(f[i], 0.f, zero);  // NaN once a value is not finite
             }
             if (po) {
               if (active) {
@@ -702,7 +731,15 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
                                pack_bf16x2(f[8 * i + 6] * inv_l, f[8 * i + 7] * inv_l));
             }
           }
-          if (!po) {
+          if (whole_rows) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_4d(&P.o_map, staged, h * 64, 0, hk, q0 + tok0 + tile * TQ + qq * (32 / G));
+              if (h + 1 < D / 64) tma_store_wait_read();  // the staging rows are written again
+            }
+            __syncwarp();
+          } else if (!po) {
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -719,7 +756,11 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
         // Rows that are not finite: was it a value that they must not see?
         const int taken = min(nk, (b0 + n) * kKeys);
         const int seen = limit + b0 * kKeys;
-        uint32_t todo = __ballot_sync(0xffffffffu, bad && active && seen < taken);
+        uint32_t todo = __ballot_sync(0xffffffffu, zero != 0.f && active && seen < taken);
+        if (todo) {  // rows handed to a TMA store have to land before they are written again
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+          __syncwarp();
+        }
         while (todo) {
           const int src = __ffs(todo) - 1;
           todo &= todo - 1;
@@ -754,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.item_free[k & 1]);
     }
+    if (lane == 0) tma_store_wait_read();
   }
 
   tc_fence_before();
@@ -822,6 +864,9 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
   if (!encode_tmap_bf16(&P.q_map, a.q, 4, qd, qs, qb)) return cudaErrorInvalidValue;
   if (!encode_tmap_bf16(&P.k_map, k, 3, kd, ks, kb)) return cudaErrorInvalidValue;
   if (!encode_tmap_bf16(&P.v_map, v, 3, kd, vs, kb)) return cudaErrorInvalidValue;
+  const uint64_t os[3] = {D * 2, G * D * 2, (uint64_t)a.ldo * 2};
+  const uint32_t ob[4] = {64, (uint32_t)G, 1, (uint32_t)(32 % G == 0 ? 32 / G : 1)};
+  if (!encode_tmap_bf16(&P.o_map, a.out, 4, qd, os, ob)) return cudaErrorInvalidValue;
   P.a = a;
   P.group = p.group;
   P.tq = p.tq;
