@@ -913,14 +913,414 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
   return cudaSuccess;
 }
 
+// ---- few query rows ---------------------------------------------------------------------------
+
+// Up to 16 query rows per key head (new tokens, heads of the group among them): reading the keys and
+// values bounds the time, so what counts is bytes in flight, not the MMA rate.  One CTA per (run of
+// keys, key head, sequence), two per SM, each with three stages of 64 keys (64 * D * 4 bytes) on their
+// way by TMA; four warps take 16 keys of a stage each through mma.sync with their own running maximum
+// and sum and add up at the end, in order.  Runs of several CTAs are joined by a second kernel.  A
+// 128-row tcgen05 tile of mostly empty rows took 153 us where this takes 120 (48 tokens over 100 to
+// 8192 keys, 8 key heads of 128).
+constexpr int kFewRows = 16, kFewKeys = 64, kFewStages = 3, kFewThreads = 160;
+
+struct FewPlan {
+  int rows, chunk, splits;  // query rows per key head, keys per CTA, CTAs per sequence and head
+};
+
+bool few_rows(const TextAttnArgs& a) { return (long long)a.max_q * (a.heads_q / a.heads_k) <= kFewRows; }
+
+// Runs of at most 1024 keys, so that ragged lengths even out over the CTAs, and of at least 128,
+// that cut the keys into about eight waves of CTAs; and no more than 16384 runs in all, which
+// bounds the workspace.
+FewPlan few_plan(const TextAttnArgs& a) {
+  FewPlan p;
+  p.rows = a.max_q * (a.heads_q / a.heads_k);
+  const long long items = (long long)a.seqs * a.heads_k;
+  long long chunk = (long long)a.max_k * items / (16 * kSMs);
+  if (chunk > 1024) chunk = 1024;
+  const long long least = (long long)a.max_k * items / 16384;
+  if (chunk < least) chunk = least;
+  if (chunk < 128) chunk = 128;
+  p.chunk = (int)((chunk + kFewKeys - 1) / kFewKeys * kFewKeys);
+  p.splits = (a.max_k + p.chunk - 1) / p.chunk;
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+
+Parts few_parts(const FewPlan& p, const TextAttnArgs& a) {
+  Parts l;
+  const size_t n = p.splits > 1 ? (size_t)a.seqs * a.heads_k * p.splits * p.rows : 0;
+  l.list = l.desc = l.ml = 0;
+  l.o = up256(n * 8);
+  l.total = l.o + up256(n * (size_t)a.head_dim * 4);
+  return l;
+}
+
+struct alignas(64) FewParams {
+  CUtensorMap k_map, v_map;
+  TextAttnArgs a;
+  int group, rows, chunk, splits;
+  float scale_log2;
+  float2* ml;
+  float* o;
+};
+
+enum : uint32_t { kSiteFewFull = 0x521, kSiteFewEmpty };
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// D += A B, 16 x 8 x 16, bf16 in, fp32 out.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(const __grid_constant__ FewParams P) {
+  constexpr uint32_t kHalf = kFewKeys * 128;            // 64 keys x 64 dims
+  constexpr uint32_t kTile = (D / 64) * kHalf, kStage = 2 * kTile;
+  constexpr int V = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[kFewStages], empty[kFewStages];
+  __shared__ float2 ml[4][kFewRows];
+  __shared__ int abort_flag;
+  const TextAttnArgs& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = P.group;
+  const int split = blockIdx.x % P.splits, hk = (blockIdx.x / P.splits) % a.heads_k;
+  const int seq = blockIdx.x / P.splits / a.heads_k;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFewStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  allow_dependents();
+  const Span sp = load_span(a, seq);
+  if (!sp.ok) {
+    if (split == 0 && hk == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteTextLengths);
+    return;
+  }
+  const int rows = sp.nq * G;
+  const int first = split * P.chunk, last = min(sp.nk, first + P.chunk);  // this CTA's keys
+  const bool direct = sp.nk <= P.chunk;                                   // ... are all of them
+  if (rows == 0 || (first >= last && split > 0)) return;
+  const int blocks = first < last ? (last - first + kFewKeys - 1) / kFewKeys : 0;
+  const WaitCtx wc{a.status, &abort_flag, kWaitLimitNs};
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int issued = 0;
+      bool ok = true;
+      for (int j = 0; j < blocks; ++j) {
+        const int st = j % kFewStages;
+        if (!mbar_wait_sleep(&empty[st], ((uint32_t)(j / kFewStages) & 1u) ^ 1u, wc, kSiteFewEmpty)) {
+          ok = false;
+          break;
+        }
+        uint8_t* at = smem + st * kStage;
+        mbar_arrive_expect_tx(&full[st], kStage);
+        for (int h = 0; h < D / 64; ++h) {
+          tma_load_3d(at + h * kHalf, &P.k_map, &full[st], h * 64, hk, sp.k0 + first + j * kFewKeys);
+          tma_load_3d(at + kTile + h * kHalf, &P.v_map, &full[st], h * 64, hk, sp.k0 + first + j * kFewKeys);
+        }
+        issued = j + 1;
+      }
+      if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        for (int j = issued > kFewStages ? issued - kFewStages : 0; j < issued; ++j)
+          while (!mbar_try(&full[j % kFewStages], (uint32_t)(j / kFewStages) & 1u) &&
+                 global_timer_ns() - t0 < 200000000ull) {
+          }
+      }
+    }
+  }
+
+  // Fragments: this lane's rows are lane / 4 and lane / 4 + 8, its columns 2 (lane % 4) + {0, 1}.
+  const int r0 = lane >> 2, c0 = (lane & 3) * 2;
+  float o[D / 8][4];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  const float c = P.scale_log2;
+  if (warp < 4) {
+    uint32_t q[D / 16][4];
+    int limit[2];  // keys that the lane's rows see
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 8 * i, token = r / G;
+      const bool ok = r < rows;
+      const bf16* src = a.q + (long long)(sp.q0 + (ok ? token : 0)) * a.ldq + (hk * G + (ok ? r - token * G : 0)) * D + c0;
+      limit[i] = !ok ? 0 : (a.causal ? min(sp.nk, token + sp.nk - sp.nq + 1) : sp.nk);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][i] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+        q[k][i + 2] = ok ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    // ldmatrix rows: K as (keys 0-7 | 0-7 | 8-15 | 8-15) x (dims 0-7 | 8-15 | 0-7 | 8-15), V transposed as
+    // (keys 0-7 | 8-15 | 0-7 | 8-15) x (dims 0-7 | 0-7 | 8-15 | 8-15), each of this warp's 16 keys
+    const int kk = warp * 16 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+    const int vk = warp * 16 + (lane & 15), vc = lane >> 4;
+    for (int j = 0; j < blocks; ++j) {
+      const int st = j % kFewStages;
+      bool ok = mbar_wait(&full[st], (uint32_t)(j / kFewStages) & 1u, wc, kSiteFewFull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint8_t* at = smem + st * kStage;
+      const int key0 = first + j * kFewKeys + warp * 16;
+      if (key0 < last) {
+        if (key0 + 16 > last) {
+          // V rows past this run's keys must read as zeros: a zero probability does not silence a NaN
+          for (int h = 0; h < D / 64; ++h)
+            for (int i = lane; i < 16 * 8; i += 32)
+              if (key0 + (i >> 3) >= last)
+                *reinterpret_cast<uint4*>(at + kTile + h * kHalf + (warp * 16 + (i >> 3)) * 128 + (i & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          __syncwarp();
+        }
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          ldmatrix4(b, smem_u32(at + (k >> 2) * kHalf + kk * 128 + (((((k & 3) * 2) + kc) ^ (kk & 7)) << 4)));
+          mma_bf16(s[0], q[k], b[0], b[1]);
+          mma_bf16(s[1], q[k], b[2], b[3]);
+        }
+        float alpha[2];
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // the lane's two rows
+          float x[4];
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + (e >> 1) * 8 + c0 + (e & 1);
+            x[e] = key < min(limit[i], last) ? s[e >> 1][2 * i + (e & 1)] * c : -INFINITY;
+            mx = fmaxf(mx, x[e]);
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
+          alpha[i] = ex2_approx(m[i] - ref);
+          m[i] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = ex2_approx(x[e] - ref);
+            sum += x[e];
+          }
+          l[i] = l[i] * alpha[i] + sum;
+          p[i] = pack_bf16x2(x[0], x[1]);
+          p[i + 2] = pack_bf16x2(x[2], x[3]);
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= alpha[0];
+            o[i][1] *= alpha[0];
+            o[i][2] *= alpha[1];
+            o[i][3] *= alpha[1];
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, smem_u32(at + kTile + (d >> 2) * kHalf + vk * 128 + (((((d & 3) * 2) + vc) ^ (vk & 7)) << 4)));
+          mma_bf16(o[2 * d], p, b[0], b[1]);
+          mma_bf16(o[2 * d + 1], p, b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+  }
+
+  // The four warps' rows through shared memory (all stages have been read)
+  __syncthreads();
+  float* parts = reinterpret_cast<float*>(smem);  // [warp][row][dim]
+  if (warp < 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int r = r0 + 8 * i;
+      if ((lane & 3) == 0) ml[warp][r] = make_float2(m[i], l[i]);
+      if (r < rows) {
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+          *reinterpret_cast<float2*>(parts + (warp * kFewRows + r) * D + d * 8 + c0) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 4 || abort_flag) return;
+  for (int r = warp; r < rows; r += 4) {
+    float mr = -INFINITY, lr = 0.f, out[V];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mr = fmaxf(mr, ml[w][r].x);
+    const float ref = mr == -INFINITY ? 0.f : mr;
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 x = ml[w][r];
+      if (x.y == 0.f) continue;  // no key that the row sees
+      const float f = ex2_approx(x.x - ref);
+      lr += f * x.y;
+#pragma unroll
+      for (int e = 0; e < V; ++e) out[e] += f * parts[(w * kFewRows + r) * D + lane * V + e];
+    }
+    const int token = r / G, g = r - token * G;
+    float zero = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) zero = fmaf(out[e], 0.f, zero);
+    const int seen = a.causal ? min(sp.nk, token + sp.nk - sp.nq + 1) : sp.nk;
+    if (seen < last && __any_sync(0xffffffffu, zero != 0.f)) {
+      // not finite: was it a value behind the keys that the row sees?
+      const bf16* vp = a.v + (long long)sp.k0 * a.ldv + hk * D;
+      bool blame = false;
+      for (int j = max(seen, first); j < last; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          blame |= !(fabsf(__bfloat162float(vp[(long long)j * a.ldv + lane * V + e])) <= 3.4028235e38f);
+      if (__any_sync(0xffffffffu, blame))
+        attend_row<D>(a, a.q + (long long)(sp.q0 + token) * a.ldq + (hk * G + g) * D,
+                      a.k + (long long)(sp.k0 + first) * a.ldk + hk * D, vp + (long long)first * a.ldv,
+                      max(0, seen - first), c, lane, mr, lr, out);
+    }
+    if (direct) {
+      const float inv = lr == 0.f ? 0.f : 1.0f / lr;
+      bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + g) * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = lr == 0.f ? 0u : pack_bf16x2(out[e] * inv, out[e + 1] * inv);
+    } else {
+      const long long at = (long long)blockIdx.x * P.rows + r;
+      if (lane == 0) P.ml[at] = make_float2(mr, lr);
+#pragma unroll
+      for (int e = 0; e < V; e += 2)
+        *reinterpret_cast<float2*>(P.o + at * D + lane * V + e) = make_float2(out[e], out[e + 1]);
+    }
+  }
+}
+
+// Adds up the runs of the sequences that took several, in order: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) text_attention_few_join_kernel(const __grid_constant__ FewParams P) {
+  constexpr int V = D / 32;
+  grid_dependency_wait();
+  allow_dependents();
+  const TextAttnArgs& a = P.a;
+  const int lane = threadIdx.x & 31, G = P.group;
+  const int hk = blockIdx.x % a.heads_k, seq = blockIdx.x / a.heads_k;
+  const Span sp = load_span(a, seq);
+  if (!sp.ok || sp.nk <= P.chunk) return;
+  const int runs = (sp.nk + P.chunk - 1) / P.chunk;
+  for (int r = threadIdx.x >> 5; r < sp.nq * G; r += 4) {
+    const long long at = (long long)blockIdx.x * P.splits * P.rows + r;
+    float m = -INFINITY;
+    for (int s = lane; s < runs; s += 32) m = fmaxf(m, P.ml[at + (long long)s * P.rows].x);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < runs; ++s) {
+      const long long p = at + (long long)s * P.rows;
+      const float2 x = P.ml[p];
+      const float f = x.y == 0.f ? 0.f : ex2_approx(x.x - ref);  // no key that the row sees: adds nothing
+      l += f * x.y;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = P.o[p * D + lane * V + e];
+        o[e] += x.y == 0.f ? 0.f : f * v;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const int token = r / G;
+    bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + r - token * G) * D + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  }
+}
+
+std::atomic<bool> g_few_attr_set[32];  // (device, head_dim)
+
+template <int D>
+cudaError_t launch_few(const TextAttnArgs& a, cudaStream_t s) {
+  const FewPlan p = few_plan(a);
+  FewParams P;
+  memset(&P, 0, sizeof(P));
+  const uint64_t rk = a.rows_k > 0 ? a.rows_k : 1, Hk = a.heads_k;
+  const uint64_t kd[3] = {D, Hk, rk}, ks[2] = {D * 2, (uint64_t)a.ldk * 2}, vs[2] = {D * 2, (uint64_t)a.ldv * 2};
+  const uint32_t kb[3] = {64, 1, kFewKeys};
+  if (a.rows_k > 0 &&
+      (!encode_tmap_bf16(&P.k_map, a.k, 3, kd, ks, kb) || !encode_tmap_bf16(&P.v_map, a.v, 3, kd, vs, kb)))
+    return cudaErrorInvalidValue;
+  const Parts l = few_parts(p, a);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.parts);
+  P.a = a;
+  P.group = a.heads_q / a.heads_k;
+  P.rows = p.rows;
+  P.chunk = p.chunk;
+  P.splits = p.splits;
+  P.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
+  P.ml = reinterpret_cast<float2*>(ws + l.ml);
+  P.o = reinterpret_cast<float*>(ws + l.o);
+  const size_t smem = 1024 + (size_t)kFewStages * kFewKeys * D * 4;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int slot = dev * 2 + (D == 64);
+  if (dev >= 16 || !g_few_attr_set[slot].load(std::memory_order_acquire)) {
+    cudaError_t e =
+        cudaFuncSetAttribute(text_attention_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 16) g_few_attr_set[slot].store(true, std::memory_order_release);
+  }
+  const long long grid = (long long)a.seqs * a.heads_k * p.splits;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  {
+    LaunchScope scope(kClsTextAttention, s);
+    cudaError_t e = launch_k(text_attention_few_kernel<D>, dim3((unsigned)grid), dim3(kFewThreads), smem, s, P);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.splits > 1) {
+    LaunchScope scope(kClsTextJoin, s);
+    return launch_k(text_attention_few_join_kernel<D>, dim3((unsigned)(a.seqs * a.heads_k)), dim3(128), 0, s, P);
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 size_t text_attention_parts_bytes(const TextAttnArgs& a) {
   if (a.seqs == 0 || a.rows_q == 0 || a.max_q == 0) return 0;
+  if (few_rows(a)) return few_parts(few_plan(a), a).total;
   return parts_layout(make_plan(a), a.heads_k, a.head_dim).total;
 }
 
 cudaError_t launch_text_attention(const TextAttnArgs& a, cudaStream_t s) {
+  if (few_rows(a)) return a.head_dim == 64 ? launch_few<64>(a, s) : launch_few<128>(a, s);
   const Plan p = make_plan(a);
   return a.head_dim == 64 ? launch<64>(a, p, s) : launch<128>(a, p, s);
 }
