@@ -1048,8 +1048,10 @@ dit_status dit_text_rope_table(const dit_text_rope* rope, const int32_t* pos_dev
   a.pos = pos_dev;
   a.n = n;
   a.table = table_dev;
+  const double step = -2.0 * log2(theta) / c.rot_dim;
   for (int j = 0; j < a.half; ++j) {
-    double w = pow(theta, -2.0 * j / c.rot_dim);
+    // |w log2 w| <= 0.54, so the exponent's rounding moves an angle by under p 2^-54
+    double w = exp2(step * j);
     if (c.scaling == DIT_ROPE_SCALE_LINEAR) w /= c.factor;
     if (c.scaling == DIT_ROPE_SCALE_BY_PARTS) {
       double g = (w * c.original_len / kTwoPi - c.low) / (c.high - c.low);
