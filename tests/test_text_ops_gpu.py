@@ -252,6 +252,52 @@ def test_text_attention_few_queries_over_long_keys(dit, ws, nq, nk, hq, hk):
         _check_attention(*_attend(dit, ws, [nq, 1, nq], [nk, 5, nk - 300], hq, hk, 128, causal))
 
 
+@pytest.mark.parametrize("seqs", [65, 300, 1500])
+@pytest.mark.parametrize("hq,hk,d,causal", [(4, 1, 128, True), (3, 3, 64, False)])
+def test_text_attention_many_sequences(dit, ws, seqs, hq, hk, d, causal):
+    """More sequences than one warp can search: the tiles are listed first.  Every 7th is empty,
+    every 11th longer than a tile."""
+    kl = [0 if i % 7 == 3 else 300 + i % 50 if i % 11 == 0 and i < 200 else 1 + (i * 37) % 40 for i in range(seqs)]
+    kl[0] = 301
+    _check_attention(*_attend(dit, ws, kl, kl, hq, hk, d, causal, lens=False))
+    _check_attention(*_attend(dit, ws, [min(n, 17) for n in kl], kl, hq, hk, d, causal, gap_q=1, gap_k=1, fill=math.inf))
+
+
+@pytest.mark.parametrize("hq,hk", [(3, 1), (5, 1), (12, 4), (16, 2), (32, 1)])
+def test_text_attention_group_sizes_over_items(dit, ws, hq, hk):
+    """Groups that do and do not divide a warp's rows, more items than SMs in one call."""
+    ql = [700, 33, 512, 1, 257, 640, 128, 90]
+    _check_attention(*_attend(dit, ws, ql, ql, hq, hk, 64, True))
+
+
+def test_text_attention_single_tokens_without_keys(dit, ws):
+    got, want, size, qk = _attend(dit, ws, [1, 1, 0, 1], [0, 700, 3, 5], 4, 2, 128, True)
+    assert (got[0] == 0).all()
+    _check_attention(got, want, size, qk)
+    got, _, _, _ = _attend(dit, ws, [1], [0], 8, 8, 64, False)
+    assert (got == 0).all()
+    # causal queries before the first key
+    got, want, size, qk = _attend(dit, ws, [4], [2], 4, 1, 128, True)
+    assert (got[:2] == 0).all()
+    _check_attention(got, want, size, qk)
+
+
+def test_text_attention_bounds_wider_than_the_lengths(dit, ws):
+    """max_q and max_k are upper bounds only: the same bits as with tight ones, on the same kernel."""
+    hq, hk, d = 8, 2, 128
+    q, k, v = _randn(300, hq, d, seed=1), _randn(300, hk, d, seed=2), _randn(300, hk, d, seed=3)
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device=DEV)  # noqa: E731
+    want, size, _ = R.attention(q, k, v, [(0, 200, 0, 200), (200, 100, 200, 100)], True, d ** -0.5)
+    dev = [t.flatten(1).to(DEV) for t in (q, k, v)]
+    for mq, mk in ((200, 200), (300, 300), (100000, 1 << 24)):
+        out = torch.zeros(300, hq * d, dtype=torch.bfloat16, device=DEV)
+        a = dit.make_text_attn(2, hq, hk, d, 300, 300, mq, mk)
+        dit.dit_text_attention(a, i32([0, 200, 300]), None, i32([0, 200, 300]), None, dev[0], hq * d, dev[1], hk * d, dev[2],
+                               hk * d, out, hq * d, ws, ws.numel())
+        _ok(dit, ws)
+        _check_attention(out.reshape(300, hq, d).cpu(), want, size, (q, k, d ** -0.5))
+
+
 @pytest.mark.parametrize("scale,qstd", [(1.0, 4.0), (0.02, 1.0), (3.0, 1.0)])
 def test_text_attention_sharp_and_flat_scores(dit, ws, scale, qstd):
     """Scores over hundreds (one key takes everything, the running maximum moves often) and flat ones."""
@@ -295,6 +341,19 @@ def test_text_attention_bad_value_reaches_only_queries_that_see_it(dit, ws, ql, 
     assert not got[blind:, :, 3].isfinite().any()
     keep = [c for c in range(128) if c != 3]
     assert got[blind:][..., keep].isfinite().all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("nk", [4, 300, 1000, 3000])
+def test_text_attention_bad_value_between_few_queries(dit, ws, nk, bad):
+    """Four last queries, the last but one key's value bad: the first two do not see it."""
+    def edit(q, k, v, spans):
+        v[nk - 2, 0, 3] = bad
+    got, want, size, qk = _attend(dit, ws, [4], [nk], 4, 1, 128, True, edit=edit)
+    clean = R.attention(qk[0], qk[1], _randn(nk, 1, 128, seed=2), [(0, 4, 0, nk)], True, qk[2])
+    _check_attention(got[:2], clean[0][:2], clean[1][:2], qk)
+    assert not got[2:, :, 3].isfinite().any()
+    assert got[2:][..., [c for c in range(128) if c != 3]].isfinite().all()
 
 
 def test_text_attention_bad_key_reaches_only_queries_that_see_it(dit, ws):
