@@ -1006,6 +1006,12 @@ TextAttnArgs text_attn_sizes(const dit_text_attn& a) {
   return t;
 }
 
+// Whether two byte ranges share an address.
+inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + nb && y < x + na;
+}
+
 inline bool linear_fp8_sizes_ok(int rows, int n_out, int k) {
   return rows >= 1 && rows <= kMaxTokens && n_out >= 1 && n_out <= kMaxTokens && n_out % 8 == 0 && k >= 1 &&
          k <= kMaxTokens && k % 16 == 0;
@@ -1152,6 +1158,11 @@ dit_status dit_quantize_blocks_fp8(const void* x_dev, long long ld, int rows, in
       ld % 8 != 0 || (block_rows != 1 && block_rows != 128))
     return DIT_ERR_INVALID_ARG;
   if (!aligned16(x_dev) || !aligned16(q_dev) || !aligned16(scale_dev)) return DIT_ERR_INVALID_ARG;
+  const size_t nx = ((size_t)(rows - 1) * ld + cols) * 2, nq = (size_t)rows * cols;
+  const size_t ns = (size_t)((rows + block_rows - 1) / block_rows) * ((cols + 127) / 128) * 4;
+  if (ranges_overlap(x_dev, nx, q_dev, nq) || ranges_overlap(x_dev, nx, scale_dev, ns) ||
+      ranges_overlap(q_dev, nq, scale_dev, ns))
+    return DIT_ERR_INVALID_ARG;
   return cuda_status(launch_quantize_blocks((const bf16*)x_dev, ld, rows, cols, block_rows, (uint8_t*)q_dev, scale_dev,
                                             (cudaStream_t)stream));
 }
@@ -1170,6 +1181,11 @@ dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev
       !aligned16(out_dev) || !aligned16(ws))
     return DIT_ERR_INVALID_ARG;
   if (ws_bytes < sizeof(DeviceStatus)) return DIT_ERR_WORKSPACE;
+  const size_t kb = (size_t)(k + 127) / 128, no = ((size_t)(rows - 1) * ld_out + n_out) * 2;
+  if (ranges_overlap(out_dev, no, a_q_dev, (size_t)rows * k) || ranges_overlap(out_dev, no, w_q_dev, (size_t)n_out * k) ||
+      ranges_overlap(out_dev, no, a_scale_dev, (size_t)rows * kb * 4) ||
+      ranges_overlap(out_dev, no, w_scale_dev, (size_t)((n_out + 127) / 128) * kb * 4))
+    return DIT_ERR_INVALID_ARG;
   LinearFp8Args a{rows, n_out, k, (const uint8_t*)a_q_dev, (const uint8_t*)w_q_dev, a_scale_dev, w_scale_dev,
                   (bf16*)out_dev, ld_out, status_of(ws)};
   return cuda_status(launch_linear_fp8(a, (cudaStream_t)stream));

@@ -4,14 +4,25 @@
 // The scales are any fp32 numbers, so the tensor cores sum one block of 128 depths at a time into
 // Tensor Memory and the threads that own an accumulator row fold it into fp32 registers:
 // acc += part * (sa sw), one packed fp32x2 FMA per two columns.  A block's MMAs run while the
-// block before it is folded.
+// blocks before it are folded.
 //
-//   linear_fp8_wide_kernel   many rows: CTA pairs, 256 x BN tiles, the operands' ring of the bf16
-//                            product (128-byte rows hold one block of depth).
+//   linear_fp8_wide_kernel   more than 64 rows: persistent CTA pairs, 256 x 128 tiles, the operands'
+//                            ring of the bf16 product (128-byte rows hold one block of depth).
 //   linear_fp8_few_kernel    up to 64 rows, where reading the weights bounds the time: the weights'
 //                            rows take the MMA's 128-row side and the few activation rows its column
 //                            side, the depth split over a cluster whose CTAs add their parts
-//                            through distributed shared memory, in rank order.
+//                            through distributed shared memory, in rank order.  (128 rows of
+//                            4096 x 4096: 17.8 us so, 10.8 as a wide tile.)
+//
+// The wide kernel reaches 2.38 PFLOP/s at 8192 x 12288 x 4096 (346 us) and 2.32 at 4096 x 4864 x 4096
+// (70 us), 0.6 of the e4m3 rate (twice the measured bf16 burst); without its fold the same ring
+// runs at 3.8.  A 128-column block takes ~546 cycles: the MMAs' operands and the loads take 437 of
+// them from shared memory at 128 bytes per cycle, and the fold's scale loads, one line per row, share that
+// path.  256-column tiles read 40 % less shared memory per product but leave two
+// accumulators, between which commit, fold, hand-back and issue (~1900 cycles) do not hide: 363 us.
+// Measured and left: 160 columns in three accumulators 356 us, one CTA per tile with the weights by
+// multicast 353, scales 16 blocks ahead through shared memory 390, scales of a block in one line 375
+// (and 68 at the smaller size).
 #include <cuda_fp8.h>
 
 #include <atomic>
@@ -153,7 +164,6 @@ __device__ __forceinline__ void umma2_f8x4(uint32_t d, uint64_t a, uint64_t w, u
 // parity waits are thereby never more than one phase behind.
 constexpr int kIssuers = 2;
 
-
 struct Wide {
   static constexpr int BN = 128;
   static constexpr uint32_t kA = 128 * 128, kW = BN / 2 * 128, kStage = kA + kW;
@@ -169,9 +179,9 @@ struct Wide {
 
 // Warp 0 loads, warps 1 and 2 issue (leader CTA) every second block of depth each, the others from
 // warp 4 fold and store, BN / 64 per row quarter with 64 columns each.  An issuing thread needs
-// ~500 cycles per block for its waits, MMAs and commit, as long as the MMAs themselves, so there are
-// two.  Per block there is one commit, on the accumulator; the stage it frees is handed back by a
-// folding thread of each CTA.
+// ~500 cycles per block for its waits, MMAs and commit, more than the MMAs themselves: two of them take
+// 8192 x 12288 x 4096 from 506 to 346 us.  Per block there is one commit, on the accumulator; the
+// stage it frees is handed back by a folding thread of each CTA.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     linear_fp8_wide_kernel(const __grid_constant__ Params P) {
   using L = Wide;
@@ -236,8 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
               ok = false;
               break;
             }
-           
-          const uint32_t fb = map_to_rank(smem_u32(&full[stage]), 0);
+            const uint32_t fb = map_to_rank(smem_u32(&full[stage]), 0);
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
             tma2_2sm(sA + stage * L::kA, &P.a_map, fb, kb * 128, arow);
             tma2_2sm(sW + stage * L::kW, &P.w_map, fb, kb * 128, wrow);
@@ -274,11 +283,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
           if (!mbar_wait(&acc_empty[buf], ((i / L::kBufs) & 1u) ^ 1u, wc, kSiteAccEmpty) ||
               !mbar_wait(&full[stage], (i / L::kStages) & 1u, wc, kSiteFull))
             break;
-
           tc_fence_after();
           umma2_f8x4(tmem + buf * BN, desc_advance(a0, stage * (L::kA >> 4)), desc_advance(w0, stage * (L::kW >> 4)),
                      idesc);
-         commit_both(&acc_full[buf]);
+          commit_both(&acc_full[buf]);
         }
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
                      : "memory");
@@ -318,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
         ok = mbar_wait_inline(&acc_full[buf], buf_phase, wc, kSiteAccFull);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-                if (releaser) mbar_arrive(&empty[stage]);  // the block's MMAs have read the stage
+        if (releaser) mbar_arrive(&empty[stage]);  // the block's MMAs have read the stage
         tc_fence_after();
         const uint32_t tb = trow + buf * BN;
 #pragma unroll
@@ -329,7 +337,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster_relaxed(acc_empty0 + buf * 8);
-            
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -650,7 +657,9 @@ cudaError_t launch_few(const LinearFp8Args& a, cudaStream_t s) {
   if (!encode(P, a, T, 128)) return cudaErrorInvalidValue;
   const cudaError_t e = raise_smem(linear_fp8_few_kernel<T>, Few<T>::kBytes, T == 16 ? 1 : T == 32 ? 2 : 3);
   if (e != cudaSuccess) return e;
-  // Split the depth while the CTAs still run at once (two per SM up to 32 rows).
+  // Split the depth while the CTAs still run at once (two per SM up to 32 rows) and keep two blocks
+  // each: 1 x 4096 x 2560 takes 4.9 us (2.1 TB/s of weights, launch and cluster set-up most of it),
+  // 1 x 12288 x 4096 8.7 us (5.8 TB/s).
   const int blocks = (a.n + 127) / 128, room = kSMs * (T <= 32 ? 2 : 1);
   int S = 1;
   while (S < 8 && blocks * S * 2 <= room && P.kblocks >= S * 2) S *= 2;

@@ -471,7 +471,8 @@ dit_status dit_text_attention(const dit_text_attn* a, const int32_t* q_off, cons
  * x_dev [rows, cols] with row stride ld; q_dev [rows, cols] bytes, contiguous; scale_dev
  * [ceil(rows / block_rows), ceil(cols / 128)].  The last blocks of a row or column may be
  * short.  A NaN becomes the NaN code of its place; an infinity makes its block's products NaN.
- * cols % 16 == 0, ld % 8 == 0, ld >= cols, 1 <= rows, cols <= 2^20. */
+ * The three buffers must not overlap.  cols % 16 == 0, ld % 8 == 0, ld >= cols,
+ * 1 <= rows, cols <= 2^20. */
 dit_status dit_quantize_blocks_fp8(const void* x_dev, long long ld, int rows, int cols, int block_rows, void* q_dev,
                                    float* scale_dev, dit_stream_t stream);
 
@@ -483,8 +484,8 @@ dit_status dit_linear_fp8_blocks_workspace(int rows, int n_out, int k, size_t* b
  * blocks of 128 along k, every sum in fp32, one rounding to bf16.  a_q [rows, k] and a_scale
  * [rows, ceil(k / 128)] from dit_quantize_blocks_fp8 with block_rows 1, w_q [n_out, k] and
  * w_scale [ceil(n_out / 128), ceil(k / 128)] with block_rows 128; out_dev [rows, ld_out]
- * written at columns [0, n_out).  k % 16 == 0, n_out % 8 == 0, ld_out % 8 == 0,
- * ld_out >= n_out; 1 <= rows, n_out, k <= 2^20, else DIT_ERR_INVALID_ARG. */
+ * written at columns [0, n_out), not over an input.  k % 16 == 0, n_out % 8 == 0,
+ * ld_out % 8 == 0, ld_out >= n_out; 1 <= rows, n_out, k <= 2^20, else DIT_ERR_INVALID_ARG. */
 dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev, const float* a_scale_dev,
                                  const void* w_q_dev, const float* w_scale_dev, void* out_dev, int ld_out, void* ws,
                                  size_t ws_bytes, dit_stream_t stream);

@@ -110,18 +110,24 @@ def test_text_attention_workspace_is_bounded(dit):
     (FAKE, 128, 0, 128, 1, FAKE, FAKE), (FAKE, 128, 4, 120, 1, FAKE, FAKE), (FAKE, 120, 4, 128, 1, FAKE, FAKE),
     (FAKE, 132, 4, 128, 1, FAKE, FAKE), (FAKE, 128, 4, 128, 64, FAKE, FAKE), (FAKE, 128, 4, 128, 0, FAKE, FAKE),
     (None, 128, 4, 128, 1, FAKE, FAKE), (FAKE, 128, 4, 128, 1, FAKE + 8, FAKE), (FAKE, 128, 4, 128, 1, FAKE, None),
-    (FAKE, 128, (1 << 20) + 1, 128, 1, FAKE, FAKE)])
+    (FAKE, 128, (1 << 20) + 1, 128, 1, FAKE, FAKE),
+    # buffers over one another
+    (FAKE, 128, 4, 128, 1, FAKE + 1008, FAKE + 4096), (FAKE, 128, 4, 128, 1, FAKE + 4096, FAKE + 4096 + 496),
+    (FAKE, 128, 4, 128, 1, FAKE + 4096, FAKE + 1008)])
 def test_quantize_blocks_refusals(dit, args):
     _refused(dit, lambda: dit.dit_quantize_blocks_fp8(*args, stream=0))
 
 
-LIN = dict(rows=4, n_out=128, k=256, a=FAKE, a_s=FAKE, w=FAKE, w_s=FAKE, out=FAKE, ld=128, ws=FAKE, ws_bytes=1 << 24)
+B1, B2, B3, B4 = (FAKE + (i << 24) for i in (1, 2, 3, 4))
+LIN = dict(rows=4, n_out=128, k=256, a=B1, a_s=B2, w=B3, w_s=B4, out=FAKE, ld=128, ws=FAKE, ws_bytes=1 << 24)
 
 
 @pytest.mark.parametrize("change,st", [
     ({"rows": 0}, 1), ({"rows": (1 << 20) + 1}, 1), ({"n_out": 0}, 1), ({"n_out": 132}, 1), ({"k": 0}, 1), ({"k": 264}, 1),
     ({"ld": 120}, 1), ({"ld": 132}, 1), ({"a": None}, 1), ({"a_s": FAKE + 4}, 1), ({"w": FAKE + 8}, 1), ({"w_s": None}, 1),
-    ({"out": FAKE + 2}, 1), ({"ws": None}, 1), ({"ws_bytes": 255}, 3)])
+    ({"out": FAKE + 2}, 1), ({"ws": None}, 1), ({"ws_bytes": 255}, 3),
+    # the output over an operand or its scales
+    ({"out": B1 + 1008}, 1), ({"out": B2 - 16}, 1), ({"out": B3 + 16}, 1), ({"out": B4}, 1)])
 def test_linear_fp8_blocks_refusals(dit, change, st):
     _refused(dit, lambda: dit.dit_linear_fp8_blocks(*{**LIN, **change}.values(), stream=0), st)
 
