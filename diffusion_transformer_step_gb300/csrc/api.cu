@@ -42,7 +42,8 @@ const char* kernel_class_name(int cls) {
       "gemm_swiglu",    "gemm_plain",            "attention",           "modulation_gemv",
       "rope_table",     "pack_mlp_in",           "gemm_dual_out_proj",  "gemm_dual_mlp_out",
       "gemm_single_out_proj", "quantize_act",    "text_rope_table",     "qk_norm_rope",
-      "text_attention", "text_attention_join",   "quantize_blocks_fp8", "linear_fp8_blocks"};
+      "text_attention", "text_attention_join",   "quantize_blocks_fp8", "linear_fp8_blocks",
+      "linear_fp8_join"};
   return (cls >= 0 && cls < kClsCount) ? names[cls] : "?";
 }
 
@@ -100,6 +101,11 @@ static bool encode_tmap_typed(CUtensorMap* map, CUtensorMapDataType dtype, const
 bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                       const uint64_t* strides_bytes, const uint32_t* box) {
   return encode_tmap_typed(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box);
+}
+
+bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides_bytes, const uint32_t* box) {
+  return encode_tmap_typed(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, rank, dims, strides_bytes, box);
 }
 
 bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
@@ -1169,7 +1175,7 @@ dit_status dit_quantize_blocks_fp8(const void* x_dev, long long ld, int rows, in
 
 dit_status dit_linear_fp8_blocks_workspace(int rows, int n_out, int k, size_t* bytes) {
   if (!linear_fp8_sizes_ok(rows, n_out, k) || !bytes) return DIT_ERR_INVALID_ARG;
-  *bytes = sizeof(DeviceStatus);
+  *bytes = sizeof(DeviceStatus) + linear_fp8_parts_bytes(rows, n_out, k);
   return DIT_OK;
 }
 
@@ -1180,14 +1186,14 @@ dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev
   if (!aligned16(a_q_dev) || !aligned16(a_scale_dev) || !aligned16(w_q_dev) || !aligned16(w_scale_dev) ||
       !aligned16(out_dev) || !aligned16(ws))
     return DIT_ERR_INVALID_ARG;
-  if (ws_bytes < sizeof(DeviceStatus)) return DIT_ERR_WORKSPACE;
+  if (ws_bytes < sizeof(DeviceStatus) + linear_fp8_parts_bytes(rows, n_out, k)) return DIT_ERR_WORKSPACE;
   const size_t kb = (size_t)(k + 127) / 128, no = ((size_t)(rows - 1) * ld_out + n_out) * 2;
   if (ranges_overlap(out_dev, no, a_q_dev, (size_t)rows * k) || ranges_overlap(out_dev, no, w_q_dev, (size_t)n_out * k) ||
       ranges_overlap(out_dev, no, a_scale_dev, (size_t)rows * kb * 4) ||
       ranges_overlap(out_dev, no, w_scale_dev, (size_t)((n_out + 127) / 128) * kb * 4))
     return DIT_ERR_INVALID_ARG;
   LinearFp8Args a{rows, n_out, k, (const uint8_t*)a_q_dev, (const uint8_t*)w_q_dev, a_scale_dev, w_scale_dev,
-                  (bf16*)out_dev, ld_out, status_of(ws)};
+                  (bf16*)out_dev, ld_out, status_of(ws), reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)))};
   return cuda_status(launch_linear_fp8(a, (cudaStream_t)stream));
 }
 

@@ -117,25 +117,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   return mbar_wait_slow(bar, parity, w, site);
 }
 
-// The same without a call, for threads whose accumulators fill their registers: values live
-// across a call would have to sit in the registers that it preserves, or be spilled.
-__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
-  if (mbar_try(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t i = 0;; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 63u) == 63u) {
-      if (*w.abort_flag) return false;
-      if (global_timer_ns() - t0 > w.limit_ns) {
-        if (w.status && atomicOr(&w.status->word, kStatusTimeout) == 0u) atomicExch(&w.status->where, site);
-        *w.abort_flag = 1;
-        __threadfence_block();
-        return false;
-      }
-    }
-  }
-}
-
 // The same bounded wait for warps that have nothing else to do meanwhile: try_wait with a
 // suspend-time hint lets the thread sleep in hardware until the phase completes (or the hint
 // elapses) instead of spinning on issue slots that a computing or MMA-issuing warp of the

@@ -14,8 +14,8 @@
 //                            through distributed shared memory, in rank order.  (128 rows of
 //                            4096 x 4096: 17.8 us so, 10.8 as a wide tile.)
 //
-// The wide kernel reaches 2.38 PFLOP/s at 8192 x 12288 x 4096 (346 us) and 2.32 at 4096 x 4864 x 4096
-// (70 us), 0.6 of the e4m3 rate (twice the measured bf16 burst); without its fold the same ring
+// The wide kernel reaches 2.43 PFLOP/s at 8192 x 12288 x 4096 (339 us) and 2.38 at 4096 x 4864 x 4096
+// (69 us), 0.6 of the e4m3 rate (twice the measured bf16 burst); without its fold the same ring
 // runs at 3.8.  A 128-column block takes ~546 cycles: the MMAs' operands and the loads take 437 of
 // them from shared memory at 128 bytes per cycle, and the fold's scale loads, one line per row, share that
 // path.  256-column tiles read 40 % less shared memory per product but leave two
@@ -122,10 +122,33 @@ __global__ void __launch_bounds__(256) quantize_square_blocks_kernel(const bf16*
 enum : uint32_t { kSiteEmpty = 0x701, kSiteFull, kSiteAccEmpty, kSiteAccFull };
 
 struct alignas(64) Params {
-  CUtensorMap a_map, w_map, out_map;
+  CUtensorMap a_map, w_map, out_map;  // out_map: the output, or the splits' parts
   LinearFp8Args a;
-  int kblocks, m_tiles, tiles;
+  int kblocks, m_tiles, items, splits;
 };
+
+// Work item t of the wide kernel: a tile, and a run [kb0, kb1) of its blocks of depth.
+struct Item {
+  int mt, nt, split, kb0, kb1;
+};
+template <bool kSplit>
+__device__ __forceinline__ Item item_of(const Params& P, int t) {
+  Item it;
+  if (!kSplit) {
+    it.nt = t / P.m_tiles;
+    it.mt = t - it.nt * P.m_tiles;
+    it.split = it.kb0 = 0;
+    it.kb1 = P.kblocks;
+    return it;
+  }
+  const int tile = t / P.splits;
+  it.split = t - tile * P.splits;
+  it.nt = tile / P.m_tiles;
+  it.mt = tile - it.nt * P.m_tiles;
+  it.kb0 = (int)((long long)P.kblocks * it.split / P.splits);
+  it.kb1 = (int)((long long)P.kblocks * (it.split + 1) / P.splits);
+  return it;
+}
 
 // Arrival at the leader's barrier that publishes no memory: the accumulator's reads are complete
 // (tcgen05.wait::ld) and ordered by tcgen05.fence.  With release semantics at cluster scope each of the
@@ -136,10 +159,10 @@ __device__ __forceinline__ void arrive_cluster_relaxed(uint32_t caddr) {
 
 // A box of the output from shared memory (128-byte swizzle), and the wait until every box of this
 // thread has been read out of it.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(m)),
-               "r"(smem_u32(src)), "r"(x), "r"(y)
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -180,8 +203,9 @@ struct Wide {
 // Warp 0 loads, warps 1 and 2 issue (leader CTA) every second block of depth each, the others from
 // warp 4 fold and store, BN / 64 per row quarter with 64 columns each.  An issuing thread needs
 // ~500 cycles per block for its waits, MMAs and commit, more than the MMAs themselves: two of them take
-// 8192 x 12288 x 4096 from 506 to 346 us.  Per block there is one commit, on the accumulator; the
+// 8192 x 12288 x 4096 from 506 to 346 us, sleeping instead of spinning folders to 339.  Per block there is one commit, on the accumulator; the
 // stage it frees is handed back by a folding thread of each CTA.
+template <bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     linear_fp8_wide_kernel(const __grid_constant__ Params P) {
   using L = Wide;
@@ -238,10 +262,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
         uint32_t stage = 0, phase = 0;
         long long issued = 0;
         bool ok = true;
-        for (int t = pair; t < P.tiles && ok; t += npairs) {
-          const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
-          const int arow = mt * 256 + (int)rank * 128, wrow = nt * BN + (int)rank * (BN / 2);
-          for (int kb = 0; kb < P.kblocks; ++kb) {
+        for (int t = pair; t < P.items && ok; t += npairs) {
+          const Item it = item_of<kSplit>(P, t);
+          const int arow = it.mt * 256 + (int)rank * 128, wrow = it.nt * BN + (int)rank * (BN / 2);
+          for (int kb = it.kb0; kb < it.kb1; ++kb) {
             if (!mbar_wait_sleep(&empty[stage], phase ^ 1u, wc, kSiteEmpty)) {
               ok = false;
               break;
@@ -276,8 +300,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
       if (lane == 0 && rank == 0) {
         const uint32_t idesc = make_idesc_e4m3(256, BN);
         const uint64_t a0 = make_sdesc_sw128(smem_u32(sA), 16, 1024), w0 = make_sdesc_sw128(smem_u32(sW), 16, 1024);
-        // Blocks of depth over all of this pair's tiles, every kIssuers-th.
-        const uint32_t blocks = (uint32_t)((P.tiles - pair + npairs - 1) / npairs) * (uint32_t)P.kblocks;
+        // Every kIssuers-th block of depth over all of this pair's items.
+        uint32_t blocks = (uint32_t)((P.items - pair + npairs - 1) / npairs) * (uint32_t)P.kblocks;
+        if (kSplit) {
+          blocks = 0;
+          for (int t = pair; t < P.items; t += npairs) {
+            const Item it = item_of<kSplit>(P, t);
+            blocks += (uint32_t)(it.kb1 - it.kb0);
+          }
+        }
         for (uint32_t i = warp - 1; i < blocks; i += kIssuers) {
           const uint32_t stage = i % L::kStages, buf = i % L::kBufs;
           if (!mbar_wait(&acc_empty[buf], ((i / L::kBufs) & 1u) ^ 1u, wc, kSiteAccEmpty) ||
@@ -303,10 +334,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     uint8_t* staged = smem + L::kOut + (warp - 4) * 2048;
     uint32_t stage = 0, buf = 0, buf_phase = 0;
     bool ok = true;
-    for (int t = pair; t < P.tiles && ok; t += npairs) {
-      const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
-      const int row = mt * 256 + (int)rank * 128 + q * 32 + lane;
-      const int col = nt * BN + eh * kCols;
+    for (int t = pair; t < P.items && ok; t += npairs) {
+      const Item it = item_of<kSplit>(P, t);
+      const int row = it.mt * 256 + (int)rank * 128 + q * 32 + lane;
+      const int col = it.nt * BN + eh * kCols;
       // rows and column blocks past the end: any scale of the matrix does, nothing is stored
       const float* sa = P.a.a_scale + (long long)min(row, P.a.rows - 1) * P.kblocks;
       const float* sw = P.a.w_scale + (long long)(min(col, P.a.n - 1) / 128) * P.kblocks;
@@ -314,16 +345,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       // scales of this block and the next; the one after is in flight while this one is folded
-      const int last = P.kblocks - 1;
-      float sa0 = __ldg(sa), sw0 = __ldg(sw), sa1 = __ldg(sa + min(1, last)), sw1 = __ldg(sw + min(1, last));
-      for (int kb = 0; kb < P.kblocks; ++kb) {
+      const int last = it.kb1 - 1, k1 = min(it.kb0 + 1, last);
+      float sa0 = __ldg(sa + it.kb0), sw0 = __ldg(sw + it.kb0), sa1 = __ldg(sa + k1), sw1 = __ldg(sw + k1);
+      for (int kb = it.kb0; kb < it.kb1; ++kb) {
         const float s = sa0 * sw0;
         const float2 s2 = make_float2(s, s);
         sa0 = sa1;
         sw0 = sw1;
         sa1 = __ldg(sa + min(kb + 2, last));
         sw1 = __ldg(sw + min(kb + 2, last));
-        ok = mbar_wait_inline(&acc_full[buf], buf_phase, wc, kSiteAccFull);
+        ok = mbar_wait_sleep(&acc_full[buf], buf_phase, wc, kSiteAccFull);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (releaser) mbar_arrive(&empty[stage]);  // the block's MMAs have read the stage
@@ -351,23 +382,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
       }
       if (!ok) break;
       // 16 rows at a time through this warp's staging rows (128-byte swizzle) to a TMA store, which
-      // clips rows and columns past the matrix.
+      // clips rows and columns past the matrix: 64 columns of bf16, or 32 of a split's fp32.
+      if (!kSplit) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (lane == 0) tma_store_wait_read();
-        __syncwarp();
-        if ((lane >> 4) == h) {
+        for (int h = 0; h < 2; ++h) {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+          if ((lane >> 4) == h) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2* f = acc + i * 4;
-            *reinterpret_cast<uint4*>(staged + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
-                make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
-                           pack_bf16x2(f[3].x, f[3].y));
+            for (int i = 0; i < 8; ++i) {
+              const float2* f = acc + i * 4;
+              *reinterpret_cast<uint4*>(staged + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                             pack_bf16x2(f[3].x, f[3].y));
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && col < P.a.n && row + h * 16 < P.a.rows)
+            tma_store_3d(&P.out_map, staged, col, row + h * 16, 0);
         }
-        __syncwarp();
-        if (lane == 0 && col < P.a.n && row + h * 16 < P.a.rows) tma_store_2d(&P.out_map, staged, col, row + h * 16);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+          if ((lane >> 4) == (h & 1)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2* f = acc + (h >> 1) * 16 + i * 2;
+              *reinterpret_cast<float4*>(staged + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                  make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0 && col + (h >> 1) * 32 < P.a.n && row + (h & 1) * 16 < P.a.rows)
+            tma_store_3d(&P.out_map, staged, col + (h >> 1) * 32, row + (h & 1) * 16, it.split);
+        }
       }
     }
     if (lane == 0) tma_store_wait_read();
@@ -379,6 +431,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+// Adds the splits' parts [split][row][column] up, in split order: eight columns per thread.
+__global__ void __launch_bounds__(256) linear_fp8_join_kernel(const float* __restrict__ parts, int splits, int rows,
+                                                              int n, bf16* __restrict__ out, int ld_out) {
+  grid_dependency_wait();
+  allow_dependents();
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int per_row = n / 8;
+  if (i >= (long long)rows * per_row) return;
+  const int row = (int)(i / per_row), c = (int)(i - (long long)row * per_row) * 8;
+  const float4* p = reinterpret_cast<const float4*>(parts + (long long)row * n + c);
+  const long long step = (long long)rows * n / 4;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 a = p[s * step], b = p[s * step + 1];
+    x.x += a.x, x.y += a.y, x.z += a.z, x.w += a.w;
+    y.x += b.x, y.y += b.y, y.z += b.z, y.w += b.w;
+  }
+  *reinterpret_cast<uint4*>(out + (long long)row * ld_out + c) =
+      make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+}
+
+// Splits of the depth: only where the tiles leave pairs idle, one item per pair, at least eight blocks
+// each (2.1 us; a split costs ~3, its part's store and the join).  489 x 1168 x 9616: 28.5 us without,
+// 15.5 with three (20 tiles, 76 blocks).
+int wide_splits(int rows, int n, int k) {
+  const int tiles = ((rows + 255) / 256) * ((n + Wide::BN - 1) / Wide::BN), kb = (k + 127) / 128;
+  if (tiles > kSMs / 4) return 1;
+  const int s = kSMs / 2 / tiles, most = kb / 8;
+  return s < most ? s : most > 1 ? most : 1;
 }
 
 // ---- product, few rows -------------------------------------------------------------------
@@ -639,16 +723,35 @@ bool encode(Params& P, const LinearFp8Args& a, uint32_t a_box, uint32_t w_box) {
 cudaError_t launch_wide(const LinearFp8Args& a, cudaStream_t s) {
   Params P;
   if (!encode(P, a, 128, Wide::BN / 2)) return cudaErrorInvalidValue;
-  const uint64_t od[2] = {(uint64_t)a.n, (uint64_t)a.rows}, ost[1] = {(uint64_t)a.ld_out * 2};
-  const uint32_t obox[2] = {64, 16};
-  if (!encode_tmap_bf16(&P.out_map, a.out, 2, od, ost, obox)) return cudaErrorInvalidValue;
+  P.splits = wide_splits(a.rows, a.n, a.k);
+  const uint64_t od[3] = {(uint64_t)a.n, (uint64_t)a.rows, (uint64_t)P.splits};
+  if (P.splits > 1) {
+    const uint64_t ost[2] = {(uint64_t)a.n * 4, (uint64_t)a.n * a.rows * 4};
+    const uint32_t obox[3] = {32, 16, 1};
+    if (!encode_tmap_f32(&P.out_map, a.parts, 3, od, ost, obox)) return cudaErrorInvalidValue;
+  } else {
+    const uint64_t ost[2] = {(uint64_t)a.ld_out * 2, (uint64_t)a.ld_out * a.rows * 2};
+    const uint32_t obox[3] = {64, 16, 1};
+    if (!encode_tmap_bf16(&P.out_map, a.out, 3, od, ost, obox)) return cudaErrorInvalidValue;
+  }
   P.m_tiles = (a.rows + 255) / 256;
-  P.tiles = P.m_tiles * ((a.n + Wide::BN - 1) / Wide::BN);
-  const cudaError_t e = raise_smem(linear_fp8_wide_kernel, Wide::kBytes, 0);
+  P.items = P.m_tiles * ((a.n + Wide::BN - 1) / Wide::BN) * P.splits;
+  auto kernel = P.splits > 1 ? linear_fp8_wide_kernel<true> : linear_fp8_wide_kernel<false>;
+  cudaError_t e = raise_smem(kernel, Wide::kBytes, P.splits > 1 ? 4 : 0);
   if (e != cudaSuccess) return e;
-  const int most = sm_count() / 2, pairs = P.tiles < most ? P.tiles : most;
-  LaunchScope scope(kClsLinearFp8Blocks, s);
-  return launch_k(linear_fp8_wide_kernel, dim3(2 * pairs), dim3(Wide::kThreads), Wide::kBytes, s, P);
+  const int most = sm_count() / 2, pairs = P.items < most ? P.items : most;
+  {
+    LaunchScope scope(kClsLinearFp8Blocks, s);
+    e = launch_k(kernel, dim3(2 * pairs), dim3(Wide::kThreads), Wide::kBytes, s, P);
+    if (e != cudaSuccess) return e;
+  }
+  if (P.splits > 1) {
+    const long long threads = (long long)a.rows * (a.n / 8);
+    LaunchScope scope(kClsLinearFp8Join, s);
+    return launch_k(linear_fp8_join_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s,
+                    (const float*)a.parts, P.splits, a.rows, a.n, a.out, a.ld_out);
+  }
+  return cudaSuccess;
 }
 
 template <int T>
@@ -694,6 +797,11 @@ cudaError_t launch_quantize_blocks(const bf16* x, long long ld, int rows, int co
   const int ty = 256 / tx;
   return launch_k(quantize_row_blocks_kernel, dim3((unsigned)((rows + ty - 1) / ty), (unsigned)((cb * 8 + tx - 1) / tx)),
                   dim3(tx, ty), 0, s, x, ld, rows, cols, q, scale);
+}
+
+size_t linear_fp8_parts_bytes(int rows, int n, int k) {
+  const int splits = rows > 64 ? wide_splits(rows, n, k) : 1;
+  return splits > 1 ? (size_t)splits * rows * n * 4 : 0;
 }
 
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s) {

@@ -32,7 +32,8 @@ enum KernelClass : int {
   kClsTextJoin = 17,       // joining its key splits
   kClsQuantBlocks = 18,    // e4m3 quantisation with a scale per block
   kClsLinearFp8Blocks = 19,  // e4m3 product with block scales
-  kClsCount = 20
+  kClsLinearFp8Join = 20,  // joining its depth splits
+  kClsCount = 21
 };
 
 const char* kernel_class_name(int cls);
@@ -78,7 +79,9 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 // first; strides are in bytes for dims 1..rank-1.  Returns false on failure.
 bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                       const uint64_t* strides_bytes, const uint32_t* box);
-// The same for a one-byte element type (e4m3 operands).
+// The same for fp32 elements, and for a one-byte element type (e4m3 operands).
+bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides_bytes, const uint32_t* box);
 bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box);
 
@@ -248,7 +251,9 @@ struct LinearFp8Args {
   bf16* out;
   int ld_out;
   DeviceStatus* status;
+  float* parts;  // workspace of the depth splits
 };
+size_t linear_fp8_parts_bytes(int rows, int n, int k);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
 
 }  // namespace dit

@@ -476,7 +476,8 @@ dit_status dit_text_attention(const dit_text_attn* a, const int32_t* q_off, cons
 dit_status dit_quantize_blocks_fp8(const void* x_dev, long long ld, int rows, int cols, int block_rows, void* q_dev,
                                    float* scale_dev, dit_stream_t stream);
 
-/* Bytes of workspace that dit_linear_fp8_blocks needs (its status word). */
+/* Bytes of workspace that dit_linear_fp8_blocks needs (at least the 256 of the status word;
+ * more where the depth of few tiles is split over the GPU, at most 10 MB). */
 dit_status dit_linear_fp8_blocks_workspace(int rows, int n_out, int k, size_t* bytes);
 
 /* Linear layer on e4m3 operands with block scales:

@@ -132,10 +132,20 @@ def test_linear_fp8_blocks_refusals(dit, change, st):
     _refused(dit, lambda: dit.dit_linear_fp8_blocks(*{**LIN, **change}.values(), stream=0), st)
 
 
+def test_linear_fp8_blocks_workspace(dit):
+    """Bounded for any sizes, and refused when it is a byte short."""
+    for m, n, k in ((1, 8, 16), (300, 256, 4096), (65, 128, 1 << 20), (489, 1168, 9616), (8192, 12288, 4096), (1 << 20, 8, 1 << 20)):
+        assert 256 <= dit.dit_linear_fp8_blocks_workspace(m, n, k) <= 256 + 10 * (1 << 20)
+    need = dit.dit_linear_fp8_blocks_workspace(300, 256, 4096)
+    assert need > 256
+    _refused(dit, lambda: dit.dit_linear_fp8_blocks(*{**LIN, "rows": 300, "n_out": 256, "k": 4096, "ld": 256,
+                                                      "ws_bytes": need - 1}.values(), stream=0), dit.DIT_ERR_WORKSPACE)
+
+
 def test_kernel_classes_have_names(dit):
     names = [dit.dit_kernel_class_name(i) for i in range(32)]
     for n in ("text_rope_table", "qk_norm_rope", "text_attention", "text_attention_join", "quantize_blocks_fp8",
-              "linear_fp8_blocks"):
+              "linear_fp8_blocks", "linear_fp8_join"):
         assert names.count(n) == 1
 
 

@@ -449,7 +449,7 @@ def test_quantize_blocks_bit_exact(dit, block_rows, rows, cols):
 
 @pytest.mark.parametrize("m,n,k", [(1, 8, 16), (1, 4096, 2560), (2, 136, 272), (16, 1000, 1008), (17, 264, 144), (64, 128, 128),
                                    (65, 512, 640), (127, 2568, 400), (128, 256, 256), (129, 520, 384), (300, 256, 4096),
-                                   (257, 1288, 1296), (1777, 2568, 2064), (3, 8, 20000), (513, 128, 16), (40, 3000, 512)])
+                                   (257, 1288, 1296), (1777, 2568, 2064), (3, 8, 20000), (513, 128, 16), (40, 3000, 512), (489, 1168, 9616), (65, 8, 2048), (1567, 408, 5120)])
 def test_linear_fp8_blocks(dit, ws, m, n, k):
     x, w = _randn(m, k, seed=1), _randn(n, k, seed=2, std=0.05)
     x[:, :min(k, 40)] *= 30  # blocks of unlike scales
