@@ -998,7 +998,7 @@ dit_status check_text_attn(const dit_text_attn* a) {
   if (a->seqs < 0 || a->seqs > kMaxSeqs || a->rows_q < 0 || a->rows_q > kMaxAttnRows || a->rows_k < 0 ||
       a->rows_k > kMaxAttnRows || a->max_q < 0 || a->max_q > kMaxLen || a->max_k < 0 || a->max_k > kMaxLen)
     return DIT_ERR_INVALID_ARG;
-  if (!finite_pos(a->scale) || a->scale > 3.0e38f) return DIT_ERR_INVALID_ARG;
+  if (!finite_pos(a->scale) || a->scale > 1e30f) return DIT_ERR_INVALID_ARG;  // times log2(e) stays finite
   return DIT_OK;
 }
 

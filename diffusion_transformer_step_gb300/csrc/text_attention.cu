@@ -54,7 +54,7 @@ constexpr int kKeys = 128;                     // keys per block
 constexpr uint32_t kHalfBytes = 128 * 64 * 2;  // 64 dims of a 128-row tile
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPsumLimit = 4096.0f;  // row sum of P that sends a key block down the slow path
-constexpr int kInlineSeqs = 64;        // up to here a CTA finds its tile itself
+constexpr int kInlineSeqs = 64;        // up to here one warp finds its item itself
 constexpr int kSMs = 152;
 constexpr int kLevels = 1024;          // tile-index levels of the listing kernel
 
@@ -164,7 +164,7 @@ struct Smem {
   static constexpr size_t kBytes = 1024 + kBar + 384;
 };
 
-// One work item of a CTA, as the loading warp found it.
+// One work item of a CTA, as warp 10 found it.
 struct Item {
   int q0, nq, k0, nk, tok0;  // the sequence's rows, and the pair's first token
   int n0, n1, b0;            // key blocks of each tile, and the first of them (of this split)

@@ -428,7 +428,7 @@ dit_status dit_qk_norm_rope(int rows, int heads_q, int heads_k, int head_dim, in
 /* Sizes of one dit_text_attention call.  heads_q % heads_k == 0, heads_q / heads_k <= 64,
  * head_dim 64 or 128; 0 <= seqs <= 16384; rows_q and rows_k (rows of the whole buffers)
  * 0 .. 2^28; max_q and max_k: upper bounds of the sequences' lengths, 0 .. 2^24, which choose
- * how the work is split; scale > 0 and finite (the usual one is 1 / sqrt(head_dim)). */
+ * how the work is split; 0 < scale <= 1e30 (the usual one is 1 / sqrt(head_dim)). */
 typedef struct {
   int seqs, heads_q, heads_k, head_dim;
   int rows_q, rows_k, max_q, max_k;
@@ -448,7 +448,8 @@ dit_status dit_text_attention_workspace(const dit_text_attn* a, size_t* bytes);
  *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j   over the visible keys j < nk,
  * all of them, or with `causal` those with j <= i + nk - nq (the last query sees the last
  * key: nq = nk is a whole prompt, nq = 1 a new token over a cache that holds its key).
- * A query that sees no key (nk == 0, or causal with nk < nq) gets zeros.
+ * A query that sees no key (nk == 0, or causal with nk < nq) gets zeros, and so does one whose
+ * visible scores are all minus infinity.
  * q_dev + row * ldq + h * head_dim, k and v likewise with heads_k, out_dev + row * ldo +
  * h * head_dim; all bf16.  Rows of out_dev that belong to no sequence are not written, rows
  * behind a sequence's keys not used, whatever they hold.  A visible value that is infinite

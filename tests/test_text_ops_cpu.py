@@ -80,7 +80,7 @@ AT_ARGS = dict(q_off=FAKE, q_len=None, k_off=FAKE, k_len=None, q_dev=FAKE, ldq=1
 @pytest.mark.parametrize("change,st", [
     ({"head_dim": 96}, 2), ({"heads_q": 7}, 1), ({"heads_q": 0}, 1), ({"heads_k": 0}, 1), ({"heads_q": 130}, 1), ({"seqs": -1}, 1),
     ({"seqs": 16385}, 1), ({"rows_q": -1}, 1), ({"rows_k": (1 << 28) + 1}, 1), ({"max_q": -1}, 1), ({"max_k": (1 << 24) + 1}, 1),
-    ({"scale": 0.0}, 1), ({"scale": -1.0}, 1), ({"scale": math.nan}, 1), ({"scale": math.inf}, 1)])
+    ({"scale": 0.0}, 1), ({"scale": -1.0}, 1), ({"scale": math.nan}, 1), ({"scale": math.inf}, 1), ({"scale": 2e30}, 1)])
 def test_text_attention_size_refusals(dit, change, st):
     a = dit.make_text_attn(**{**AT, **change})
     _refused(dit, lambda: dit.dit_text_attention(a, *AT_ARGS.values(), stream=0), st)
