@@ -94,7 +94,8 @@ Plan make_plan(const TextAttnArgs& a) {
   p.tiles = (int)(packed < padded ? packed : padded);
   p.list = a.seqs > kInlineSeqs;
   // Splits only fill SMs that would stay idle, and leave each part four key blocks: a part costs
-  // a fixed ~3 us (launch, first loads, join) against ~1.3 us per block.
+  // a fixed ~3 us (launch, first loads, join) against ~1.3 us per block.  300 tokens of 3 heads over
+  // 3366 keys of one: 49.8 us whole, 20.6 in six parts.
   const long long items = (long long)p.tiles * a.heads_k;
   const int blocks = (a.max_k + kKeys - 1) / kKeys;
   p.splits = 1;
@@ -354,7 +355,7 @@ __device__ __noinline__ void attend_row(const TextAttnArgs& a, const bf16* qp, c
   }
 }
 
-template <int D>
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __grid_constant__ TextAttnParams P) {
   using L = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -551,8 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       bool found = false;
       if (!stop) {
         hk = id % a.heads_k;
-        split = (id / a.heads_k) % P.splits;
-        rank = id / a.heads_k / P.splits;
+        rank = id / a.heads_k;
+        if (kSplit) {
+          split = rank % P.splits;
+          rank /= P.splits;
+        }
         if (P.list) {
           const int2 e = P.list[rank];
           found = e.x >= 0;
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
         } else {
           found = find_tile(a, TP, P.levels, P.tiles, rank, lane, k == 0 && blockIdx.x == 0, sp, index);
         }
-        if (P.splits > 1 && hk == 0 && split == 0 && lane == 0)
+        if (kSplit && hk == 0 && split == 0 && lane == 0)
           P.desc[rank] = found ? make_int2(sp.q0 + index * TP, min(TP, sp.nq - index * TP)) : make_int2(0, 0);
       }
       if (!stop && !found) continue;
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
         };
         it.n0 = blocks(it.tok0);
         it.n1 = blocks(it.tok0 + TQ);
-        if (P.splits > 1) {
+        if (kSplit) {
           const int nb = max(it.n0, it.n1);
           it.b0 = (int)((long long)nb * split / P.splits);
           const int b1 = (int)((long long)nb * (split + 1) / P.splits);
@@ -702,12 +706,14 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
         const int prow = (tile * TQ + token) * G + g;
         const long long out_at = active ? (long long)(q0 + qi) * a.ldo + (hk * G + g) * D : -1;  // this row's output
         const long long part = ((long long)it.rank * a.heads_k + hk) * P.splits + it.split;
-        float* po = P.splits > 1 ? P.o + (part * 256 + prow) * D : nullptr;
+        // this warp's first row: a tile's rows r < TQ G are consecutive in the part
+        float* po = kSplit ? P.o + (part * 256 + tile * TQ * G + qq * 32) * D : nullptr;
+        const uint32_t rows_in = __ballot_sync(0xffffffffu, active);
         // 64 dims at a time through the warp's staging rows (16-byte pieces swizzled): a warp that holds
         // whole tokens of the sequence hands them to a TMA store and goes on (1.1 us a tile less than
-        // stores of 128-byte pieces of four rows each, as the others do it).  A split's fp32 rows go
-        // out as they are.
-        const bool whole_rows = P.splits == 1 && 32 % G == 0 && __all_sync(0xffffffffu, active);
+        // stores of 128-byte pieces of four rows each, as the others do it).  A split's fp32 rows leave
+        // 32 dims at a time.
+        const bool whole_rows = !kSplit && 32 % G == 0 && __all_sync(0xffffffffu, active);
         if (lane == 0) tma_store_wait_read();  // the item before has left the staging rows
         __syncwarp();
         float zero = 0.f;
@@ -723,13 +729,20 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
               f[i] = none ? 0.f : __uint_as_float(r[i]);
               zero = fmaf(f[i], 0.f, zero);  // NaN once a value is not finite
             }
-            if (po) {
-              if (active) {
+            if (kSplit) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  reinterpret_cast<float4*>(po + h * 64 + cc * 32)[i] =
-                      make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(staged + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                    make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3);
+                if ((rows_in >> r) & 1u)
+                  *reinterpret_cast<float4*>(po + r * D + h * 64 + cc * 32 + (lane & 7) * 4) =
+                      *reinterpret_cast<const float4*>(staged + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
               }
+              __syncwarp();
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -748,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
               if (h + 1 < D / 64) tma_store_wait_read();  // the staging rows are written again
             }
             __syncwarp();
-          } else if (!po) {
+          } else if (!kSplit) {
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -761,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
             __syncwarp();
           }
         }
-        if (active && po) P.ml[part * 256 + prow] = none ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
+        if (active && kSplit) P.ml[part * 256 + prow] = none ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
         // Rows that are not finite: was it a value that they must not see?
         const int taken = min(nk, (b0 + n) * kKeys);
         const int seen = limit + b0 * kKeys;
@@ -788,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
           attend_row<D>(a, a.q + (long long)(q0 + r_qi) * a.ldq + (hk * G + r_g) * D,
                         a.k + (long long)(k0 + j0) * a.ldk + hk * D, vp + (long long)j0 * a.ldv, max(0, r_lim - j0), c,
                         lane, m, l, o);
-          if (P.splits > 1) {
+          if (kSplit) {
             float* dst = P.o + (part * 256 + r_prow) * D;
 #pragma unroll
             for (int e = 0; e < V; ++e) dst[lane * V + e] = o[e];
@@ -820,42 +833,71 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
   }
 }
 
-// Adds the splits of every row of a pair of tiles up, in split order: one CTA per (pair, key
-// head), one warp per row at a time.
+// One output row from its n parts, in order: part i has (max, sum) at ml[i step] and the unnormalised
+// row at o[i step D].  One warp; the parts' rows are fetched eight at a time, since what a join costs
+// is the latency of its loads.
 template <int D>
-__global__ void __launch_bounds__(256) text_attention_join_kernel(const __grid_constant__ TextAttnParams P) {
+__device__ __forceinline__ void join_row(const float2* ml, const float* o, int step, int n, int lane, bf16* out) {
   constexpr int V = D / 32;
-  grid_dependency_wait();
-  allow_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hk = blockIdx.x % P.a.heads_k, t = blockIdx.x / P.a.heads_k;
-  const int2 d = P.desc[t];
-  const int G = P.group;
-  for (int r = warp; r < d.y * G; r += 8) {
-    const long long at = (long long)blockIdx.x * P.splits * 256 + r;
-    float m = -INFINITY;
-    for (int s = 0; s < P.splits; ++s) m = fmaxf(m, P.ml[at + s * 256].x);
-    const float mr = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[V];
+  float m = -INFINITY;
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[(long long)s * step].x);
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-    for (int s = 0; s < P.splits; ++s) {
-      const float2 ml = P.ml[at + s * 256];
-      if (ml.y == 0.f) continue;  // this run held no key that the row sees
-      const float w = ex2_approx(ml.x - mr);
-      l += w * ml.y;
-      const float* po = P.o + (at + s * 256) * D + lane * V;
+  for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, sum[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] += w * po[e];
+  for (int e = 0; e < V; ++e) sum[e] = 0.f;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    float2 x = make_float2(0.f, 0.f);
+    if (s0 + lane < n) x = ml[(long long)(s0 + lane) * step];
+    // a part that held no key the row sees adds nothing, whatever its row holds
+    const float f = x.y == 0.f ? -1.f : ex2_approx(x.x - ref);
+    l += f < 0.f ? 0.f : f * x.y;
+    for (int i = 0; i < 32 && s0 + i < n; i += 8) {
+      float v[8][V];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float* p = o + (long long)min(s0 + i + u, n - 1) * step * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 t = *reinterpret_cast<const float2*>(p + e);
+          v[u][e] = t.x;
+          v[u][e + 1] = t.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = __shfl_sync(0xffffffffu, f, i + u);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e] += w < 0.f ? 0.f : w * v[u][e];
+      }
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    bf16* out = P.a.out + (long long)(d.x + r / G) * P.a.ldo + (hk * G + r % G) * D + lane * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = __float2bfloat16(o[e] * inv);
   }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    *reinterpret_cast<uint32_t*>(out + lane * V + e) = pack_bf16x2(sum[e] * inv, sum[e + 1] * inv);
 }
 
-std::atomic<bool> g_attr_set[32];  // (device, head_dim): the shared-memory attribute is raised
+// Adds the splits of every row of a pair of tiles up, in split order: one warp per row, grid (pair
+// and key head, eight rows).
+template <int D>
+__global__ void __launch_bounds__(256) text_attention_join_kernel(const __grid_constant__ TextAttnParams P) {
+  grid_dependency_wait();
+  allow_dependents();
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int hk = blockIdx.x % P.a.heads_k, G = P.group;
+  const int2 d = P.desc[blockIdx.x / P.a.heads_k];
+  if (r >= d.y * G) return;
+  const long long at = (long long)blockIdx.x * P.splits * 256 + r;
+  const int token = r / G;
+  join_row<D>(P.ml + at, P.o + at * D, 256, P.splits, threadIdx.x & 31,
+              P.a.out + (long long)(d.x + token) * P.a.ldo + (hk * G + r - token * G) * D);
+}
+
+std::atomic<bool> g_attr_set[64];  // (device, split, head_dim): the shared-memory attribute is raised
 
 template <int D>
 cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
@@ -891,12 +933,12 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
   P.ml = reinterpret_cast<float2*>(ws + l.ml);
   P.o = reinterpret_cast<float*>(ws + l.o);
   const size_t smem = Smem<D>::kBytes;
+  auto kernel = p.splits > 1 ? text_attention_kernel<D, true> : text_attention_kernel<D, false>;
   int dev = 0;
   cudaGetDevice(&dev);
-  const int slot = dev * 2 + (D == 64);
+  const int slot = dev * 4 + (p.splits > 1) * 2 + (D == 64);
   if (dev >= 16 || !g_attr_set[slot].load(std::memory_order_acquire)) {
-    cudaError_t e =
-        cudaFuncSetAttribute(text_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev < 16) g_attr_set[slot].store(true, std::memory_order_release);
   }
@@ -912,12 +954,12 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
   const int sms = sm_count(), grid = items < sms ? (int)items : sms;
   {
     LaunchScope scope(kClsTextAttention, s);
-    cudaError_t e = launch_k(text_attention_kernel<D>, dim3((unsigned)grid), dim3(kThreads), smem, s, P);
+    cudaError_t e = launch_k(kernel, dim3((unsigned)grid), dim3(kThreads), smem, s, P);
     if (e != cudaSuccess) return e;
   }
   if (p.splits > 1) {
     LaunchScope scope(kClsTextJoin, s);
-    return launch_k(text_attention_join_kernel<D>, dim3((unsigned)(p.tiles * a.heads_k)), dim3(256), 0, s, P);
+    return launch_k(text_attention_join_kernel<D>, dim3((unsigned)(p.tiles * a.heads_k), 32), dim3(256), 0, s, P);
   }
   return cudaSuccess;
 }
@@ -939,18 +981,20 @@ struct FewPlan {
 
 bool few_rows(const TextAttnArgs& a) { return (long long)a.max_q * (a.heads_q / a.heads_k) <= kFewRows; }
 
-// Runs of at most 1024 keys, so that ragged lengths even out over the CTAs, and of at least 128,
-// that cut the keys into about eight waves of CTAs; and no more than 16384 runs in all, which
-// bounds the workspace.
+// Runs of at most 1024 keys, so that ragged lengths even out over the CTAs, and of at least 256 (a
+// run costs ~3 us besides its keys), that cut the longest sequences' keys into two waves of CTAs; and
+// no more than 16384 runs in all, which bounds the workspace.  Eight waves of 128 keys or more took
+// 27 tokens over 2021 to 3362 keys (3 heads of 128) from 27.6 to 40.6 us, one token over 8192 (8
+// heads) from 13.4 to 20.4.
 FewPlan few_plan(const TextAttnArgs& a) {
   FewPlan p;
   p.rows = a.max_q * (a.heads_q / a.heads_k);
   const long long items = (long long)a.seqs * a.heads_k;
-  long long chunk = (long long)a.max_k * items / (16 * kSMs);
+  long long chunk = (long long)a.max_k * items / (4 * kSMs);
   if (chunk > 1024) chunk = 1024;
   const long long least = (long long)a.max_k * items / 16384;
   if (chunk < least) chunk = least;
-  if (chunk < 128) chunk = 128;
+  if (chunk < 256) chunk = 256;
   p.chunk = (int)((chunk + kFewKeys - 1) / kFewKeys * kFewKeys);
   p.splits = (a.max_k + p.chunk - 1) / p.chunk;
   if (p.splits < 1) p.splits = 1;
@@ -1231,46 +1275,21 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
   }
 }
 
-// Adds up the runs of the sequences that took several, in order: one warp per row.
+// Adds up the runs of the sequences that took several, in order: one warp per row, grid (sequence
+// and key head, four rows).
 template <int D>
 __global__ void __launch_bounds__(128) text_attention_few_join_kernel(const __grid_constant__ FewParams P) {
-  constexpr int V = D / 32;
   grid_dependency_wait();
   allow_dependents();
   const TextAttnArgs& a = P.a;
-  const int lane = threadIdx.x & 31, G = P.group;
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), G = P.group;
   const int hk = blockIdx.x % a.heads_k, seq = blockIdx.x / a.heads_k;
   const Span sp = load_span(a, seq);
-  if (!sp.ok || sp.nk <= P.chunk) return;
-  const int runs = (sp.nk + P.chunk - 1) / P.chunk;
-  for (int r = threadIdx.x >> 5; r < sp.nq * G; r += 4) {
-    const long long at = (long long)blockIdx.x * P.splits * P.rows + r;
-    float m = -INFINITY;
-    for (int s = lane; s < runs; s += 32) m = fmaxf(m, P.ml[at + (long long)s * P.rows].x);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < runs; ++s) {
-      const long long p = at + (long long)s * P.rows;
-      const float2 x = P.ml[p];
-      const float f = x.y == 0.f ? 0.f : ex2_approx(x.x - ref);  // no key that the row sees: adds nothing
-      l += f * x.y;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float v = P.o[p * D + lane * V + e];
-        o[e] += x.y == 0.f ? 0.f : f * v;
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    const int token = r / G;
-    bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + r - token * G) * D + lane * V;
-#pragma unroll
-    for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-  }
+  if (!sp.ok || sp.nk <= P.chunk || r >= sp.nq * G) return;
+  const long long at = (long long)blockIdx.x * P.splits * P.rows + r;
+  const int token = r / G;
+  join_row<D>(P.ml + at, P.o + at * D, P.rows, (sp.nk + P.chunk - 1) / P.chunk, threadIdx.x & 31,
+              a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + r - token * G) * D);
 }
 
 std::atomic<bool> g_few_attr_set[32];  // (device, head_dim)
@@ -1315,7 +1334,8 @@ cudaError_t launch_few(const TextAttnArgs& a, cudaStream_t s) {
   }
   if (p.splits > 1) {
     LaunchScope scope(kClsTextJoin, s);
-    return launch_k(text_attention_few_join_kernel<D>, dim3((unsigned)(a.seqs * a.heads_k)), dim3(128), 0, s, P);
+    return launch_k(text_attention_few_join_kernel<D>, dim3((unsigned)(a.seqs * a.heads_k), (unsigned)((p.rows + 3) / 4)),
+                    dim3(128), 0, s, P);
   }
   return cudaSuccess;
 }

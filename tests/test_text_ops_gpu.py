@@ -252,6 +252,27 @@ def test_text_attention_few_queries_over_long_keys(dit, ws, nq, nk, hq, hk):
         _check_attention(*_attend(dit, ws, [nq, 1, nq], [nk, 5, nk - 300], hq, hk, 128, causal))
 
 
+@pytest.mark.parametrize("nq,nk,hq,hk,d", [(1, 20000, 4, 1, 128), (4, 9001, 8, 2, 64), (20, 17000, 3, 1, 128), (130, 4500, 1, 1, 64)])
+def test_text_attention_joins_of_many_parts(dit, ws, nq, nk, hq, hk, d):
+    """Few rows over so many keys that a row's parts are more than a warp's lanes, or as many as the
+    tiles are cut into; the sequences behind them have keys for some of their parts only."""
+    _check_attention(*_attend(dit, ws, [nq, min(nq, 3), nq], [nk, 3, nk // 3], hq, hk, d, True, gap_k=1, fill=math.nan))
+
+
+@pytest.mark.parametrize("nq,nk", [(40, 3000), (3, 12000)])
+def test_text_attention_bad_value_in_one_of_many_parts(dit, ws, nq, nk):
+    """A value in the last part is infinite: the queries before it keep their results over all parts."""
+    at = nk - nq // 2 - 1
+    def edit(q, k, v, spans):
+        v[at, 0, 3] = math.inf
+    got, want, size, qk = _attend(dit, ws, [nq], [nk], 3, 1, 128, True, edit=edit)
+    blind = at - (nk - nq)  # queries that do not see it
+    clean = R.attention(qk[0], qk[1], _randn(nk, 1, 128, seed=2), [(0, nq, 0, nk)], True, qk[2])
+    _check_attention(got[:blind], clean[0][:blind], clean[1][:blind], qk)
+    assert not got[blind:, :, 3].isfinite().any()
+    assert got[blind:][..., [c for c in range(128) if c != 3]].isfinite().all()
+
+
 @pytest.mark.parametrize("seqs", [65, 300, 1500])
 @pytest.mark.parametrize("hq,hk,d,causal", [(4, 1, 128, True), (3, 3, 64, False)])
 def test_text_attention_many_sequences(dit, ws, seqs, hq, hk, d, causal):
