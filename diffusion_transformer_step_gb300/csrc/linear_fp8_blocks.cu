@@ -467,16 +467,23 @@ int wide_splits(int rows, int n, int k) {
 
 // ---- product, few rows -------------------------------------------------------------------
 
-constexpr int kFewThreads = 192;
-
 template <int T>  // activation rows, rounded up: 16, 32 or 64
 struct Few {
   static constexpr uint32_t kW = 128 * 128, kA = T * 128, kStage = kW + kA;
-  static constexpr int kStages = T <= 32 ? 5 : 6;  // two CTAs per SM up to 32 rows
-  static constexpr int kBufs = 4;                  // accumulators in Tensor Memory
-  static constexpr uint32_t kTmem = kBufs * T;     // 64 .. 512 columns
+  // Two CTAs per SM up to 32 rows.  64 rows fill an SM's folding with one, and a deeper ring then
+  // beats two CTAs of four stages (150 x 128 columns, k 8192: 32.1 us against 38.0).
+  static constexpr int kResident = T <= 32 ? 2 : 1;
+  static constexpr int kStages = T == 16 ? 6 : T == 32 ? 5 : 8;
+  static constexpr int kBufs = 4;  // accumulators in Tensor Memory
+  static constexpr uint32_t kTmem = kBufs * T;     // 64 .. 256 columns
+  static constexpr int kFold = T / 32 > 0 ? T / 32 : 1;  // folding warps per 32 output columns
+  static constexpr int kMine = T / kFold;                // activation rows of a folding warp
+  static constexpr int kThreads = 128 + kFold * 128;
   static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256 + 4 * T * 4;
   static_assert((size_t)kStages * kStage >= (size_t)T * 128 * 4, "the parts reuse the ring");
+  // An issuer that waits for an accumulator knows every block before the one that held it folded, so
+  // the stage's last use too: its parity waits are never more than one phase behind.
+  static_assert(kBufs % kIssuers == 0 && kBufs <= kStages, "see above");
 };
 
 __device__ __forceinline__ void umma1_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -506,17 +513,20 @@ __device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
                :
                : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
 // One cluster per 128 output columns (one row block of w_scale); rank r of S takes the depth
-// blocks [K r / S, K (r + 1) / S).  Warp 0 loads, warp 1 issues, warps 2-5 fold: thread = one
-// output column, registers = the activation rows.
+// blocks [K r / S, K (r + 1) / S).  Warp 0 loads, warps 1 and 2 issue every second block each, the
+// others from warp 4 fold: thread = one output column, registers = up to 32 activation rows.
 template <int T>
-__global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __grid_constant__ Params P, int S) {
+__global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident) linear_fp8_few_kernel(const __grid_constant__ Params P, int S) {
   using L = Few<T>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -540,9 +550,9 @@ __global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __gri
     }
     for (int i = 0; i < L::kBufs; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 4 * L::kFold);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, kIssuers);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.a_map);
@@ -561,9 +571,11 @@ __global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __gri
   grid_dependency_wait();
   allow_dependents();
 
-  float2 acc[T / 2];
+  constexpr int M = L::kMine;
+  const int q = warp & 3, eh = (warp - 4) >> 2;  // folding warps: their 32 columns and their rows [eh M, eh M + M)
+  float2 acc[M / 2];
 #pragma unroll
-  for (int i = 0; i < T / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+  for (int i = 0; i < M / 2; ++i) acc[i] = make_float2(0.f, 0.f);
   const int n = kb1 - kb0;
   if (warp == 0) {
     if (lane == 0) {
@@ -588,11 +600,11 @@ __global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __gri
           }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp <= kIssuers) {
     if (lane == 0) {
       const uint32_t idesc = make_idesc_e4m3(128, T);
       const uint64_t w0 = make_sdesc_sw128(smem_u32(sW), 16, 1024), a0 = make_sdesc_sw128(smem_u32(sA), 16, 1024);
-      for (int i = 0; i < n; ++i) {
+      for (int i = warp - 1; i < n; i += kIssuers) {
         const int s = i % L::kStages, b = i % L::kBufs;
         if (!mbar_wait(&acc_empty[b], ((uint32_t)(i / L::kBufs) & 1u) ^ 1u, wc, kSiteAccEmpty) ||
             !mbar_wait(&full[s], (uint32_t)(i / L::kStages) & 1u, wc, kSiteFull))
@@ -609,62 +621,47 @@ __global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __gri
       while (!mbar_try(drain, 0) && global_timer_ns() - t0 < 1000000000ull) {
       }
     }
-  } else {
-    const int q = warp & 3;
-    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+  } else if (warp >= 4) {
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(eh * M);
     const float* sw = P.a.w_scale + (long long)nb * P.kblocks + kb0;
-    // Each warp keeps a block's factors sa sw, one per activation row, in shared memory; every
-    // thread needs all of them.  Lane l fetches rows l, l + 32, ... one block ahead.
-    float* factors = reinterpret_cast<float*>(smem + L::kStages * L::kStage + 256) + q * T;
-    constexpr int kMine = T < 32 ? 1 : T / 32;
-    const float* sa[kMine];
-    float mine[kMine];
-#pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-      sa[e] = P.a.a_scale + (long long)min(lane + 32 * e, P.a.rows - 1) * P.kblocks + kb0;
-      mine[e] = n > 0 ? __ldg(sa[e]) * __ldg(sw) : 0.f;
-    }
+    // Each warp keeps a block's factors sa sw, one per activation row of its own, in shared memory;
+    // every thread needs all of them.  Lane l fetches row l's one block ahead.
+    float* factors = reinterpret_cast<float*>(smem + L::kStages * L::kStage + 256) + (warp - 4) * M;
+    const float* sa = P.a.a_scale + (long long)min(eh * M + lane % M, P.a.rows - 1) * P.kblocks + kb0;
+    float mine = n > 0 ? __ldg(sa) * __ldg(sw) : 0.f;
     for (int i = 0; i < n; ++i) {
       const int b = i % L::kBufs;
-#pragma unroll
-      for (int e = 0; e < kMine; ++e)
-        if (lane + 32 * e < T) factors[lane + 32 * e] = mine[e];
+      if (lane < M) factors[lane] = mine;
       __syncwarp();
       const int next = min(i + 1, n - 1);
-      const float ws = __ldg(sw + next);
-#pragma unroll
-      for (int e = 0; e < kMine; ++e) mine[e] = __ldg(sa[e] + next) * ws;
+      mine = __ldg(sa + next) * __ldg(sw + next);
       bool ok = mbar_wait(&acc_full[b], (uint32_t)(i / L::kBufs) & 1u, wc, kSiteAccFull);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (warp == 2 && lane == 0) mbar_arrive(&empty[i % L::kStages]);
+      if (warp == 4 && lane == 0) mbar_arrive(&empty[i % L::kStages]);
       tc_fence_after();
+      uint32_t v[M];
+      if constexpr (M == 16) tmem_load16(trow + b * T, v);
+      else tmem_load32(trow + b * T, v);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
 #pragma unroll
-      for (int c = 0; c < T / 16; ++c) {
-        uint32_t v[16];
-        tmem_load16(trow + b * T + c * 16, v);
-        if (c + 1 == T / 16) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[b]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = c * 16 + 2 * e;
-          acc[r / 2] = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
-                                  *reinterpret_cast<const float2*>(factors + r), acc[r / 2]);
-        }
-      }
+      for (int e = 0; e < M / 2; ++e)
+        acc[e] = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                            *reinterpret_cast<const float2*>(factors + 2 * e), acc[e]);
       __syncwarp();
     }
   }
 
-  const int c = nb * 128 + (warp & 3) * 32 + lane;  // this folding thread's output column
+  const int c = nb * 128 + q * 32 + lane;  // this folding thread's output column
   if (S == 1) {
-    if (warp >= 2 && c < P.a.n) {
+    if (warp >= 4 && c < P.a.n) {
 #pragma unroll
-      for (int r = 0; r < T; ++r)
-        if (r < P.a.rows) P.a.out[(long long)r * P.a.ld_out + c] = __float2bfloat16(r & 1 ? acc[r / 2].y : acc[r / 2].x);
+      for (int e = 0; e < M; ++e) {
+        const int r = eh * M + e;
+        if (r < P.a.rows) P.a.out[(long long)r * P.a.ld_out + c] = __float2bfloat16(e & 1 ? acc[e / 2].y : acc[e / 2].x);
+      }
     }
     tc_fence_before();
     __syncthreads();
@@ -674,21 +671,23 @@ __global__ void __launch_bounds__(kFewThreads) linear_fp8_few_kernel(const __gri
     float* part = reinterpret_cast<float*>(smem);
     tc_fence_before();
     __syncthreads();
-    if (warp >= 2) {
+    if (warp >= 4) {
 #pragma unroll
-      for (int r = 0; r < T; ++r)
-        if (r < P.a.rows) part[r * 128 + (warp & 3) * 32 + lane] = r & 1 ? acc[r / 2].y : acc[r / 2].x;
+      for (int e = 0; e < M; ++e)
+        if (eh * M + e < P.a.rows) part[(eh * M + e) * 128 + q * 32 + lane] = e & 1 ? acc[e / 2].y : acc[e / 2].x;
     }
     cluster_sync_all();
-    if (warp >= 2 && c < P.a.n) {
-      for (int r = rank; r < P.a.rows; r += S) {
-        const uint32_t at = smem_u32(part + r * 128 + (warp & 3) * 32 + lane);
-        float v[8], sum = 0.f;
+    const int c4 = nb * 128 + lane * 4;
+    if (warp >= 4 && c4 < P.a.n) {  // a row per warp, four columns per thread (n is a multiple of 8)
+      for (int r = rank + (warp - 4) * S; r < P.a.rows; r += S * 4 * L::kFold) {
+        const uint32_t at = smem_u32(part + r * 128 + lane * 4);
+        float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k < S ? ld_cluster_f32(map_to_rank(at, k)) : 0.f;  // all on their way
+        for (int k = 0; k < 8; ++k) v[k] = k < S ? ld_cluster_f32x4(map_to_rank(at, k)) : sum;  // all on their way
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum += v[k];
-        P.a.out[(long long)r * P.a.ld_out + c] = __float2bfloat16(sum);
+        for (int k = 0; k < 8; ++k) sum.x += v[k].x, sum.y += v[k].y, sum.z += v[k].z, sum.w += v[k].w;
+        *reinterpret_cast<uint2*>(P.a.out + (long long)r * P.a.ld_out + c4) =
+            make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
       }
     }
     cluster_sync_all();  // no rank leaves while another reads its part
@@ -754,21 +753,57 @@ cudaError_t launch_wide(const LinearFp8Args& a, cudaStream_t s) {
   return cudaSuccess;
 }
 
+// Clusters of S CTAs, one CTA per SM, that the current device runs at once; it depends on which SMs
+// each of its processing clusters has.  Asked once per (device, S).
+int clusters_at_once(int S) {
+  static std::atomic<int> known[16 * 9];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::atomic<int>* slot = dev < 16 ? &known[dev * 9 + S] : nullptr;
+  int n = slot ? slot->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S);
+  cfg.blockDim = dim3(Few<64>::kThreads);
+  cfg.dynamicSmemBytes = Few<64>::kBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (raise_smem(linear_fp8_few_kernel<64>, Few<64>::kBytes, 3) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, linear_fp8_few_kernel<64>, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return sm_count() / S / 2;
+  }
+  if (slot) slot->store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Splits of the depth: as many as still run at once, of two blocks at least.  One too many for that
+// costs a second wave: 56 x 2288 x 4816 in 18 clusters of 8, where 15 fit, took 15.0 us, in 18 of 6 8.7.
+// With the pass that quantises: 1 x 4096 x 2560 5.6 us, 1 x 12288 x 4096 9.2 (5.5 TB/s of weights), 64 x
+// 4096 x 4096 8.9, 64 x 12288 x 4096 15.2, within 10 % of the best S at 60 sizes but for depths of 1024
+// (up to 1.7 us).
+template <int T>
+int few_splits(int n, int k) {
+  const int blocks = (n + 127) / 128, most = (k + 127) / 128 / 2;
+  int S = most < 8 ? most : 8;
+  while (S > 1 && blocks > Few<T>::kResident * clusters_at_once(S)) --S;
+  return S > 1 ? S : 1;
+}
+
 template <int T>
 cudaError_t launch_few(const LinearFp8Args& a, cudaStream_t s) {
   Params P;
   if (!encode(P, a, T, 128)) return cudaErrorInvalidValue;
   const cudaError_t e = raise_smem(linear_fp8_few_kernel<T>, Few<T>::kBytes, T == 16 ? 1 : T == 32 ? 2 : 3);
   if (e != cudaSuccess) return e;
-  // Split the depth while the CTAs still run at once (two per SM up to 32 rows) and keep two blocks
-  // each: 1 x 4096 x 2560 takes 4.9 us (2.1 TB/s of weights, launch and cluster set-up most of it),
-  // 1 x 12288 x 4096 8.7 us (5.8 TB/s).
-  const int blocks = (a.n + 127) / 128, room = kSMs * (T <= 32 ? 2 : 1);
-  int S = 1;
-  while (S < 8 && blocks * S * 2 <= room && P.kblocks >= S * 2) S *= 2;
+  const int S = few_splits<T>(a.n, a.k);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks * S));
-  cfg.blockDim = dim3(kFewThreads);
+  cfg.gridDim = dim3((unsigned)((a.n + 127) / 128 * S));
+  cfg.blockDim = dim3(Few<T>::kThreads);
   cfg.dynamicSmemBytes = Few<T>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
