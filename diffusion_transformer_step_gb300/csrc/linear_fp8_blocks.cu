@@ -194,8 +194,8 @@ struct Wide {
   static constexpr int kBufs = 512 / BN;  // accumulators in Tensor Memory
   // folding warps: one per 32 rows and 64 columns, so that accumulators leave room in the registers
   static constexpr int kWarps = BN / 16, kThreads = 128 + kWarps * 32;
-  // behind the ring: 2 KB per folding warp, 16 rows x 64 columns of output on their way to TMA stores
-  static constexpr uint32_t kOut = kStages * kStage, kBar = kOut + kWarps * 2048;
+  // behind the ring: 4 KB per folding warp, 32 rows x 64 columns of output on their way to a TMA store
+  static constexpr uint32_t kOut = kStages * kStage, kBar = kOut + kWarps * 4096;
   static constexpr size_t kBytes = 1024 + kBar + 256;
   static_assert(kStages % kIssuers == 0 && kBufs % kIssuers == 0, "see kIssuers");
 };
@@ -331,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     const bool releaser = warp == 4 && lane == 0;
     const uint32_t acc_empty0 = map_to_rank(smem_u32(&acc_empty[0]), 0);
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(eh * kCols);
-    uint8_t* staged = smem + L::kOut + (warp - 4) * 2048;
+    uint8_t* staged = smem + L::kOut + (warp - 4) * 4096;
     uint32_t stage = 0, buf = 0, buf_phase = 0;
     bool ok = true;
     for (int t = pair; t < P.items && ok; t += npairs) {
@@ -381,44 +381,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
         }
       }
       if (!ok) break;
-      // 16 rows at a time through this warp's staging rows (128-byte swizzle) to a TMA store, which
-      // clips rows and columns past the matrix: 64 columns of bf16, or 32 of a split's fp32.
+      // Through this warp's staging rows (128-byte swizzle) to a TMA store, which clips rows and columns
+      // past the matrix: 64 columns of bf16, or twice 32 of a split's fp32.
+      if (lane == 0) tma_store_wait_read();
+      __syncwarp();
       if (!kSplit) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (lane == 0) tma_store_wait_read();
-          __syncwarp();
-          if ((lane >> 4) == h) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2* f = acc + i * 4;
-              *reinterpret_cast<uint4*>(staged + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
-                  make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
-                             pack_bf16x2(f[3].x, f[3].y));
-            }
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0 && col < P.a.n && row + h * 16 < P.a.rows)
-            tma_store_3d(&P.out_map, staged, col, row + h * 16, 0);
+        for (int i = 0; i < 8; ++i) {
+          const float2* f = acc + i * 4;
+          *reinterpret_cast<uint4*>(staged + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                         pack_bf16x2(f[3].x, f[3].y));
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && col < P.a.n && row < P.a.rows) tma_store_3d(&P.out_map, staged, col, row, 0);
       } else {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          if (lane == 0) tma_store_wait_read();
-          __syncwarp();
-          if ((lane >> 4) == (h & 1)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2* f = acc + (h >> 1) * 16 + i * 2;
-              *reinterpret_cast<float4*>(staged + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
-                  make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-            }
-            fence_proxy_async_smem();
+        for (int h = 0; h < 2; ++h) {
+          if (h > 0) {
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2* f = acc + h * 16 + i * 2;
+            *reinterpret_cast<float4*>(staged + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+          }
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && col + (h >> 1) * 32 < P.a.n && row + (h & 1) * 16 < P.a.rows)
-            tma_store_3d(&P.out_map, staged, col + (h >> 1) * 32, row + (h & 1) * 16, it.split);
+          if (lane == 0 && col + h * 32 < P.a.n && row < P.a.rows)
+            tma_store_3d(&P.out_map, staged, col + h * 32, row, it.split);
         }
       }
     }
@@ -726,11 +720,11 @@ cudaError_t launch_wide(const LinearFp8Args& a, cudaStream_t s) {
   const uint64_t od[3] = {(uint64_t)a.n, (uint64_t)a.rows, (uint64_t)P.splits};
   if (P.splits > 1) {
     const uint64_t ost[2] = {(uint64_t)a.n * 4, (uint64_t)a.n * a.rows * 4};
-    const uint32_t obox[3] = {32, 16, 1};
+    const uint32_t obox[3] = {32, 32, 1};
     if (!encode_tmap_f32(&P.out_map, a.parts, 3, od, ost, obox)) return cudaErrorInvalidValue;
   } else {
     const uint64_t ost[2] = {(uint64_t)a.ld_out * 2, (uint64_t)a.ld_out * a.rows * 2};
-    const uint32_t obox[3] = {64, 16, 1};
+    const uint32_t obox[3] = {64, 32, 1};
     if (!encode_tmap_bf16(&P.out_map, a.out, 3, od, ost, obox)) return cudaErrorInvalidValue;
   }
   P.m_tiles = (a.rows + 255) / 256;
