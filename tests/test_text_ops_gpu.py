@@ -121,6 +121,56 @@ def test_qk_norm_rope(dit, ws, layout, rows, hq, hk, d, rot, norm):
         assert torch.equal(yd[:, :hq * d], qo[:, :hq * d])
 
 
+@pytest.mark.parametrize("layout,rows,hq,hk,d,rot,norm", [
+    ("half", 4099, 36, 8, 128, 128, True), ("interleaved", 10003, 33, 0, 64, 48, True), ("half", 4001, 40, 1, 128, 64, False),
+    ("interleaved", 5003, 17, 17, 128, 128, True), ("half", 7001, 40, 16, 64, 64, True), ("half", 4999, 33, 0, 128, 0, True)])
+def test_qk_norm_rope_many_rows(dit, ws, layout, rows, hq, hk, d, rot, norm):
+    """Enough rows to be streamed through shared memory: strided, in place, two rows without a table row."""
+    ld, heads = (hq + hk) * d + 24, hq + hk
+    x = _randn(rows, ld, seed=rows)
+    wq, wk = (_randn(d, seed=2, std=0.2) + 1, _randn(d, seed=3, std=0.2) + 1) if norm else (None, None)
+    top = 600
+    table = torch.from_numpy(R.rope_table(np.arange(top), rot=max(rot, 2), theta=1e4)).float()
+    index = torch.randint(0, top, (rows,), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    bad = [5, rows - 1] if rot else []
+    given = index.clone()
+    given[bad] = torch.tensor([top, -7][:len(bad)], dtype=torch.int32)
+    dv = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    lay = dit.DIT_ROPE_HALF if layout == "half" else dit.DIT_ROPE_INTERLEAVED
+    xd, td = x.to(DEV), dv(table) if rot else None
+    qo = torch.full((rows, hq * d + 8), 3.0, dtype=torch.bfloat16, device=DEV)
+    ko = torch.full((rows, hk * d + 16), 3.0, dtype=torch.bfloat16, device=DEV)
+    k = xd[:, hq * d:] if hk else None
+    norms = dv(wq), dv(wk) if hk else None
+    dit.dit_qk_norm_rope(rows, hq, hk, d, rot, lay, xd, ld, k, ld, *norms, 1e-6, td, top, dv(given), qo, hq * d + 8,
+                         ko if hk else None, hk * d + 16, ws, ws.numel())
+    st, where = dit.dit_sync_status(ws)
+    assert (st, where) == (dit.DIT_ERR_INVALID_ARG, 0x601) if bad else st == dit.DIT_OK
+    good = torch.ones(rows, dtype=torch.bool)
+    good[bad] = False
+    for part, out, w, h in ((x[:, :hq * d], qo, wq, hq), (x[:, hq * d:heads * d], ko, wk, hk)):
+        if h == 0:
+            continue
+        want, size = R.qk_norm_rope(part.reshape(rows, h, d), w, float(np.float32(1e-6)), table[index.long()], rot, layout)
+        tol = 2.0 ** -8 * want.abs() + 16 * 2.0 ** -24 * size + 1e-30  # as above
+        _within(out[:, :h * d].reshape(rows, h, d)[good.to(DEV)], want[good], tol[good])
+        assert (out[:, h * d:] == 3.0).all() and (out[(~good).to(DEV)] == 3.0).all()
+    yd = x.to(DEV)
+    dit.dit_qk_norm_rope(rows, hq, hk, d, rot, lay, yd, ld, yd[:, hq * d:] if hk else None, ld, *norms, 1e-6, td, top,
+                         dv(index), yd, ld, yd[:, hq * d:] if hk else None, ld, ws, ws.numel())
+    _ok(dit, ws)
+    g = good.to(DEV)
+    assert torch.equal(yd[g, :hq * d], qo[g, :hq * d]) and torch.equal(yd[g, hq * d:heads * d], ko[g, :hk * d])
+    assert torch.equal(yd[:, heads * d:].cpu(), x[:, heads * d:])
+    # a few rows alone, row by row, give the same bits
+    n = 9
+    few = torch.empty(n, hq * d, dtype=torch.bfloat16, device=DEV)
+    dit.dit_qk_norm_rope(n, hq, 0, d, rot, lay, xd, ld, None, 0, norms[0], None, 1e-6, td, top, dv(index), few, hq * d, None, 0,
+                         ws, ws.numel())
+    _ok(dit, ws)
+    assert torch.equal(few, yd[:n, :hq * d])
+
+
 def test_qk_norm_rope_zero_rows_of_x_and_nan(dit, ws):
     """A head of zeros stays zeros (eps keeps the root finite); a NaN stays in its own head."""
     x = _randn(3, 256, seed=1)
