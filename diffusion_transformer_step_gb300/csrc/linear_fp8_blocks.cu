@@ -749,10 +749,8 @@ cudaError_t launch_wide(const LinearFp8Args& a, cudaStream_t s) {
 
 // Clusters of S CTAs, one CTA per SM, that the current device runs at once; it depends on which SMs
 // each of its processing clusters has.  Asked once per (device, S).
-int clusters_at_once(int S) {
+int clusters_at_once(int dev, int S) {
   static std::atomic<int> known[16 * 9];
-  int dev = 0;
-  cudaGetDevice(&dev);
   std::atomic<int>* slot = dev < 16 ? &known[dev * 9 + S] : nullptr;
   int n = slot ? slot->load(std::memory_order_relaxed) : 0;
   if (n > 0) return n;
@@ -783,8 +781,9 @@ int clusters_at_once(int S) {
 template <int T>
 int few_splits(int n, int k) {
   const int blocks = (n + 127) / 128, most = (k + 127) / 128 / 2;
-  int S = most < 8 ? most : 8;
-  while (S > 1 && blocks > Few<T>::kResident * clusters_at_once(S)) --S;
+  int S = most < 8 ? most : 8, dev = 0;
+  cudaGetDevice(&dev);
+  while (S > 1 && blocks > Few<T>::kResident * clusters_at_once(dev, S)) --S;
   return S > 1 ? S : 1;
 }
 
