@@ -11,18 +11,18 @@
 //   linear_fp8_few_kernel    up to 64 rows, where reading the weights bounds the time: the weights'
 //                            rows take the MMA's 128-row side and the few activation rows its column
 //                            side, the depth split over a cluster whose CTAs add their parts
-//                            through distributed shared memory, in rank order.  (128 rows of
-//                            4096 x 4096: 17.8 us so, 10.8 as a wide tile.)
+//                            through distributed shared memory, in rank order.  (128 rows so: 16.9 us
+//                            at 8192 x 4096, as wide tiles 12.7.)
 //
-// The wide kernel reaches 2.43 PFLOP/s at 8192 x 12288 x 4096 (339 us) and 2.38 at 4096 x 4864 x 4096
-// (69 us), 0.6 of the e4m3 rate (twice the measured bf16 burst); without its fold the same ring
-// runs at 3.8.  A 128-column block takes ~546 cycles: the MMAs' operands and the loads take 437 of
-// them from shared memory at 128 bytes per cycle, and the fold's scale loads, one line per row, share that
-// path.  256-column tiles read 40 % less shared memory per product but leave two
-// accumulators, between which commit, fold, hand-back and issue (~1900 cycles) do not hide: 363 us.
-// Measured and left: 160 columns in three accumulators 356 us, one CTA per tile with the weights by
-// multicast 353, scales 16 blocks ahead through shared memory 390, scales of a block in one line 375
-// (and 68 at the smaller size).
+// With the pass that quantises its rows the wide kernel takes 361 us at 8192 x 12288 x 4096 (the product
+// 348, 2.37 PFLOP/s) and 79 at 4096 x 4864 x 4096 (73), 0.6 of the e4m3 rate (twice the measured bf16
+// burst).  Without its fold the same ring runs at 3.8 PFLOP/s.  A 128-column block takes ~546 cycles: the MMAs'
+// operands and the loads take 437 of them from shared memory at 128 bytes per cycle, and the fold's scale
+// loads, one line per row, share that path.  256-column tiles read 40 % less shared memory per product but leave two
+// accumulators, between which commit, fold, hand-back and issue (~1900 cycles) do not hide.  Measured
+// and left, products of zeros (which draw less power) where this form took 339 us: 256 columns 363, 160
+// columns in three accumulators 356, one CTA per tile with the weights by multicast 353, scales 16 blocks
+// ahead through shared memory 390, scales of a block in one line 375.
 #include <cuda_fp8.h>
 
 #include <atomic>
@@ -203,7 +203,7 @@ struct Wide {
 // Warp 0 loads, warps 1 and 2 issue (leader CTA) every second block of depth each, the others from
 // warp 4 fold and store, BN / 64 per row quarter with 64 columns each.  An issuing thread needs
 // ~500 cycles per block for its waits, MMAs and commit, more than the MMAs themselves: two of them take
-// 8192 x 12288 x 4096 from 506 to 346 us, sleeping instead of spinning folders to 339.  Per block there is one commit, on the accumulator; the
+// 8192 x 12288 x 4096 from 506 to 346 us (on zeros), sleeping instead of spinning folders to 339.  Per block there is one commit, on the accumulator; the
 // stage it frees is handed back by a folding thread of each CTA.
 template <bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
