@@ -5,7 +5,7 @@
 // token r / G and head r % G of the group (G = heads_q / heads_k), so a key tile is read once for
 // the whole group and a short sequence still fills its tile.  TQ = 128 / G tokens per tile; a work
 // item is two tiles (2 TQ tokens) of one key head.  Up to 16 rows per key head in all (single new
-// tokens) take text_attention_few_kernel, further down.
+// tokens), and small calls, take text_attention_few_kernel, further down.
 //
 // text_attention_kernel, one persistent CTA per SM, 352 threads, runs the two-tile pipeline of the
 // joint attention: warp 0 loads (Q through a 4-D tensor map whose box is G heads x TQ tokens), warp
@@ -966,20 +966,20 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
 
 // ---- few query rows ---------------------------------------------------------------------------
 
-// Up to 16 query rows per key head (new tokens, heads of the group among them): reading the keys and
-// values bounds the time, so what counts is bytes in flight, not the MMA rate.  One CTA per (run of
-// keys, key head, sequence), two per SM, each with three stages of 64 keys (64 * D * 4 bytes) on their
-// way by TMA; four warps take 16 keys of a stage each through mma.sync with their own running maximum
-// and sum and add up at the end, in order.  Runs of several CTAs are joined by a second kernel.  A
-// 128-row tcgen05 tile of mostly empty rows took 153 us where this takes 120 (48 tokens over 100 to
-// 8192 keys, 8 key heads of 128).
+// Tiles of 16 query rows of a key head (new tokens, heads of the group among them): with one tile reading
+// the keys and values bounds the time, so what counts is bytes in flight, not the MMA rate.  One CTA
+// per (run of keys, key head, sequence, tile), two per SM, each with three stages of 64 keys (64 * D * 4
+// bytes) on their way by TMA; four warps take 16 keys of a stage each through mma.sync with their own
+// running maximum and sum and add up at the end, in order.  Runs of several CTAs are joined by a second
+// kernel.  A 128-row tcgen05 tile of mostly empty rows took 153 us where this takes 116 (48 tokens over
+// 100 to 8192 keys, 8 key heads of 128).
+constexpr int kFewMost = 2 * kSMs * 16;  // rows per key head that one wave can hold
 constexpr int kFewRows = 16, kFewKeys = 64, kFewStages = 3, kFewThreads = 160;
 
 struct FewPlan {
-  int rows, chunk, splits;  // query rows per key head, keys per CTA, CTAs per sequence and head
+  int rows, tiles;    // query rows per key head, and tiles of 16 of them
+  int chunk, splits;  // keys per CTA, CTAs per sequence, head and tile
 };
-
-bool few_rows(const TextAttnArgs& a) { return (long long)a.max_q * (a.heads_q / a.heads_k) <= kFewRows; }
 
 // Runs of at most 1024 keys, so that ragged lengths even out over the CTAs, and of at least 256 (a
 // run costs ~3 us besides its keys), that cut the longest sequences' keys into two waves of CTAs; and
@@ -988,8 +988,10 @@ bool few_rows(const TextAttnArgs& a) { return (long long)a.max_q * (a.heads_q / 
 // heads) from 13.4 to 20.4.
 FewPlan few_plan(const TextAttnArgs& a) {
   FewPlan p;
-  p.rows = a.max_q * (a.heads_q / a.heads_k);
-  const long long items = (long long)a.seqs * a.heads_k;
+  const long long rows = (long long)a.max_q * (a.heads_q / a.heads_k);
+  p.rows = rows < kFewMost ? (int)rows : kFewMost;
+  p.tiles = (p.rows + kFewRows - 1) / kFewRows;
+  const long long items = (long long)a.seqs * a.heads_k * p.tiles;
   long long chunk = (long long)a.max_k * items / (4 * kSMs);
   if (chunk > 1024) chunk = 1024;
   const long long least = (long long)a.max_k * items / 16384;
@@ -999,6 +1001,18 @@ FewPlan few_plan(const TextAttnArgs& a) {
   p.splits = (a.max_k + p.chunk - 1) / p.chunk;
   if (p.splits < 1) p.splits = 1;
   return p;
+}
+
+// Up to 16 rows per key head always; more where all the CTAs run at once.  Then reading the keys again
+// for every 16 rows costs less than the tile kernel's longer way to its first score: 40 causal tokens
+// of 32 heads on 8 take 4.7 us against 7.9, 77 6.8 and 8.2, 8 single tokens of 32 heads on one over 4000
+// keys 11.9 and 16.5; past one wave it turns (256 tokens 13.9 and 9.8, 4 x 64 tokens 11.5 and 8.3).
+bool few_rows(const TextAttnArgs& a) {
+  const long long rows = (long long)a.max_q * (a.heads_q / a.heads_k);
+  if (rows <= kFewRows) return true;
+  if (rows > kFewMost) return false;
+  const FewPlan p = few_plan(a);
+  return (long long)a.seqs * a.heads_k * p.tiles * p.splits <= 2 * kSMs;
 }
 
 Parts few_parts(const FewPlan& p, const TextAttnArgs& a) {
@@ -1013,7 +1027,7 @@ Parts few_parts(const FewPlan& p, const TextAttnArgs& a) {
 struct alignas(64) FewParams {
   CUtensorMap k_map, v_map;
   TextAttnArgs a;
-  int group, rows, chunk, splits;
+  int group, rows, tiles, chunk, splits;
   float scale_log2;
   float2* ml;
   float* o;
@@ -1041,6 +1055,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Keys that the tile of query rows [base, base + 16) of a sequence sees: those of its last row.
+__device__ __forceinline__ int few_keys(const TextAttnArgs& a, const Span& sp, int G, int base) {
+  if (!a.causal) return sp.nk;
+  return min(sp.nk, max(0, min(base + kFewRows, sp.nq * G) - 1) / G + sp.nk - sp.nq + 1);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(const __grid_constant__ FewParams P) {
   constexpr uint32_t kHalf = kFewKeys * 128;            // 64 keys x 64 dims
@@ -1053,8 +1073,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
   __shared__ int abort_flag;
   const TextAttnArgs& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = P.group;
-  const int split = blockIdx.x % P.splits, hk = (blockIdx.x / P.splits) % a.heads_k;
-  const int seq = blockIdx.x / P.splits / a.heads_k;
+  // the tiles of the same keys run side by side
+  const int run = blockIdx.x / P.tiles, base = (blockIdx.x - run * P.tiles) * kFewRows;
+  const int split = run % P.splits, hk = (run / P.splits) % a.heads_k;
+  const int seq = run / P.splits / a.heads_k;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kFewStages; ++i) {
       mbar_init(&full[i], 1);
@@ -1068,13 +1090,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
   allow_dependents();
   const Span sp = load_span(a, seq);
   if (!sp.ok) {
-    if (split == 0 && hk == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteTextLengths);
+    if (split == 0 && hk == 0 && base == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteTextLengths);
     return;
   }
-  const int rows = sp.nq * G;
-  const int first = split * P.chunk, last = min(sp.nk, first + P.chunk);  // this CTA's keys
-  const bool direct = sp.nk <= P.chunk;                                   // ... are all of them
-  if (rows == 0 || (first >= last && split > 0)) return;
+  const int rows = min(kFewRows, sp.nq * G - base);  // this CTA's query rows
+  if (rows <= 0) return;
+  // this CTA's keys, none behind the last that its rows see
+  const int first = split * P.chunk, last = min(few_keys(a, sp, G, base), first + P.chunk);
+  const bool direct = sp.nk <= P.chunk;  // it has all the keys of its rows
+  if (first >= last && split > 0) return;
   const int blocks = first < last ? (last - first + kFewKeys - 1) / kFewKeys : 0;
   const WaitCtx wc{a.status, &abort_flag, kWaitLimitNs};
 
@@ -1116,8 +1140,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
     int limit[2];  // keys that the lane's rows see
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 8 * i, token = r / G;
-      const bool ok = r < rows;
+      const int r = base + r0 + 8 * i, token = r / G;
+      const bool ok = r0 + 8 * i < rows;
       const bf16* src = a.q + (long long)(sp.q0 + (ok ? token : 0)) * a.ldq + (hk * G + (ok ? r - token * G : 0)) * D + c0;
       limit[i] = !ok ? 0 : (a.causal ? min(sp.nk, token + sp.nk - sp.nq + 1) : sp.nk);
 #pragma unroll
@@ -1241,7 +1265,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
 #pragma unroll
       for (int e = 0; e < V; ++e) out[e] += f * parts[(w * kFewRows + r) * D + lane * V + e];
     }
-    const int token = r / G, g = r - token * G;
+    const int token = (base + r) / G, g = base + r - token * G;
     float zero = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) zero = fmaf(out[e], 0.f, zero);
@@ -1266,7 +1290,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
       for (int e = 0; e < V; e += 2)
         *reinterpret_cast<uint32_t*>(dst + e) = lr == 0.f ? 0u : pack_bf16x2(out[e] * inv, out[e + 1] * inv);
     } else {
-      const long long at = (long long)blockIdx.x * P.rows + r;
+      const long long at = (long long)run * P.rows + base + r;
       if (lane == 0) P.ml[at] = make_float2(mr, lr);
 #pragma unroll
       for (int e = 0; e < V; e += 2)
@@ -1287,8 +1311,8 @@ __global__ void __launch_bounds__(128) text_attention_few_join_kernel(const __gr
   const Span sp = load_span(a, seq);
   if (!sp.ok || sp.nk <= P.chunk || r >= sp.nq * G) return;
   const long long at = (long long)blockIdx.x * P.splits * P.rows + r;
-  const int token = r / G;
-  join_row<D>(P.ml + at, P.o + at * D, P.rows, (sp.nk + P.chunk - 1) / P.chunk, threadIdx.x & 31,
+  const int token = r / G, runs = (few_keys(a, sp, G, r / kFewRows * kFewRows) + P.chunk - 1) / P.chunk;
+  join_row<D>(P.ml + at, P.o + at * D, P.rows, max(1, runs), threadIdx.x & 31,
               a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + r - token * G) * D);
 }
 
@@ -1310,6 +1334,7 @@ cudaError_t launch_few(const TextAttnArgs& a, cudaStream_t s) {
   P.a = a;
   P.group = a.heads_q / a.heads_k;
   P.rows = p.rows;
+  P.tiles = p.tiles;
   P.chunk = p.chunk;
   P.splits = p.splits;
   P.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
@@ -1325,7 +1350,7 @@ cudaError_t launch_few(const TextAttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 16) g_few_attr_set[slot].store(true, std::memory_order_release);
   }
-  const long long grid = (long long)a.seqs * a.heads_k * p.splits;
+  const long long grid = (long long)a.seqs * a.heads_k * p.splits * p.tiles;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   {
     LaunchScope scope(kClsTextAttention, s);

@@ -414,6 +414,56 @@ def test_text_attention_bad_value_reaches_only_queries_that_see_it(dit, ws, ql, 
     assert got[blind:][..., keep].isfinite().all()
 
 
+# Calls of more than 304 tiles of 16 query rows (heads of a group among them) are worked on in tiles
+# of 128 rows, smaller ones 16 rows at a time: the next tests hold what the ones above hold on either side.
+@pytest.mark.parametrize("hq,hk,d", [(32, 8, 128), (12, 12, 64), (40, 8, 128), (64, 16, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_text_attention_many_tiles(dit, ws, hq, hk, d, causal):
+    """Odd lengths, sequences without queries or keys, more queries than keys, gaps of NaN between."""
+    ql = [129, 1, 0, 64, 300, 65, 7, 250]
+    kl = [129, 200, 5, 0, 300, 30, 129, 511]
+    _check_attention(*_attend(dit, ws, ql, kl, hq, hk, d, causal, gap_q=3, gap_k=2, fill=math.nan))
+    _check_attention(*_attend(dit, ws, ql, kl, hq, hk, d, causal, lens=False, ld_extra=8))
+
+
+@pytest.mark.parametrize("seqs,n,hq,hk,d,causal", [
+    (1, 17, 4, 1, 128, True), (1, 100, 32, 32, 64, False), (1, 77, 32, 8, 128, True), (3, 300, 2, 1, 64, True), (2, 40, 8, 2, 128, False),
+    (1, 1200, 2, 2, 64, True), (70, 5, 8, 2, 64, True)])
+def test_text_attention_small_prompts(dit, ws, seqs, n, hq, hk, d, causal):
+    """Prompts of a few tiles of 16 rows, ragged, and their last parts over a cache."""
+    kl = [max(1, n - 3 * i) for i in range(seqs)]
+    _check_attention(*_attend(dit, ws, kl, kl, hq, hk, d, causal, lens=False))
+    _check_attention(*_attend(dit, ws, [max(1, x // 2) for x in kl], kl, hq, hk, d, causal, gap_q=1, gap_k=3, fill=math.inf))
+    _check_attention(*_attend(dit, ws, kl, [x // 2 for x in kl], hq, hk, d, causal))  # rows that see nothing
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("nk", [300, 129, 1000])
+def test_text_attention_bad_value_in_a_tile(dit, ws, nk, bad):
+    """As below and above, with enough heads for tiles of 128 rows: the queries that do not see the bad
+    value keep their results, and so do the other heads."""
+    at, hq, hk = nk - 40, 32, 8
+    def edit(q, k, v, spans):
+        v[at, 3, 5] = bad
+    got, want, size, qk = _attend(dit, ws, [nk], [nk], hq, hk, 128, True, edit=edit)
+    clean = R.attention(qk[0], qk[1], _randn(nk, hk, 128, seed=2), [(0, nk, 0, nk)], True, qk[2])
+    mine = [h for h in range(hq) if h // 4 == 3]
+    other = [h for h in range(hq) if h // 4 != 3]
+    keep = [c for c in range(128) if c != 5]
+    _check_attention(got[:at], clean[0][:at], clean[1][:at], qk)
+    assert got[:, other].isfinite().all() and got[at:, mine][..., keep].isfinite().all()
+    assert not got[at:, mine][..., 5].isfinite().any()
+
+
+def test_text_attention_bad_key_in_a_tile(dit, ws):
+    def edit(q, k, v, spans):
+        k[250, 2, 7] = math.nan
+    got, want, size, qk = _attend(dit, ws, [300], [300], 32, 8, 128, True, edit=edit)
+    mine = [h for h in range(32) if h // 4 == 2]
+    assert got[:250].isfinite().all() and got[250:, mine].isnan().all()
+    assert got[:, [h for h in range(32) if h not in mine]].isfinite().all()
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("nk", [4, 300, 1000, 3000])
 def test_text_attention_bad_value_between_few_queries(dit, ws, nk, bad):
