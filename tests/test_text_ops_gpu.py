@@ -541,6 +541,48 @@ def test_text_attention_bad_lengths_are_reported_and_skipped(dit, ws):
         assert (out[10:] == 5.0).all() and (out[:10] != 5.0).any()  # the good sequence is done, nothing else written
 
 
+def test_text_attention_far_rows_in_tiles(dit, ws):
+    """Far key rows as above, with enough heads for tiles of 128 rows."""
+    hq, hk, d = 32, 8, 64
+    ld, rows = 1 << 12, (1 << 20) + 300
+    k = torch.zeros(rows, ld, dtype=torch.bfloat16, device=DEV)
+    nk, nq = 300, 200
+    kk, vv, q = _randn(nk, hk, d, seed=1), _randn(nk, hk, d, seed=2), _randn(nq, hq, d, seed=3)
+    k[rows - nk:, :hk * d] = kk.flatten(1).to(DEV)
+    k[rows - nk:, hk * d:2 * hk * d] = vv.flatten(1).to(DEV)
+    out = torch.zeros(nq, hq * d, dtype=torch.bfloat16, device=DEV)
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device=DEV)  # noqa: E731
+    want, size, _ = R.attention(q, kk, vv, [(0, nq, 0, nk)], True, d ** -0.5)
+    a = dit.make_text_attn(1, hq, hk, d, nq, rows, nq, nk, causal=True)
+    dit.dit_text_attention(a, i32([0, nq]), None, i32([rows - nk, rows]), None, q.flatten(1).to(DEV), hq * d, k, ld,
+                           k[:, hk * d:], ld, out, hq * d, ws, ws.numel())
+    _ok(dit, ws)
+    _check_attention(out.reshape(nq, hq, d).cpu(), want, size, (q, kk, d ** -0.5))
+
+
+@pytest.mark.parametrize("seqs", [2, 66])
+def test_text_attention_bad_lengths_in_tiles(dit, ws, seqs):
+    """Bad entries as above, with enough heads for tiles of 128 rows, and so many sequences that the
+    tiles are listed first."""
+    hq, hk, d = 128, 64, 64
+    q, k = _randn(20 * seqs, hq * d).to(DEV), _randn(30 * seqs, hk * d).to(DEV)
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device=DEV)  # noqa: E731
+    good = ([20 * i for i in range(seqs + 1)], [10] + [20] * (seqs - 1), [30 * i for i in range(seqs + 1)], [30] * seqs)
+    for which, value in ((0, -1), (0, 20 * seqs), (1, -1), (1, 21), (2, 30 * seqs - 29), (3, 31), (3, -2)):
+        arr = [list(x) for x in good]
+        arr[which][seqs - 1] = value
+        out = torch.full((20 * seqs, hq * d), 5.0, dtype=torch.bfloat16, device=DEV)
+        a = dit.make_text_attn(seqs, hq, hk, d, 20 * seqs, 30 * seqs, 20, 30, causal=False)
+        need = dit.dit_text_attention_workspace(a)
+        qo, ql, ko, kl = map(i32, arr)
+        dit.dit_text_attention(a, qo, ql, ko, kl, q, hq * d, k, hk * d, k, hk * d, out, hq * d, ws, need)
+        st, where = dit.dit_sync_status(ws)
+        assert st == dit.DIT_ERR_INVALID_ARG and where == 0x501, (which, value, st, hex(where))
+        last = 20 * (seqs - 1)
+        assert (out[last:] == 5.0).all() and (out[:10] != 5.0).any()  # the bad sequence is left, the others done
+        assert (out[10:20] == 5.0).all() and (seqs == 2 or (out[20:last] != 5.0).any(1).all())
+
+
 # ------------------------------------------------------------------------------ block-scaled e4m3
 @pytest.mark.parametrize("block_rows", [1, 128])
 @pytest.mark.parametrize("rows,cols", [(1, 16), (5, 128), (127, 144), (129, 400), (300, 4096), (128, 2560), (1000, 1008)])
