@@ -1000,6 +1000,7 @@ FewPlan few_plan(const TextAttnArgs& a) {
   if (chunk > 1024) chunk = 1024;
   const long long least = (long long)a.max_k * items / 16384;
   if (chunk < least) chunk = least;
+  if (chunk > a.max_k) chunk = a.max_k;  // `least` passes 32 bits where many sequences may be long
   if (chunk < 256) chunk = 256;
   p.chunk = (int)((chunk + kFewKeys - 1) / kFewKeys * kFewKeys);
   p.splits = (a.max_k + p.chunk - 1) / p.chunk;
@@ -1015,6 +1016,7 @@ bool few_rows(const TextAttnArgs& a) {
   const long long rows = (long long)a.max_q * (a.heads_q / a.heads_k);
   if (rows <= kFewRows) return true;
   if (rows > kFewMost) return false;
+  if ((long long)a.seqs * a.heads_k * ((rows + kFewRows - 1) / kFewRows) > 2 * kSMs) return false;
   const FewPlan p = few_plan(a);
   return (long long)a.seqs * a.heads_k * p.tiles * p.splits <= 2 * kSMs;
 }
