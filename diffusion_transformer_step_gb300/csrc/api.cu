@@ -888,15 +888,15 @@ dit_status dit_sync_status(void* ws, dit_stream_t stream, uint32_t* where_out) {
   if (!aligned16(ws)) return DIT_ERR_INVALID_ARG;
   const cudaStream_t st = (cudaStream_t)stream;
   DeviceStatus h;
-  DIT_CUDA(cudaMemcpyAsync(&h, ws, 8, cudaMemcpyDeviceToHost, st));
+  DIT_CUDA(cudaMemcpyAsync(&h, ws, kStatusBytes, cudaMemcpyDeviceToHost, st));
   DIT_CUDA(cudaStreamSynchronize(st));
   if (where_out) *where_out = h.where;
-  if (h.word != 0) {
-    DIT_CUDA(cudaMemsetAsync(ws, 0, 8, st));
+  if (h.word != 0 || h.where != 0 || h.next_item != 0 || h.items_done != 0) {
+    DIT_CUDA(cudaMemsetAsync(ws, 0, kStatusBytes, st));
     DIT_CUDA(cudaStreamSynchronize(st));
-    return (h.word & ~(uint32_t)kStatusBadEntry) ? DIT_ERR_TIMEOUT : DIT_ERR_INVALID_ARG;
   }
-  return DIT_OK;
+  if (h.word == 0) return DIT_OK;
+  return (h.word & ~(uint32_t)kStatusBadEntry) ? DIT_ERR_TIMEOUT : DIT_ERR_INVALID_ARG;
 }
 
 dit_status dit_selftest_wait_timeout(void* ws, size_t ws_bytes, unsigned int limit_us, dit_stream_t stream) {

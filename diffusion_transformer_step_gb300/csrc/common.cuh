@@ -29,6 +29,7 @@ struct DeviceStatus {
   uint32_t items_done;
   uint32_t pad[60];
 };
+constexpr size_t kStatusBytes = 16;  // the fields in use, read and cleared by dit_sync_status()
 
 // ---------------------------------------------------------------------------------
 // Small utilities

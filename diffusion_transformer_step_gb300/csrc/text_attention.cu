@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
         if (lane == 0) id = (int)(gridDim.x + atomicAdd(&a.status->next_item, 1u));
         id = __shfl_sync(0xffffffffu, id, 0);
       }
-      const bool stop = id >= P.items;
+      const bool stop = (uint32_t)id >= (uint32_t)P.items;  // a counter that was not zero wraps to no item
       Span sp{0, -1, 0, 0, true};
       int index = 0, hk = 0, split = 0, rank = 0;
       bool found = false;

@@ -275,7 +275,9 @@ dit_status dit_step_host(const dit_weights* w, const dit_shape* shape, const voi
                          const float* sigma_host, void* velocity_host, void* ws, size_t ws_bytes,
                          dit_stream_t stream);
 
-/* Synchronise `stream`, read and clear the workspace's device status word.  Returns
+/* Synchronise `stream`, read and clear the workspace's device status word, and zero the work
+ * counters beside it (a workspace whose first 256 bytes were not zeroed, or on which two calls
+ * overlapped, is usable again).  Returns
  * DIT_ERR_TIMEOUT if a kernel gave up on a wait since the last call, else
  * DIT_ERR_INVALID_ARG if a kernel met a length, start or position out of range in a device
  * array (text-side operations), else DIT_OK (or DIT_ERR_CUDA if the stream reports an
@@ -437,7 +439,8 @@ typedef struct {
 } dit_text_attn;
 
 /* Bytes of workspace that dit_text_attention needs for these sizes (at least the 256 of the
- * status word; more where the keys of few rows are split over the GPU). */
+ * status word and the work counters, which must be zeroed once before the first use as for
+ * dit_workspace_size; more where the keys of few rows are split over the GPU). */
 dit_status dit_text_attention_workspace(const dit_text_attn* a, size_t* bytes);
 
 /* Attention with grouped heads over packed or padded sequences.  Sequence s has the query
