@@ -894,7 +894,9 @@ __global__ void __launch_bounds__(256) text_attention_join_kernel(const __grid_c
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int hk = blockIdx.x % P.a.heads_k, G = P.group;
   const int2 d = P.desc[blockIdx.x / P.a.heads_k];
-  if (r >= d.y * G) return;
+  // A call that gave up on a wait may leave rows of the list as they were: whatever they hold, stay in
+  // the output.
+  if (d.x < 0 || d.y < 0 || d.y > 2 * P.tq || d.x > P.a.rows_q - d.y || r >= d.y * G) return;
   const long long at = (long long)blockIdx.x * P.splits * 256 + r;
   const int token = r / G;
   join_row<D>(P.ml + at, P.o + at * D, 256, P.splits, threadIdx.x & 31,
