@@ -19,9 +19,12 @@
 //   - Keys past the sequence's end are other sequences' or unwritten memory.  Their scores are
 //     replaced, not added to; their V rows, which a zero probability would not silence if they
 //     hold NaN, are zeroed in shared memory before the last block's MMA.
-//   - V rows that a causal row must not see but its tile needs can hold NaN as well.  A row whose
-//     output is not finite looks at the (under 256) keys behind its limit that its tile took in,
-//     and if one of them is to blame computes itself again, alone.
+//   - V rows that a causal row must not see but its tile needs can hold NaN as well.  Rows that come out
+//     not finite are noted down; when its CTA is through with its items, or with room for notes, each
+//     softmax warp looks at the (under 256) keys behind its rows' limits that the tile took in, and
+//     where one of them is to blame works the rows out again, sixteen at a time (repair_rows).  One NaN
+//     near the end of 8192 tokens costs 2.0 ms so; one row at a time, within the item while the other
+//     roles waited, it cost 123 ms and from some 130 thousand tokens on more than a wait may take.
 //   - Work order.  Items come longest first over all sequences (index within the sequence,
 //     descending) from a counter, so the last ones are short.  For up to 64 sequences warp 10 finds
 //     an item itself: with n_s items in sequence s, C(v) = sum max(0, n_s - v) items have an index
@@ -157,8 +160,17 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* s
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void mbar_inval(uint64_t* bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // Every store of this thread has been read out of shared memory.
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Records (work item, rows) of rows that came out not finite: how many a softmax warp can hold, and with
+// how many of them its CTA takes no further items for now (two may be on their way when warp 10 looks).
+constexpr int kOddMost = 24, kOddFull = kOddMost - 3;
+constexpr int kBars = 17;  // mbarriers
+enum : int { kRepair = 1, kAgain = 2 };  // after a pass over work items: rows to repair; more items
 
 template <int D>
 struct Smem {
@@ -166,7 +178,8 @@ struct Smem {
   static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile;
   static constexpr uint32_t kOut = 6 * kTile;            // 32 rows x 64 dims of output per softmax warp
   static constexpr uint32_t kBar = kOut + 8 * 4096;
-  static constexpr size_t kBytes = 1024 + kBar + 384;
+  static constexpr uint32_t kOdd = kBar + 288;           // kOddMost records of each softmax warp
+  static constexpr size_t kBytes = 1024 + kOdd + 8 * kOddMost * sizeof(uint2);
 };
 
 // One work item of a CTA, as warp 10 found it.
@@ -328,86 +341,325 @@ __device__ __forceinline__ bool mma_block(const Descs<D>& d, uint32_t tmem, int 
   return true;
 }
 
-// One row alone, by a whole warp: keys [j0, j1) of the sequence.  Lane l holds dims
-// [l D/32, (l + 1) D/32).  m in log2 units.
+// ---- rows that met a value they do not see ------------------------------------------------
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// D += A B, 16 x 8 x 16, bf16 in, fp32 out.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A head of V: whether a value of it is infinite or NaN, and whether all are NaN.
 template <int D>
-__device__ __noinline__ void attend_row(const TextAttnArgs& a, const bf16* qp, const bf16* kp, const bf16* vp, int n,
-                                        float c, int lane, float& m, float& l, float (&o)[D / 32]) {
-  constexpr int V = D / 32;
-  float q[V];
+__device__ __forceinline__ void scan_values(const bf16* v, bool& bad, bool& all_nan) {
+  bad = false;
+  all_nan = true;
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 u = *reinterpret_cast<const uint4*>(v + i * 8);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    q[e] = __bfloat162float(qp[lane * V + e]);
-    o[e] = 0.f;
-  }
-  m = -INFINITY;
-  l = 0.f;
-  for (int j = 0; j < n; ++j) {
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) x += q[e] * __bfloat162float(kp[(long long)j * a.ldk + lane * V + e]);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    x *= c;
-    const float mn = fmaxf(m, x);
-    const float mr = mn == -INFINITY ? 0.f : mn;
-    const float al = ex2_approx(m - mr), p = ex2_approx(x - mr);
-    m = mn;
-    l = l * al + p;
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = o[e] * al + p * __bfloat162float(vp[(long long)j * a.ldv + lane * V + e]);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
+      bad |= lo >= 0x7f80u || hi >= 0x7f80u;
+      all_nan &= lo > 0x7f80u && hi > 0x7f80u;
+    }
   }
 }
 
-template <int D, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __grid_constant__ TextAttnParams P) {
-  using L = Smem<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  const Bars bar{bars + 0, bars + 1, bars + 3, bars + 5, bars + 7, bars + 9, bars + 11, bars + 12, bars + 13, bars + 15};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Item* items = reinterpret_cast<Item*>(bars + 18);  // two: the current one and the next
+// Of the rows (one per lane, those in `rows`) whose sums came out not finite, those that may owe it to a
+// key they do not see: lane's row sees the keys below `seen`, its tile took in those of [first, end).  Rows
+// whose last visible key is NaN throughout are so by right.
+template <int D>
+__device__ __noinline__ uint32_t spoiled_rows(const bf16* vp, long long ldv, uint32_t rows, int seen, int first, int end,
+                                              int lane) {
+  const bool mine = (rows >> lane) & 1u;
+  const int lo = __reduce_min_sync(0xffffffffu, mine ? max(seen, first) : end);
+  int last = -1;  // the last key with a bad value
+  for (int top = end; top > lo && last < 0; top -= 32) {
+    const int j = top - 1 - lane;
+    bool bad = false, all_nan;
+    if (j >= lo) scan_values<D>(vp + j * ldv, bad, all_nan);
+    const uint32_t b = __ballot_sync(0xffffffffu, bad);
+    if (b) last = top - __ffs(b);
+  }
+  bool redo = mine && seen <= last;
+  if (redo && seen > first) {
+    bool bad, all_nan;
+    scan_values<D>(vp + (seen - 1) * ldv, bad, all_nan);
+    redo = !all_nan;
+  }
+  return __ballot_sync(0xffffffffu, redo);
+}
 
-  const TextAttnArgs& a = P.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = P.group, TQ = P.tq, TP = 2 * TQ;
-
-  if (threadIdx.x == 32) {
-    mbar_init(bar.q_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.ready[i], 1);
-      mbar_init(&bar.slot_free[i], 1);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4);
-      mbar_init(&bar.o_done[i], 1);
-      mbar_init(&bar.item_full[i], 1);
-      mbar_init(&bar.item_free[i], 10);  // the loader, the issuer and eight softmax warps
+// Up to 16 rows of a key head by one warp, apart from the tiles.  Lane r < 16 brings row r: its query, the
+// keys it sees (0: no row) and where it goes: the normalised output row, or a part's unnormalised one and
+// its (max, sum).  16 keys a step through mma.sync, V by way of `stage` (16 x D bf16 of this warp's shared
+// memory); in the last steps, where some rows see fewer keys than others, P V is done by plain FMAs, in which
+// a key that a row does not see is left out and not multiplied by zero.  m in log2 units.
+// Bound by the latency of a step's loads.
+template <int D, bool kParts>
+__device__ __noinline__ void attend_rows(const TextAttnArgs& a, const bf16* qp, const bf16* kp, const bf16* vp, int limit,
+                                         float c, int lane, void* dst, float2* ml, uint8_t* stage) {
+  const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // fragments: rows r0 and r0 + 8, columns c0 + {0, 1}
+  const int most = __reduce_max_sync(0xffffffffu, limit);
+  const int least = __reduce_min_sync(0xffffffffu, limit > 0 ? limit : most);
+  uint32_t q[D / 16][4];
+  int lim[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    lim[i] = __shfl_sync(0xffffffffu, limit, r0 + 8 * i);
+    const bf16* src = reinterpret_cast<const bf16*>(
+                          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(qp), r0 + 8 * i)) + c0;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      q[k][i] = lim[i] > 0 ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+      q[k][i + 2] = lim[i] > 0 ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
     }
-    mbar_init(bar.fixed, 1);
-    mbar_init(bar.drain, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
   }
-  if (warp == 2 && lane == 0) {
-    tma_prefetch_desc(&P.q_map);
-    tma_prefetch_desc(&P.k_map);
-    tma_prefetch_desc(&P.v_map);
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+  for (int j = 0; j < most; j += 16) {
+    // V rows in 16-byte pieces (swizzled), on their way while the scores are worked out
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const int piece = i * 32 + lane, row = piece / (D / 8), col = piece % (D / 8);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage + row * D * 2 + ((col ^ (row & 7)) << 4))),
+                   "l"(vp + min(j + row, most - 1) * a.ldv + col * 8)
+                   : "memory");
+    }
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    uint32_t kb[2][D / 8];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const bf16* key = kp + min(j + n * 8 + r0, most - 1) * a.ldk + c0;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) kb[n][k] = *reinterpret_cast<const uint32_t*>(key + k * 8);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) mma_bf16(s[n], q[k], kb[n][2 * k], kb[n][2 * k + 1]);
+    float p[2][4], alpha[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[i][e] = j + (e >> 1) * 8 + c0 + (e & 1) < lim[i] ? s[e >> 1][2 * i + (e & 1)] * c : -INFINITY;
+        mx = fmaxf(mx, p[i][e]);
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
+      alpha[i] = m[i] == mn ? 1.f : ex2_approx(m[i] - ref);
+      m[i] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += p[i][e] = ex2_approx(p[i][e] - ref);
+      l[i] = l[i] * alpha[i] + sum;
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d) o[d][0] *= alpha[0], o[d][1] *= alpha[0], o[d][2] *= alpha[1], o[d][3] *= alpha[1];
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (j + 16 <= least) {
+      const uint32_t pf[4] = {pack_bf16x2(p[0][0], p[0][1]), pack_bf16x2(p[1][0], p[1][1]), pack_bf16x2(p[0][2], p[0][3]),
+                              pack_bf16x2(p[1][2], p[1][3])};
+      const int vk = lane & 15, vc = lane >> 4;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t b[4];
+        ldmatrix4_trans(b, smem_u32(stage + vk * D * 2 + (((d * 2 + vc) ^ (vk & 7)) << 4)));
+        mma_bf16(o[2 * d], pf, b[0], b[1]);
+        mma_bf16(o[2 * d + 1], pf, b[2], b[3]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll 1
+        for (int t = 0; t < 4; ++t) {  // a key of the step, whose probabilities lane t of the four holds
+          const int row = (e >> 1) * 8 + t * 2 + (e & 1);
+          const float p0 = __shfl_sync(0xffffffffu, p[0][e], (lane & 28) + t);
+          const float p1 = __shfl_sync(0xffffffffu, p[1][e], (lane & 28) + t);
+          const bool see0 = j + row < lim[0], see1 = j + row < lim[1];
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            const uint8_t* v = stage + row * D * 2 + ((d ^ (row & 7)) << 4) + c0 * 2;
+            const float2 x = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(v));
+            if (see0) o[d][0] = fmaf(p0, x.x, o[d][0]), o[d][1] = fmaf(p0, x.y, o[d][1]);
+            if (see1) o[d][2] = fmaf(p1, x.x, o[d][2]), o[d][3] = fmaf(p1, x.y, o[d][3]);
+          }
+        }
+    }
+    __syncwarp();  // V has been read
   }
-  __syncwarp();
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    const unsigned long long to = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r0 + 8 * i);
+    const unsigned long long at = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(ml), r0 + 8 * i);
+    if (lim[i] <= 0) continue;
+    const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) {
+      if (kParts)
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(to) + d * 8 + c0) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+      else
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<bf16*>(to) + d * 8 + c0) =
+            l[i] == 0.f ? 0u : pack_bf16x2(o[d][2 * i] * inv, o[d][2 * i + 1] * inv);
+    }
+    if (kParts && (lane & 3) == 0) *reinterpret_cast<float2*>(at) = make_float2(m[i], l[i]);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const WaitCtx wc{a.status, abort_flag, kWaitLimitNs};
-  grid_dependency_wait();  // lengths, Q, K, V and the output belong to earlier kernels of the stream
-  allow_dependents();
+}
 
+// Work item `id`: its place, and where its sequence has tiles, its rows and key blocks (whole warp).
+template <bool kSplit>
+__device__ __forceinline__ bool locate_item(const TextAttnParams& P, int id, int lane, bool report, Item& it) {
+  const TextAttnArgs& a = P.a;
+  const int TP = 2 * P.tq;
+  int index = 0, rank = id / a.heads_k, split = 0;
+  const int hk = id - rank * a.heads_k;
+  if (kSplit) {
+    split = rank % P.splits;
+    rank /= P.splits;
+  }
+  Span sp{0, -1, 0, 0, true};
+  bool found;
+  if (P.list) {
+    const int2 e = P.list[rank];
+    found = e.x >= 0;
+    if (found) sp = load_span(a, e.x);
+    index = e.y;
+  } else {
+    found = find_tile(a, TP, P.levels, P.tiles, rank, lane, report, sp, index);
+  }
+  it = Item{sp.q0, sp.nq, sp.k0, sp.nk, index * TP, 0, 0, 0, hk, split, rank, 0};
+  if (found) {
+    // key blocks of each tile, and this split's run [b0, b0 + n) of them
+    const int shift = it.nk - it.nq;
+    auto blocks = [&](int first) {
+      if (first >= it.nq) return 0;
+      const int last = min(first + P.tq, it.nq) - 1;
+      const int end = a.causal ? min(it.nk, last + shift + 1) : it.nk;
+      return end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    };
+    it.n0 = blocks(it.tok0);
+    it.n1 = blocks(it.tok0 + P.tq);
+    if (kSplit) {
+      const int nb = max(it.n0, it.n1);
+      it.b0 = (int)((long long)nb * split / P.splits);
+      const int b1 = (int)((long long)nb * (split + 1) / P.splits);
+      it.n0 = max(0, min(it.n0, b1) - it.b0);
+      it.n1 = max(0, min(it.n1, b1) - it.b0);
+    }
+  }
+  return found;
+}
+
+// The rows of a softmax warp (bits of `rows`) that came out not finite in work item `id`, worked out again
+// where a value behind their keys may be why.
+template <int D, bool kSplit>
+__device__ __forceinline__ void repair_rows(const TextAttnParams& P, int id, uint32_t rows, int warp, int lane,
+                                            uint8_t* stage) {
+  const TextAttnArgs& a = P.a;
+  Item it;
+  locate_item<kSplit>(P, id, lane, false, it);
+  const int G = P.group, tile = (warp - 2) >> 2, row = (warp & 3) * 32 + lane, token = row / G;
+  const int begin = it.b0 * kKeys, end = min(it.nk, begin + (tile ? it.n1 : it.n0) * kKeys);
+  const int seen = a.causal ? min(it.nk, it.tok0 + tile * P.tq + token + it.nk - it.nq + 1) : it.nk;
+  rows &= __ballot_sync(0xffffffffu, seen < end);
+  if (!rows) return;
+  const bf16* vp = a.v + (long long)it.k0 * a.ldv + it.hk * D;
+  rows = spoiled_rows<D>(vp, a.ldv, rows, seen, begin, end, lane);
+  const long long part = (((long long)it.rank * a.heads_k + it.hk) * P.splits + it.split) * 256;
+  while (rows) {
+    const uint32_t src = lane < 16 ? __fns(rows, 0, lane + 1) : 32u;  // lane r < 16 takes the r-th of them
+    const bool have = src < 32u;
+    const int r = (warp & 3) * 32 + (have ? (int)src : 0), r_token = r / G, r_col = (it.hk * G + r - r_token * G) * D;
+    const int r_seen = __shfl_sync(0xffffffffu, seen, src & 31u);
+    const long long q_row = it.q0 + it.tok0 + tile * P.tq + r_token, prow = part + tile * P.tq * G + r;
+    void* dst = kSplit ? (void*)(P.o + prow * D) : (void*)(a.out + q_row * a.ldo + r_col);
+    attend_rows<D, kSplit>(a, a.q + q_row * a.ldq + r_col, a.k + (long long)(it.k0 + begin) * a.ldk + it.hk * D,
+                           vp + begin * a.ldv, have ? r_seen - begin : 0, P.scale_log2, lane, dst, P.ml + prow, stage);
+    for (int i = 0; i < 16 && rows; ++i) rows &= rows - 1;
+  }
+}
+
+// The kernel's shared memory behind the tiles.
+template <int D>
+struct Shared {
+  uint8_t* smem;
+  uint64_t* bars;
+  Bars bar;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  Item* items;           // two: the current one and the next
+  int* after;            // what follows the pass: kRepair, kAgain
+  volatile int* odd_n;   // each softmax warp's records, and how many there are
+  uint2* odd;
+  __device__ __forceinline__ explicit Shared(uint8_t* base)
+      : smem(base),
+        bars(reinterpret_cast<uint64_t*>(base + Smem<D>::kBar)),
+        bar{bars + 0, bars + 1, bars + 3, bars + 5, bars + 7, bars + 9, bars + 11, bars + 12, bars + 13, bars + 15},
+        tmem_slot(reinterpret_cast<uint32_t*>(bars + kBars)),
+        abort_flag(reinterpret_cast<volatile int*>(tmem_slot + 1)),
+        items(reinterpret_cast<Item*>(bars + kBars + 1)),
+        after(reinterpret_cast<int*>(items + 2)),
+        odd_n(after + 1),
+        odd(reinterpret_cast<uint2*>(base + Smem<D>::kOdd)) {}
+};
+
+template <int D>
+__device__ __forceinline__ void init_pass(const Shared<D>& sh) {
+  const Bars& bar = sh.bar;
+  mbar_init(bar.q_full, 1);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&bar.ready[i], 1);
+    mbar_init(&bar.slot_free[i], 1);
+    mbar_init(&bar.s_full[i], 1);
+    mbar_init(&bar.p_full[i], 4);
+    mbar_init(&bar.o_done[i], 1);
+    mbar_init(&bar.item_full[i], 1);
+    mbar_init(&bar.item_free[i], 10);  // the loader, the issuer and eight softmax warps
+  }
+  mbar_init(bar.fixed, 1);
+  mbar_init(bar.drain, 1);
+  *sh.after = 0;
+  for (int i = 0; i < 8; ++i) sh.odd_n[i] = 0;
+  fence_mbar_init();
+}
+
+// A CTA's work items, until there are none left or a softmax warp's records are full: each warp's role.
+template <int D, bool kSplit>
+__device__ __forceinline__ void run_items(const TextAttnParams& P, const Shared<D>& sh, uint32_t tmem, bool first_pass) {
+  using L = Smem<D>;
+  uint8_t* const smem = sh.smem;
+  const Bars& bar = sh.bar;
+  Item* const items = sh.items;
+  const TextAttnArgs& a = P.a;
+  int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("" : "+r"(warp), "+r"(lane));  // not carried from pass to pass either (see the kernel)
+  const int G = P.group, TQ = P.tq;
+  const WaitCtx wc{a.status, sh.abort_flag, kWaitLimitNs};
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     // Ring slot j & 1 carries V_j and K_{j+1}; slot j >= 1 is loaded once the scores of block
@@ -546,53 +798,21 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
     for (int k = 0; ok; ++k) {
       // the first item by place, the others as they come, longest first
       int id = (int)blockIdx.x;
-      if (k > 0) {
-        if (lane == 0) id = (int)(gridDim.x + atomicAdd(&a.status->next_item, 1u));
+      bool full = false;  // of records: the CTA repairs rows before it goes on
+      if (!first_pass || k > 0) {
+        full = __any_sync(0xffffffffu, lane < 8 && sh.odd_n[lane] >= kOddFull);
+        if (lane == 0 && !full) id = (int)(gridDim.x + atomicAdd(&a.status->next_item, 1u));
         id = __shfl_sync(0xffffffffu, id, 0);
       }
-      const bool stop = (uint32_t)id >= (uint32_t)P.items;  // a counter that was not zero wraps to no item
-      Span sp{0, -1, 0, 0, true};
-      int index = 0, hk = 0, split = 0, rank = 0;
-      bool found = false;
+      const bool stop = full || (uint32_t)id >= (uint32_t)P.items;  // a counter that was not zero wraps to no item
+      Item it{0, -1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1};
       if (!stop) {
-        hk = id % a.heads_k;
-        rank = id / a.heads_k;
-        if (kSplit) {
-          split = rank % P.splits;
-          rank /= P.splits;
-        }
-        if (P.list) {
-          const int2 e = P.list[rank];
-          found = e.x >= 0;
-          if (found) sp = load_span(a, e.x);
-          index = e.y;
-        } else {
-          found = find_tile(a, TP, P.levels, P.tiles, rank, lane, k == 0 && blockIdx.x == 0, sp, index);
-        }
-        if (kSplit && hk == 0 && split == 0 && lane == 0)
-          P.desc[rank] = found ? make_int2(sp.q0 + index * TP, min(TP, sp.nq - index * TP)) : make_int2(0, 0);
+        const bool found = locate_item<kSplit>(P, id, lane, first_pass && k == 0 && blockIdx.x == 0, it);
+        if (kSplit && it.hk == 0 && it.split == 0 && lane == 0)
+          P.desc[it.rank] = found ? make_int2(it.q0 + it.tok0, min(2 * TQ, it.nq - it.tok0)) : make_int2(0, 0);
+        if (!found) continue;
       }
-      if (!stop && !found) continue;
-      Item it{sp.q0, sp.nq, sp.k0, sp.nk, index * TP, 0, 0, 0, hk, split, rank, stop};
-      if (found) {
-        // key blocks of each tile, and this split's run [b0, b0 + n) of them
-        const int shift = it.nk - it.nq;
-        auto blocks = [&](int first) {
-          if (first >= it.nq) return 0;
-          const int last = min(first + TQ, it.nq) - 1;
-          const int end = a.causal ? min(it.nk, last + shift + 1) : it.nk;
-          return end > 0 ? (end + kKeys - 1) / kKeys : 0;
-        };
-        it.n0 = blocks(it.tok0);
-        it.n1 = blocks(it.tok0 + TQ);
-        if (kSplit) {
-          const int nb = max(it.n0, it.n1);
-          it.b0 = (int)((long long)nb * split / P.splits);
-          const int b1 = (int)((long long)nb * (split + 1) / P.splits);
-          it.n0 = max(0, min(it.n0, b1) - it.b0);
-          it.n1 = max(0, min(it.n1, b1) - it.b0);
-        }
-      }
+      if (full && lane == 0) atomicOr(sh.after, kAgain);
       ok = mbar_wait_sleep(&bar.item_free[out & 1], ((out >> 1) & 1u) ^ 1u, wc, kSiteItemFree);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -706,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
       if (ok) {
         const bool none = n == 0 || l_run == 0.f;  // no key seen: zeros
         const float inv_l = none ? 0.f : 1.0f / l_run;
-        const int q0 = it.q0, k0 = it.k0, nk = it.nk, b0 = it.b0, hk = it.hk, tok0 = it.tok0;
+        const int q0 = it.q0, hk = it.hk, tok0 = it.tok0;
         const int prow = (tile * TQ + token) * G + g;
         const long long out_at = active ? (long long)(q0 + qi) * a.ldo + (hk * G + g) * D : -1;  // this row's output
         const long long part = ((long long)it.rank * a.heads_k + hk) * P.splits + it.split;
@@ -779,42 +999,15 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
           }
         }
         if (active && kSplit) P.ml[part * 256 + prow] = none ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
-        // Rows that are not finite: was it a value that they must not see?
-        const int taken = min(nk, (b0 + n) * kKeys);
-        const int seen = limit + b0 * kKeys;
-        uint32_t todo = __ballot_sync(0xffffffffu, zero != 0.f && active && seen < taken);
-        if (todo) {  // rows handed to a TMA store have to land before they are written again
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-          __syncwarp();
-        }
-        while (todo) {
-          const int src = __ffs(todo) - 1;
-          todo &= todo - 1;
-          const int r_lim = __shfl_sync(0xffffffffu, seen, src), r_qi = __shfl_sync(0xffffffffu, qi, src);
-          const int r_g = __shfl_sync(0xffffffffu, g, src), r_prow = __shfl_sync(0xffffffffu, prow, src);
-          constexpr int V = D / 32;
-          const bf16* vp = a.v + (long long)k0 * a.ldv + hk * D;
-          bool blame = false;
-          for (int j = max(r_lim, b0 * kKeys); j < taken; ++j)
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-              blame |= !(fabsf(__bfloat162float(vp[(long long)j * a.ldv + lane * V + e])) <= 3.4028235e38f);
-          if (!__any_sync(0xffffffffu, blame)) continue;
-          const int j0 = b0 * kKeys;
-          float m, l, o[V];
-          attend_row<D>(a, a.q + (long long)(q0 + r_qi) * a.ldq + (hk * G + r_g) * D,
-                        a.k + (long long)(k0 + j0) * a.ldk + hk * D, vp + (long long)j0 * a.ldv, max(0, r_lim - j0), c,
-                        lane, m, l, o);
-          if (kSplit) {
-            float* dst = P.o + (part * 256 + r_prow) * D;
-#pragma unroll
-            for (int e = 0; e < V; ++e) dst[lane * V + e] = o[e];
-            if (lane == 0) P.ml[part * 256 + r_prow] = make_float2(m, l);
-          } else {
-            bf16* dst = a.out + (long long)(q0 + r_qi) * a.ldo + (hk * G + r_g) * D;
-#pragma unroll
-            for (int e = 0; e < V; ++e) dst[lane * V + e] = __float2bfloat16(l == 0.f ? 0.f : o[e] / l);
-          }
+        // Rows that are not finite: whether a value that they do not see is to blame is looked into once the
+        // CTA has no item left that waits for this warp.
+        const uint32_t rows = __ballot_sync(0xffffffffu, zero != 0.f && active);
+        if (rows && lane == 0) {
+          const int at = sh.odd_n[warp - 2];
+          const int id = (it.rank * P.splits + it.split) * a.heads_k + hk;
+          sh.odd[(warp - 2) * kOddMost + at] = make_uint2((uint32_t)id, rows);
+          sh.odd_n[warp - 2] = at + 1;
+          atomicOr(sh.after, kRepair);
         }
       }
       tc_fence_before();  // O has been read before the next item's first P is announced
@@ -824,12 +1017,78 @@ __global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __gri
     if (lane == 0) tma_store_wait_read();
   }
 
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
+}
+
+// The rows that came out not finite, each softmax warp its own; nothing is in flight and no role waits.
+template <int D, bool kSplit>
+__device__ __noinline__ void repair_all(const TextAttnParams& P, uint8_t* smem) {
+  const Shared<D> sh(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < 2 || warp >= 10) return;
+  const int records = sh.odd_n[warp - 2];
+  if (records == 0) return;
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // rows may be written again
+  __syncwarp();
+  const uint2* mine = sh.odd + (warp - 2) * kOddMost;
+  for (int i = 0; i < records; ++i)
+    repair_rows<D, kSplit>(P, (int)mine[i].x, mine[i].y, warp, lane, smem + Smem<D>::kOut + (warp - 2) * 4096);
+}
+
+template <int D, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1) text_attention_kernel(const __grid_constant__ TextAttnParams P) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const TextAttnArgs& a = P.a;
+  uint32_t tmem;
+  {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Shared<D> sh(smem);
+    if (threadIdx.x == 32) {
+      *sh.abort_flag = 0;
+      init_pass(sh);
+    }
+    if (warp == 2 && lane == 0) {
+      tma_prefetch_desc(&P.q_map);
+      tma_prefetch_desc(&P.k_map);
+      tma_prefetch_desc(&P.v_map);
+    }
+    __syncwarp();
+    if (warp == 1) {
+      tmem_alloc(sh.tmem_slot, kTmemCols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem = *sh.tmem_slot;
   }
+  grid_dependency_wait();  // lengths, Q, K, V and the output belong to earlier kernels of the stream
+  allow_dependents();
+
+  for (bool first_pass = true;; first_pass = false) {
+    // A pass finds its addresses anew: carried from pass to pass they cost the key loop registers (8192 tokens
+    // 378 -> 397 us).
+    asm volatile("" : "+l"(smem), "+r"(tmem));
+    const Shared<D> sh(smem);
+    run_items<D, kSplit>(P, sh, tmem, first_pass);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // Nothing is in flight and no role waits: the rows that came out not finite, each warp its own.
+    const int after = *(volatile int*)sh.after;
+    if (after == 0 || *sh.abort_flag) break;
+    repair_all<D, kSplit>(P, sh.smem);
+    if (!(after & kAgain)) break;
+    __syncthreads();
+    if (threadIdx.x == 32) {
+      for (int i = 0; i < kBars; ++i) mbar_inval(sh.bars + i);
+      init_pass(sh);
+    }
+    __syncthreads();
+  }
+
+  if ((threadIdx.x >> 5) == 1) tmem_dealloc(tmem, kTmemCols);
   // the last CTA leaves the counters as it found them, for the next call on this workspace
   if (threadIdx.x == 0 && atomicAdd(&a.status->items_done, 1u) == gridDim.x - 1) {
     a.status->next_item = 0;
@@ -1043,26 +1302,6 @@ struct alignas(64) FewParams {
 
 enum : uint32_t { kSiteFewFull = 0x521, kSiteFewEmpty };
 
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// D += A B, 16 x 8 x 16, bf16 in, fp32 out.
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Keys that the tile of query rows [base, base + 16) of a sequence sees: those of its last row.
 __device__ __forceinline__ int few_keys(const TextAttnArgs& a, const Span& sp, int G, int base) {
   if (!a.causal) return sp.nk;
@@ -1257,6 +1496,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
   }
   __syncthreads();
   if (warp == 4 || abort_flag) return;
+  uint32_t odd = 0;  // rows that are not finite
   for (int r = warp; r < rows; r += 4) {
     float mr = -INFINITY, lr = 0.f, out[V];
 #pragma unroll
@@ -1277,20 +1517,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
     float zero = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) zero = fmaf(out[e], 0.f, zero);
-    const int seen = a.causal ? min(sp.nk, token + sp.nk - sp.nq + 1) : sp.nk;
-    if (seen < last && __any_sync(0xffffffffu, zero != 0.f)) {
-      // not finite: was it a value behind the keys that the row sees?
-      const bf16* vp = a.v + (long long)sp.k0 * a.ldv + hk * D;
-      bool blame = false;
-      for (int j = max(seen, first); j < last; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          blame |= !(fabsf(__bfloat162float(vp[(long long)j * a.ldv + lane * V + e])) <= 3.4028235e38f);
-      if (__any_sync(0xffffffffu, blame))
-        attend_row<D>(a, a.q + (long long)(sp.q0 + token) * a.ldq + (hk * G + g) * D,
-                      a.k + (long long)(sp.k0 + first) * a.ldk + hk * D, vp + (long long)first * a.ldv,
-                      max(0, seen - first), c, lane, mr, lr, out);
-    }
+    if (__any_sync(0xffffffffu, zero != 0.f)) odd |= 1u << r;
     if (direct) {
       const float inv = lr == 0.f ? 0.f : 1.0f / lr;
       bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + g) * D + lane * V;
@@ -1303,6 +1530,26 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
 #pragma unroll
       for (int e = 0; e < V; e += 2)
         *reinterpret_cast<float2*>(P.o + at * D + lane * V + e) = make_float2(out[e], out[e + 1]);
+    }
+  }
+  if (odd) {
+    // was it a value behind the keys that the row sees?
+    const bool mine = (odd >> lane) & 1u;
+    const int token = (base + lane) / G, g = base + lane - token * G;
+    const int seen = a.causal ? min(sp.nk, token + sp.nk - sp.nq + 1) : sp.nk;
+    const bf16* vp = a.v + (long long)sp.k0 * a.ldv + hk * D;
+    odd = __ballot_sync(0xffffffffu, mine && seen < last);
+    if (odd) odd = spoiled_rows<D>(vp, a.ldv, odd, seen, first, last, lane);
+    if (odd) {
+      __syncwarp();  // the rows have been written by other lanes
+      const bool redo = (odd >> lane) & 1u;
+      const long long row = sp.q0 + (redo ? token : 0), at = (long long)run * P.rows + base + lane;
+      const int col = (hk * G + (redo ? g : 0)) * D, keys = redo ? seen - first : 0;
+      const bf16 *q = a.q + row * a.ldq + col, *k = a.k + (long long)(sp.k0 + first) * a.ldk + hk * D;
+      vp += (long long)first * a.ldv;
+      uint8_t* stage = smem + 4 * kFewRows * D * 4 + warp * 16 * D * 2;  // behind the warps' parts
+      if (direct) attend_rows<D, false>(a, q, k, vp, keys, c, lane, a.out + row * a.ldo + col, nullptr, stage);
+      else attend_rows<D, true>(a, q, k, vp, keys, c, lane, P.o + at * D, P.ml + at, stage);
     }
   }
 }

@@ -114,3 +114,51 @@ def linear_blocks(a_q, a_scale, w_q, w_scale):
     """(out, sum of |a| |w|) in float64."""
     a, w = dequantize(a_q, a_scale, 1), dequantize(w_q, w_scale, 128)
     return a @ w.t(), a.abs() @ w.abs().t()
+
+
+def attention_bound(q, k, v, spans, causal, scale, exact_scores=False):
+    """As `attention`, but nothing that a row does not see takes part, in the values or in the tolerance,
+    whatever it holds: (out, tolerance, bad, owned) with `bad` where a visible value of V is infinite or NaN
+    (out and tolerance 0 there).  The tolerance is each value's own.  With size = sum p |v|:
+
+    - the probabilities and the output are rounded to bf16: 2^-8 size, 2^-8 |out|;
+    - a score is a sum of d exact products in fp32, each step off by at most 2^-23 (truncation) of
+      A = scale * max over the visible keys of sum |q_i k_i|, and its exponent is rounded twice at up to 2 A
+      in units of log2: e = (d + 4) 2^-23 A.  Scores off by e move p / l by at most exp(2 e) - 1.  With
+      `exact_scores` (integers whose sums fp32 holds, which the caller sees to) e = 4 * 2^-24 A;
+    - sums over n visible keys, the exponential (2^-22) and the running rescales: (n + 128) 2^-23 size.
+
+    The relative part of the tolerance is asserted to be under 5 %, so that no input makes the comparison empty."""
+    Hq, Hk, d = q.shape[1], k.shape[1], q.shape[2]
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    tol, bad, owned = torch.zeros_like(out), torch.zeros(q.shape, dtype=torch.bool), torch.zeros(q.shape[0], dtype=torch.bool)
+    for q0, nq, k0, nk in spans:
+        owned[q0:q0 + nq] = True
+        if nq == 0 or nk == 0:
+            continue
+        i, j = torch.arange(nq)[:, None], torch.arange(nk)[None]
+        seen = j <= i + (nk - nq) if causal else torch.ones(nq, nk, dtype=torch.bool)
+        used = seen.any(0)  # keys that some row sees
+        for h in range(Hk):
+            heads = slice(h * Hq // Hk, (h + 1) * Hq // Hk)
+            kk, vv = k[k0:k0 + nk, h].double(), v[k0:k0 + nk, h].double()
+            kk = torch.where(used[:, None], kk, torch.zeros_like(kk))
+            vbad = ~vv.isfinite()
+            vv = torch.where(vbad | ~used[:, None], torch.zeros_like(vv), vv)
+            qq = q[q0:q0 + nq, heads].double().transpose(0, 1)  # [g, nq, d]
+            s = (qq @ kk.t() * scale).masked_fill(~seen, -math.inf)
+            a = (qq.abs() @ kk.abs().t() * abs(scale)).masked_fill(~seen, 0.0).amax(-1, keepdim=True)
+            m = s.amax(-1, keepdim=True)
+            p = torch.where(seen, torch.exp(s - torch.where(m == -math.inf, torch.zeros_like(m), m)), torch.zeros_like(s))
+            l = p.sum(-1, keepdim=True)
+            p = torch.where(l > 0, p / l, torch.zeros_like(p))
+            o, size = p @ vv, p @ vv.abs()
+            e = 4 * 2.0 ** -24 * a if exact_scores else (d + 4) * 2.0 ** -23 * a
+            rel = 2.0 ** -8 + torch.expm1(2 * e) + (seen.sum(-1)[None, :, None] + 128) * 2.0 ** -23
+            assert float(rel.max()) < 0.05, float(rel.max())
+            b = (seen.double() @ vbad.double() > 0)[None].expand_as(o)
+            put = lambda x: x.transpose(0, 1)  # noqa: E731
+            out[q0:q0 + nq, heads] = put(torch.where(b, torch.zeros_like(o), o))
+            tol[q0:q0 + nq, heads] = put(torch.where(b, torch.zeros_like(o), rel * size + 2.0 ** -8 * o.abs() + 1e-30))
+            bad[q0:q0 + nq, heads] = put(b)
+    return out, tol, bad, owned
