@@ -125,7 +125,9 @@ def attention_bound(q, k, v, spans, causal, scale, exact_scores=False):
     - a score is a sum of d exact products in fp32, each step off by at most 2^-23 (truncation) of
       A = scale * max over the visible keys of sum |q_i k_i|, and its exponent is rounded twice at up to 2 A
       in units of log2: e = (d + 4) 2^-23 A.  Scores off by e move p / l by at most exp(2 e) - 1.  With
-      `exact_scores` (integers whose sums fp32 holds, which the caller sees to) e = 4 * 2^-24 A;
+      `exact_scores` (integers whose sums fp32 holds, which the caller sees to) only the exponent's roundings
+      are left: a score times scale log2(e), half a step of 2^-24 relative, and the running maximum's share,
+      e = 2 * 2^-24 A;
     - sums over n visible keys, the exponential (2^-22) and the running rescales: (n + 128) 2^-23 size.
 
     The relative part of the tolerance is asserted to be under 5 %, so that no input makes the comparison empty."""
@@ -153,7 +155,7 @@ def attention_bound(q, k, v, spans, causal, scale, exact_scores=False):
             l = p.sum(-1, keepdim=True)
             p = torch.where(l > 0, p / l, torch.zeros_like(p))
             o, size = p @ vv, p @ vv.abs()
-            e = 4 * 2.0 ** -24 * a if exact_scores else (d + 4) * 2.0 ** -23 * a
+            e = 2 * 2.0 ** -24 * a if exact_scores else (d + 4) * 2.0 ** -23 * a
             rel = 2.0 ** -8 + torch.expm1(2 * e) + (seen.sum(-1)[None, :, None] + 128) * 2.0 ** -23
             assert float(rel.max()) < 0.05, float(rel.max())
             b = (seen.double() @ vbad.double() > 0)[None].expand_as(o)
