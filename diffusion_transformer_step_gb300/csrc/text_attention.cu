@@ -999,10 +999,10 @@ __device__ __forceinline__ void run_items(const TextAttnParams& P, const Shared<
           }
         }
         if (active && kSplit) P.ml[part * 256 + prow] = none ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
-        // Rows that are not finite: whether a value that they do not see is to blame is looked into once the
-        // CTA has no item left that waits for this warp.
+        // Rows that are not finite: whether a value that they do not see is to blame (causal calls only: the
+        // others' tiles hold nothing else) is looked into once the CTA has no item left that waits for this warp.
         const uint32_t rows = __ballot_sync(0xffffffffu, zero != 0.f && active);
-        if (rows && lane == 0) {
+        if (rows && a.causal && lane == 0) {
           const int at = sh.odd_n[warp - 2];
           const int id = (it.rank * P.splits + it.split) * a.heads_k + hk;
           sh.odd[(warp - 2) * kOddMost + at] = make_uint2((uint32_t)id, rows);

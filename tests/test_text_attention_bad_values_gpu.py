@@ -103,3 +103,12 @@ def test_a_bad_value_at_the_end_of_a_long_sequence(dit):  # noqa: F811
         m = 32
         rows = [(0, m, 0, first + m)]
         check(got[first:first + m], R.attention_bound(q[first:first + m], k[:first + m], v[:first + m], rows, True, d ** -0.5))
+
+
+@pytest.mark.parametrize("hq,hk,d,n", [(32, 8, 128, 700), (4, 1, 64, 60), (3, 1, 128, 300)])
+def test_every_row_sees_every_value_without_a_mask(dit, hq, hk, d, n):  # noqa: F811
+    nk = 3366 if hq == 3 else n
+    q, k, v = _qkv(n, nk, hq, hk, d, seed=9)
+    v[5, hk - 1, 3], v[nk - 1, 0, 7], v[nk // 2] = math.nan, -math.inf, math.nan if hq == 3 else 1.0
+    spans = [(0, n, 0, nk)]
+    check(attend(dit, q, k, v, spans, causal=False)[0], R.attention_bound(q, k, v, spans, False, d ** -0.5))
