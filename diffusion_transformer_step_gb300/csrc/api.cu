@@ -971,7 +971,7 @@ namespace dit {
 namespace {
 
 constexpr int kMaxTextRows = 1 << 26, kMaxAttnRows = 1 << 28, kMaxSeqs = 16384, kMaxLen = 1 << 24;
-constexpr long long kMaxLd = 1 << 24;
+constexpr long long kMaxLd = 1 << 24, kMaxTextHeads = 1ll << 35;
 
 inline bool finite_pos(double v) { return v > 0.0 && v <= 1.7e308; }
 
@@ -1083,7 +1083,8 @@ dit_status dit_qk_norm_rope(int rows, int heads_q, int heads_k, int head_dim, in
                             long long ldk_out, void* ws, size_t ws_bytes, dit_stream_t stream) {
   if (head_dim != 64 && head_dim != 128) return DIT_ERR_UNSUPPORTED;
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0) return DIT_ERR_UNSUPPORTED;
-  if (rows < 0 || rows > kMaxTextRows || heads_q < 1 || heads_q > 1024 || heads_k < 0 || heads_k > 1024)
+  if (rows < 0 || rows > kMaxTextRows || heads_q < 1 || heads_q > 1024 || heads_k < 0 || heads_k > 1024 ||
+      (long long)rows * (heads_q + heads_k) > kMaxTextHeads)
     return DIT_ERR_INVALID_ARG;
   if (layout != DIT_ROPE_INTERLEAVED && layout != DIT_ROPE_HALF) return DIT_ERR_INVALID_ARG;
   if (!(eps >= 0.f && eps <= 3.0e38f) || (heads_k > 0 && (q_norm == nullptr) != (k_norm == nullptr)))

@@ -1213,8 +1213,9 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
         launch_k(text_attention_list_kernel, dim3(1), dim3(1024), 0, s, a, p.tq * 2, p.levels, p.tiles, list);
     if (e != cudaSuccess) return e;
   }
+  // Under 2^31 - 2^16 at any sizes that are accepted: pairs of tiles x key heads come to 1.55e9 at most (2^28
+  // rows, groups of 44 heads), and keys are split only where that leaves fewer than an item per SM.
   const long long items = (long long)p.tiles * a.heads_k * p.splits;
-  if (items > 0x7fff0000ll) return cudaErrorInvalidValue;
   P.items = (int)items;
   const int sms = sm_count(), grid = items < sms ? (int)items : sms;
   {
@@ -1605,8 +1606,8 @@ cudaError_t launch_few(const TextAttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 16) g_few_attr_set[slot].store(true, std::memory_order_release);
   }
+  // up to 2^24 sequences x key heads of one run, or about 16384 runs
   const long long grid = (long long)a.seqs * a.heads_k * p.splits * p.tiles;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   {
     LaunchScope scope(kClsTextAttention, s);
     cudaError_t e = launch_k(text_attention_few_kernel<D>, dim3((unsigned)grid), dim3(kFewThreads), smem, s, P);

@@ -362,8 +362,7 @@ cudaError_t launch_qk(const QKNormRopeArgs& a, cudaStream_t s) {
                     ch);
   }
   const int per_warp = 32 / (D / 8) * kUnroll, chunks = (a.heads_q + a.heads_k + per_warp - 1) / per_warp;
-  const long long grid = ((long long)a.rows * chunks + 7) / 8;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  const long long grid = ((long long)a.rows * chunks + 7) / 8;  // under 2^31: rows x heads <= 2^35
   return launch_k(qk_norm_rope_kernel<D, kHalf>, dim3((unsigned)grid), dim3(256), 0, s, a, chunks);
 }
 

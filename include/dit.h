@@ -419,7 +419,7 @@ dit_status dit_text_rope_table(const dit_text_rope* rope, const int32_t* pos_dev
  * rows <= table_rows.
  * head_dim 64 or 128, rot_dim % 8 == 0, 0 <= rot_dim <= head_dim (0: no rotation, table_dev
  * NULL); ld* % 8 == 0 and >= heads * head_dim, <= 2^24; 0 <= rows <= 2^26, heads_q and
- * heads_k <= 1024, heads_q >= 1; eps >= 0 and finite.  ws: any workspace of >= 256 bytes
+ * heads_k <= 1024, heads_q >= 1, rows * (heads_q + heads_k) <= 2^35; eps >= 0 and finite.  ws: any workspace of >= 256 bytes
  * (only its status word is used). */
 dit_status dit_qk_norm_rope(int rows, int heads_q, int heads_k, int head_dim, int rot_dim, dit_rope_layout layout,
                             const void* q_dev, long long ldq, const void* k_dev, long long ldk, const void* q_norm,
