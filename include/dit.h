@@ -456,7 +456,9 @@ dit_status dit_text_attention_workspace(const dit_text_attn* a, size_t* bytes);
  * q_dev + row * ldq + h * head_dim, k and v likewise with heads_k, out_dev + row * ldo +
  * h * head_dim; all bf16.  Rows of out_dev that belong to no sequence are not written, rows
  * behind a sequence's keys not used, whatever they hold.  A visible value that is infinite
- * or NaN reaches the queries that see it, and no others.
+ * or NaN reaches the queries that see it, and no others.  The sums of probabilities times values
+ * are divided by the sum of the probabilities at the end: visible values of up to 2^98 cannot make
+ * them overflow, larger ones may, to infinity.
  * Sequences may share key rows; query rows of two sequences must not overlap.
  * Scores, statistics and sums in fp32; the probabilities are rounded to bf16 for the product
  * with V.  The order of sums depends only on the sizes and lengths: equal calls give equal bits.

@@ -112,3 +112,13 @@ def test_every_row_sees_every_value_without_a_mask(dit, hq, hk, d, n):  # noqa: 
     v[5, hk - 1, 3], v[nk - 1, 0, 7], v[nk // 2] = math.nan, -math.inf, math.nan if hq == 3 else 1.0
     spans = [(0, n, 0, nk)]
     check(attend(dit, q, k, v, spans, causal=False)[0], R.attention_bound(q, k, v, spans, False, d ** -0.5))
+
+
+@pytest.mark.parametrize("hq,hk,d,nq,nk", [(32, 8, 128, 700, 700), (4, 1, 64, 60, 60), (3, 1, 128, 300, 3366), (8, 8, 128, 1, 9000)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_large_values_do_not_overflow_the_sums(dit, causal, hq, hk, d, nq, nk):  # noqa: F811
+    """Up to 2^98, as documented: the sums of probabilities times values are divided at the end."""
+    q, k, v = _qkv(nq, nk, hq, hk, d, seed=13)
+    v = (v.float().clamp(-4, 4) * 2.0 ** 96).to(torch.bfloat16)
+    spans = [(0, nq, 0, nk)]
+    check(attend(dit, q, k, v, spans, causal)[0], R.attention_bound(q, k, v, spans, causal, d ** -0.5))
