@@ -14,15 +14,18 @@
 //                            through distributed shared memory, in rank order.  (128 rows so: 16.9 us
 //                            at 8192 x 4096, as wide tiles 12.7.)
 //
-// With the pass that quantises its rows the wide kernel takes 361 us at 8192 x 12288 x 4096 (the product
-// 348, 2.37 PFLOP/s) and 79 at 4096 x 4864 x 4096 (73), 0.6 of the e4m3 rate (twice the measured bf16
-// burst).  Without its fold the same ring runs at 3.8 PFLOP/s.  A 128-column block takes ~546 cycles: the MMAs'
+// On random values, with the pass that quantises the rows, the wide kernel takes 362 us at 8192 x 12288 x 4096
+// in a burst of twenty (the product 349, 2.36 PFLOP/s) and 386 to 395 call after call for a second, at the
+// clocks that power leaves (2.1 PFLOP/s with the quantising); 79 us at 4096 x 4864 x 4096 in a burst
+// (73): 0.6 of the e4m3 rate (twice the measured bf16 burst).  A 128-column block takes ~546 cycles: the MMAs'
 // operands and the loads take 437 of them from shared memory at 128 bytes per cycle, and the fold's scale
 // loads, one line per row, share that path.  256-column tiles read 40 % less shared memory per product but leave two
-// accumulators, between which commit, fold, hand-back and issue (~1900 cycles) do not hide.  Measured
-// and left, products of zeros (which draw less power) where this form took 339 us: 256 columns 363, 160
-// columns in three accumulators 356, one CTA per tile with the weights by multicast 353, scales 16 blocks
-// ahead through shared memory 390, scales of a block in one line 375.
+// accumulators, between which commit, fold, hand-back and issue (~1900 cycles) do not hide.
+//
+// Forms were compared on products of zeros, which draw less power and do not wait for the clock.  The
+// product of 8192 x 12288 x 4096 took 339 us so, 290 without its fold, and 215 in 256-column tiles without
+// theirs (3.8 PFLOP/s); measured and left: 256 columns 363, 160 columns in three accumulators 356, one CTA per tile with the weights by multicast 353,
+// scales 16 blocks ahead through shared memory 390, scales of a block in one line 375.
 #include <cuda_fp8.h>
 
 #include <atomic>
@@ -62,7 +65,7 @@ __device__ __forceinline__ uint2 codes8(const uint4& u, float inv) {
 
 // A scale per row and 128 columns: eight threads of 16 values each per block, so a row's read
 // and write are whole 16-byte accesses of neighbouring threads.  blockDim = (8 x blocks of one
-// row, up to 256; rows).
+// row, up to 256; rows).  8192 x 4096: 16.7 us, 6.05 TB/s; 512 x 4096, which L2 holds, 2.1 us.
 __global__ void __launch_bounds__(256) quantize_row_blocks_kernel(const bf16* __restrict__ x, long long ld, int rows,
                                                                   int cols, uint8_t* __restrict__ q,
                                                                   float* __restrict__ scale) {
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(256) quantize_row_blocks_kernel(const bf16* __
   if (c % 128 == 0) scale[(long long)row * ((cols + 127) / 128) + c / 128] = m / 448.0f;
 }
 
-// A scale per 128 x 128 block: one CTA each, the block held in registers.
+// A scale per 128 x 128 block: one CTA each, the block held in registers.  12288 x 4096: 24.9 us, 6.05 TB/s.
 __global__ void __launch_bounds__(256) quantize_square_blocks_kernel(const bf16* __restrict__ x, long long ld, int rows,
                                                                      int cols, uint8_t* __restrict__ q,
                                                                      float* __restrict__ scale) {
@@ -202,9 +205,9 @@ struct Wide {
 
 // Warp 0 loads, warps 1 and 2 issue (leader CTA) every second block of depth each, the others from
 // warp 4 fold and store, BN / 64 per row quarter with 64 columns each.  An issuing thread needs
-// ~500 cycles per block for its waits, MMAs and commit, more than the MMAs themselves: two of them take
-// 8192 x 12288 x 4096 from 506 to 346 us (on zeros), sleeping instead of spinning folders to 339.  Per block there is one commit, on the accumulator; the
-// stage it frees is handed back by a folding thread of each CTA.
+// ~500 cycles per block for its waits, MMAs and commit, more than the MMAs themselves: two of them take a product
+// of zeros of 8192 x 12288 x 4096 from 506 to 346 us, sleeping instead of spinning folders to 339.  Per block
+// there is one commit, on the accumulator; the stage it frees is handed back by a folding thread of each CTA.
 template <bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::kThreads, 1)
     linear_fp8_wide_kernel(const __grid_constant__ Params P) {

@@ -23,7 +23,7 @@
 //     not finite are noted down; when its CTA is through with its items, or with room for notes, each
 //     softmax warp looks at the (under 256) keys behind its rows' limits that the tile took in, and
 //     where one of them is to blame works the rows out again, sixteen at a time (repair_rows).  One NaN
-//     near the end of 8192 tokens costs 2.0 ms so; one row at a time, within the item while the other
+//     near the end of 8192 tokens costs 2.1 ms so; one row at a time, within the item while the other
 //     roles waited, it cost 123 ms and from some 130 thousand tokens on more than a wait may take.
 //   - Work order.  Items come longest first over all sequences (index within the sequence,
 //     descending) from a counter, so the last ones are short.  For up to 64 sequences warp 10 finds
@@ -37,10 +37,16 @@
 //     text_attention_join_kernel adds them up in split order.
 //
 // Bound, as the joint attention, by the softmax and MMAs of a key block taking turns: 1.57 us per
-// 256 rows x 128 keys x 128 dims.  Causal, 32 query heads on 8 of 128: one sequence of 8192 tokens
-// 379 us (1450 TFLOP/s of visible pairs), eleven of 17 to 1500 tokens 116 us (922 TFLOP/s): there an
+// 256 rows x 128 keys x 128 dims.  Causal, 32 query heads on 8 of 128: one sequence of 8192 tokens 376 us in
+// a burst of twenty (1460 TFLOP/s of visible pairs), 394 call after call for a second, at the clocks that
+// power leaves (1395 TFLOP/s); eleven of 17 to 1500 tokens 114 and 115 us (936 TFLOP/s): there an
 // item's ends (first block without its neighbour's overlap 1 us, last PV 0.8 us, output 1.5 us) stand
-// against five blocks.  One sequence of 512: 13.3 us, 64 items of up to four blocks on 64 SMs.
+// against five blocks.  One sequence of 512: 13.6 us, 64 items of up to four blocks on 64 SMs.
+//
+// Probabilities are rounded to bf16 for the product with V, here and in the few-row kernel: an MMA takes A
+// and B of one 16-bit type and V is bf16, and a second product with what the rounding leaves would make three
+// products per key block of two.  It costs 0.0020 to 0.0023 relative error against 64 bits, where fp32 probabilities
+// and the output's own rounding give 0.0015 to 0.0017.  Sums and statistics are of the unrounded ones, in fp32.
 //
 // Measured and left: an issuing thread per tile (8192 tokens 378 -> 504 us: the tiles' MMAs interleave and
 // both wait longer); for heads of 64, P beside S in Tensor Memory and the next QK ahead of the PV (8192
@@ -481,6 +487,7 @@ __device__ __noinline__ void attend_rows(const TextAttnArgs& a, const bf16* qp, 
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     if (j + 16 <= least) {
+      // rounded to bf16 as in the tiles
       const uint32_t pf[4] = {pack_bf16x2(p[0][0], p[0][1]), pack_bf16x2(p[1][0], p[1][1]), pack_bf16x2(p[0][2], p[0][3]),
                               pack_bf16x2(p[1][2], p[1][3])};
       const int vk = lane & 15, vc = lane >> 4;
@@ -1237,7 +1244,7 @@ cudaError_t launch(const TextAttnArgs& a, const Plan& p, cudaStream_t s) {
 // per (run of keys, key head, sequence, tile), two per SM, each with three stages of 64 keys (64 * D * 4
 // bytes) on their way by TMA; four warps take 16 keys of a stage each through mma.sync with their own
 // running maximum and sum and add up at the end, in order.  Runs of several CTAs are joined by a second
-// kernel.  A 128-row tcgen05 tile of mostly empty rows took 153 us where this takes 116 (48 tokens over
+// kernel.  A 128-row tcgen05 tile of mostly empty rows took 153 us where this takes 115 (48 tokens over
 // 100 to 8192 keys, 8 key heads of 128).
 constexpr int kFewMost = 2 * kSMs * 16;  // rows per key head that one wave can hold
 constexpr int kFewRows = 16, kFewKeys = 64, kFewStages = 3, kFewThreads = 160;
@@ -1430,7 +1437,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) text_attention_few_kernel(cons
           mma_bf16(s[1], q[k], b[2], b[3]);
         }
         float alpha[2];
-        uint32_t p[4];
+        uint32_t p[4];  // probabilities, rounded to bf16 for the product with V (see the top)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // the lane's two rows
           float x[4];

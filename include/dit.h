@@ -413,7 +413,7 @@ dit_status dit_text_rope_table(const dit_text_rope* rope, const int32_t* pos_dev
  * q_norm and k_norm [head_dim] bf16: both NULL for the rotation alone (no norm), else both
  * given.  Head h of row r is at q_dev + r * ldq + h * head_dim, the outputs likewise with
  * ldq_out, ldk_out.  The outputs may be the inputs themselves (same pointer and stride);
- * any other overlap is DIT_ERR_INVALID_ARG.  heads_k may be 0 (k pointers ignored).
+ * any other overlap of q, k and the outputs is DIT_ERR_INVALID_ARG.  heads_k may be 0 (k pointers ignored).
  * table_dev [table_rows, rot_dim / 2, 2] fp32.  A row whose index lies outside
  * [0, table_rows) is left as it was and recorded (see above); without table_row_dev,
  * rows <= table_rows.
