@@ -24,8 +24,9 @@
 //
 // Forms were compared on products of zeros, which draw less power and do not wait for the clock.  The
 // product of 8192 x 12288 x 4096 took 339 us so, 290 without its fold, and 215 in 256-column tiles without
-// theirs (3.8 PFLOP/s); measured and left: 256 columns 363, 160 columns in three accumulators 356, one CTA per tile with the weights by multicast 353,
-// scales 16 blocks ahead through shared memory 390, scales of a block in one line 375.
+// theirs (3.8 PFLOP/s); measured and left: 256 columns 363, 160 columns in three accumulators 356, one CTA per
+// tile with the weights by multicast 353, scales 16 blocks ahead through shared memory 390, scales of a block in
+// one line 375.
 #include <cuda_fp8.h>
 
 #include <atomic>

@@ -623,6 +623,8 @@ struct Shared {
   int* after;            // what follows the pass: kRepair, kAgain
   volatile int* odd_n;   // each softmax warp's records, and how many there are
   uint2* odd;
+  static_assert(Smem<D>::kBar + (kBars + 1) * 8 + 2 * sizeof(Item) + 9 * sizeof(int) <= Smem<D>::kOdd, "room for all of it");
+  static_assert(Smem<D>::kBytes <= 227 * 1024, "what a CTA may have");
   __device__ __forceinline__ explicit Shared(uint8_t* base)
       : smem(base),
         bars(reinterpret_cast<uint64_t*>(base + Smem<D>::kBar)),

@@ -62,18 +62,20 @@ def test_values_that_are_all_nan(dit):  # noqa: F811
         check(attend(dit, q, k, v, [(0, n, 0, n)])[0], R.attention_bound(q, k, v, [(0, n, 0, n)], True, 128 ** -0.5))
 
 
-def test_more_bad_rows_than_a_block_notes_down(dit):  # noqa: F811
-    """4096 work items with a bad value each, 27 to a CTA, more than it takes before it repairs rows and goes
-    on.  Against the same call on values that are all finite, and the size of the sums from |v|."""
-    n, h, d = 16384, 64, 64
+@pytest.mark.parametrize("seqs", [1, 64, 72])
+def test_more_bad_rows_than_a_block_notes_down(dit, seqs):  # noqa: F811
+    """4096 work items or more with a bad value each, 27 to a CTA, more than it takes before it repairs rows
+    and goes on: of one sequence, of as many as one warp searches, and of more, whose tiles are listed first.
+    Against the same call on values that are all finite, and the size of the sums from |v|."""
+    n, h, d = 16384 if seqs == 1 else 256 * seqs, 64, 64
     g = torch.Generator(device=DEV).manual_seed(1)
     q, k, v = (torch.randn(n, h * d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(3))
     dirty = v.clone().view(n, h, d)
     t = torch.arange(n // 256, device=DEV)
     dirty[256 * t + 200, :, t % d] = math.nan
-    a = dit.make_text_attn(1, h, h, d, n, n, n, n)
+    a = dit.make_text_attn(seqs, h, h, d, n, n, n // seqs, n // seqs)
     ws = torch.zeros(dit.dit_text_attention_workspace(a), dtype=torch.uint8, device=DEV)
-    off = i32([0, n])
+    off = i32([i * (n // seqs) for i in range(seqs + 1)])
 
     def run(values):
         out = torch.full_like(q, 5.0)
@@ -81,8 +83,9 @@ def test_more_bad_rows_than_a_block_notes_down(dit):  # noqa: F811
         assert dit.dit_sync_status(ws)[0] == dit.DIT_OK
         return out.view(n, h, d)
     got, want, size = run(dirty.view(n, h * d)), run(v), run(v.abs())
-    row = torch.arange(n, device=DEV)
-    sees = (row[:, None] >= 256 * t + 200).view(n, 1, d)  # dimension t's value
+    sees = torch.zeros(n, 1, d, dtype=torch.bool, device=DEV)
+    for i in t.tolist():  # the value of tokens 256 i + 200, dimension i mod d, and the rows of its sequence behind it
+        sees[256 * i + 200:(256 * i // (n // seqs) + 1) * (n // seqs), 0, i % d] = True
     assert torch.equal(got.isnan(), sees.expand(n, h, d))
     # both sides: probabilities and outputs rounded to bf16, sums of up to 16384 terms and the error of a
     # score (64 products, |q| |k| scale <= 20) in fp32; `size` itself within 2 %
