@@ -43,7 +43,8 @@ const char* kernel_class_name(int cls) {
       "rope_table",     "pack_mlp_in",           "gemm_dual_out_proj",  "gemm_dual_mlp_out",
       "gemm_single_out_proj", "quantize_act",    "text_rope_table",     "qk_norm_rope",
       "text_attention", "text_attention_join",   "quantize_blocks_fp8", "linear_fp8_blocks",
-      "linear_fp8_join"};
+      "linear_fp8_join", "add_rms_norm",         "linear_act",          "linear_act_join",
+      "text_cache4_append", "text_cache4_read",  "text_cache4_attention", "text_cache4_join"};
   return (cls >= 0 && cls < kClsCount) ? names[cls] : "?";
 }
 
@@ -1023,6 +1024,69 @@ inline bool linear_fp8_sizes_ok(int rows, int n_out, int k) {
          k <= kMaxTokens && k % 16 == 0;
 }
 
+inline bool bad_ld(long long ld, long long width) { return ld < width || ld > kMaxLd || ld % 8 != 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+dit_status check_cache4(const dit_text_cache4* c) {
+  if (!c) return DIT_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return DIT_ERR_UNSUPPORTED;
+  const int ps = c->page_size;
+  if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return DIT_ERR_UNSUPPORTED;
+  if (c->heads_k < 1 || c->heads_k > 1024 || c->pages < 1 || c->pages > kMaxLen || c->max_pages < 1 ||
+      c->max_pages > kMaxLen / ps)
+    return DIT_ERR_INVALID_ARG;
+  return DIT_OK;
+}
+
+Cache4 cache4_of(const dit_text_cache4& c) {
+  int shift = 4;
+  while ((1 << shift) < c.page_size) ++shift;
+  return Cache4{c.heads_k, c.head_dim, c.pages, shift, c.max_pages};
+}
+
+inline size_t cache4_bytes(const Cache4& c) { return (size_t)c.pages * c.heads * c.slab(); }
+
+// The checks that append and read share; `rows` rows of k and v.
+dit_status check_cache4_move(const dit_text_cache4* c, int seqs, int rows, int max_len, const void* k, long long ldk,
+                             const void* v, long long ldv, const void* ws, size_t ws_bytes) {
+  DIT_TRY(check_cache4(c));
+  if (seqs < 0 || seqs > kMaxSeqs || rows < 0 || rows > kMaxAttnRows || max_len < 0 || max_len > kMaxLen)
+    return DIT_ERR_INVALID_ARG;
+  const long long width = (long long)c->heads_k * c->head_dim;
+  if (bad_ld(ldk, width) || bad_ld(ldv, width) || !aligned16(ws)) return DIT_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(DeviceStatus)) return DIT_ERR_WORKSPACE;
+  if (seqs == 0 || rows == 0 || max_len == 0) return DIT_OK;
+  if (!aligned16(k) || !aligned16(v)) return DIT_ERR_INVALID_ARG;
+  return DIT_OK;
+}
+
+// Bytes from a strided matrix's first element to its last, of elements of `size` bytes.
+inline size_t extent(long long rows, long long ld, long long width, int size) {
+  return rows > 0 ? ((size_t)(rows - 1) * ld + width) * size : 0;
+}
+
+dit_status check_cache4_attn(const dit_text_cache4* c, const dit_text_attn* a) {
+  DIT_TRY(check_cache4(c));
+  DIT_TRY(check_text_attn(a));
+  if (a->heads_k != c->heads_k || a->head_dim != c->head_dim) return DIT_ERR_INVALID_ARG;
+  return DIT_OK;
+}
+
+Cache4AttnArgs cache4_attn_sizes(const dit_text_cache4& c, const dit_text_attn& a) {
+  Cache4AttnArgs t;
+  memset(&t, 0, sizeof(t));
+  t.c = cache4_of(c);
+  t.seqs = a.seqs; t.heads_q = a.heads_q; t.rows_q = a.rows_q; t.causal = a.causal != 0; t.scale = a.scale;
+  const int most = c.max_pages * c.page_size;
+  t.max_q = a.max_q < a.rows_q ? a.max_q : a.rows_q;
+  t.max_k = a.max_k < most ? a.max_k : most;
+  return t;
+}
+
+inline bool linear_act_sizes_ok(int rows, int n_out, int k) {
+  return rows >= 0 && rows <= kMaxTokens && n_out >= 1 && n_out <= kMaxTokens && k >= 8 && k <= kMaxTokens && k % 8 == 0;
+}
+
 }  // namespace
 }  // namespace dit
 
@@ -1196,6 +1260,175 @@ dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev
   LinearFp8Args a{rows, n_out, k, (const uint8_t*)a_q_dev, (const uint8_t*)w_q_dev, a_scale_dev, w_scale_dev,
                   (bf16*)out_dev, ld_out, status_of(ws), reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)))};
   return cuda_status(launch_linear_fp8(a, (cudaStream_t)stream));
+}
+
+dit_status dit_add_rms_norm(int rows, int cols, const void* x_dev, long long ldx, const void* res_dev,
+                            long long ld_res, const void* w_dev, float gain_offset, float eps, void* sum_out_dev,
+                            long long ld_sum, void* y_dev, long long ldy, void* q_dev, float* scale_dev,
+                            dit_stream_t stream) {
+  if (cols < 8 || cols > 32768 || cols % 8 != 0 || (q_dev && cols % 16 != 0)) return DIT_ERR_UNSUPPORTED;
+  if (rows < 0 || rows > kMaxTextRows || !(eps >= 0.f && eps <= 3.0e38f) || !(fabsf(gain_offset) <= 3.0e38f))
+    return DIT_ERR_INVALID_ARG;
+  if ((!y_dev && !q_dev) || (q_dev == nullptr) != (scale_dev == nullptr)) return DIT_ERR_INVALID_ARG;
+  if (bad_ld(ldx, cols) || (res_dev && bad_ld(ld_res, cols)) || (sum_out_dev && bad_ld(ld_sum, cols)) ||
+      (y_dev && bad_ld(ldy, cols)))
+    return DIT_ERR_INVALID_ARG;
+  auto bad_ptr = [](const void* p) { return p && !aligned16(p); };
+  if (!aligned16(x_dev) || bad_ptr(res_dev) || bad_ptr(w_dev) || bad_ptr(sum_out_dev) || bad_ptr(y_dev) ||
+      bad_ptr(q_dev) || bad_ptr(scale_dev))
+    return DIT_ERR_INVALID_ARG;
+  if (rows == 0) return DIT_OK;
+  // a thread reads its values before it writes any: exactly in place is the one overlap allowed
+  struct Mat { const void* p; long long ld; };
+  const Mat in[2] = {{x_dev, ldx}, {res_dev, ld_res}}, out[2] = {{sum_out_dev, ld_sum}, {y_dev, ldy}};
+  const size_t nq = (size_t)rows * cols, ns = (size_t)rows * ((cols + 127) / 128) * 4;
+  for (const Mat& o : out) {
+    if (!o.p) continue;
+    for (const Mat& i : in)
+      if (i.p && !(i.p == o.p && i.ld == o.ld) && strided_overlap(i.p, i.ld, rows, cols, o.p, o.ld, rows, cols))
+        return DIT_ERR_INVALID_ARG;
+    if (w_dev && ranges_overlap(w_dev, (size_t)cols * 2, o.p, extent(rows, o.ld, cols, 2))) return DIT_ERR_INVALID_ARG;
+  }
+  if (sum_out_dev && y_dev && strided_overlap(sum_out_dev, ld_sum, rows, cols, y_dev, ldy, rows, cols))
+    return DIT_ERR_INVALID_ARG;
+  if (q_dev) {
+    for (const Mat& m : {in[0], in[1], out[0], out[1], Mat{w_dev, 0}})
+      if (m.p && (ranges_overlap(q_dev, nq, m.p, m.ld ? extent(rows, m.ld, cols, 2) : (size_t)cols * 2) ||
+                  ranges_overlap(scale_dev, ns, m.p, m.ld ? extent(rows, m.ld, cols, 2) : (size_t)cols * 2)))
+        return DIT_ERR_INVALID_ARG;
+    if (ranges_overlap(q_dev, nq, scale_dev, ns)) return DIT_ERR_INVALID_ARG;
+  }
+  AddRmsNormArgs a{rows, cols, (const bf16*)x_dev, (const bf16*)res_dev, (const bf16*)w_dev, ldx, ld_res, ld_sum, ldy,
+                   gain_offset, eps, (bf16*)sum_out_dev, (bf16*)y_dev, (uint8_t*)q_dev, scale_dev};
+  return cuda_status(launch_add_rms_norm(a, (cudaStream_t)stream));
+}
+
+dit_status dit_linear_act_workspace(int rows, int n_out, int k, size_t* bytes) {
+  if (!linear_act_sizes_ok(rows, n_out, k) || !bytes) return DIT_ERR_INVALID_ARG;
+  *bytes = sizeof(DeviceStatus) + linear_act_parts_bytes(rows, n_out, k);
+  return DIT_OK;
+}
+
+dit_status dit_linear_act(int rows, int n_out, int k, const void* a_dev, long long lda, const void* w_dev,
+                          long long ldw, const void* bias_dev, dit_activation act, const void* res_dev,
+                          long long ld_res, void* out_dev, long long ld_out, int out_f32, void* ws, size_t ws_bytes,
+                          dit_stream_t stream) {
+  if (!linear_act_sizes_ok(rows, n_out, k)) return DIT_ERR_INVALID_ARG;
+  if (act < DIT_ACT_NONE || act > DIT_ACT_SILU) return DIT_ERR_INVALID_ARG;
+  if (bad_ld(lda, k) || bad_ld(ldw, k) || bad_ld(ld_out, n_out) || (res_dev && bad_ld(ld_res, n_out)))
+    return DIT_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return DIT_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(DeviceStatus) + linear_act_parts_bytes(rows, n_out, k)) return DIT_ERR_WORKSPACE;
+  if (rows == 0) return DIT_OK;
+  if (!aligned16(a_dev) || !aligned16(w_dev) || !aligned16(out_dev) || (bias_dev && !aligned16(bias_dev)) ||
+      (res_dev && !aligned16(res_dev)))
+    return DIT_ERR_INVALID_ARG;
+  const int osz = out_f32 ? 4 : 2;
+  const size_t no = extent(rows, ld_out, n_out, osz);
+  auto clash = [&](const void* p, long long ld, long long r, long long width) {
+    return out_f32 ? ranges_overlap(out_dev, no, p, extent(r, ld, width, 2))
+                   : strided_overlap(p, ld, r, width, out_dev, ld_out, rows, n_out);
+  };
+  if (clash(a_dev, lda, rows, k) || clash(w_dev, ldw, n_out, k) ||
+      (bias_dev && ranges_overlap(out_dev, no, bias_dev, (size_t)n_out * 2)) ||
+      (res_dev && !(res_dev == out_dev && ld_res == ld_out && !out_f32) && clash(res_dev, ld_res, rows, n_out)))
+    return DIT_ERR_INVALID_ARG;
+  LinearActArgs p;
+  memset(&p, 0, sizeof(p));
+  p.rows = rows; p.n = n_out; p.k = k; p.act = act; p.out_f32 = out_f32 != 0;
+  p.a = (const bf16*)a_dev; p.w = (const bf16*)w_dev; p.bias = (const bf16*)bias_dev; p.res = (const bf16*)res_dev;
+  p.out = out_dev; p.lda = lda; p.ldw = ldw; p.ld_res = ld_res; p.ld_out = ld_out;
+  p.status = status_of(ws);
+  p.parts = reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)));
+  return cuda_status(launch_linear_act(p, (cudaStream_t)stream));
+}
+
+dit_status dit_text_cache4_bytes(const dit_text_cache4* c, size_t* bytes) {
+  DIT_TRY(check_cache4(c));
+  if (!bytes) return DIT_ERR_INVALID_ARG;
+  *bytes = cache4_bytes(cache4_of(*c));
+  return DIT_OK;
+}
+
+dit_status dit_text_cache4_append(const dit_text_cache4* c, int seqs, int rows, int max_q, const int32_t* q_off,
+                                  const int32_t* q_len, const int32_t* k_len, const int32_t* page_table,
+                                  const void* k_dev, long long ldk, const void* v_dev, long long ldv, void* cache_dev,
+                                  void* ws, size_t ws_bytes, dit_stream_t stream) {
+  DIT_TRY(check_cache4_move(c, seqs, rows, max_q, k_dev, ldk, v_dev, ldv, ws, ws_bytes));
+  if (seqs == 0 || rows == 0 || max_q == 0) return DIT_OK;
+  if (!q_off || !k_len || !page_table || !aligned4(q_off) || !aligned4(q_len) || !aligned4(k_len) ||
+      !aligned4(page_table) || !aligned16(cache_dev))
+    return DIT_ERR_INVALID_ARG;
+  Cache4MoveArgs a;
+  memset(&a, 0, sizeof(a));
+  a.c = cache4_of(*c);
+  const long long width = (long long)c->heads_k * c->head_dim;
+  if (ranges_overlap(cache_dev, cache4_bytes(a.c), k_dev, extent(rows, ldk, width, 2)) ||
+      ranges_overlap(cache_dev, cache4_bytes(a.c), v_dev, extent(rows, ldv, width, 2)))
+    return DIT_ERR_INVALID_ARG;
+  a.seqs = seqs; a.rows = rows; a.max_len = max_q < rows ? max_q : rows;
+  a.off = q_off; a.len = q_len; a.k_len = k_len; a.table = page_table;
+  a.k_in = (const bf16*)k_dev; a.v_in = (const bf16*)v_dev; a.ldk = ldk; a.ldv = ldv;
+  a.cache = (uint8_t*)cache_dev;
+  a.status = status_of(ws);
+  return cuda_status(launch_cache4_append(a, (cudaStream_t)stream));
+}
+
+dit_status dit_text_cache4_read(const dit_text_cache4* c, int seqs, int rows, int max_k, const int32_t* k_off,
+                                const int32_t* k_len, const int32_t* page_table, const void* cache_dev,
+                                void* k_out_dev, long long ldk, void* v_out_dev, long long ldv, void* ws,
+                                size_t ws_bytes, dit_stream_t stream) {
+  DIT_TRY(check_cache4_move(c, seqs, rows, max_k, k_out_dev, ldk, v_out_dev, ldv, ws, ws_bytes));
+  if (seqs == 0 || rows == 0 || max_k == 0) return DIT_OK;
+  if (!k_off || !page_table || !aligned4(k_off) || !aligned4(k_len) || !aligned4(page_table) || !aligned16(cache_dev))
+    return DIT_ERR_INVALID_ARG;
+  Cache4MoveArgs a;
+  memset(&a, 0, sizeof(a));
+  a.c = cache4_of(*c);
+  const long long width = (long long)c->heads_k * c->head_dim;
+  if (ranges_overlap(cache_dev, cache4_bytes(a.c), k_out_dev, extent(rows, ldk, width, 2)) ||
+      ranges_overlap(cache_dev, cache4_bytes(a.c), v_out_dev, extent(rows, ldv, width, 2)) ||
+      strided_overlap(k_out_dev, ldk, rows, width, v_out_dev, ldv, rows, width))
+    return DIT_ERR_INVALID_ARG;
+  const int most = c->max_pages * c->page_size;
+  a.seqs = seqs; a.rows = rows; a.max_len = max_k < rows ? max_k : rows;
+  if (a.max_len > most) a.max_len = most;
+  a.off = k_off; a.len = k_len; a.table = page_table;
+  a.k_out = (bf16*)k_out_dev; a.v_out = (bf16*)v_out_dev; a.ldk = ldk; a.ldv = ldv;
+  a.cache = (uint8_t*)const_cast<void*>(cache_dev);
+  a.status = status_of(ws);
+  return cuda_status(launch_cache4_read(a, (cudaStream_t)stream));
+}
+
+dit_status dit_text_cache4_attention_workspace(const dit_text_cache4* c, const dit_text_attn* a, size_t* bytes) {
+  DIT_TRY(check_cache4_attn(c, a));
+  if (!bytes) return DIT_ERR_INVALID_ARG;
+  *bytes = sizeof(DeviceStatus) + cache4_attention_parts_bytes(cache4_attn_sizes(*c, *a));
+  return DIT_OK;
+}
+
+dit_status dit_text_cache4_attention(const dit_text_cache4* c, const dit_text_attn* a, const int32_t* q_off,
+                                     const int32_t* q_len, const int32_t* k_len, const int32_t* page_table,
+                                     const void* q_dev, long long ldq, const void* cache_dev, void* out_dev,
+                                     long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream) {
+  DIT_TRY(check_cache4_attn(c, a));
+  const long long wq = (long long)a->heads_q * a->head_dim;
+  if (bad_ld(ldq, wq) || bad_ld(ldo, wq) || !aligned16(ws)) return DIT_ERR_INVALID_ARG;
+  Cache4AttnArgs t = cache4_attn_sizes(*c, *a);
+  if (ws_bytes < sizeof(DeviceStatus) + cache4_attention_parts_bytes(t)) return DIT_ERR_WORKSPACE;
+  if (a->seqs == 0 || a->rows_q == 0 || a->max_q == 0) return DIT_OK;
+  if (!q_off || !k_len || !page_table || !aligned4(q_off) || !aligned4(q_len) || !aligned4(k_len) ||
+      !aligned4(page_table) || !aligned16(q_dev) || !aligned16(cache_dev) || !aligned16(out_dev))
+    return DIT_ERR_INVALID_ARG;
+  if (strided_overlap(q_dev, ldq, a->rows_q, wq, out_dev, ldo, a->rows_q, wq) ||
+      ranges_overlap(cache_dev, cache4_bytes(t.c), out_dev, extent(a->rows_q, ldo, wq, 2)))
+    return DIT_ERR_INVALID_ARG;
+  t.q_off = q_off; t.q_len = q_len; t.k_len = k_len; t.table = page_table;
+  t.q = (const bf16*)q_dev; t.out = (bf16*)out_dev; t.ldq = ldq; t.ldo = ldo;
+  t.cache = (const uint8_t*)cache_dev;
+  t.status = status_of(ws);
+  t.parts = reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)));
+  return cuda_status(launch_cache4_attention(t, (cudaStream_t)stream));
 }
 
 unsigned long long dit_launch_count(void) { return g_launches.load(); }

@@ -33,7 +33,14 @@ enum KernelClass : int {
   kClsQuantBlocks = 18,    // e4m3 quantisation with a scale per block
   kClsLinearFp8Blocks = 19,  // e4m3 product with block scales
   kClsLinearFp8Join = 20,  // joining its depth splits
-  kClsCount = 21
+  kClsAddRmsNorm = 21,     // residual addition + RMSNorm (+ e4m3 blocks)
+  kClsLinearAct = 22,      // product with bias, activation and residual
+  kClsLinearActJoin = 23,  // joining its depth splits
+  kClsCache4Append = 24,   // new tokens into the 4-bit cache
+  kClsCache4Read = 25,     // tokens back out of it
+  kClsCache4Attention = 26,  // attention over it
+  kClsCache4Join = 27,     // joining its key splits
+  kClsCount = 28
 };
 
 const char* kernel_class_name(int cls);
@@ -255,5 +262,66 @@ struct LinearFp8Args {
 };
 size_t linear_fp8_parts_bytes(int rows, int n, int k);
 cudaError_t launch_linear_fp8(const LinearFp8Args& a, cudaStream_t s);
+
+struct AddRmsNormArgs {
+  int rows, cols;
+  const bf16 *x, *res, *w;  // res, w: may be null
+  long long ldx, ld_res, ld_sum, ldy;
+  float offset, eps;
+  bf16 *sum, *y;   // either may be null
+  uint8_t* q;      // null: no e4m3 output
+  float* scale;
+};
+cudaError_t launch_add_rms_norm(const AddRmsNormArgs& a, cudaStream_t s);
+
+struct LinearActArgs {
+  int rows, n, k, act, out_f32;
+  const bf16 *a, *w, *bias, *res;  // bias, res: may be null
+  void* out;
+  long long lda, ldw, ld_res, ld_out;
+  DeviceStatus* status;
+  float* parts;  // workspace of the depth splits
+};
+size_t linear_act_parts_bytes(int rows, int n, int k);
+cudaError_t launch_linear_act(const LinearActArgs& a, cudaStream_t s);
+
+constexpr uint32_t kSiteCache4Lengths = 0x801, kSiteCache4Page = 0x802;
+
+// Bytes of one head of a page: codes and scales of its keys, then of its values.
+struct Cache4 {
+  int heads, head_dim, pages, page_shift, max_pages;
+  __host__ __device__ int code_bytes() const { return (head_dim / 2) << page_shift; }
+  __host__ __device__ int scale_bytes() const { return (head_dim / 16) << page_shift; }
+  __host__ __device__ int slab() const { return 2 * (code_bytes() + scale_bytes()); }
+};
+
+// Tokens moved into or out of the cache: rows off[s] onwards of k and v.
+struct Cache4MoveArgs {
+  Cache4 c;
+  int seqs, rows, max_len;
+  const int32_t *off, *len, *k_len, *table;
+  const bf16 *k_in, *v_in;  // append
+  bf16 *k_out, *v_out;      // read
+  long long ldk, ldv;
+  uint8_t* cache;
+  DeviceStatus* status;
+};
+cudaError_t launch_cache4_append(const Cache4MoveArgs& a, cudaStream_t s);
+cudaError_t launch_cache4_read(const Cache4MoveArgs& a, cudaStream_t s);
+
+struct Cache4AttnArgs {
+  Cache4 c;
+  int seqs, heads_q, rows_q, max_q, max_k, causal;
+  float scale;
+  const int32_t *q_off, *q_len, *k_len, *table;
+  const bf16* q;
+  bf16* out;
+  long long ldq, ldo;
+  const uint8_t* cache;
+  DeviceStatus* status;
+  float* parts;  // workspace of the key splits
+};
+size_t cache4_attention_parts_bytes(const Cache4AttnArgs& a);
+cudaError_t launch_cache4_attention(const Cache4AttnArgs& a, cudaStream_t s);
 
 }  // namespace dit

@@ -18,6 +18,7 @@ DIT_OK, DIT_ERR_INVALID_ARG, DIT_ERR_UNSUPPORTED, DIT_ERR_WORKSPACE, DIT_ERR_CUD
 DIT_EPI_STORE, DIT_EPI_GATED_RESIDUAL, DIT_EPI_SWIGLU = range(3)
 DIT_ROPE_INTERLEAVED, DIT_ROPE_HALF = range(2)
 DIT_ROPE_SCALE_NONE, DIT_ROPE_SCALE_LINEAR, DIT_ROPE_SCALE_NTK, DIT_ROPE_SCALE_BY_PARTS = range(4)
+DIT_ACT_NONE, DIT_ACT_RELU, DIT_ACT_GELU, DIT_ACT_GELU_TANH, DIT_ACT_SILU = range(5)
 
 
 class DitError(RuntimeError):
@@ -85,6 +86,10 @@ class dit_text_attn(C.Structure):
                                        "causal")] + [("scale", C.c_float)]
 
 
+class dit_text_cache4(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("heads_k", "head_dim", "pages", "page_size", "max_pages")]
+
+
 _P = C.c_void_p
 _I = C.c_int
 _SZ = C.c_size_t
@@ -126,6 +131,16 @@ _SIGS = {
     "dit_quantize_blocks_fp8": (_I, [_P, _LL, _I, _I, _I, _P, _P, _P]),
     "dit_linear_fp8_blocks_workspace": (_I, [_I, _I, _I, C.POINTER(_SZ)]),
     "dit_linear_fp8_blocks": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "dit_add_rms_norm": (_I, [_I, _I, _P, _LL, _P, _LL, _P, _F, _F, _P, _LL, _P, _LL, _P, _P, _P]),
+    "dit_linear_act_workspace": (_I, [_I, _I, _I, C.POINTER(_SZ)]),
+    "dit_linear_act": (_I, [_I, _I, _I, _P, _LL, _P, _LL, _P, _I, _P, _LL, _P, _LL, _I, _P, _SZ, _P]),
+    "dit_text_cache4_bytes": (_I, [C.POINTER(dit_text_cache4), C.POINTER(_SZ)]),
+    "dit_text_cache4_append": (_I, [C.POINTER(dit_text_cache4), _I, _I, _I, _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _P, _SZ,
+                                    _P]),
+    "dit_text_cache4_read": (_I, [C.POINTER(dit_text_cache4), _I, _I, _I, _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _SZ, _P]),
+    "dit_text_cache4_attention_workspace": (_I, [C.POINTER(dit_text_cache4), C.POINTER(dit_text_attn), C.POINTER(_SZ)]),
+    "dit_text_cache4_attention": (_I, [C.POINTER(dit_text_cache4), C.POINTER(dit_text_attn), _P, _P, _P, _P, _P, _LL, _P,
+                                       _P, _LL, _P, _SZ, _P]),
     "dit_launch_count": (C.c_ulonglong, []),
     "dit_timing_begin": (_I, [_I]),
     "dit_timing_select": (_I, [C.c_uint]),
@@ -203,6 +218,10 @@ def make_text_attn(seqs, heads_q, heads_k, head_dim, rows_q, rows_k, max_q, max_
     """Sizes of a dit_text_attention call; `scale` None means 1 / sqrt(head_dim)."""
     return dit_text_attn(seqs, heads_q, heads_k, head_dim, rows_q, rows_k, max_q, max_k, 1 if causal else 0,
                          head_dim ** -0.5 if scale is None else scale)
+
+
+def make_text_cache4(heads_k, head_dim, pages, page_size, max_pages) -> dit_text_cache4:
+    return dit_text_cache4(heads_k, head_dim, pages, page_size, max_pages)
 
 
 # ---------------------------------------------------------------------------------- calls
@@ -379,6 +398,60 @@ def dit_linear_fp8_blocks(rows, n_out, k, a_q_dev, a_scale_dev, w_q_dev, w_scale
     _check("dit_linear_fp8_blocks", lib().dit_linear_fp8_blocks(
         rows, n_out, k, _ptr(a_q_dev), _ptr(a_scale_dev), _ptr(w_q_dev), _ptr(w_scale_dev), _ptr(out_dev), ld_out,
         _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dit_add_rms_norm(rows, cols, x_dev, ldx, res_dev, ld_res, w_dev, gain_offset, eps, sum_out_dev, ld_sum, y_dev, ldy,
+                     q_dev, scale_dev, stream=None):
+    _check("dit_add_rms_norm", lib().dit_add_rms_norm(
+        rows, cols, _ptr(x_dev), ldx, _ptr(res_dev), ld_res, _ptr(w_dev), gain_offset, eps, _ptr(sum_out_dev), ld_sum,
+        _ptr(y_dev), ldy, _ptr(q_dev), _ptr(scale_dev), _stream(stream)))
+
+
+def dit_linear_act_workspace(rows, n_out, k) -> int:
+    n = _SZ(0)
+    _check("dit_linear_act_workspace", lib().dit_linear_act_workspace(rows, n_out, k, C.byref(n)))
+    return n.value
+
+
+def dit_linear_act(rows, n_out, k, a_dev, lda, w_dev, ldw, bias_dev, act, res_dev, ld_res, out_dev, ld_out, out_f32, ws,
+                   ws_bytes, stream=None):
+    _check("dit_linear_act", lib().dit_linear_act(
+        rows, n_out, k, _ptr(a_dev), lda, _ptr(w_dev), ldw, _ptr(bias_dev), act, _ptr(res_dev), ld_res, _ptr(out_dev),
+        ld_out, 1 if out_f32 else 0, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dit_text_cache4_bytes(c: dit_text_cache4) -> int:
+    n = _SZ(0)
+    _check("dit_text_cache4_bytes", lib().dit_text_cache4_bytes(C.byref(c), C.byref(n)))
+    return n.value
+
+
+def dit_text_cache4_append(c: dit_text_cache4, seqs, rows, max_q, q_off, q_len, k_len, page_table, k_dev, ldk, v_dev, ldv,
+                           cache_dev, ws, ws_bytes, stream=None):
+    _check("dit_text_cache4_append", lib().dit_text_cache4_append(
+        C.byref(c), seqs, rows, max_q, _ptr(q_off), _ptr(q_len), _ptr(k_len), _ptr(page_table), _ptr(k_dev), ldk,
+        _ptr(v_dev), ldv, _ptr(cache_dev), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dit_text_cache4_read(c: dit_text_cache4, seqs, rows, max_k, k_off, k_len, page_table, cache_dev, k_out_dev, ldk,
+                         v_out_dev, ldv, ws, ws_bytes, stream=None):
+    _check("dit_text_cache4_read", lib().dit_text_cache4_read(
+        C.byref(c), seqs, rows, max_k, _ptr(k_off), _ptr(k_len), _ptr(page_table), _ptr(cache_dev), _ptr(k_out_dev), ldk,
+        _ptr(v_out_dev), ldv, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dit_text_cache4_attention_workspace(c: dit_text_cache4, a: dit_text_attn) -> int:
+    n = _SZ(0)
+    _check("dit_text_cache4_attention_workspace",
+           lib().dit_text_cache4_attention_workspace(C.byref(c), C.byref(a), C.byref(n)))
+    return n.value
+
+
+def dit_text_cache4_attention(c: dit_text_cache4, a: dit_text_attn, q_off, q_len, k_len, page_table, q_dev, ldq, cache_dev,
+                              out_dev, ldo, ws, ws_bytes, stream=None):
+    _check("dit_text_cache4_attention", lib().dit_text_cache4_attention(
+        C.byref(c), C.byref(a), _ptr(q_off), _ptr(q_len), _ptr(k_len), _ptr(page_table), _ptr(q_dev), ldq, _ptr(cache_dev),
+        _ptr(out_dev), ldo, _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def dit_modulation_static(w: dit_weights, sigma_dev, batch: int, mod_dev, stream=None):

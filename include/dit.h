@@ -362,7 +362,7 @@ dit_status dit_attention(int batch, int heads, int n, const void* q_dev, const v
  * with other lengths.  The host cannot see them: the kernels check each one, and an entry
  * that is out of range is skipped (what it would have written stays as it was) and recorded
  * in the workspace status word, which dit_sync_status then reports as
- * DIT_ERR_INVALID_ARG with the site id 0x501 (attention) or 0x601 (rotation). */
+ * DIT_ERR_INVALID_ARG with the site id 0x501 (attention), 0x601 (rotation), 0x801 or 0x802 (4-bit cache). */
 
 /* Which values of a head turn together: adjacent pairs (2j, 2j + 1), or the halves
  * (j, j + rot_dim / 2) of the head's first rot_dim values. */
@@ -496,6 +496,117 @@ dit_status dit_linear_fp8_blocks_workspace(int rows, int n_out, int k, size_t* b
 dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev, const float* a_scale_dev,
                                  const void* w_q_dev, const float* w_scale_dev, void* out_dev, int ld_out, void* ws,
                                  size_t ws_bytes, dit_stream_t stream);
+
+/* The residual's addition and the RMSNorm behind it, in one pass.  For each row:
+ *   s = x + res                                   (res_dev NULL: s = x)
+ *   y = s / sqrt(mean(s^2) + eps) * (gain_offset + w)      (w_dev NULL: w = 1)
+ * in fp32, y from the unrounded s.  Outputs, each one optional but y_dev or q_dev: sum_out_dev, s rounded to
+ * bf16; y_dev, y rounded to bf16; q_dev and scale_dev (both or neither), y in e4m3 with a scale per 128 values
+ * of a row, as dit_quantize_blocks_fp8 with block_rows 1 takes them from a matrix: q_dev [rows, cols]
+ * contiguous, scale_dev [rows, ceil(cols / 128)], the operand of dit_linear_fp8_blocks; the codes are of
+ * the unrounded y.  Squares are summed in fp32: rows whose values stay below 2^56 cannot overflow them.
+ * x, res, sum and y have row strides ld*, % 8 == 0, >= cols, <= 2^24; w_dev [cols] bf16.  sum_out_dev and y_dev may
+ * each be x_dev or res_dev itself (same pointer and stride); any other overlap of outputs with inputs or with
+ * one another is DIT_ERR_INVALID_ARG.  cols % 8 == 0 (q_dev: % 16), 8 <= cols <= 32768, 0 <= rows <= 2^26;
+ * eps >= 0 and gain_offset finite. */
+dit_status dit_add_rms_norm(int rows, int cols, const void* x_dev, long long ldx, const void* res_dev,
+                            long long ld_res, const void* w_dev, float gain_offset, float eps, void* sum_out_dev,
+                            long long ld_sum, void* y_dev, long long ldy, void* q_dev, float* scale_dev,
+                            dit_stream_t stream);
+
+/* Activations of dit_linear_act, of z in fp32: max(z, 0); z Phi(z) = z (1 + erf(z / sqrt 2)) / 2; the same with
+ * Phi(z) ~ 1 / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))); z / (1 + exp(-z)).  A NaN stays NaN in all of them. */
+typedef enum {
+  DIT_ACT_NONE = 0,
+  DIT_ACT_RELU = 1,
+  DIT_ACT_GELU = 2,
+  DIT_ACT_GELU_TANH = 3,
+  DIT_ACT_SILU = 4
+} dit_activation;
+
+/* Bytes of workspace that dit_linear_act needs (at least the 256 of the status word; more where the
+ * depth of few tiles is split over the GPU, at most 48 MB). */
+dit_status dit_linear_act_workspace(int rows, int n_out, int k, size_t* bytes);
+
+/* Linear layer with bias, activation and residual in its epilogue:
+ *   out[r, c] = act(sum_i a[r, i] w[c, i] + bias[c]) + res[r, c]
+ * everything after the bf16 operands in fp32, rounded once, to bf16, or not at all (out_f32 != 0: out_dev holds
+ * fp32).  a_dev [rows, k], w_dev [n_out, k], res_dev and out_dev [rows, n_out] with row strides ld* in elements
+ * (% 8 == 0, at least the row, <= 2^24); bias_dev [n_out] bf16.  bias_dev and res_dev may be NULL.  res_dev may be
+ * out_dev itself (same stride, bf16); any other overlap of out_dev with an operand is DIT_ERR_INVALID_ARG.
+ * Columns of out_dev from n_out on are not written.  k % 8 == 0, 8 <= k <= 2^20, 1 <= n_out <= 2^20, any n_out,
+ * 0 <= rows <= 2^20.  The order of sums depends only on the sizes: equal calls give equal bits. */
+dit_status dit_linear_act(int rows, int n_out, int k, const void* a_dev, long long lda, const void* w_dev,
+                          long long ldw, const void* bias_dev, dit_activation act, const void* res_dev,
+                          long long ld_res, void* out_dev, long long ld_out, int out_f32, void* ws, size_t ws_bytes,
+                          dit_stream_t stream);
+
+/* A paged cache of keys and values in 4 bits.  The cache is one buffer of `pages` pages of page_size tokens (16, 32,
+ * 64, 128 or 256), each with heads_k heads of head_dim (64 or 128) values.  Every 32 neighbouring values of a
+ * token's head share a scale:
+ *   m = max(max|x|, 7 * 2^-118),  scale = bf16(m / 7),  n = rint(x * (1 / scale)),  value = n * scale,
+ * n from -7 to 7, each operation rounded to fp32.  Where one of the 32 is infinite or NaN the scale is NaN, and all
+ * of them read as NaN.
+ * Layout (for callers that save, move or share pages; page_bytes as dit_text_cache4_bytes / pages): page p, head h
+ * at (p * heads_k + h) * page_size * head_dim * 9 / 8 bytes, there
+ *   key codes   [page_size][head_dim / 2] bytes,   key scales   [page_size][head_dim / 32] bf16,
+ *   value codes [page_size][head_dim / 2] bytes,   value scales [page_size][head_dim / 32] bf16.
+ * A code is n + 8, the even one of two in the low half of their byte.  A row of key codes is 32-bit words of 8
+ * values, word t * (head_dim / 32) + j (t < 4) with the values 32 j + 8 t onwards; a row of value codes is 16-bit words
+ * of 4, word g * (head_dim / 32) + j (g < 8) with the values 32 j + 4 g onwards.
+ * Token i of sequence s lies in page page_table[s * max_pages + i / page_size] (int32, device), row
+ * i % page_size.  Sequences may share pages for reading.
+ * 1 <= heads_k <= 1024, 1 <= pages <= 2^24, max_pages >= 1, max_pages * page_size <= 2^24. */
+typedef struct {
+  int heads_k, head_dim, pages, page_size, max_pages;
+} dit_text_cache4;
+
+/* Bytes of the cache's buffer. */
+dit_status dit_text_cache4_bytes(const dit_text_cache4* c, size_t* bytes);
+
+/* Quantise the keys and values of new tokens into the cache.  Sequence s brings the rows [q_off[s], q_off[s] + nq)
+ * of k_dev and v_dev (nq = q_len[s], or q_off[s + 1] - q_off[s] where q_len is NULL), which become its tokens
+ * k_len[s] - nq .. k_len[s] - 1: k_len, the sequences' lengths with the new tokens, is the same array that
+ * dit_text_cache4_attention takes.  `rows` rows in the buffers, max_q an upper bound of nq (0 .. 2^24).  Head h of
+ * row r is at k_dev + r * ldk + h * head_dim, v likewise; all bf16.  A sequence whose lengths are out of range
+ * (nq > max_q, rows outside the buffer, nq > k_len, k_len > max_pages * page_size) writes nothing and a token whose page is
+ * outside [0, pages) is not written; both are recorded (sites 0x801 and 0x802).  Two tokens of one call that are to lie in
+ * one place leave there any mixture of the two; every other place is unaffected.  k_dev and v_dev
+ * must not overlap the cache.  0 <= seqs <= 16384, 0 <= rows <= 2^28; ld* % 8 == 0, >= heads_k * head_dim,
+ * <= 2^24.  ws: any workspace of >= 256 bytes. */
+dit_status dit_text_cache4_append(const dit_text_cache4* c, int seqs, int rows, int max_q, const int32_t* q_off,
+                                  const int32_t* q_len, const int32_t* k_len, const int32_t* page_table,
+                                  const void* k_dev, long long ldk, const void* v_dev, long long ldv, void* cache_dev,
+                                  void* ws, size_t ws_bytes, dit_stream_t stream);
+
+/* The tokens of whole sequences back in bf16 (n * scale, rounded): token i of sequence s, i < nk = k_len[s] (or
+ * k_off[s + 1] - k_off[s] where k_len is NULL), to row k_off[s] + i of k_out_dev and v_out_dev, which have `rows` rows;
+ * max_k is an upper bound of nk (0 .. 2^24).  For many query rows over a cache (a further chunk of a long prompt)
+ * this and dit_text_attention on its output are faster than dit_text_cache4_attention.  Lengths out of
+ * range and pages outside the cache as in dit_text_cache4_append: their rows are left as they were, and recorded.  Sequences' rows
+ * must not overlap.  Other limits as dit_text_cache4_append. */
+dit_status dit_text_cache4_read(const dit_text_cache4* c, int seqs, int rows, int max_k, const int32_t* k_off,
+                                const int32_t* k_len, const int32_t* page_table, const void* cache_dev,
+                                void* k_out_dev, long long ldk, void* v_out_dev, long long ldv, void* ws,
+                                size_t ws_bytes, dit_stream_t stream);
+
+/* Bytes of workspace that dit_text_cache4_attention needs for these sizes (at least the 256 of the status word; more where
+ * the keys of a sequence are split over the GPU). */
+dit_status dit_text_cache4_attention_workspace(const dit_text_cache4* c, const dit_text_attn* a, size_t* bytes);
+
+/* dit_text_attention over the cache: the same sums with the keys and values that the cache holds.  Sequence s has
+ * the nk = k_len[s] tokens of its page table as keys, and the queries [q_off[s], q_off[s] + nq).  What `a` says holds as
+ * there (heads_k and head_dim as in `c`; rows_k is not used; causal: the last query sees the last key), and so does
+ * what is said there of queries without keys, of rows that belong to no sequence, and of values behind a
+ * sequence's keys.  Scores from exact products of the bf16 queries and the cache's integers, scaled and summed in fp32;
+ * probabilities times the values' scales are rounded to bf16 for the product with V.  A key on a page outside
+ * [0, pages) is left out of the sums, and recorded (0x802); a sequence whose lengths are out of range is skipped, and
+ * recorded (0x801).  Meant for few queries per sequence: every 16 rows (tokens x heads_q / heads_k) of a key head read its
+ * cache once.  out_dev must not overlap q_dev or the cache; page_table is not read behind a sequence's last token. */
+dit_status dit_text_cache4_attention(const dit_text_cache4* c, const dit_text_attn* a, const int32_t* q_off,
+                                     const int32_t* q_len, const int32_t* k_len, const int32_t* page_table,
+                                     const void* q_dev, long long ldq, const void* cache_dev, void* out_dev,
+                                     long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream);
 
 /* ---- Allocation-free variant -------------------------------------------------------- */
 
