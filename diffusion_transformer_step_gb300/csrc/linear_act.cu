@@ -67,62 +67,81 @@ __device__ __forceinline__ float2 activate(float2 z) {
   return z;
 }
 
-__device__ __forceinline__ float2 activate_by(float2 z, int act) {
-  switch (act) {
-    case 1: return activate<1>(z);
-    case 2: return activate<2>(z);
-    case 3: return activate<3>(z);
-    case 4: return activate<4>(z);
-    default: return z;
+constexpr int kAnyAct = -1;  // looked up at run time
+
+template <int kAct>
+__device__ __forceinline__ void activate4(float2& a, float2& b, int act) {
+  if constexpr (kAct != kAnyAct) {
+    a = activate<kAct>(a);
+    b = activate<kAct>(b);
+  } else if (act != 0) {
+    if (act == 1) activate4<1>(a, b, 1);
+    else if (act == 2) activate4<2>(a, b, 2);
+    else if (act == 3) activate4<3>(a, b, 3);
+    else activate4<4>(a, b, 4);
   }
 }
 
-// Four neighbouring columns [c, c + 4) of row r, c % 4 == 0 and c < n: rows are 16-byte aligned, so that
-// only the last group of a row may need single values.
-__device__ __forceinline__ void finish4(const LinearActArgs& p, long long r, int c, float4 v) {
+// Four neighbouring values [c, c + 4) of a row of n, c % 4 == 0 and c < n: rows are 16-byte aligned, so that only
+// the last group of a row may need single ones.
+__device__ __forceinline__ uint2 load4(const bf16* row, int c, int n) {
+  if (c + 4 <= n) return *reinterpret_cast<const uint2*>(row + c);
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(row + c);
+  uint2 u = make_uint2(s[0], 0u);
+  if (c + 1 < n) u.x |= (uint32_t)s[1] << 16;
+  if (c + 2 < n) u.y = s[2];
+  return u;
+}
+
+// Sums v of columns [c, c + 4) of row r to the output; bias and res as load4 gives them.
+template <int kAct>
+__device__ __forceinline__ void finish4(const LinearActArgs& p, long long r, int c, float4 v, uint2 bias, uint2 res) {
   const bool whole = c + 4 <= p.n;
-  float f[4] = {v.x, v.y, v.z, v.w};
-  float b[4] = {0.f, 0.f, 0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f};
-  auto load = [&](const bf16* src, float (&to)[4]) {
-    if (whole) {
-      const uint2 u = *reinterpret_cast<const uint2*>(src);
-      const float2 lo = unpack_bf16x2(u.x), hi = unpack_bf16x2(u.y);
-      to[0] = lo.x, to[1] = lo.y, to[2] = hi.x, to[3] = hi.y;
-    } else {
-      for (int e = 0; c + e < p.n; ++e) to[e] = __bfloat162float(src[e]);
-    }
-  };
-  if (p.bias) load(p.bias + c, b);
-  if (p.res) load(p.res + r * p.ld_res + c, x);
-  float2 lo = activate_by(make_float2(f[0] + b[0], f[1] + b[1]), p.act);
-  float2 hi = activate_by(make_float2(f[2] + b[2], f[3] + b[3]), p.act);
-  if (p.res) lo.x += x[0], lo.y += x[1], hi.x += x[2], hi.y += x[3];
-  f[0] = lo.x, f[1] = lo.y, f[2] = hi.x, f[3] = hi.y;
+  float2 lo = make_float2(v.x, v.y), hi = make_float2(v.z, v.w);
+  if (p.bias) {
+    lo = __fadd2_rn(lo, unpack_bf16x2(bias.x));
+    hi = __fadd2_rn(hi, unpack_bf16x2(bias.y));
+  }
+  activate4<kAct>(lo, hi, p.act);
+  if (p.res) {
+    lo = __fadd2_rn(lo, unpack_bf16x2(res.x));
+    hi = __fadd2_rn(hi, unpack_bf16x2(res.y));
+  }
   if (p.out_f32) {
     float* o = reinterpret_cast<float*>(p.out) + r * p.ld_out + c;
-    if (whole) *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
-    else
-      for (int e = 0; c + e < p.n; ++e) o[e] = f[e];
+    if (whole) {
+      *reinterpret_cast<float4*>(o) = make_float4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+      o[0] = lo.x;
+      if (c + 1 < p.n) o[1] = lo.y;
+      if (c + 2 < p.n) o[2] = hi.x;
+    }
   } else {
     bf16* o = reinterpret_cast<bf16*>(p.out) + r * p.ld_out + c;
-    if (whole) *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-    else
-      for (int e = 0; c + e < p.n; ++e) o[e] = __float2bfloat16(f[e]);
+    const uint2 u = make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
+    if (whole) {
+      *reinterpret_cast<uint2*>(o) = u;
+    } else {
+      uint16_t* h = reinterpret_cast<uint16_t*>(o);
+      h[0] = (uint16_t)u.x;
+      if (c + 1 < p.n) h[1] = (uint16_t)(u.x >> 16);
+      if (c + 2 < p.n) h[2] = (uint16_t)u.y;
+    }
   }
 }
 
-// 32 columns [c, c + 32) of one row, all below n.
+// 32 columns [c, c + 32) of one row, all below n; res: that piece of the residual.
 template <int kAct>
-__device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, int c, const uint32_t (&v)[32]) {
-  auto load8 = [](const bf16* src, float2 (&f)[4]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, int c, const uint32_t (&v)[32],
+                                         const uint4 (&res)[4]) {
+  auto eight = [](const uint4& u, float2 (&f)[4]) {
     f[0] = unpack_bf16x2(u.x), f[1] = unpack_bf16x2(u.y), f[2] = unpack_bf16x2(u.z), f[3] = unpack_bf16x2(u.w);
   };
   float2 o[16];
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float2 b[4];
-    if (p.bias) load8(p.bias + c + g * 8, b);
+    if (p.bias) eight(__ldg(reinterpret_cast<const uint4*>(p.bias + c + g * 8)), b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 z = make_float2(__uint_as_float(v[g * 8 + 2 * i]), __uint_as_float(v[g * 8 + 2 * i + 1]));
@@ -131,11 +150,10 @@ __device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, in
     }
   }
   if (p.res) {
-    const bf16* src = p.res + r * p.ld_res + c;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       float2 x[4];
-      load8(src + g * 8, x);
+      eight(res[g], x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[g * 4 + i] = __fadd2_rn(o[g * 4 + i], x[i]);
     }
@@ -160,6 +178,42 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+// The rows r0, r0 + step, ... below `rows` (of the output: m0 further), four columns from c on per thread; part(r, k) is what
+// rank k's shared memory holds of them, added in rank order.  Parts and residual of one row are fetched ahead of the
+// arithmetic of the row before.  Not unrolled further: a loop that runs a few times waits for its code as
+// much as for its data (128 rows of one block of depth, eight rows at once: 8.8 us, two 6.4).
+template <int K, typename Part>
+__device__ __forceinline__ void finish_rows(const Params& P, int r0, int step, int rows, int m0, int c, Part part) {
+  const LinearActArgs& p = P.a;
+  struct Row {
+    float4 v[K];
+    uint2 res;
+  };
+  auto load = [&](int r, Row& x) {
+    x.res = make_uint2(0, 0);
+    if (r < rows && p.res) x.res = load4(p.res + (long long)(m0 + r) * p.ld_res, c, p.n);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      x.v[k] = r < rows && (K == 1 || k < P.splits) ? part(r, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  const uint2 bias = p.bias ? load4(p.bias, c, p.n) : make_uint2(0, 0);
+  auto finish = [&](int r, const Row& x) {
+    float4 sum = x.v[0];
+#pragma unroll
+    for (int k = 1; k < K; ++k) sum.x += x.v[k].x, sum.y += x.v[k].y, sum.z += x.v[k].z, sum.w += x.v[k].w;
+    if (r < rows) finish4<kAnyAct>(p, m0 + r, c, sum, bias, x.res);
+  };
+  Row one, two;
+  load(r0, one);
+#pragma unroll 1
+  for (int r = r0; r < rows; r += 2 * step) {
+    load(r + step, two);
+    finish(r, one);
+    load(r + 2 * step, one);
+    finish(r + step, two);
+  }
 }
 
 // ---- many rows -------------------------------------------------------------------------------
@@ -311,19 +365,34 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
     int local = 0;
     for (int t = first; t < P.tiles; t += step, ++local) {
       const int acc = local & 1;
+      const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
+      const int r = q * 32 + lane, row = mt * 256 + (int)half * 128 + r, col = nt * 256 + eh * 128;
+      // the residual's pieces one ahead, the first before the accumulator is waited for
+      uint4 ahead[4];
+      auto fetch = [&](int c) {
+        if (kSplit || !P.a.res || row >= P.a.rows || c + 32 > P.a.n) return;
+        const uint4* src = reinterpret_cast<const uint4*>(P.a.res + row * P.a.ld_res + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ahead[i] = src[i];
+      };
+      fetch(col);
       bool ok = mbar_wait_sleep(&acc_full[acc], (uint32_t)(local >> 1) & 1u, wc, kSiteAccFull);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
       const uint32_t tb = tmem + (uint32_t)(acc * 256 + eh * 128) + ((uint32_t)(q * 32) << 16);
-      const int r = q * 32 + lane, row = mt * 256 + (int)half * 128 + r, col = nt * 256 + eh * 128;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
+        const int cc = col + c * 32;
+        if (cc >= P.a.n) break;
+        uint4 res[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) res[i] = ahead[i];
+        if (c < 3) fetch(cc + 32);
         uint32_t v[32];
         tmem_load32(tb + c * 32, v);
         if (kSplit) {
-          // 16-byte pieces of a row turned by the row's number, so that a quarter warp's rows lie in different banks
+          // 16-byte pieces of a row are turned by the row's number, so that eight rows lie in different banks
           float4* part = reinterpret_cast<float4*>(smem) + r * 64;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -331,15 +400,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
                 make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
                             __uint_as_float(v[4 * i + 3]));
         } else if (row < P.a.rows) {
-          const int cc = col + c * 32;
           if (cc + 32 <= P.a.n) {
-            finish32<kAct>(P.a, row, cc, v);
+            finish32<kAct>(P.a, row, cc, v, res);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (cc + 4 * i < P.a.n)
-                finish4(P.a, row, cc + 4 * i, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                                          __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+              if (cc + 4 * i < P.a.n) {
+                uint2 b4 = make_uint2(0, 0), r4 = b4;
+                if (P.a.bias) b4 = load4(P.a.bias, cc + 4 * i, P.a.n);
+                if (P.a.res) r4 = load4(P.a.res + row * P.a.ld_res, cc + 4 * i, P.a.n);
+                finish4<kAct>(P.a, row, cc + 4 * i, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                                __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
+                              b4, r4);
+              }
           }
         }
       }
@@ -355,23 +428,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
     cluster_sync_all();  // all parts are written
     const int nt = first / P.m_tiles, mt = first - nt * P.m_tiles;
     if (warp >= 2 && first < P.tiles && !*abort_flag) {
-      // this CTA's share of its half's rows, one row per warp
-      for (int r = split + (warp - 2) * S; r < 128; r += 8 * S) {
-        const int row = mt * 256 + (int)half * 128 + r;
-        if (row >= P.a.rows) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = nt * 256 + h * 128 + lane * 4;
-          if (c >= P.a.n) continue;
-          const uint32_t at = smem_u32(smem) + (uint32_t)(r * 64 + ((h * 32 + lane) ^ (r & 7))) * 16;
-          float4 v[4], sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = k < S ? ld_cluster_f32x4(map_to_rank(at, 2 * k + half)) : sum;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sum.x += v[k].x, sum.y += v[k].y, sum.z += v[k].z, sum.w += v[k].w;
-          finish4(P.a, row, c, sum);
-        }
-      }
+      // this CTA's share of its half's rows: 128 columns of one row per warp
+      const int m0 = mt * 256 + (int)half * 128, h = warp & 1, c = nt * 256 + h * 128 + lane * 4;
+      auto at = [&](int r) { return smem_u32(smem) + (uint32_t)(r * 64 + ((h * 32 + lane) ^ (r & 7))) * 16; };
+      if (c < P.a.n)
+        finish_rows<4>(P, split + ((warp - 2) >> 1) * S, 4 * S, min(128, P.a.rows - m0), m0, c, [&](int r, int k) {
+          return ld_cluster_f32x4(map_to_rank(at(r), 2 * k + half));
+        });
     }
   }
   __syncwarp();
@@ -394,6 +457,7 @@ struct Few {
   static constexpr uint32_t kTmem = T < 32 ? 32 : T;
   static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256;
   static_assert((size_t)kStages * kStage >= (size_t)T * 128 * 4, "the part reuses the ring");
+  static_assert(kThreads == 256, "eight warps finish");
 };
 
 __device__ __forceinline__ void umma1(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -509,19 +573,19 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
   // Every rank leaves its part [row][column] in its own shared memory: all loads have landed and all MMAs read them
   // when `done` arrives.
   float* part = reinterpret_cast<float*>(smem);
-  if (warp >= 4) {
-    bool ok = mbar_wait_sleep(done, 0, wc, kSiteAccFull);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
+  __syncwarp();
+  bool ok = mbar_wait_sleep(done, 0, wc, kSiteAccFull);
+  ok = __all_sync(0xffffffffu, ok);
+  tc_fence_after();
+  if (ok && !*abort_flag) {
+    // warp w reads the columns [16, 32, ...) of its half, of the rows of its quarter
     const int q = warp & 3;
-    if (ok && !*abort_flag) {
 #pragma unroll 1
-      for (int c = 0; c < T && c < P.a.rows; c += 16) {
-        uint32_t v[16];
-        tmem_load16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+    for (int c = (warp >> 2) * 16; c < T && c < P.a.rows; c += 32) {
+      uint32_t v[16];
+      tmem_load16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part[(c + e) * 128 + q * 32 + lane] = __uint_as_float(v[e]);
-      }
+      for (int e = 0; e < 16; ++e) part[(c + e) * 128 + q * 32 + lane] = __uint_as_float(v[e]);
     }
   }
   __syncwarp();
@@ -529,16 +593,13 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
   cluster_sync_all();
   const int c = nb * 128 + lane * 4;
   if (c < P.a.n && !*abort_flag) {
-    // a row per warp, every S-th row a rank's, the parts added in rank order
-    for (int r = rank + warp * S; r < P.a.rows; r += S * (L::kThreads / 32)) {
-      const uint32_t at = smem_u32(part + r * 128 + lane * 4);
-      float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = k < S ? ld_cluster_f32x4(map_to_rank(at, k)) : sum;  // all on their way
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum.x += v[k].x, sum.y += v[k].y, sum.z += v[k].z, sum.w += v[k].w;
-      finish4(P.a, r, c, sum);
-    }
+    // a row per warp, every S-th row a rank's
+    const float* at = part + lane * 4;
+    auto remote = [&](int r, int k) { return ld_cluster_f32x4(map_to_rank(smem_u32(at + r * 128), k)); };
+    if (S == 1)
+      finish_rows<1>(P, warp, 8, P.a.rows, 0, c, [&](int r, int) { return *reinterpret_cast<const float4*>(at + r * 128); });
+    else if (S <= 4) finish_rows<4>(P, rank + warp * S, 8 * S, P.a.rows, 0, c, remote);
+    else finish_rows<8>(P, rank + warp * S, 8 * S, P.a.rows, 0, c, remote);
   }
   __syncwarp();
   cluster_sync_all();  // no rank leaves while another reads its part
@@ -636,11 +697,15 @@ Shape few_shape_of(int rows, int splits) {
        : rows <= 128 ? few_shape<128>(splits) : few_shape<256>(splits);
 }
 
-// Splits of the depth: as many as still run at once, of two blocks at least.
+// Splits of the depth: as many as still run at once, of two blocks at least.  (The clusters that the runtime says run
+// at once count one CTA per SM; two are placed where they fit.)
 int few_splits(int rows, int n, int kblocks) {
   const int blocks = (n + 127) / 128, most = kblocks / 2;
   int S = most < 8 ? most : 8;
+  const int start = S;
   while (S > 1 && blocks > clusters_at_once(few_shape_of(rows, S))) --S;
+  if (S < 3 && rows <= 64)  // two CTAs per SM
+    for (S = start; S > 1 && blocks > 2 * clusters_at_once(few_shape_of(rows, S));) --S;
   return S > 1 ? S : 1;
 }
 
@@ -687,7 +752,7 @@ cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
 size_t linear_act_parts_bytes(int, int, int) { return 0; }
 
 cudaError_t launch_linear_act(const LinearActArgs& a, cudaStream_t s) {
-  if (a.rows <= 128) return launch_few(a, s);
+  if (a.rows <= 128 || (a.rows <= 256 && few_splits(a.rows, a.n, (a.k + 63) / 64) >= 4)) return launch_few(a, s);
   return launch_wide(a, s);
 }
 
