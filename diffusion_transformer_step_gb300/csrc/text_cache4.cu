@@ -5,8 +5,12 @@
 // of a row are ordered for the attention's matrix fragments: a lane of four finds its eight values of every group of
 // 32 keys side by side, a lane of eight its four of every group of 32 values.
 #include <math.h>
+#include <string.h>
+
+#include <atomic>
 
 #include "runtime.h"
+#include "text_join.cuh"
 
 namespace dit {
 
@@ -113,56 +117,548 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 
 // ---- attention ----------------------------------------------------------------------------------
 
-// One warp per query token and head: a lane holds D / 32 values of the query and of the output.
+// One CTA takes a run of keys of one sequence and key head for up to 8 NT query rows (tokens x heads of the
+// group): warp 4 brings stages of 128 tokens in by bulk copies, page by page, and warps 0 to 3 take 32 tokens of a
+// stage each through mma.sync with a running maximum and sum of their own, which add up at the end in order. Runs of
+// several CTAs are joined by a second kernel.
+//
+// The tokens are the rows of both products, the few queries their columns: S^T = K Q^T and O^T = V^T P^T. Codes
+// become bf16 operands without a conversion: a code c under the bits of 128 is the number 128 + c, one masked
+// word per two values.  For the scores the 136 = 128 + 8 that is too much is taken off by what the accumulator starts
+// with, -136 sum(q) per group of 32; group sums are exact products in fp32, times the key's scale.  For the values it
+// is subtracted (exactly), since a sum over thousands of tokens would lose by it.  The values' scales, one per
+// token and 32 values, belong to the index that the product sums over: they go into the probabilities.
+constexpr int kKeys = 128, kStages = 3, kThreads = 160;
+
+enum : uint32_t { kSiteCache4Full = 0x811, kSiteCache4Empty };
+
+struct Plan {
+  int rows, tile, tiles, walk;  // query rows per key head, of a CTA, tiles, tiles side by side
+  int chunk, splits;            // keys per CTA, CTAs per sequence, head and tile
+};
+
+struct Params {
+  Cache4AttnArgs a;
+  int group, rows, tiles, walk, chunk, splits;
+  float scale_log2;
+  float2* ml;
+  float* o;
+};
+
+Plan make_plan(const Cache4AttnArgs& a) {
+  Plan p;
+  const long long G = a.heads_q / a.c.heads, rows = (long long)a.max_q * G, heads = (long long)a.seqs * a.c.heads;
+  p.rows = (int)(rows < (1ll << 30) ? rows : (1ll << 30));
+  p.tile = rows <= 8 ? 8 : 16;
+  p.tiles = (p.rows + p.tile - 1) / p.tile;
+  const long long items = heads * p.tiles < (1ll << 30) ? heads * p.tiles : (1ll << 30);
+  long long chunk = (long long)a.max_k * items / (6 * 152);
+  if (chunk > 1024) chunk = 1024;
+  // no more than 2^17 rows of parts (68 MB): splits <= 2^16 / rows + 1, one split past 2^16 rows
+  const long long all = heads <= (1 << 16) ? heads * p.rows : (1 << 17);
+  const long long least = all <= (1 << 16) ? ((a.max_k * all) >> 16) + 1 : a.max_k;
+  if (chunk < least) chunk = least;
+  if (chunk > a.max_k) chunk = a.max_k;
+  if (chunk < 256) chunk = 256;
+  p.chunk = (int)((chunk + kKeys - 1) / kKeys * kKeys);
+  p.splits = (a.max_k + p.chunk - 1) / p.chunk;
+  if (p.splits < 1) p.splits = 1;
+  const long long most = (1ll << 30) / (heads * p.splits);
+  p.walk = p.tiles < most ? p.tiles : (int)(most < 1 ? 1 : most);
+  return p;
+}
+
+struct Parts {
+  size_t ml, o, total;
+};
+Parts parts_of(const Plan& p, const Cache4AttnArgs& a) {
+  const size_t n = p.splits > 1 ? (size_t)a.seqs * a.c.heads * p.splits * p.rows : 0;
+  Parts l;
+  l.ml = 0;
+  l.o = (n * 8 + 255) & ~size_t(255);
+  l.total = l.o + n * (size_t)a.c.head_dim * 4;
+  return l;
+}
+
+struct Span {
+  int q0, nq, nk;
+  bool ok;
+};
+__device__ __forceinline__ Span load_span(const Cache4AttnArgs& a, int s) {
+  Span r;
+  r.q0 = a.q_off[s];
+  const long long nq = a.q_len ? (long long)a.q_len[s] : (long long)a.q_off[s + 1] - r.q0;
+  r.nk = a.k_len[s];
+  r.ok = r.q0 >= 0 && nq >= 0 && nq <= a.max_q && r.q0 + nq <= a.rows_q && r.nk >= 0 && r.nk <= a.max_k;
+  r.nq = r.ok ? (int)nq : 0;
+  return r;
+}
+
+// Keys that the query rows [base, base + rows) of a sequence see: those of the last one.
+__device__ __forceinline__ int keys_seen(const Cache4AttnArgs& a, const Span& sp, int G, int base, int rows) {
+  if (!a.causal) return sp.nk;
+  return min(sp.nk, max(0, (base + rows - 1) / G + sp.nk - sp.nq + 1));
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Codes i and i + 4 of a word's eight as bf16 128 + c.
+__device__ __forceinline__ uint32_t codes(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t less136(uint32_t v) {
+  const uint32_t k = 0x43084308u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 template <int D>
-__global__ void __launch_bounds__(128) cache4_attention_kernel(const Cache4AttnArgs a) {
-  constexpr int V = D / 32, G = D / 32;
+struct Stage {  // 128 tokens of one head
+  static constexpr int G = D / 32;
+  static constexpr uint32_t kCodes = kKeys * D / 2, kScales = kKeys * G * 2, kBytes = 2 * (kCodes + kScales);
+};
+
+template <int N>  // N words at once, N = 1, 2 or 4
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const uint8_t* at) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(at);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(at);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
+  }
+}
+
+template <int G>  // a token's G scales
+__device__ __forceinline__ void scales(float (&s)[G], const uint8_t* at) {
+  uint32_t w[G / 2];
+  lds<G / 2>(w, at);
+#pragma unroll
+  for (int i = 0; i < G / 2; ++i) {
+    s[2 * i] = __uint_as_float(w[i] << 16);
+    s[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
+  using L = Stage<D>;
+  constexpr int G = L::G, R = 8 * NT, V = D / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ uint32_t live[kStages];  // the tiles of 16 tokens that a stage holds
+  __shared__ float2 ml[4][R];
+  __shared__ int abort_flag;
+  const Cache4AttnArgs& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = P.group;
+  // the tiles of the same keys run side by side
+  const int run = blockIdx.x / P.walk, tile0 = blockIdx.x - run * P.walk;
+  const int split = run % P.splits, hk = (run / P.splits) % a.c.heads, seq = run / P.splits / a.c.heads;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   grid_dependency_wait();
   allow_dependents();
-  const int s = blockIdx.y, lane = threadIdx.x & 31;
-  const int q0 = a.q_off[s];
-  const long long nq = a.q_len ? (long long)a.q_len[s] : (long long)a.q_off[s + 1] - q0;
-  const int nk = a.k_len[s];
-  if (q0 < 0 || nq < 0 || nq > a.max_q || q0 + nq > a.rows_q || nk < 0 || nk > a.max_k) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteCache4Lengths);
+  const Span sp = load_span(a, seq);
+  if (!sp.ok) {
+    if (split == 0 && hk == 0 && tile0 == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteCache4Lengths);
     return;
   }
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int token = (int)(item / a.heads_q), head = (int)(item % a.heads_q), hk = head / (a.heads_q / a.c.heads);
-  if (token >= nq) return;
-  float q[V], o[V] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < V; ++e)
-    q[e] = __bfloat162float(a.q[(long long)(q0 + token) * a.ldq + head * D + lane * V + e]);
-  const int seen = a.causal ? min(nk, token + nk - (int)nq + 1) : nk;
-  for (int pos = 0; pos < seen; ++pos) {
-    const int page = a.table[(long long)s * a.c.max_pages + (pos >> a.c.page_shift)], slot = pos & ((1 << a.c.page_shift) - 1);
-    if (page < 0 || page >= a.c.pages) {
-      if (lane == 0) report_bad_entry(a.status, kSiteCache4Page);
-      continue;
+  const WaitCtx wc{a.status, &abort_flag, kWaitLimitNs};
+  const int first = split * P.chunk;
+  const bool direct = sp.nk <= P.chunk;  // this CTA has all the keys of its rows
+  const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // fragment row, and first of two columns
+  int used = 0;  // stages filled (or emptied) so far
+
+  for (int tile = tile0; tile < P.tiles; tile += P.walk) {
+    const int base = tile * R, rows = min(R, sp.nq * group - base);  // this tile's query rows
+    if (rows <= 0) break;
+    const int last = min(keys_seen(a, sp, group, base, rows), first + P.chunk);
+    if (first >= last && split > 0) continue;
+    const int blocks = first < last ? (last - first + kKeys - 1) / kKeys : 0;
+
+    if (warp == 4) {
+      // Lane 4 i + part copies one part (codes or scales of the keys or values) of a stage's i-th page.
+      const int ps = 1 << a.c.page_shift, width = min(ps, kKeys), part = lane & 3, t0 = (lane >> 2) * width;
+      const int slab = a.c.slab(), cb = a.c.code_bytes(), sb = a.c.scale_bytes();
+      const int each = part & 1 ? G * 2 : D / 2;  // bytes of a token
+      const int src0 = (part & 2 ? cb + sb : 0) + (part & 1 ? cb : 0);
+      const int dst0 = (part & 2 ? (int)(L::kCodes + L::kScales) : 0) + (part & 1 ? (int)L::kCodes : 0) + t0 * each;
+      const int32_t* table = a.table + (long long)seq * a.c.max_pages;
+      auto page_of = [&](int j) {
+        const int t = first + j * kKeys + t0;
+        return t0 < kKeys && t < last ? table[t >> a.c.page_shift] : -2;
+      };
+      int page = page_of(0), issued = 0;
+      for (int j = 0; j < blocks; ++j) {
+        const int n = used + j, st = n % kStages, at = first + j * kKeys + t0;
+        const int next = j + 1 < blocks ? page_of(j + 1) : -2;
+        const bool wanted = t0 < kKeys && at < last, ok = wanted && page >= 0 && page < a.c.pages;
+        if (wanted && !ok && part == 0) report_bad_entry(a.status, kSiteCache4Page);
+        const int tiles = ok ? (min(width, last - at) + 15) / 16 : 0;  // of 16 tokens
+        const uint32_t bytes = (uint32_t)(tiles * 16 * each);
+        const uint32_t mask = part == 0 ? ((1u << tiles) - 1u) << (t0 / 16) : 0u;
+        const uint32_t all = __reduce_or_sync(0xffffffffu, mask), total = __reduce_add_sync(0xffffffffu, bytes);
+        if (!mbar_wait_sleep(&empty[st], ((uint32_t)(n / kStages) & 1u) ^ 1u, wc, kSiteCache4Empty)) break;
+        if (lane == 0) {
+          live[st] = all;
+          mbar_arrive_expect_tx(&full[st], total);
+        }
+        __syncwarp();
+        if (bytes)
+          bulk_load(smem + st * L::kBytes + dst0,
+                    a.cache + ((long long)page * a.c.heads + hk) * slab + src0 + (at & (ps - 1)) * each, bytes, &full[st]);
+        page = next;
+        issued = j + 1;
+      }
+      // A wait that gave up: nothing leaves before the copies on their way have landed (bounded).
+      if (*(volatile int*)&abort_flag && lane == 0) {
+        const uint64_t t = global_timer_ns();
+        for (int n = max(0, used + issued - kStages); n < used + issued; ++n)
+          while (!mbar_try(&full[n % kStages], (uint32_t)(n / kStages) & 1u) && global_timer_ns() - t < 200000000ull) {
+          }
+      }
+      __syncwarp();
     }
-    const uint8_t* slab = a.cache + ((long long)page * a.c.heads + hk) * a.c.slab();
-    float kv[2][V];
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* at = slab + h * (a.c.slab() / 2);
-      for (int e = 0; e < V; ++e) {
-        const int i = lane * V + e, j = i / 32, u = i % 32;
-        const int byte = h == 0 ? ((u / 8) * G + j) * 4 + (u % 8) / 2 : ((u / 4) * G + j) * 2 + (u % 4) / 2;
-        const int code = (at[slot * (D / 2) + byte] >> ((u & 1) * 4)) & 15;
-        kv[h][e] = (float)(code - 8) * __bfloat162float(reinterpret_cast<const bf16*>(at + a.c.code_bytes())[slot * G + j]);
+
+    float o[NT][2 * G][4], m[NT][2], l[NT][2];
+    if (warp < 4) {
+      uint32_t q[NT][2 * G][2];  // the queries as the scores' column operand
+      float start[NT][G][2];     // -136 sum of a group's query values, of the lane's two columns
+      int limit[NT][2];          // keys that they see
+      int open = last;           // keys below it are seen by all rows
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int r = base + n * 8 + r0, token = r / group;
+        const bool ok = n * 8 + r0 < rows;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (long long)(sp.q0 + (ok ? token : 0)) * a.ldq +
+                              (hk * group + (ok ? r - token * group : 0)) * D + (lane & 3) * 8;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const uint4 u = ok ? *reinterpret_cast<const uint4*>(src + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+          // values i and i + 4 side by side, as the keys' codes are
+          q[n][2 * j][0] = __byte_perm(u.x, u.z, 0x5410);
+          q[n][2 * j][1] = __byte_perm(u.x, u.z, 0x7632);
+          q[n][2 * j + 1][0] = __byte_perm(u.y, u.w, 0x5410);
+          q[n][2 * j + 1][1] = __byte_perm(u.y, u.w, 0x7632);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16x2(w[e]);
+            sum += f.x + f.y;
+          }
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          sum *= -136.0f;
+          start[n][j][0] = __shfl_sync(0xffffffffu, sum, c0 * 4);
+          start[n][j][1] = __shfl_sync(0xffffffffu, sum, c0 * 4 + 4);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = n * 8 + c0 + e;
+          limit[n][e] = i < rows && a.causal ? min(sp.nk, (base + i) / group + sp.nk - sp.nq + 1) : sp.nk;
+          open = min(open, limit[n][e]);
+          m[n][e] = -INFINITY;
+          l[n][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+      }
+      open = min(open, __shfl_xor_sync(0xffffffffu, open, 1));
+      open = min(open, __shfl_xor_sync(0xffffffffu, open, 2));
+
+      const float scale = P.scale_log2;
+      for (int j = 0; j < blocks; ++j) {
+        const int nn = used + j, st = nn % kStages;
+        bool ok = mbar_wait(&full[st], (uint32_t)(nn / kStages) & 1u, wc, kSiteCache4Full);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t here = (live[st] >> (2 * warp)) & 3u;
+        const int t0 = first + j * kKeys + warp * 32;
+        if (here) {
+          const uint8_t* at = smem + st * L::kBytes;
+          const bool masked = here != 3u || t0 + 32 > open;
+          float x[2][NT][4];  // scores, then probabilities, of two tiles of 16 tokens
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int tok = warp * 32 + i * 16 + r0;
+            uint32_t lo[G], hi[G];  // codes of the tokens r0 and r0 + 8
+            float slo[G], shi[G];
+            lds<G>(lo, at + tok * (D / 2) + (lane & 3) * (G * 4));
+            lds<G>(hi, at + (tok + 8) * (D / 2) + (lane & 3) * (G * 4));
+            scales<G>(slo, at + L::kCodes + tok * (G * 2));
+            scales<G>(shi, at + L::kCodes + (tok + 8) * (G * 2));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              float acc[NT][4];
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                acc[n][0] = acc[n][2] = start[n][g][0];
+                acc[n][1] = acc[n][3] = start[n][g][1];
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t A[4] = {codes(lo[g], 2 * k), codes(hi[g], 2 * k), codes(lo[g], 2 * k + 1), codes(hi[g], 2 * k + 1)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16(acc[n], A, q[n][2 * g + k]);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                x[i][n][0] = g ? fmaf(slo[g], acc[n][0], x[i][n][0]) : slo[g] * acc[n][0];
+                x[i][n][1] = g ? fmaf(slo[g], acc[n][1], x[i][n][1]) : slo[g] * acc[n][1];
+                x[i][n][2] = g ? fmaf(shi[g], acc[n][2], x[i][n][2]) : shi[g] * acc[n][2];
+                x[i][n][3] = g ? fmaf(shi[g], acc[n][3], x[i][n][3]) : shi[g] * acc[n][3];
+              }
+            }
+          }
+          // whether column e of n sees this lane's token r0 + 8 h of tile i
+          auto sees = [&](int i, int n, int h, int e) {
+            return ((here >> i) & 1u) && t0 + i * 16 + r0 + 8 * h < min(limit[n][e], last);
+          };
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!sees(i, n, e >> 1, e & 1)) x[i][n][e] = -INFINITY;
+          }
+          // Maxima move rarely: only where a score is 2^8 above what the probabilities refer to.
+          bool move = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float top = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2])) * scale;
+              move = move || top > m[n][e] + 8.0f;  // also from minus infinity
+            }
+          if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float alpha[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2])) * scale;
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const float mn = fmaxf(m[n][e], top);
+                alpha[e] = ex2_approx(m[n][e] - (mn == -INFINITY ? 0.f : mn));
+                m[n][e] = mn;
+                l[n][e] *= alpha[e];
+              }
+#pragma unroll
+              for (int i = 0; i < 2 * G; ++i) {
+                o[n][i][0] *= alpha[0];
+                o[n][i][1] *= alpha[1];
+                o[n][i][2] *= alpha[0];
+                o[n][i][3] *= alpha[1];
+              }
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                x[i][n][e] = ex2_approx(fmaf(x[i][n][e], scale, -ref));
+                x[i][n][e + 2] = ex2_approx(fmaf(x[i][n][e + 2], scale, -ref));
+                l[n][e] += x[i][n][e] + x[i][n][e + 2];
+              }
+            }
+          at += L::kCodes + L::kScales;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // codes of the tokens c0, c0 + 1, c0 + 8 and c0 + 9: this lane's columns of V^T
+            const uint8_t* row = at + (warp * 32 + i * 16 + c0) * (D / 2) + r0 * (G * 2);
+            uint32_t w0[G / 2], w1[G / 2], w2[G / 2], w3[G / 2];
+            lds<G / 2>(w0, row);
+            lds<G / 2>(w1, row + D / 2);
+            lds<G / 2>(w2, row + 8 * (D / 2));
+            lds<G / 2>(w3, row + 9 * (D / 2));
+            float slo[G], shi[G];
+            const uint8_t* sc = at + L::kCodes + (warp * 32 + i * 16 + r0) * (G * 2);
+            scales<G>(slo, sc);
+            scales<G>(shi, sc + 8 * (G * 2));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              uint32_t b[NT][2];
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float f[4] = {x[i][n][0] * slo[g], x[i][n][1] * slo[g], x[i][n][2] * shi[g], x[i][n][3] * shi[g]};
+                if (masked) {  // a probability of zero does not silence a scale that is not finite
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (!sees(i, n, e >> 1, e & 1)) f[e] = 0.f;
+                }
+                b[n][0] = transpose8x8(pack_bf16x2(f[0], f[1]));
+                b[n][1] = transpose8x8(pack_bf16x2(f[2], f[3]));
+              }
+              const uint32_t near = __byte_perm(w0[g / 2], w1[g / 2], g & 1 ? 0x7632 : 0x5410);
+              const uint32_t far = __byte_perm(w2[g / 2], w3[g / 2], g & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t A[4] = {less136(codes(near, 2 * h)), less136(codes(near, 2 * h + 1)), less136(codes(far, 2 * h)),
+                                       less136(codes(far, 2 * h + 1))};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16(o[n][2 * g + h], A, b[n]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
       }
     }
-    float x = 0.f;
-    for (int e = 0; e < V; ++e) x = fmaf(q[e], kv[0][e], x);
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    x *= a.scale;
-    const float mn = fmaxf(m, x), ref = mn == -INFINITY ? 0.f : mn, f = expf(m - ref), p = expf(x - ref);
-    m = mn;
-    l = l * f + p;
-    for (int e = 0; e < V; ++e) o[e] = o[e] * f + p * kv[1][e];
+    used += blocks;
+
+    // The four warps' rows through shared memory: all stages have been read.
+    __syncthreads();
+    float* parts = reinterpret_cast<float*>(smem);  // [warp][row][dim]
+    if (warp < 4) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+          const int r = n * 8 + c0 + e;
+          if (r0 == 0) ml[warp][r] = make_float2(m[n][e], l[n][e]);
+          if (r < rows) {
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i)
+              *reinterpret_cast<float2*>(parts + (warp * R + r) * D + (i >> 1) * 32 + 4 * r0 + 2 * (i & 1)) =
+                  make_float2(o[n][i][e], o[n][i][e + 2]);
+          }
+        }
+    }
+    __syncthreads();
+    if (warp < 4 && !abort_flag) {
+      for (int r = warp; r < rows; r += 4) {
+        float mr = -INFINITY, lr = 0.f, out[V];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mr = fmaxf(mr, ml[w][r].x);
+        const float ref = mr == -INFINITY ? 0.f : mr;
+#pragma unroll
+        for (int e = 0; e < V; ++e) out[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 y = ml[w][r];
+          if (y.y == 0.f) continue;  // no key that the row sees
+          const float f = ex2_approx((y.x == -INFINITY ? 0.f : y.x) - ref);
+          lr += f * y.y;
+#pragma unroll
+          for (int e = 0; e < V; ++e) out[e] += f * parts[(w * R + r) * D + lane * V + e];
+        }
+        if (direct) {
+          const int token = (base + r) / group, g = base + r - token * group;
+          const float inv = lr == 0.f ? 0.f : 1.0f / lr;
+          bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * group + g) * D + lane * V;
+#pragma unroll
+          for (int e = 0; e < V; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) = lr == 0.f ? 0u : pack_bf16x2(out[e] * inv, out[e + 1] * inv);
+        } else {
+          const long long to = (long long)run * P.rows + base + r;
+          if (lane == 0) P.ml[to] = make_float2(mr, lr);
+#pragma unroll
+          for (int e = 0; e < V; e += 2)
+            *reinterpret_cast<float2*>(P.o + to * D + lane * V + e) = make_float2(out[e], out[e + 1]);
+        }
+      }
+    }
+    if (P.walk < P.tiles) fence_proxy_async_smem();  // before the next tile's copies
+    __syncthreads();
+    if (abort_flag) return;
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  for (int e = 0; e < V; ++e)
-    a.out[(long long)(q0 + token) * a.ldo + head * D + lane * V + e] = __float2bfloat16(l == 0.f ? 0.f : o[e] * inv);
+}
+
+// Adds up the runs of the sequences that took several, in order: one warp per row, grid (sequence and key head,
+// four rows).
+template <int D>
+__global__ void __launch_bounds__(128) cache4_join_kernel(const __grid_constant__ Params P) {
+  grid_dependency_wait();
+  allow_dependents();
+  const Cache4AttnArgs& a = P.a;
+  const int G = P.group, hk = blockIdx.x % a.c.heads, seq = blockIdx.x / a.c.heads;
+  const Span sp = load_span(a, seq);
+  if (!sp.ok || sp.nk <= P.chunk) return;
+  const int tile = P.rows <= 8 ? 8 : 16;
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < sp.nq * G; r += gridDim.y * 4) {
+    const int base = r / tile * tile;
+    const int seen = keys_seen(a, sp, G, base, min(tile, sp.nq * G - base)), runs = (seen + P.chunk - 1) / P.chunk;
+    const long long at = (long long)blockIdx.x * P.splits * P.rows + r;
+    const int token = r / G;
+    join_row<D>(P.ml + at, P.o + at * D, P.rows, max(1, runs), threadIdx.x & 31,
+                a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + r - token * G) * D);
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStream_t s) {
+  static std::atomic<bool> raised[16];  // per device
+  Params P;
+  memset(&P, 0, sizeof(P));
+  const Parts l = parts_of(p, a);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(a.parts);
+  P.a = a;
+  P.group = a.heads_q / a.c.heads;
+  P.rows = p.rows;
+  P.tiles = p.tiles;
+  P.walk = p.walk;
+  P.chunk = p.chunk;
+  P.splits = p.splits;
+  P.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
+  P.ml = reinterpret_cast<float2*>(ws + l.ml);
+  P.o = reinterpret_cast<float*>(ws + l.o);
+  constexpr size_t smem = kStages * Stage<D>::kBytes;
+  static_assert(smem >= 4 * 8 * NT * D * 4, "the parts reuse the stages");
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 16 || !raised[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(cache4_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 16) raised[dev].store(true, std::memory_order_release);
+  }
+  const long long heads = (long long)a.seqs * a.c.heads;
+  {
+    LaunchScope scope(kClsCache4Attention, s);
+    const cudaError_t e = launch_k(cache4_attention_kernel<D, NT>, dim3((unsigned)(heads * p.splits * p.walk)),
+                                   dim3(kThreads), smem, s, P);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.splits > 1) {
+    const int fours = (p.rows + 3) / 4;
+    LaunchScope scope(kClsCache4Join, s);
+    return launch_k(cache4_join_kernel<D>, dim3((unsigned)heads, (unsigned)(fours < 65535 ? fours : 65535)), dim3(128), 0, s, P);
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -175,14 +671,15 @@ cudaError_t launch_cache4_read(const Cache4MoveArgs& a, cudaStream_t s) {
   return launch_move<false>(a, kClsCache4Read, s);
 }
 
-size_t cache4_attention_parts_bytes(const Cache4AttnArgs&) { return 0; }
+size_t cache4_attention_parts_bytes(const Cache4AttnArgs& a) {
+  if (a.seqs == 0 || a.rows_q == 0 || a.max_q == 0) return 0;
+  return parts_of(make_plan(a), a).total;
+}
 
 cudaError_t launch_cache4_attention(const Cache4AttnArgs& a, cudaStream_t s) {
-  const long long blocks = ((long long)a.max_q * a.heads_q + 3) / 4;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  LaunchScope scope(kClsCache4Attention, s);
-  auto kernel = a.c.head_dim == 64 ? cache4_attention_kernel<64> : cache4_attention_kernel<128>;
-  return launch_k(kernel, dim3((unsigned)blocks, (unsigned)a.seqs), dim3(128), 0, s, a);
+  const Plan p = make_plan(a);
+  if (a.c.head_dim == 64) return p.tile == 8 ? launch_attention_as<64, 1>(a, p, s) : launch_attention_as<64, 2>(a, p, s);
+  return p.tile == 8 ? launch_attention_as<128, 1>(a, p, s) : launch_attention_as<128, 2>(a, p, s);
 }
 
 }  // namespace dit
