@@ -122,12 +122,25 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 // stage each through mma.sync with a running maximum and sum of their own, which add up at the end in order. Runs of
 // several CTAs are joined by a second kernel.
 //
-// The tokens are the rows of both products, the few queries their columns: S^T = K Q^T and O^T = V^T P^T. Codes
-// become bf16 operands without a conversion: a code c under the bits of 128 is the number 128 + c, one masked
-// word per two values.  For the scores the 136 = 128 + 8 that is too much is taken off by what the accumulator starts
-// with, -136 sum(q) per group of 32; group sums are exact products in fp32, times the key's scale.  For the values it
-// is subtracted (exactly), since a sum over thousands of tokens would lose by it.  The values' scales, one per
-// token and 32 values, belong to the index that the product sums over: they go into the probabilities.
+// The tokens are the rows of both products, the few queries their columns: S^T = K Q^T and O^T = V^T P^T. What bounds
+// this kernel is not the MMA but the integer pipe, which has to spread 4-bit codes over 16-bit operands, half a
+// warp per cycle: so a code is left where one AND leaves it. As the bits of an fp16 number, a code c in the lowest four
+// bits is the subnormal c 2^-24, in the next four c 2^-20: both exact operands, five operations per eight codes of the keys
+// and six of the values. (As bf16 128 + c, with an OR and more shifts, and an exact subtraction of 136 for the values: 458
+// instructions per 16 tokens instead of XXX, 260 us instead of XXX.)
+//
+// Keys: the queries become fp16 times a power of two per row (largest magnitude in [2^13, 2^14)), exact down to 2^-28 of the
+// row's largest; those that meet the higher codes are divided by 16. The 8 that every code is too large is taken off
+// by -8 sum(q) per group: scales times those sums is one more small product (they go in as three bf16 parts, 24 bits), and
+// the accumulators of the groups are added to it, times the key's scale, in fp32.
+// Values: the scales, one per token and 32 values, belong to the index that the product sums over, so they go into the
+// probabilities. f = p s is rounded to fp16 (2^-11): the reference that a row's exponents are taken from is that of its largest
+// p s, 2^6 below it, so that f stays under 2^15, and what is rounded coarser (subnormal) is below 2^-20 of the row's
+// largest weight, within 2^-31 of it. The 8 is taken off at the end: -8 sum(f) of the rounded f, which one more product
+// with ones gives.
+// The unit that sums a step's sixteen products lines them up by the exponents of their operands, and a subnormal has that of
+// 2^-14: of each product what lies below 2^-24 2^-14 of the largest other operand is cut off, 2^-14 of that operand per code
+// (measured: one step of random codes is within 2^-20.5 of the sum of magnitudes, eight steps 2^-24.4).
 constexpr int kKeys = 128, kStages = 3, kThreads = 160;
 
 enum : uint32_t { kSiteCache4Full = 0x811, kSiteCache4Empty };
@@ -206,11 +219,24 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// The same from an accumulator of zeros.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_new(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -219,11 +245,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-// Codes i and i + 4 of a word's eight as bf16 128 + c.
-__device__ __forceinline__ uint32_t codes(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
-__device__ __forceinline__ uint32_t less136(uint32_t v) {
-  const uint32_t k = 0x43084308u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&k));
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// bf16 pairs, both halves' larger ones (a NaN loses).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -246,19 +282,197 @@ __device__ __forceinline__ void lds(uint32_t (&w)[N], const uint8_t* at) {
   }
 }
 
-template <int G>  // a token's G scales
-__device__ __forceinline__ void scales(float (&s)[G], const uint8_t* at) {
-  uint32_t w[G / 2];
-  lds<G / 2>(w, at);
+template <int N>  // scales of bf16 pairs
+__device__ __forceinline__ void scales(float (&s)[2 * N], const uint32_t (&w)[N]) {
 #pragma unroll
-  for (int i = 0; i < G / 2; ++i) {
+  for (int i = 0; i < N; ++i) {
     s[2 * i] = __uint_as_float(w[i] << 16);
     s[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 
+// What a warp keeps of its query rows: columns 8 n + c0 + {0, 1} of the scores and the output, c0 = 2 (lane % 4).
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
+struct Rows {
+  static constexpr int G = D / 32;
+  uint32_t q[NT][2 * G][2];  // the queries as the scores' column operand
+  uint32_t eight[NT][2];     // -8 sums of their groups, in three bf16 parts
+  float scale[NT][2];        // from sums of products to exponents of two
+  int limit[NT][2];          // keys that the columns see
+  float o[NT][2 * G][4], f[NT][G][4];  // sums of c f, times 2^-24 (the codes' odd places: 2^-20), and of f
+  float m[NT][2], l[NT][2];            // what exponents are taken from, sums of probabilities
+};
+
+constexpr float kRoom = 6.0f;  // a row's largest weight lies 2^6 above its reference when that is set, 2^15 at most
+
+// A warp's 32 tokens of a stage, from token t0 of the sequence on. kMasked: some column does not see some of them.
+template <int D, int NT, bool kMasked>
+__device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* at, int tok0, int t0, uint32_t here, int last, int lane) {
+  using L = Stage<D>;
+  constexpr int G = L::G;
+  const int r0 = lane >> 2, c0 = (lane & 3) * 2;
+  // whether column e of n sees this lane's token r0 + 8 h of tile i
+  auto sees = [&](int i, int n, int h, int e) {
+    return ((here >> i) & 1u) && t0 + i * 16 + r0 + 8 * h < min(R.limit[n][e], last);
+  };
+  const uint8_t* vat = at + L::kCodes + L::kScales;
+  float x[2][NT][4];           // scores, then probabilities, of two tiles of 16 tokens
+  uint32_t vs[2][2][G / 2];    // scales of the values of the tokens r0 and r0 + 8
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int tok = tok0 + i * 16 + r0;
+    lds<G / 2>(vs[i][0], vat + L::kCodes + tok * (G * 2));
+    lds<G / 2>(vs[i][1], vat + L::kCodes + (tok + 8) * (G * 2));
+    uint32_t lo[G], hi[G], wlo[G / 2], whi[G / 2];  // codes and scales of the tokens r0 and r0 + 8
+    lds<G>(lo, at + tok * (D / 2) + (lane & 3) * (G * 4));
+    lds<G>(hi, at + (tok + 8) * (D / 2) + (lane & 3) * (G * 4));
+    lds<G / 2>(wlo, at + L::kCodes + tok * (G * 2));
+    lds<G / 2>(whi, at + L::kCodes + (tok + 8) * (G * 2));
+    {
+      const bool odd = G == 4 && (lane & 1);
+      const uint32_t u = wlo[odd ? G / 2 - 1 : 0], w = whi[odd ? G / 2 - 1 : 0], A[4] = {u, w, u, w};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_bf16_new(x[i][n], A, R.eight[n]);
+    }
+    float slo[G], shi[G];
+    scales<G / 2>(slo, wlo);
+    scales<G / 2>(shi, whi);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float acc[NT][4];
+      const uint32_t A[4] = {lo[g] & 0x000f000fu, hi[g] & 0x000f000fu, lo[g] & 0x00f000f0u, hi[g] & 0x00f000f0u};
+      const uint32_t l8 = lo[g] >> 8, h8 = hi[g] >> 8;
+      const uint32_t B[4] = {l8 & 0x000f000fu, h8 & 0x000f000fu, l8 & 0x00f000f0u, h8 & 0x00f000f0u};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16_new(acc[n], A, R.q[n][2 * g]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(acc[n], B, R.q[n][2 * g + 1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        x[i][n][0] = fmaf(slo[g], acc[n][0], x[i][n][0]);
+        x[i][n][1] = fmaf(slo[g], acc[n][1], x[i][n][1]);
+        x[i][n][2] = fmaf(shi[g], acc[n][2], x[i][n][2]);
+        x[i][n][3] = fmaf(shi[g], acc[n][3], x[i][n][3]);
+      }
+    }
+  }
+  if constexpr (kMasked) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!sees(i, n, e >> 1, e & 1)) x[i][n][e] = -INFINITY;
+  }
+  // References move rarely: only where a weight could pass 2^8 times what it was when the reference was set. The check
+  // takes the largest score and the largest scale of the lane's four tokens together, which errs on that side.
+  auto largest = [](const uint32_t (&w)[G / 2]) {
+    uint32_t u = w[0];
+    if constexpr (G == 4) u = max2(w[0], w[1]);
+    return u;
+  };
+  auto exponent = [](uint32_t u) {
+    const float s = fmaxf(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    return fmaxf(lg2_approx(s), -64.0f);
+  };
+  const float most = exponent(max2(max2(largest(vs[0][0]), largest(vs[0][1])), max2(largest(vs[1][0]), largest(vs[1][1]))));
+  bool move = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float top = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2]));
+      move = move || fmaf(top, R.scale[n][e], most) > R.m[n][e] + (kRoom + 8.0f);  // also from minus infinity
+    }
+  if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float alpha[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) top = fmaxf(top, fmaf(x[i][n][e + 2 * h], R.scale[n][e], exponent(largest(vs[i][h]))));
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        const float mn = fmaxf(R.m[n][e], top - kRoom);
+        alpha[e] = ex2_approx(R.m[n][e] - (mn == -INFINITY ? 0.f : mn));
+        R.m[n][e] = mn;
+        R.l[n][e] *= alpha[e];
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        R.f[n][g][0] *= alpha[0];
+        R.f[n][g][1] *= alpha[1];
+        R.f[n][g][2] = R.f[n][g][3] = 0.f;  // rows 8 to 15, the same again, are not read
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * G; ++i) {
+        R.o[n][i][0] *= alpha[0];
+        R.o[n][i][1] *= alpha[1];
+        R.o[n][i][2] *= alpha[0];
+        R.o[n][i][3] *= alpha[1];
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float ref = R.m[n][e] == -INFINITY ? 0.f : R.m[n][e];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i][n][e] = ex2_approx(fmaf(x[i][n][e], R.scale[n][e], -ref));
+        x[i][n][e + 2] = ex2_approx(fmaf(x[i][n][e + 2], R.scale[n][e], -ref));
+        R.l[n][e] += x[i][n][e] + x[i][n][e + 2];
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // codes of the tokens c0, c0 + 1, c0 + 8 and c0 + 9: this lane's columns of V^T
+    const uint8_t* row = vat + (tok0 + i * 16 + c0) * (D / 2) + r0 * (G * 2);
+    uint32_t w0[G / 2], w1[G / 2], w2[G / 2], w3[G / 2];
+    lds<G / 2>(w0, row);
+    lds<G / 2>(w1, row + D / 2);
+    lds<G / 2>(w2, row + 8 * (D / 2));
+    lds<G / 2>(w3, row + 9 * (D / 2));
+    float slo[G], shi[G];
+    scales<G / 2>(slo, vs[i][0]);
+    scales<G / 2>(shi, vs[i][1]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      uint32_t b[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float f[4] = {x[i][n][0] * slo[g], x[i][n][1] * slo[g], x[i][n][2] * shi[g], x[i][n][3] * shi[g]};
+        if constexpr (kMasked) {  // a probability of zero does not silence a scale that is not finite
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!sees(i, n, e >> 1, e & 1)) f[e] = 0.f;
+        }
+        b[n][0] = transpose8x8(pack_f16x2(f[0], f[1]));
+        b[n][1] = transpose8x8(pack_f16x2(f[2], f[3]));
+        const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+        mma_f16(R.f[n][g], one, b[n]);
+      }
+      // the codes' low bytes of the group's half-words, then the high ones
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t pick = g & 1 ? (h ? 0x4743u : 0x4642u) : (h ? 0x4541u : 0x4440u);
+        const uint32_t near = __byte_perm(w0[g / 2], w1[g / 2], pick), far = __byte_perm(w2[g / 2], w3[g / 2], pick);
+        const uint32_t A[4] = {near & 0x000f000fu, near & 0x00f000f0u, far & 0x000f000fu, far & 0x00f000f0u};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(R.o[n][2 * g + h], A, b[n]);
+      }
+    }
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) cache4_attention_kernel(const __grid_constant__ Params P) {
   using L = Stage<D>;
   constexpr int G = L::G, R = 8 * NT, V = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -344,54 +558,88 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
       __syncwarp();
     }
 
-    float o[NT][2 * G][4], m[NT][2], l[NT][2];
+    Rows<D, NT> Q;
     if (warp < 4) {
-      uint32_t q[NT][2 * G][2];  // the queries as the scores' column operand
-      float start[NT][G][2];     // -136 sum of a group's query values, of the lane's two columns
-      int limit[NT][2];          // keys that they see
-      int open = last;           // keys below it are seen by all rows
+      int open = last;  // keys below it are seen by all rows
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = base + n * 8 + r0, token = r / group;
         const bool ok = n * 8 + r0 < rows;
         const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (long long)(sp.q0 + (ok ? token : 0)) * a.ldq +
                               (hk * group + (ok ? r - token * group : 0)) * D + (lane & 3) * 8;
+        uint32_t w[G][4], top = 0;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
           const uint4 u = ok ? *reinterpret_cast<const uint4*>(src + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
-          // values i and i + 4 side by side, as the keys' codes are
-          q[n][2 * j][0] = __byte_perm(u.x, u.z, 0x5410);
-          q[n][2 * j][1] = __byte_perm(u.x, u.z, 0x7632);
-          q[n][2 * j + 1][0] = __byte_perm(u.y, u.w, 0x5410);
-          q[n][2 * j + 1][1] = __byte_perm(u.y, u.w, 0x7632);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          float sum = 0.f;
+          w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[j][e] & 0x7fffu, (w[j][e] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^up takes the row's largest magnitude to [2^13, 2^14): its biased exponent to 140
+        const int up = top == 0 ? 0 : min(140 - (int)max(top >> 7, 1u), 126);
+        const float factor = __uint_as_float((uint32_t)(127 + up) << 23);
+        float part[4 * 3];  // three bf16 parts of -8 sum(q) 2^-24, part p of group j at [p G + j]
+#pragma unroll
+        for (int i = 0; i < 12; ++i) part[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          // values i and i + 4 side by side, as the keys' codes are; those of the higher codes divided by 16
+          float v[8], sum = 0.f;
+          uint32_t h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16x2(w[e]);
-            sum += f.x + f.y;
+            const float2 f = unpack_bf16x2(w[j][e]);
+            v[2 * e] = f.x * factor;
+            v[2 * e + 1] = f.y * factor;
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float d = e & 1 ? 0.0625f : 1.0f;
+            h[e] = pack_f16x2(v[e] * d, v[e + 4] * d);
+            sum += v[e] + v[e + 4];
+          }
+          Q.q[n][2 * j][0] = h[0];
+          Q.q[n][2 * j][1] = h[1];
+          Q.q[n][2 * j + 1][0] = h[2];
+          Q.q[n][2 * j + 1][1] = h[3];
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum *= -136.0f;
-          start[n][j][0] = __shfl_sync(0xffffffffu, sum, c0 * 4);
-          start[n][j][1] = __shfl_sync(0xffffffffu, sum, c0 * 4 + 4);
+          sum *= -8.0f * 0x1p-24f;
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            const float f = __bfloat162float(__float2bfloat16(sum));
+            part[p * G + j] = f;
+            sum -= f;
+          }
+        }
+        // rows 2 t, 2 t + 1 and 2 t + 8, 2 t + 9 of the column operand
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float lo = 0.f, hi = 0.f;
+#pragma unroll
+          for (int i = 0; i < 12; i += 2)
+            if (i == c0 + 8 * h) lo = part[i], hi = part[i + 1];
+          Q.eight[n][h] = pack_bf16x2(lo, hi);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = n * 8 + c0 + e;
-          limit[n][e] = i < rows && a.causal ? min(sp.nk, (base + i) / group + sp.nk - sp.nq + 1) : sp.nk;
-          open = min(open, limit[n][e]);
-          m[n][e] = -INFINITY;
-          l[n][e] = 0.f;
+          Q.scale[n][e] = ldexpf(P.scale_log2, 24 - __shfl_sync(0xffffffffu, up, (c0 + e) * 4));
+          Q.limit[n][e] = i < rows && a.causal ? min(sp.nk, (base + i) / group + sp.nk - sp.nq + 1) : sp.nk;
+          open = min(open, Q.limit[n][e]);
+          Q.m[n][e] = -INFINITY;
+          Q.l[n][e] = 0.f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) Q.f[n][g][e] = Q.f[n][g][e + 2] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 2 * G; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+        for (int i = 0; i < 2 * G; ++i) Q.o[n][i][0] = Q.o[n][i][1] = Q.o[n][i][2] = Q.o[n][i][3] = 0.f;
       }
       open = min(open, __shfl_xor_sync(0xffffffffu, open, 1));
       open = min(open, __shfl_xor_sync(0xffffffffu, open, 2));
 
-      const float scale = P.scale_log2;
       for (int j = 0; j < blocks; ++j) {
         const int nn = used + j, st = nn % kStages;
         bool ok = mbar_wait(&full[st], (uint32_t)(nn / kStages) & 1u, wc, kSiteCache4Full);
@@ -399,142 +647,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
         if (!ok) break;
         const uint32_t here = (live[st] >> (2 * warp)) & 3u;
         const int t0 = first + j * kKeys + warp * 32;
-        if (here) {
-          const uint8_t* at = smem + st * L::kBytes;
-          const bool masked = here != 3u || t0 + 32 > open;
-          float x[2][NT][4];  // scores, then probabilities, of two tiles of 16 tokens
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int tok = warp * 32 + i * 16 + r0;
-            uint32_t lo[G], hi[G];  // codes of the tokens r0 and r0 + 8
-            float slo[G], shi[G];
-            lds<G>(lo, at + tok * (D / 2) + (lane & 3) * (G * 4));
-            lds<G>(hi, at + (tok + 8) * (D / 2) + (lane & 3) * (G * 4));
-            scales<G>(slo, at + L::kCodes + tok * (G * 2));
-            scales<G>(shi, at + L::kCodes + (tok + 8) * (G * 2));
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              float acc[NT][4];
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                acc[n][0] = acc[n][2] = start[n][g][0];
-                acc[n][1] = acc[n][3] = start[n][g][1];
-              }
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t A[4] = {codes(lo[g], 2 * k), codes(hi[g], 2 * k), codes(lo[g], 2 * k + 1), codes(hi[g], 2 * k + 1)};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16(acc[n], A, q[n][2 * g + k]);
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                x[i][n][0] = g ? fmaf(slo[g], acc[n][0], x[i][n][0]) : slo[g] * acc[n][0];
-                x[i][n][1] = g ? fmaf(slo[g], acc[n][1], x[i][n][1]) : slo[g] * acc[n][1];
-                x[i][n][2] = g ? fmaf(shi[g], acc[n][2], x[i][n][2]) : shi[g] * acc[n][2];
-                x[i][n][3] = g ? fmaf(shi[g], acc[n][3], x[i][n][3]) : shi[g] * acc[n][3];
-              }
-            }
-          }
-          // whether column e of n sees this lane's token r0 + 8 h of tile i
-          auto sees = [&](int i, int n, int h, int e) {
-            return ((here >> i) & 1u) && t0 + i * 16 + r0 + 8 * h < min(limit[n][e], last);
-          };
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (!sees(i, n, e >> 1, e & 1)) x[i][n][e] = -INFINITY;
-          }
-          // Maxima move rarely: only where a score is 2^8 above what the probabilities refer to.
-          bool move = false;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float top = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2])) * scale;
-              move = move || top > m[n][e] + 8.0f;  // also from minus infinity
-            }
-          if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float alpha[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float top = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2])) * scale;
-#pragma unroll
-                for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                const float mn = fmaxf(m[n][e], top);
-                alpha[e] = ex2_approx(m[n][e] - (mn == -INFINITY ? 0.f : mn));
-                m[n][e] = mn;
-                l[n][e] *= alpha[e];
-              }
-#pragma unroll
-              for (int i = 0; i < 2 * G; ++i) {
-                o[n][i][0] *= alpha[0];
-                o[n][i][1] *= alpha[1];
-                o[n][i][2] *= alpha[0];
-                o[n][i][3] *= alpha[1];
-              }
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                x[i][n][e] = ex2_approx(fmaf(x[i][n][e], scale, -ref));
-                x[i][n][e + 2] = ex2_approx(fmaf(x[i][n][e + 2], scale, -ref));
-                l[n][e] += x[i][n][e] + x[i][n][e + 2];
-              }
-            }
-          at += L::kCodes + L::kScales;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // codes of the tokens c0, c0 + 1, c0 + 8 and c0 + 9: this lane's columns of V^T
-            const uint8_t* row = at + (warp * 32 + i * 16 + c0) * (D / 2) + r0 * (G * 2);
-            uint32_t w0[G / 2], w1[G / 2], w2[G / 2], w3[G / 2];
-            lds<G / 2>(w0, row);
-            lds<G / 2>(w1, row + D / 2);
-            lds<G / 2>(w2, row + 8 * (D / 2));
-            lds<G / 2>(w3, row + 9 * (D / 2));
-            float slo[G], shi[G];
-            const uint8_t* sc = at + L::kCodes + (warp * 32 + i * 16 + r0) * (G * 2);
-            scales<G>(slo, sc);
-            scales<G>(shi, sc + 8 * (G * 2));
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              uint32_t b[NT][2];
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                float f[4] = {x[i][n][0] * slo[g], x[i][n][1] * slo[g], x[i][n][2] * shi[g], x[i][n][3] * shi[g]};
-                if (masked) {  // a probability of zero does not silence a scale that is not finite
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (!sees(i, n, e >> 1, e & 1)) f[e] = 0.f;
-                }
-                b[n][0] = transpose8x8(pack_bf16x2(f[0], f[1]));
-                b[n][1] = transpose8x8(pack_bf16x2(f[2], f[3]));
-              }
-              const uint32_t near = __byte_perm(w0[g / 2], w1[g / 2], g & 1 ? 0x7632 : 0x5410);
-              const uint32_t far = __byte_perm(w2[g / 2], w3[g / 2], g & 1 ? 0x7632 : 0x5410);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t A[4] = {less136(codes(near, 2 * h)), less136(codes(near, 2 * h + 1)), less136(codes(far, 2 * h)),
-                                       less136(codes(far, 2 * h + 1))};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16(o[n][2 * g + h], A, b[n]);
-              }
-            }
-          }
-        }
+        const uint8_t* at = smem + st * L::kBytes;
+        if (here == 3u && t0 + 32 <= open) attend<D, NT, false>(Q, at, warp * 32, t0, here, last, lane);
+        else if (here) attend<D, NT, true>(Q, at, warp * 32, t0, here, last, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
       }
+      // From sums of codes to values: 8 sums of f off, the codes' powers of two undone.
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) Q.l[n][e] += __shfl_xor_sync(0xffffffffu, Q.l[n][e], w);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float f = Q.f[n][g][e];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              Q.o[n][2 * g + h][e] = fmaf(Q.o[n][2 * g + h][e], 0x1p24f, -8.0f * f);
+              Q.o[n][2 * g + h][e + 2] = fmaf(Q.o[n][2 * g + h][e + 2], 0x1p20f, -8.0f * f);
+            }
+          }
+        }
     }
     used += blocks;
 
@@ -546,15 +681,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
           const int r = n * 8 + c0 + e;
-          if (r0 == 0) ml[warp][r] = make_float2(m[n][e], l[n][e]);
+          if (r0 == 0) ml[warp][r] = make_float2(Q.m[n][e], Q.l[n][e]);
           if (r < rows) {
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i)
               *reinterpret_cast<float2*>(parts + (warp * R + r) * D + (i >> 1) * 32 + 4 * r0 + 2 * (i & 1)) =
-                  make_float2(o[n][i][e], o[n][i][e + 2]);
+                  make_float2(Q.o[n][i][e], Q.o[n][i][e + 2]);
           }
         }
     }

@@ -598,8 +598,10 @@ dit_status dit_text_cache4_attention_workspace(const dit_text_cache4* c, const d
  * the nk = k_len[s] tokens of its page table as keys, and the queries [q_off[s], q_off[s] + nq).  What `a` says holds as
  * there (heads_k and head_dim as in `c`; rows_k is not used; causal: the last query sees the last key), and so does
  * what is said there of queries without keys, of rows that belong to no sequence, and of values behind a
- * sequence's keys.  Scores from exact products of the bf16 queries and the cache's integers, scaled and summed in fp32;
- * probabilities times the values' scales are rounded to bf16 for the product with V.  A key on a page outside
+ * sequence's keys.  Scores from exact products of the queries and the cache's integers (what of a query row is below 2^-28 of
+ * its largest value is rounded), scaled and summed in fp32; scale times a row's largest magnitude stays below 2^100.
+ * Probabilities times the values' scales are rounded to fp16 for the product with V, those below 2^-20 of a row's largest
+ * to 2^-31 of it.  A key on a page outside
  * [0, pages) is left out of the sums, and recorded (0x802); a sequence whose lengths are out of range is skipped, and
  * recorded (0x801).  Meant for few queries per sequence: every 16 rows (tokens x heads_q / heads_k) of a key head read its
  * cache once.  out_dev must not overlap q_dev or the cache; page_table is not read behind a sequence's last token. */

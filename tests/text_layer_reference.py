@@ -124,13 +124,20 @@ def cache_attention(q, spans, causal, scale, cache, table, left_out=()):
     does not see taking part; `bad` where a visible value of V is not finite, or a visible key's scale.  Positions in
     `left_out` (sequence, position) take no part.  The tolerance is each value's own; with size = sum p |v|:
 
-    - the probability times the value's scale and the output are rounded to bf16: 2^-8 size, 2^-8 |out|;
-    - a group's 32 products q (128 + code) are summed in fp32 over -136 sum q: terms of up to 143 |q|, at most 68
-      steps off by 2^-23 of their sum each (truncation), B = scale * max over the visible keys of
-      sum_g s_g sum |q_i|; then d / 32 products and sums, 8 steps of 2^-23 of A = scale max sum |q k|, and the exponent's
-      two roundings at up to 2 A in units of log2: e = (68 * 143 B + 12 A) 2^-23.  Scores off by e move
-      p / l by at most exp(2 e) - 1;
-    - sums over n visible keys, the exponential (2^-22) and rescales: (n + 128) 2^-23 size.
+    - the probability times the value's scale is rounded to fp16 (2^-11 size), the output to bf16 (2^-8 |out|);
+    - what of such a weight is subnormal in fp16 is off by 2^-25 where the largest of its row is 2^5 or more (2^6 when the
+      reference is set, to the accuracy of a logarithm): n visible values of at most 7 steps, n 7 2^-30 of the row's largest
+      weight W = max p s / l;
+    - a group's 32 products q c (c up to 15) are summed in fp32 in at most 34 steps, each off by 2^-23 of sum |q| 15
+      (truncation), and added, times the scale, to -8 sum(q) s, at most 8 steps at 23 sum |q| s: with B = scale * max over the
+      visible keys of sum_g s_g sum |q_i|, and A the same of sum |q k|, and the exponent's two roundings at up to 2 A
+      in units of log2: e = ((34 * 15 + 8 * 23) B + 12 A) 2^-23.  A query value below 2^-28 of its row's largest, Q, is off by
+      2^-34 Q at most: B's share of that is d Q 2^-34 scale max s 15.  Scores off by e move p / l by at most exp(2 e) - 1;
+    - codes are subnormal fp16 operands, whose products are lined up as if they were 2^-14: of each of a step's sixteen products
+      2^-14 of the step's largest other operand may be cut off.  Scores: d / 16 steps of 16 * 2^-14 Q scale max s, into e.
+      Output: 16 * 2^-14 of each step's largest weight, at most 2^-10 U;
+    - sums over n visible keys of c f and of 8 f, up to 23 U with U = sum p s, and the exponential (2^-22) and rescales:
+      (n + 128) 2^-23 of 23 U.
 
     The relative part is asserted to be under 5 %, so that no input makes the comparison empty."""
     Hq, d = q.shape[1], q.shape[2]
@@ -143,7 +150,8 @@ def cache_attention(q, spans, causal, scale, cache, table, left_out=()):
             continue
         pages = [p if 0 <= p < cache.pages else 0 for p in table[si][:-(-nk // cache.page)]]
         kn, ks = (t[:nk] for t in cache.codes(pages, True))
-        vv_all = cache.values(pages, False)[:nk]
+        vn, vs_all = (t[:nk] for t in cache.codes(pages, False))
+        vv_all = vn.double() * vs_all.repeat_interleave(32, -1)
         i, j = torch.arange(nq)[:, None], torch.arange(nk)[None]
         seen = j <= i + (nk - nq) if causal else torch.ones(nq, nk, dtype=torch.bool)
         seen = seen.clone()
@@ -166,12 +174,18 @@ def cache_attention(q, spans, causal, scale, cache, table, left_out=()):
             l = p.sum(-1, keepdim=True)
             p = torch.where(l > 0, p / l, torch.zeros_like(p))
             o, size = p @ vv, p @ vv.abs()
-            e = (68 * 143 * B + 12 * A) * 2.0 ** -23
-            rel = 2.0 ** -8 + torch.expm1(2 * e) + (seen.sum(-1)[None, :, None] + 128) * 2.0 ** -23
+            sv = torch.nan_to_num(vs_all[:, h], nan=0.0, posinf=0.0, neginf=0.0)
+            U, W = p @ sv.repeat_interleave(32, -1), (p * sv.amax(-1)).amax(-1, keepdim=True)
+            e = ((34 * 15 + 8 * 23) * B + 12 * A) * 2.0 ** -23
+            e = e + d * qq.abs().amax(-1, keepdim=True) * 2.0 ** -34 * scale * sk.max() * 15
+            e = e + d / 16 * 2.0 ** -10 * qq.abs().amax(-1, keepdim=True) * scale * sk.max()
+            n = seen.sum(-1)[None, :, None]
+            rel = 2.0 ** -11 + torch.expm1(2 * e)
             assert float(rel.max()) < 0.05, float(rel.max())
+            off = ((n + 128) * 2.0 ** -23 * 23 + 2.0 ** -10) * U + n * 7 * 2.0 ** -30 * W
             b = (seen.double() @ (vbad | kbad[:, None]).double() > 0)[None].expand_as(o)
             put = lambda x: x.transpose(0, 1)  # noqa: E731
             out[q0:q0 + nq, heads] = put(torch.where(b, torch.zeros_like(o), o))
-            tol[q0:q0 + nq, heads] = put(torch.where(b, torch.zeros_like(o), rel * size + 2.0 ** -8 * o.abs() + 1e-30))
+            tol[q0:q0 + nq, heads] = put(torch.where(b, torch.zeros_like(o), rel * size + off + 2.0 ** -8 * o.abs() + 1e-30))
             bad[q0:q0 + nq, heads] = put(b)
     return out, tol, bad, owned
