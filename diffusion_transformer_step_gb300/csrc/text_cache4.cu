@@ -264,9 +264,14 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 }
 
 template <int D>
-struct Stage {  // 128 tokens of one head
+struct Stage {  // 128 tokens of one head: pages of up to 64 tokens as they lie in the cache, larger ones' parts
   static constexpr int G = D / 32;
-  static constexpr uint32_t kCodes = kKeys * D / 2, kScales = kKeys * G * 2, kBytes = 2 * (kCodes + kScales);
+  static constexpr uint32_t kBytes = kKeys * D * 9 / 8;
+};
+
+// Where a tile of 16 tokens has its codes and scales of the keys; the values' lie `values` bytes further on.
+struct Tile {
+  const uint8_t *codes, *scales;
 };
 
 template <int N>  // N words at once, N = 1, 2 or 4
@@ -307,27 +312,25 @@ constexpr float kRoom = 6.0f;  // a row's largest weight lies 2^6 above its refe
 
 // A warp's 32 tokens of a stage, from token t0 of the sequence on. kMasked: some column does not see some of them.
 template <int D, int NT, bool kMasked>
-__device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* at, int tok0, int t0, uint32_t here, int last, int lane) {
-  using L = Stage<D>;
-  constexpr int G = L::G;
+__device__ __forceinline__ void attend(Rows<D, NT>& R, const Tile (&at)[2], int values, int t0, uint32_t here, int last, int lane) {
+  constexpr int G = Stage<D>::G;
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;
   // whether column e of n sees this lane's token r0 + 8 h of tile i
   auto sees = [&](int i, int n, int h, int e) {
     return ((here >> i) & 1u) && t0 + i * 16 + r0 + 8 * h < min(R.limit[n][e], last);
   };
-  const uint8_t* vat = at + L::kCodes + L::kScales;
   float x[2][NT][4];           // scores, then probabilities, of two tiles of 16 tokens
   uint32_t vs[2][2][G / 2];    // scales of the values of the tokens r0 and r0 + 8
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int tok = tok0 + i * 16 + r0;
-    lds<G / 2>(vs[i][0], vat + L::kCodes + tok * (G * 2));
-    lds<G / 2>(vs[i][1], vat + L::kCodes + (tok + 8) * (G * 2));
+    const uint8_t *codes = at[i].codes + r0 * (D / 2) + (lane & 3) * (G * 4), *sc = at[i].scales + r0 * (G * 2);
+    lds<G / 2>(vs[i][0], sc + values);
+    lds<G / 2>(vs[i][1], sc + values + 8 * (G * 2));
     uint32_t lo[G], hi[G], wlo[G / 2], whi[G / 2];  // codes and scales of the tokens r0 and r0 + 8
-    lds<G>(lo, at + tok * (D / 2) + (lane & 3) * (G * 4));
-    lds<G>(hi, at + (tok + 8) * (D / 2) + (lane & 3) * (G * 4));
-    lds<G / 2>(wlo, at + L::kCodes + tok * (G * 2));
-    lds<G / 2>(whi, at + L::kCodes + (tok + 8) * (G * 2));
+    lds<G>(lo, codes);
+    lds<G>(hi, codes + 8 * (D / 2));
+    lds<G / 2>(wlo, sc);
+    lds<G / 2>(whi, sc + 8 * (G * 2));
     {
       const bool odd = G == 4 && (lane & 1);
       const uint32_t u = wlo[odd ? G / 2 - 1 : 0], w = whi[odd ? G / 2 - 1 : 0], A[4] = {u, w, u, w};
@@ -433,7 +436,7 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* at, int to
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     // codes of the tokens c0, c0 + 1, c0 + 8 and c0 + 9: this lane's columns of V^T
-    const uint8_t* row = vat + (tok0 + i * 16 + c0) * (D / 2) + r0 * (G * 2);
+    const uint8_t* row = at[i].codes + values + c0 * (D / 2) + r0 * (G * 2);
     uint32_t w0[G / 2], w1[G / 2], w2[G / 2], w3[G / 2];
     lds<G / 2>(w0, row);
     lds<G / 2>(w1, row + D / 2);
@@ -472,7 +475,7 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* at, int to
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) cache4_attention_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
   using L = Stage<D>;
   constexpr int G = L::G, R = 8 * NT, V = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -506,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) cache4_attention_ke
   const bool direct = sp.nk <= P.chunk;  // this CTA has all the keys of its rows
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // fragment row, and first of two columns
   int used = 0;  // stages filled (or emptied) so far
+  const int held_shift = min(a.c.page_shift, 7), held = 1 << held_shift;  // tokens of a page that a stage holds
 
   for (int tile = tile0; tile < P.tiles; tile += P.walk) {
     const int base = tile * R, rows = min(R, sp.nq * group - base);  // this tile's query rows
@@ -515,12 +519,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) cache4_attention_ke
     const int blocks = first < last ? (last - first + kKeys - 1) / kKeys : 0;
 
     if (warp == 4) {
-      // Lane 4 i + part copies one part (codes or scales of the keys or values) of a stage's i-th page.
-      const int ps = 1 << a.c.page_shift, width = min(ps, kKeys), part = lane & 3, t0 = (lane >> 2) * width;
-      const int slab = a.c.slab(), cb = a.c.code_bytes(), sb = a.c.scale_bytes();
-      const int each = part & 1 ? G * 2 : D / 2;  // bytes of a token
-      const int src0 = (part & 2 ? cb + sb : 0) + (part & 1 ? cb : 0);
-      const int dst0 = (part & 2 ? (int)(L::kCodes + L::kScales) : 0) + (part & 1 ? (int)L::kCodes : 0) + t0 * each;
+      // Pages of up to 64 tokens come whole, lane i the i-th of a stage; of larger ones lane `part` brings a part (codes or
+      // scales, of the keys or the values). Copies this large matter: a page of 16 tokens in four of them kept the copy
+      // unit busy for as long as the arithmetic.
+      const int ps = 1 << a.c.page_shift, width = min(ps, kKeys), slab = a.c.slab();
+      const bool whole = ps <= 64;
+      const int part = whole ? 0 : lane, t0 = whole ? lane * ps : lane < 4 ? 0 : kKeys;
+      const int each = part & 1 ? G * 2 : D / 2;  // bytes of a token in a part
+      const int src0 = (part & 2 ? slab / 2 : 0) + (part & 1 ? a.c.code_bytes() : 0);
+      const int dst0 = whole ? lane * slab : (part & 2 ? (int)L::kBytes / 2 : 0) + (part & 1 ? kKeys * D / 2 : 0);
       const int32_t* table = a.table + (long long)seq * a.c.max_pages;
       auto page_of = [&](int j) {
         const int t = first + j * kKeys + t0;
@@ -533,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) cache4_attention_ke
         const bool wanted = t0 < kKeys && at < last, ok = wanted && page >= 0 && page < a.c.pages;
         if (wanted && !ok && part == 0) report_bad_entry(a.status, kSiteCache4Page);
         const int tiles = ok ? (min(width, last - at) + 15) / 16 : 0;  // of 16 tokens
-        const uint32_t bytes = (uint32_t)(tiles * 16 * each);
-        const uint32_t mask = part == 0 ? ((1u << tiles) - 1u) << (t0 / 16) : 0u;
+        const uint32_t bytes = !ok ? 0u : (uint32_t)(whole ? slab : tiles * 16 * each);
+        const uint32_t mask = part == 0 && ok ? ((1u << tiles) - 1u) << (t0 / 16) : 0u;
         const uint32_t all = __reduce_or_sync(0xffffffffu, mask), total = __reduce_add_sync(0xffffffffu, bytes);
         if (!mbar_wait_sleep(&empty[st], ((uint32_t)(n / kStages) & 1u) ^ 1u, wc, kSiteCache4Empty)) break;
         if (lane == 0) {
@@ -544,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) cache4_attention_ke
         __syncwarp();
         if (bytes)
           bulk_load(smem + st * L::kBytes + dst0,
-                    a.cache + ((long long)page * a.c.heads + hk) * slab + src0 + (at & (ps - 1)) * each, bytes, &full[st]);
+                    a.cache + ((long long)page * a.c.heads + hk) * slab + src0 + (whole ? 0 : (at & (ps - 1)) * each), bytes,
+                    &full[st]);
         page = next;
         issued = j + 1;
       }
@@ -647,9 +655,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 1) cache4_attention_ke
         if (!ok) break;
         const uint32_t here = (live[st] >> (2 * warp)) & 3u;
         const int t0 = first + j * kKeys + warp * 32;
-        const uint8_t* at = smem + st * L::kBytes;
-        if (here == 3u && t0 + 32 <= open) attend<D, NT, false>(Q, at, warp * 32, t0, here, last, lane);
-        else if (here) attend<D, NT, true>(Q, at, warp * 32, t0, here, last, lane);
+        Tile at[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = warp * 32 + i * 16, in = t & (held - 1);  // place in the page
+          const uint8_t* page = smem + st * L::kBytes + (t >> held_shift) * (held * (D * 9 / 8));
+          at[i].codes = page + in * (D / 2);
+          at[i].scales = page + held * (D / 2) + in * (G * 2);
+        }
+        const int values = held * (D * 9 / 16);
+        if (here == 3u && t0 + 32 <= open) attend<D, NT, false>(Q, at, values, t0, here, last, lane);
+        else if (here) attend<D, NT, true>(Q, at, values, t0, here, last, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
       }
