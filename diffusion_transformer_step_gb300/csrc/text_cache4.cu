@@ -36,11 +36,16 @@ __device__ __forceinline__ Run load_run(const Cache4MoveArgs& a, int s) {
   return r;
 }
 
-// Eight values of one head and token per thread: a word of key codes, or two half-words of value codes.
-// grid (tokens x heads x chunks of eight of keys, then of values; sequences).
-template <int D, bool kAppend>
-__global__ void __launch_bounds__(256) cache4_move_kernel(const Cache4MoveArgs a) {
-  constexpr int C = D / 8, G = D / 32;
+// Four threads take a token's head of keys or values: thread t the values 32 j + 8 t onwards, eight of every group j, which
+// lie side by side in the cache (a word each of the keys' codes, two half-words of the values') and in whole sectors of
+// the rows. A CTA has `tokens` tokens (a power of two), and where those do not fill it several heads side by side; each
+// thread goes through U of them with its loads ahead of its stores. The table is read once per token.
+// Memory bounds it: 512 new tokens of 16 sequences in and 700 to 8192 of each out (429 MB) take 75.7 us for both calls, 5.66
+// TB/s; with eight values a thread, and so many small CTAs, 214. A decoding step's append and read of eight short
+// sequences: 6.5 us, two launches.
+template <int D, bool kAppend, int U>
+__global__ void __launch_bounds__(256) cache4_move_kernel(const Cache4MoveArgs a, int tokens, int side, int parts) {
+  constexpr int G = D / 32;
   grid_dependency_wait();
   allow_dependents();
   const Run run = load_run(a, blockIdx.y);
@@ -48,71 +53,131 @@ __global__ void __launch_bounds__(256) cache4_move_kernel(const Cache4MoveArgs a
     if (blockIdx.x == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteCache4Lengths);
     return;
   }
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const int chunk = (int)(i % C), head = (int)(i / C % a.c.heads);
-  const bool value = (i / C / a.c.heads) & 1;
-  const long long t = i / C / a.c.heads / 2;
-  if (t >= run.n) return;  // the four threads of a group leave together
-  const int pos = run.start + (int)t, slot = pos & ((1 << a.c.page_shift) - 1);
+  const int block = blockIdx.x / parts, first = (blockIdx.x - block * parts) * side * U;  // of the heads, keys then values
+  const int t = threadIdx.x & 3, i = block * tokens + (int)(threadIdx.x >> 2) % tokens, lane = (threadIdx.x >> 2) / tokens;
+  if (i >= run.n) return;  // a token's four threads leave together
+  const int pos = run.start + i, slot = pos & ((1 << a.c.page_shift) - 1);
   const int page = a.table[(long long)blockIdx.y * a.c.max_pages + (pos >> a.c.page_shift)];
   if (page < 0 || page >= a.c.pages) {
-    if (chunk == 0 && head == 0 && !value) report_bad_entry(a.status, kSiteCache4Page);
+    if (first + lane == 0 && t == 0) report_bad_entry(a.status, kSiteCache4Page);
     return;
   }
-  uint8_t* slab = a.cache + ((long long)page * a.c.heads + head) * a.c.slab() + (value ? a.c.slab() / 2 : 0);
-  uint8_t* row = slab + slot * (D / 2);
-  bf16* scale_at = reinterpret_cast<bf16*>(slab + a.c.code_bytes()) + slot * G + chunk / 4;
-  const int j = chunk / 4, q = chunk & 3;  // group of 32, eight of it
-  uint32_t* key_at = reinterpret_cast<uint32_t*>(row) + q * G + j;
-  uint16_t* value_at = reinterpret_cast<uint16_t*>(row) + 2 * q * G + j;  // and G further on
-  const long long col = (long long)head * D + chunk * 8;
+  const int heads = a.c.heads, slab = a.c.slab(), scales = a.c.code_bytes() + slot * (G * 2);
+  uint8_t* const pages = a.cache + (long long)page * heads * slab;
+  const long long row = run.first + i;
+  const uint32_t four = 0xfu << (threadIdx.x & 28);
+  auto place = [&](int u, bool& value, int& head) {
+    const int h = first + u * side + lane;
+    value = h >= heads;
+    head = value ? h - heads : h;
+    return h < 2 * heads;
+  };
   if constexpr (kAppend) {
-    const uint4 u = *reinterpret_cast<const uint4*>(value ? a.v_in + (run.first + t) * a.ldv + col
-                                                          : a.k_in + (run.first + t) * a.ldk + col);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t top = 0;  // magnitudes of bf16 compare as integers, NaN above infinity
+    uint4 in[U][G];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-    const uint32_t four = 0xfu << (threadIdx.x & 28);
-    top = max(top, __shfl_xor_sync(four, top, 1));
-    top = max(top, __shfl_xor_sync(four, top, 2));
-    const bool bad = top >= 0x7f80u;
-    const bf16 sc = __float2bfloat16(fmaxf(__uint_as_float(top << 16), 7.0f * 0x1p-118f) / 7.0f);
-    const float inv = bad ? 0.f : 1.0f / __bfloat162float(sc);
-    uint32_t code = 0;
+    for (int u = 0; u < U; ++u) {
+      bool value;
+      int head;
+      if (!place(u, value, head)) continue;
+      const bf16* src = (value ? a.v_in + row * a.ldv : a.k_in + row * a.ldk) + head * D + t * 8;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_bf16x2(w[e]);
-      code |= (uint32_t)(max(-7, min(7, __float2int_rn(f.x * inv))) + 8) << (8 * e);
-      code |= (uint32_t)(max(-7, min(7, __float2int_rn(f.y * inv))) + 8) << (8 * e + 4);
+      for (int j = 0; j < G; ++j) in[u][j] = *reinterpret_cast<const uint4*>(src + 32 * j);
     }
-    if (bad) code = 0x88888888u;
-    if (value) {
-      value_at[0] = (uint16_t)code;
-      value_at[G] = (uint16_t)(code >> 16);
-    } else {
-      *key_at = code;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bool value;
+      int head;
+      if (!place(u, value, head)) continue;  // the same for a token's four threads
+      uint32_t code[G], sc[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t w[4] = {in[u][j].x, in[u][j].y, in[u][j].z, in[u][j].w};
+        uint32_t top = 0;  // magnitudes of bf16 compare as integers, NaN above infinity
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(four, top, 1));
+        top = max(top, __shfl_xor_sync(four, top, 2));
+        const bool bad = top >= 0x7f80u;
+        const bf16 scale = __float2bfloat16(fmaxf(__uint_as_float(top << 16), 7.0f * 0x1p-118f) / 7.0f);
+        const float inv = 1.0f / __bfloat162float(scale);
+        code[j] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_bf16x2(w[e]);
+          code[j] |= (uint32_t)(max(-7, min(7, __float2int_rn(f.x * inv))) + 8) << (8 * e);
+          code[j] |= (uint32_t)(max(-7, min(7, __float2int_rn(f.y * inv))) + 8) << (8 * e + 4);
+        }
+        if (bad) code[j] = 0x88888888u;
+        sc[j] = bad ? 0x7fffu : (uint32_t)__bfloat16_as_ushort(scale);
+      }
+      uint32_t out[G];
+#pragma unroll
+      for (int j = 0; j < G / 2; ++j) {  // keys: the groups' words; values: the groups' low half-words, then the high ones
+        out[j] = value ? __byte_perm(code[2 * j], code[2 * j + 1], 0x5410) : code[j];
+        out[G / 2 + j] = value ? __byte_perm(code[2 * j], code[2 * j + 1], 0x7632) : code[G / 2 + j];
+      }
+      uint8_t* half = pages + (long long)head * slab + (value ? slab / 2 : 0);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(half + slot * (D / 2)) + t * G;
+      uint32_t* sdst = reinterpret_cast<uint32_t*>(half + scales);
+      if constexpr (G == 4) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+        if (t == 0) *reinterpret_cast<uint2*>(sdst) = make_uint2(sc[0] | sc[1] << 16, sc[2] | sc[3] << 16);
+      } else {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+        if (t == 0) *sdst = sc[0] | sc[1] << 16;
+      }
     }
-    if (q == 0) *reinterpret_cast<uint16_t*>(scale_at) = bad ? 0x7fffu : __bfloat16_as_ushort(sc);
   } else {
-    const uint32_t code = value ? value_at[0] | ((uint32_t)value_at[G] << 16) : *key_at;
-    const float sc = __bfloat162float(*scale_at);
-    uint32_t w[4];
+    uint32_t in[U][G], sc[U][G / 2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack_bf16x2((float)((int)((code >> (8 * e)) & 15u) - 8) * sc, (float)((int)((code >> (8 * e + 4)) & 15u) - 8) * sc);
-    *reinterpret_cast<uint4*>(value ? a.v_out + (run.first + t) * a.ldv + col : a.k_out + (run.first + t) * a.ldk + col) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    for (int u = 0; u < U; ++u) {
+      bool value;
+      int head;
+      if (!place(u, value, head)) continue;
+      const uint8_t* half = pages + (long long)head * slab + (value ? slab / 2 : 0);
+      const uint8_t *src = half + slot * (D / 2) + t * (G * 4), *ssrc = half + scales;
+      if constexpr (G == 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src);
+        const uint2 s2 = *reinterpret_cast<const uint2*>(ssrc);
+        in[u][0] = w.x, in[u][1] = w.y, in[u][2] = w.z, in[u][3] = w.w, sc[u][0] = s2.x, sc[u][1] = s2.y;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(src);
+        in[u][0] = w.x, in[u][1] = w.y, sc[u][0] = *reinterpret_cast<const uint32_t*>(ssrc);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bool value;
+      int head;
+      if (!place(u, value, head)) continue;
+      bf16* dst = (value ? a.v_out + row * a.ldv : a.k_out + row * a.ldk) + head * D + t * 8;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t code = value ? __byte_perm(in[u][j / 2], in[u][G / 2 + j / 2], j & 1 ? 0x7632 : 0x5410) : in[u][j];
+        const uint32_t s2 = sc[u][j / 2];
+        const float scale = __uint_as_float(j & 1 ? s2 & 0xffff0000u : s2 << 16);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_bf16x2((float)((int)((code >> (8 * e)) & 15u) - 8) * scale,
+                             (float)((int)((code >> (8 * e + 4)) & 15u) - 8) * scale);
+        *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
   }
 }
 
 template <bool kAppend>
 cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
-  const long long threads = (long long)a.max_len * 2 * a.c.heads * (a.c.head_dim / 8), blocks = (threads + 255) / 256;
+  constexpr int U = kAppend ? 2 : 4;
+  int tokens = 1;
+  while (tokens < 64 && tokens < a.max_len) tokens *= 2;
+  const int side = 64 / tokens, parts = (2 * a.c.heads + side * U - 1) / (side * U);
+  const long long blocks = (((long long)a.max_len + tokens - 1) / tokens) * parts;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   LaunchScope scope(cls, s);
-  auto kernel = a.c.head_dim == 64 ? cache4_move_kernel<64, kAppend> : cache4_move_kernel<128, kAppend>;
-  return launch_k(kernel, dim3((unsigned)blocks, (unsigned)a.seqs), dim3(256), 0, s, a);
+  auto kernel = a.c.head_dim == 64 ? cache4_move_kernel<64, kAppend, U> : cache4_move_kernel<128, kAppend, U>;
+  return launch_k(kernel, dim3((unsigned)blocks, (unsigned)a.seqs), dim3(256), 0, s, a, tokens, side, parts);
 }
 
 // ---- attention ----------------------------------------------------------------------------------
@@ -127,7 +192,7 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 // warp per cycle: so a code is left where one AND leaves it. As the bits of an fp16 number, a code c in the lowest four
 // bits is the subnormal c 2^-24, in the next four c 2^-20: both exact operands, five operations per eight codes of the keys
 // and six of the values. (As bf16 128 + c, with an OR and more shifts, and an exact subtraction of 136 for the values: 458
-// instructions per 16 tokens instead of XXX, 260 us instead of XXX.)
+// instructions per 16 tokens instead of 355, 64 tokens over 8192 each 172 us instead of 140, all else equal.)
 //
 // Keys: the queries become fp16 times a power of two per row (largest magnitude in [2^13, 2^14)), exact down to 2^-28 of the
 // row's largest; those that meet the higher codes are divided by 16. The 8 that every code is too large is taken off
@@ -164,15 +229,21 @@ Plan make_plan(const Cache4AttnArgs& a) {
   p.rows = (int)(rows < (1ll << 30) ? rows : (1ll << 30));
   p.tile = rows <= 8 ? 8 : 16;
   p.tiles = (p.rows + p.tile - 1) / p.tile;
+  // Runs that give every SM three CTAs where the keys allow it, of 128 keys at least: a fourth CTA waits for a second
+  // round (one token over 32768 keys 25.3 us in six per SM, 19.0 in three). Up to 512 keys one run, without the second
+  // kernel (16 tokens over up to 300 keys 9.0 us in two runs, 6.5 in one; over 1000 9.7 in one, 7.1 in eight), and runs of
+  // at most 4096, so that ragged lengths even out (1024 cost 13 % more at 64 x 8192: a run takes ~3 us besides its keys).
   const long long items = heads * p.tiles < (1ll << 30) ? heads * p.tiles : (1ll << 30);
-  long long chunk = (long long)a.max_k * items / (6 * 152);
-  if (chunk > 1024) chunk = 1024;
+  long long chunk = (long long)a.max_k * items / (3 * 152);
+  if (chunk > 4096) chunk = 4096;
+  if (chunk < kKeys) chunk = kKeys;
+  if (a.max_k <= 512) chunk = a.max_k;
   // no more than 2^17 rows of parts (68 MB): splits <= 2^16 / rows + 1, one split past 2^16 rows
   const long long all = heads <= (1 << 16) ? heads * p.rows : (1 << 17);
   const long long least = all <= (1 << 16) ? ((a.max_k * all) >> 16) + 1 : a.max_k;
   if (chunk < least) chunk = least;
   if (chunk > a.max_k) chunk = a.max_k;
-  if (chunk < 256) chunk = 256;
+  if (chunk < 1) chunk = 1;
   p.chunk = (int)((chunk + kKeys - 1) / kKeys * kKeys);
   p.splits = (a.max_k + p.chunk - 1) / p.chunk;
   if (p.splits < 1) p.splits = 1;
@@ -269,9 +340,9 @@ struct Stage {  // 128 tokens of one head: pages of up to 64 tokens as they lie 
   static constexpr uint32_t kBytes = kKeys * D * 9 / 8;
 };
 
-// Where a tile of 16 tokens has its codes and scales of the keys; the values' lie `values` bytes further on.
-struct Tile {
-  const uint8_t *codes, *scales;
+// Where a lane finds what it reads of a warp's first tile of 16 tokens in a stage: bytes from the stage's start.
+struct Places {
+  int key_codes, key_scales, value_codes, value_scales;
 };
 
 template <int N>  // N words at once, N = 1, 2 or 4
@@ -310,11 +381,14 @@ struct Rows {
 
 constexpr float kRoom = 6.0f;  // a row's largest weight lies 2^6 above its reference when that is set, 2^15 at most
 
-// A warp's 32 tokens of a stage, from token t0 of the sequence on. kMasked: some column does not see some of them.
-template <int D, int NT, bool kMasked>
-__device__ __forceinline__ void attend(Rows<D, NT>& R, const Tile (&at)[2], int values, int t0, uint32_t here, int last, int lane) {
+// A warp's 32 tokens of a stage, from token t0 of the sequence on. kMasked: some column does not see some of them. kSmall: the
+// two tiles are pages of 16 tokens each, not neighbours in one.
+template <int D, int NT, bool kMasked, bool kSmall>
+__device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* stage, const Places& at, int t0, uint32_t here, int last,
+                                       int lane) {
   constexpr int G = Stage<D>::G;
-  const int r0 = lane >> 2, c0 = (lane & 3) * 2;
+  constexpr int kCodesOn = kSmall ? 16 * D * 9 / 8 : 16 * D / 2, kScalesOn = kSmall ? 16 * D * 9 / 8 : 16 * G * 2;
+  const int r0 = lane >> 2, odd = lane & 2 ? -(D / 2) : D / 2;
   // whether column e of n sees this lane's token r0 + 8 h of tile i
   auto sees = [&](int i, int n, int h, int e) {
     return ((here >> i) & 1u) && t0 + i * 16 + r0 + 8 * h < min(R.limit[n][e], last);
@@ -323,9 +397,9 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const Tile (&at)[2], int 
   uint32_t vs[2][2][G / 2];    // scales of the values of the tokens r0 and r0 + 8
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint8_t *codes = at[i].codes + r0 * (D / 2) + (lane & 3) * (G * 4), *sc = at[i].scales + r0 * (G * 2);
-    lds<G / 2>(vs[i][0], sc + values);
-    lds<G / 2>(vs[i][1], sc + values + 8 * (G * 2));
+    const uint8_t *codes = stage + at.key_codes + i * kCodesOn, *sc = stage + at.key_scales + i * kScalesOn;
+    lds<G / 2>(vs[i][0], stage + at.value_scales + i * kScalesOn);
+    lds<G / 2>(vs[i][1], stage + at.value_scales + i * kScalesOn + 8 * (G * 2));
     uint32_t lo[G], hi[G], wlo[G / 2], whi[G / 2];  // codes and scales of the tokens r0 and r0 + 8
     lds<G>(lo, codes);
     lds<G>(hi, codes + 8 * (D / 2));
@@ -435,13 +509,14 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const Tile (&at)[2], int 
     }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    // codes of the tokens c0, c0 + 1, c0 + 8 and c0 + 9: this lane's columns of V^T
-    const uint8_t* row = at[i].codes + values + c0 * (D / 2) + r0 * (G * 2);
+    // codes of the tokens c0, c0 + 1, c0 + 8 and c0 + 9: this lane's columns of V^T. Half of the lanes fetch the odd ones
+    // first, so that the four rows of a load lie in other banks (half as many conflicts), and pick them the other way round.
+    const uint8_t* row = stage + at.value_codes + i * kCodesOn;
     uint32_t w0[G / 2], w1[G / 2], w2[G / 2], w3[G / 2];
     lds<G / 2>(w0, row);
-    lds<G / 2>(w1, row + D / 2);
+    lds<G / 2>(w1, row + odd);
     lds<G / 2>(w2, row + 8 * (D / 2));
-    lds<G / 2>(w3, row + 9 * (D / 2));
+    lds<G / 2>(w3, row + 8 * (D / 2) + odd);
     float slo[G], shi[G];
     scales<G / 2>(slo, vs[i][0]);
     scales<G / 2>(shi, vs[i][1]);
@@ -464,7 +539,7 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const Tile (&at)[2], int 
       // the codes' low bytes of the group's half-words, then the high ones
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t pick = g & 1 ? (h ? 0x4743u : 0x4642u) : (h ? 0x4541u : 0x4440u);
+        const uint32_t pick = (lane & 2 ? 0x0044u : 0x0440u) + (uint32_t)(2 * (g & 1) + h) * 0x0101u;
         const uint32_t near = __byte_perm(w0[g / 2], w1[g / 2], pick), far = __byte_perm(w2[g / 2], w3[g / 2], pick);
         const uint32_t A[4] = {near & 0x000f000fu, near & 0x00f000f0u, far & 0x000f000fu, far & 0x00f000f0u};
 #pragma unroll
@@ -474,7 +549,7 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const Tile (&at)[2], int 
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kSmall>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
   using L = Stage<D>;
   constexpr int G = L::G, R = 8 * NT, V = D / 32;
@@ -509,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
   const bool direct = sp.nk <= P.chunk;  // this CTA has all the keys of its rows
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // fragment row, and first of two columns
   int used = 0;  // stages filled (or emptied) so far
-  const int held_shift = min(a.c.page_shift, 7), held = 1 << held_shift;  // tokens of a page that a stage holds
 
   for (int tile = tile0; tile < P.tiles; tile += P.walk) {
     const int base = tile * R, rows = min(R, sp.nq * group - base);  // this tile's query rows
@@ -648,26 +722,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
       open = min(open, __shfl_xor_sync(0xffffffffu, open, 1));
       open = min(open, __shfl_xor_sync(0xffffffffu, open, 2));
 
+      Places at;
+      {
+        const int held_shift = min(a.c.page_shift, 7), held = 1 << held_shift;  // tokens of a page that a stage holds
+        const int page = ((warp * 32) >> held_shift) * (held * (D * 9 / 8)), in = (warp * 32) & (held - 1);
+        at.key_codes = page + (in + r0) * (D / 2) + (lane & 3) * (G * 4);
+        at.key_scales = page + held * (D / 2) + (in + r0) * (G * 2);
+        at.value_codes = page + held * (D * 9 / 16) + (in + c0 + (lane & 2 ? 1 : 0)) * (D / 2) + r0 * (G * 2);
+        at.value_scales = at.key_scales + held * (D * 9 / 16);
+      }
+      int st = used % kStages, t0 = first + warp * 32;
+      uint32_t phase = (uint32_t)(used / kStages) & 1u;
+      const uint8_t* stage = smem + st * L::kBytes;
+#pragma unroll 1
       for (int j = 0; j < blocks; ++j) {
-        const int nn = used + j, st = nn % kStages;
-        bool ok = mbar_wait(&full[st], (uint32_t)(nn / kStages) & 1u, wc, kSiteCache4Full);
+        bool ok = mbar_wait(&full[st], phase, wc, kSiteCache4Full);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t here = (live[st] >> (2 * warp)) & 3u;
-        const int t0 = first + j * kKeys + warp * 32;
-        Tile at[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = warp * 32 + i * 16, in = t & (held - 1);  // place in the page
-          const uint8_t* page = smem + st * L::kBytes + (t >> held_shift) * (held * (D * 9 / 8));
-          at[i].codes = page + in * (D / 2);
-          at[i].scales = page + held * (D / 2) + in * (G * 2);
-        }
-        const int values = held * (D * 9 / 16);
-        if (here == 3u && t0 + 32 <= open) attend<D, NT, false>(Q, at, values, t0, here, last, lane);
-        else if (here) attend<D, NT, true>(Q, at, values, t0, here, last, lane);
+        if (here == 3u && t0 + 32 <= open) attend<D, NT, false, kSmall>(Q, stage, at, t0, here, last, lane);
+        else if (here) attend<D, NT, true, kSmall>(Q, stage, at, t0, here, last, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
+        t0 += kKeys;
+        stage += L::kBytes;
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1u;
+          stage = smem;
+        }
       }
       // From sums of codes to values: 8 sums of f off, the codes' powers of two undone.
 #pragma unroll
@@ -768,7 +851,7 @@ __global__ void __launch_bounds__(128) cache4_join_kernel(const __grid_constant_
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kSmall>
 cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStream_t s) {
   static std::atomic<bool> raised[16];  // per device
   Params P;
@@ -791,14 +874,14 @@ cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStre
   cudaGetDevice(&dev);
   if (dev >= 16 || !raised[dev].load(std::memory_order_acquire)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(cache4_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(cache4_attention_kernel<D, NT, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev < 16) raised[dev].store(true, std::memory_order_release);
   }
   const long long heads = (long long)a.seqs * a.c.heads;
   {
     LaunchScope scope(kClsCache4Attention, s);
-    const cudaError_t e = launch_k(cache4_attention_kernel<D, NT>, dim3((unsigned)(heads * p.splits * p.walk)),
+    const cudaError_t e = launch_k(cache4_attention_kernel<D, NT, kSmall>, dim3((unsigned)(heads * p.splits * p.walk)),
                                    dim3(kThreads), smem, s, P);
     if (e != cudaSuccess) return e;
   }
@@ -827,8 +910,12 @@ size_t cache4_attention_parts_bytes(const Cache4AttnArgs& a) {
 
 cudaError_t launch_cache4_attention(const Cache4AttnArgs& a, cudaStream_t s) {
   const Plan p = make_plan(a);
-  if (a.c.head_dim == 64) return p.tile == 8 ? launch_attention_as<64, 1>(a, p, s) : launch_attention_as<64, 2>(a, p, s);
-  return p.tile == 8 ? launch_attention_as<128, 1>(a, p, s) : launch_attention_as<128, 2>(a, p, s);
+  const bool small = a.c.page_shift == 4, eight = p.tile == 8;
+  if (a.c.head_dim == 64)
+    return small ? (eight ? launch_attention_as<64, 1, true>(a, p, s) : launch_attention_as<64, 2, true>(a, p, s))
+                 : (eight ? launch_attention_as<64, 1, false>(a, p, s) : launch_attention_as<64, 2, false>(a, p, s));
+  return small ? (eight ? launch_attention_as<128, 1, true>(a, p, s) : launch_attention_as<128, 2, true>(a, p, s))
+               : (eight ? launch_attention_as<128, 1, false>(a, p, s) : launch_attention_as<128, 2, false>(a, p, s));
 }
 
 }  // namespace dit
