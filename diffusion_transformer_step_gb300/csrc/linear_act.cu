@@ -9,8 +9,20 @@
 //                            MMA's row side and the activation rows its column side, the depth split over
 //                            a cluster of up to eight CTAs.
 //
-// Splits add up through distributed shared memory, in rank order: each CTA leaves its part in its own shared
-// memory (the ring has been read), then finishes its share of the rows from all parts.
+// Splits add up through distributed shared memory, in rank order: each CTA writes its part of a row to the CTA that will
+// finish it (whose ring has been read), and finishes its own share of the rows from the parts that have come. (Left where
+// they were made and fetched by the one that finishes them, every row waited for another SM's memory: 777 x 1544 x 5160 with
+// all three 33.9 us, so 27.8.)
+//
+// Measured (bursts of twenty calls on different weights): 8192 x 12288 x 4096 445 to 454 us, 1820 to 1854 TFLOP/s (0.94 to 0.96
+// of the measured burst); call after call 520 to 540, at the clocks that power leaves, with any epilogue (0.93 of the
+// measured sustained rate). 4096 x 4096 x 4096 82 us; 1 x 12288 x 4096 19.4 (5.2 TB/s of weights), 1 x 2560 x 4096 7.5,
+// 64 x 4096 x 4096 11.8, 777 x 1544 x 5160 25.5 without epilogue. A call has about 3.5 us besides its loads: launch, first
+// load, the cluster's two barriers, the last rows.
+// Measured and left: accumulators through shared memory to whole lines of the output, at six stages instead of seven (8192 x
+// 12288 x 4096 455 -> 476 us: the MMAs and the loads take all of shared memory's cycles); the first weights sent to L2 before the
+// kernel before has ended (1 x 2560 x 4096 7.3 -> 7.9: every line crosses the copy unit twice); two CTAs of three stages per
+// SM for 128 rows (11.8 -> 13.8).
 #include <math.h>
 
 #include <atomic>
@@ -69,16 +81,16 @@ __device__ __forceinline__ float2 activate(float2 z) {
 
 constexpr int kAnyAct = -1;  // looked up at run time
 
-template <int kAct>
-__device__ __forceinline__ void activate4(float2& a, float2& b, int act) {
+template <int kAct, int N>
+__device__ __forceinline__ void activate_all(float2 (&z)[N], int act) {
   if constexpr (kAct != kAnyAct) {
-    a = activate<kAct>(a);
-    b = activate<kAct>(b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = activate<kAct>(z[i]);
   } else if (act != 0) {
-    if (act == 1) activate4<1>(a, b, 1);
-    else if (act == 2) activate4<2>(a, b, 2);
-    else if (act == 3) activate4<3>(a, b, 3);
-    else activate4<4>(a, b, 4);
+    if (act == 1) activate_all<1>(z, 1);
+    else if (act == 2) activate_all<2>(z, 2);
+    else if (act == 3) activate_all<3>(z, 3);
+    else activate_all<4>(z, 4);
   }
 }
 
@@ -93,39 +105,51 @@ __device__ __forceinline__ uint2 load4(const bf16* row, int c, int n) {
   return u;
 }
 
-// Sums v of columns [c, c + 4) of row r to the output; bias and res as load4 gives them.
-template <int kAct>
-__device__ __forceinline__ void finish4(const LinearActArgs& p, long long r, int c, float4 v, uint2 bias, uint2 res) {
+// Sums v of columns [c, c + 4) of N rows r[i] to the output, of those below `rows`; bias and res as load4 gives them.
+template <int kAct, int N>
+__device__ __forceinline__ void finish4(const LinearActArgs& p, const int (&r)[N], int rows, int m0, int c,
+                                        const float4 (&v)[N], uint2 bias, const uint2 (&res)[N]) {
   const bool whole = c + 4 <= p.n;
-  float2 lo = make_float2(v.x, v.y), hi = make_float2(v.z, v.w);
-  if (p.bias) {
-    lo = __fadd2_rn(lo, unpack_bf16x2(bias.x));
-    hi = __fadd2_rn(hi, unpack_bf16x2(bias.y));
-  }
-  activate4<kAct>(lo, hi, p.act);
-  if (p.res) {
-    lo = __fadd2_rn(lo, unpack_bf16x2(res.x));
-    hi = __fadd2_rn(hi, unpack_bf16x2(res.y));
-  }
-  if (p.out_f32) {
-    float* o = reinterpret_cast<float*>(p.out) + r * p.ld_out + c;
-    if (whole) {
-      *reinterpret_cast<float4*>(o) = make_float4(lo.x, lo.y, hi.x, hi.y);
-    } else {
-      o[0] = lo.x;
-      if (c + 1 < p.n) o[1] = lo.y;
-      if (c + 2 < p.n) o[2] = hi.x;
+  float2 z[2 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    z[2 * i] = make_float2(v[i].x, v[i].y);
+    z[2 * i + 1] = make_float2(v[i].z, v[i].w);
+    if (p.bias) {
+      z[2 * i] = __fadd2_rn(z[2 * i], unpack_bf16x2(bias.x));
+      z[2 * i + 1] = __fadd2_rn(z[2 * i + 1], unpack_bf16x2(bias.y));
     }
-  } else {
-    bf16* o = reinterpret_cast<bf16*>(p.out) + r * p.ld_out + c;
-    const uint2 u = make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
-    if (whole) {
-      *reinterpret_cast<uint2*>(o) = u;
+  }
+  activate_all<kAct>(z, p.act);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (r[i] >= rows) continue;
+    float2 lo = z[2 * i], hi = z[2 * i + 1];
+    if (p.res) {
+      lo = __fadd2_rn(lo, unpack_bf16x2(res[i].x));
+      hi = __fadd2_rn(hi, unpack_bf16x2(res[i].y));
+    }
+    const long long at = (long long)(m0 + r[i]) * p.ld_out + c;
+    if (p.out_f32) {
+      float* o = reinterpret_cast<float*>(p.out) + at;
+      if (whole) {
+        *reinterpret_cast<float4*>(o) = make_float4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        o[0] = lo.x;
+        if (c + 1 < p.n) o[1] = lo.y;
+        if (c + 2 < p.n) o[2] = hi.x;
+      }
     } else {
-      uint16_t* h = reinterpret_cast<uint16_t*>(o);
-      h[0] = (uint16_t)u.x;
-      if (c + 1 < p.n) h[1] = (uint16_t)(u.x >> 16);
-      if (c + 2 < p.n) h[2] = (uint16_t)u.y;
+      bf16* o = reinterpret_cast<bf16*>(p.out) + at;
+      const uint2 u = make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(hi.x, hi.y));
+      if (whole) {
+        *reinterpret_cast<uint2*>(o) = u;
+      } else {
+        uint16_t* h = reinterpret_cast<uint16_t*>(o);
+        h[0] = (uint16_t)u.x;
+        if (c + 1 < p.n) h[1] = (uint16_t)(u.x >> 16);
+        if (c + 2 < p.n) h[2] = (uint16_t)u.y;
+      }
     }
   }
 }
@@ -171,70 +195,67 @@ __device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, in
   }
 }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // The rows r0, r0 + step, ... below `rows` (of the output: m0 further), four columns from c on per thread; part(r, k) is what
-// rank k's shared memory holds of them, added in rank order.  Parts and residual of one row are fetched ahead of the
-// arithmetic of the row before.  Not unrolled further: a loop that runs a few times waits for its code as
-// much as for its data (128 rows of one block of depth, eight rows at once: 8.8 us, two 6.4).
+// split k has sent of them, added in split order. Two rows go side by side, the residual of the next two ahead. Not
+// unrolled further: a loop that runs a few times waits for its code as much as for its data (128 rows of one
+// block of depth, eight rows at once: 8.8 us, two 6.4).
 template <int K, typename Part>
 __device__ __forceinline__ void finish_rows(const Params& P, int r0, int step, int rows, int m0, int c, Part part) {
   const LinearActArgs& p = P.a;
-  struct Row {
-    float4 v[K];
-    uint2 res;
-  };
-  auto load = [&](int r, Row& x) {
-    x.res = make_uint2(0, 0);
-    if (r < rows && p.res) x.res = load4(p.res + (long long)(m0 + r) * p.ld_res, c, p.n);
+  const uint2 none = make_uint2(0, 0), bias = p.bias ? load4(p.bias, c, p.n) : none;
+  auto residual = [&](int r) { return r < rows && p.res ? load4(p.res + (long long)(m0 + r) * p.ld_res, c, p.n) : none; };
+  auto sum = [&](int r) {
+    float4 x = part(min(r, rows - 1), 0);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      x.v[k] = r < rows && (K == 1 || k < P.splits) ? part(r, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 1; k < K; ++k)
+      if (k < P.splits) {
+        const float4 v = part(min(r, rows - 1), k);
+        x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+      }
+    return x;
   };
-  const uint2 bias = p.bias ? load4(p.bias, c, p.n) : make_uint2(0, 0);
-  auto finish = [&](int r, const Row& x) {
-    float4 sum = x.v[0];
-#pragma unroll
-    for (int k = 1; k < K; ++k) sum.x += x.v[k].x, sum.y += x.v[k].y, sum.z += x.v[k].z, sum.w += x.v[k].w;
-    if (r < rows) finish4<kAnyAct>(p, m0 + r, c, sum, bias, x.res);
-  };
-  Row one, two;
-  load(r0, one);
+  uint2 res[2] = {residual(r0), residual(r0 + step)};
 #pragma unroll 1
   for (int r = r0; r < rows; r += 2 * step) {
-    load(r + step, two);
-    finish(r, one);
-    load(r + 2 * step, one);
-    finish(r + step, two);
+    const int both[2] = {r, r + step};
+    const float4 v[2] = {sum(r), sum(r + step)};
+    const uint2 now[2] = {res[0], res[1]};
+    res[0] = residual(r + 2 * step), res[1] = residual(r + 3 * step);
+    finish4<kAnyAct>(p, both, rows, m0, c, v, bias, now);
   }
 }
 
 // ---- many rows -------------------------------------------------------------------------------
 
-constexpr int kWideStages = 7, kWideThreads = 320;
-constexpr uint32_t kWideTile = 128 * 128, kWideStage = 2 * kWideTile;
-constexpr size_t kWideBytes = 1024 + (size_t)kWideStages * kWideStage + 256;
-static_assert(kWideStages * kWideStage >= 128 * 256 * 4, "a split's part reuses the ring");
+constexpr int kWideThreads = 320;
+template <int BN>  // columns of a pair's tile: 128, 192 or 256
+struct Wide {
+  static constexpr uint32_t kA = 128 * 128, kW = BN / 2 * 128, kStage = kA + kW;
+  static constexpr int kStages = 229376 / (int)kStage;
+  static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256;
+  static_assert(kStages * kStage >= 131 * BN * 4, "the splits' parts reuse the ring");
+};
 
 // Pair `pair` of a cluster (rank = 2 pair + half) takes the depth blocks [K pair / S, K (pair + 1) / S) of its cluster's
 // tiles; with splits a cluster has one tile.  Roles as in the step's products: warp 0 loads, warp 1 issues (the
 // pair's first CTA), warps 2 to 9 finish, one thread per row of 128 columns.
-template <int kAct, bool kSplit>
+template <int kAct, bool kSplit, int BN>
 __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const __grid_constant__ Params P) {
+  using L = Wide<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
-  uint8_t* sW = smem + kWideStages * kWideTile;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kWideStages * kWideStage);
-  uint64_t* empty = full + kWideStages;
-  uint64_t* acc_full = empty + kWideStages;
+  uint8_t* sW = smem + L::kStages * L::kA;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -246,8 +267,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
   const int first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
   const int kb0 = kSplit ? (int)((long long)P.kblocks * split / S) : 0;
   const int kb1 = kSplit ? (int)((long long)P.kblocks * (split + 1) / S) : P.kblocks;
+  [[maybe_unused]] const int per = (127 + S) / S;  // rows of a half that a split finishes, at most
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kWideStages; ++s) {
+    for (int s = 0; s < L::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -282,7 +304,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
       bool ok = true;
       for (int t = first; t < P.tiles && ok; t += step) {
         const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
-        const int arow = mt * 256 + (int)half * 128, wrow = nt * 256 + (int)half * 128;
+        const int arow = mt * 256 + (int)half * 128, wrow = nt * BN + (int)half * (BN / 2);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (mt == 0 && kb + 8 < kb1) pf_l2(&P.w_map, (kb + 8) * 64, wrow);  // one prefetcher per weight column
           if (!mbar_wait_sleep(&empty[stage], phase ^ 1u, wc, kSiteEmpty)) {
@@ -290,11 +312,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
             break;
           }
           const uint32_t fb = map_to_rank(smem_u32(&full[stage]), leader);
-          if (half == 0) mbar_arrive_expect_tx(&full[stage], 2 * kWideStage);
-          tma2_2sm(sA + stage * kWideTile, &P.a_map, fb, kb * 64, arow);
-          tma2_2sm(sW + stage * kWideTile, &P.w_map, fb, kb * 64, wrow);
+          if (half == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
+          tma2_2sm(sA + stage * L::kA, &P.a_map, fb, kb * 64, arow);
+          tma2_2sm(sW + stage * L::kW, &P.w_map, fb, kb * 64, wrow);
           ++issued;
-          if (++stage == kWideStages) {
+          if (++stage == L::kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -302,10 +324,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
       }
       if (!ok && half == 0) {
         // Unwinding: let copies in flight land (bounded) before the pair exits.
-        const long long outstanding = issued < kWideStages ? issued : kWideStages;
+        const long long outstanding = issued < L::kStages ? issued : L::kStages;
         for (long long i = 0; i < outstanding; ++i) {
           if (stage == 0) {
-            stage = kWideStages;
+            stage = L::kStages;
             phase ^= 1u;
           }
           --stage;
@@ -317,7 +339,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
     }
   } else if (warp == 1) {
     if (lane == 0 && half == 0) {
-      const uint32_t idesc = make_idesc_bf16(256, 256, false);
+      const uint32_t idesc = make_idesc_bf16(256, BN, false);
       const uint16_t both = (uint16_t)(3u << leader);
       auto commit = [&](uint64_t* bar) {
         asm volatile(
@@ -340,13 +362,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
             break;
           }
           tc_fence_after();
-          const uint64_t ad = desc_advance(a0, stage * (kWideTile >> 4)), wd = desc_advance(w0, stage * (kWideTile >> 4));
+          const uint64_t ad = desc_advance(a0, stage * (L::kA >> 4)), wd = desc_advance(w0, stage * (L::kW >> 4));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma2(tmem + (uint32_t)(acc * 256), desc_advance(ad, kk * 2), desc_advance(wd, kk * 2), idesc,
+            umma2(tmem + (uint32_t)(acc * BN), desc_advance(ad, kk * 2), desc_advance(wd, kk * 2), idesc,
                   kb > kb0 || kk ? 1u : 0u);
           commit(&empty[stage]);
-          if (++stage == kWideStages) {
+          if (++stage == L::kStages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -360,46 +382,60 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
       }
     }
   } else {
-    const int q = warp & 3, eh = (warp - 2) >> 2;  // rows [32 q, 32 q + 32) of this CTA, columns [128 eh, 128 eh + 128)
-    const uint32_t free0 = map_to_rank(smem_u32(acc_empty), leader);
-    int local = 0;
-    for (int t = first; t < P.tiles; t += step, ++local) {
-      const int acc = local & 1;
-      const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
-      const int r = q * 32 + lane, row = mt * 256 + (int)half * 128 + r, col = nt * 256 + eh * 128;
-      // the residual's pieces one ahead, the first before the accumulator is waited for
-      uint4 ahead[4];
-      auto fetch = [&](int c) {
-        if (kSplit || !P.a.res || row >= P.a.rows || c + 32 > P.a.n) return;
-        const uint4* src = reinterpret_cast<const uint4*>(P.a.res + row * P.a.ld_res + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ahead[i] = src[i];
-      };
-      fetch(col);
-      bool ok = mbar_wait_sleep(&acc_full[acc], (uint32_t)(local >> 1) & 1u, wc, kSiteAccFull);
+    const int q = warp & 3, eh = (warp - 2) >> 2;  // rows [32 q, 32 q + 32) of this CTA, half the columns
+    const int r = q * 32 + lane;
+    if constexpr (kSplit) {
+      bool ok = mbar_wait_sleep(&acc_full[0], 0, wc, kSiteAccFull);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       tc_fence_after();
-      const uint32_t tb = tmem + (uint32_t)(acc * 256 + eh * 128) + ((uint32_t)(q * 32) << 16);
+      cluster_sync_all();  // every CTA's ring has been read
+      // Row r to the pair that finishes it, 16-byte pieces turned by its place there, so that eight rows lie in different banks.
+      const uint32_t owner = map_to_rank(smem_u32(smem), (uint32_t)(2 * (r % S)) + half);
+      const int place = split * per + r / S;
+      if (ok) {
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int cc = col + c * 32;
-        if (cc >= P.a.n) break;
-        uint4 res[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) res[i] = ahead[i];
-        if (c < 3) fetch(cc + 32);
-        uint32_t v[32];
-        tmem_load32(tb + c * 32, v);
-        if (kSplit) {
-          // 16-byte pieces of a row are turned by the row's number, so that eight rows lie in different banks
-          float4* part = reinterpret_cast<float4*>(smem) + r * 64;
+        for (int c = 0; c < BN / 64; ++c) {
+          uint32_t v[32];
+          tmem_load32(tmem + (uint32_t)(eh * (BN / 2) + c * 32) + ((uint32_t)(q * 32) << 16), v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            part[(eh * 32 + c * 8 + i) ^ (r & 7)] =
-                make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                            __uint_as_float(v[4 * i + 3]));
-        } else if (row < P.a.rows) {
+            st_cluster(owner + (uint32_t)(place * (BN / 4) + ((eh * (BN / 8) + c * 8 + i) ^ (r / S & 7))) * 16,
+                       make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                   __uint_as_float(v[4 * i + 3])));
+        }
+      }
+    } else {
+      const uint32_t free0 = map_to_rank(smem_u32(acc_empty), leader);
+      int local = 0;
+      for (int t = first; t < P.tiles; t += step, ++local) {
+        const int acc = local & 1;
+        const int nt = t / P.m_tiles, mt = t - nt * P.m_tiles;
+        const int row = mt * 256 + (int)half * 128 + r, col = nt * BN + eh * (BN / 2);
+        // the residual's pieces one ahead, the first before the accumulator is waited for
+        uint4 ahead[4];
+        auto fetch = [&](int c) {
+          if (!P.a.res || row >= P.a.rows || c + 32 > P.a.n) return;
+          const uint4* src = reinterpret_cast<const uint4*>(P.a.res + row * P.a.ld_res + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ahead[i] = src[i];
+        };
+        fetch(col);
+        bool ok = mbar_wait_sleep(&acc_full[acc], (uint32_t)(local >> 1) & 1u, wc, kSiteAccFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tb = tmem + (uint32_t)(acc * BN + eh * (BN / 2)) + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < BN / 64; ++c) {
+          const int cc = col + c * 32;
+          if (cc >= P.a.n) break;
+          uint4 res[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) res[i] = ahead[i];
+          if (c + 1 < BN / 64) fetch(cc + 32);
+          uint32_t v[32];
+          tmem_load32(tb + c * 32, v);
+          if (row >= P.a.rows) continue;
           if (cc + 32 <= P.a.n) {
             finish32<kAct>(P.a, row, cc, v, res);
           } else {
@@ -409,40 +445,47 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
                 uint2 b4 = make_uint2(0, 0), r4 = b4;
                 if (P.a.bias) b4 = load4(P.a.bias, cc + 4 * i, P.a.n);
                 if (P.a.res) r4 = load4(P.a.res + row * P.a.ld_res, cc + 4 * i, P.a.n);
-                finish4<kAct>(P.a, row, cc + 4 * i, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                                                __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
-                              b4, r4);
+                const int r1[1] = {row};
+                const uint2 x1[1] = {r4};
+                const float4 f[1] = {make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))};
+                finish4<kAct>(P.a, r1, P.a.rows, 0, cc + 4 * i, f, b4, x1);
               }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(free0 + (uint32_t)(acc * 8));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(free0 + (uint32_t)(acc * 8));
     }
   }
 
   __syncwarp();
-  if (kSplit) {
+  auto free_tmem = [&] {
+    if (warp == 1) {
+      tc_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+  };
+  if constexpr (kSplit) {
+    if (warp < 2) cluster_sync_all();  // the one that the finishing warps went through above
     tc_fence_before();
-    cluster_sync_all();  // all parts are written
+    cluster_sync_all();  // all parts have come, no MMA, load or remote access is still in flight
+    free_tmem();
     const int nt = first / P.m_tiles, mt = first - nt * P.m_tiles;
-    if (warp >= 2 && first < P.tiles && !*abort_flag) {
-      // this CTA's share of its half's rows: 128 columns of one row per warp
-      const int m0 = mt * 256 + (int)half * 128, h = warp & 1, c = nt * 256 + h * 128 + lane * 4;
-      auto at = [&](int r) { return smem_u32(smem) + (uint32_t)(r * 64 + ((h * 32 + lane) ^ (r & 7))) * 16; };
-      if (c < P.a.n)
+    if (warp >= 2 && !*abort_flag) {
+      // this pair's share of its half's rows, every S-th: half the columns of one row per warp
+      const int m0 = mt * 256 + (int)half * 128, piece = (warp & 1) * (BN / 8) + lane, c = nt * BN + piece * 4;
+      const float4* parts = reinterpret_cast<const float4*>(smem);
+      if (lane < BN / 8 && c < P.a.n)
         finish_rows<4>(P, split + ((warp - 2) >> 1) * S, 4 * S, min(128, P.a.rows - m0), m0, c, [&](int r, int k) {
-          return ld_cluster_f32x4(map_to_rank(at(r), 2 * k + half));
+          return parts[(k * per + r / S) * (BN / 4) + (piece ^ (r / S & 7))];
         });
     }
-  }
-  __syncwarp();
-  tc_fence_before();
-  cluster_sync_all();  // no MMA, load, remote arrive or read of the cluster is still in flight
-  if (warp == 1) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  } else {
+    tc_fence_before();
+    cluster_sync_all();  // no MMA, load or remote arrive of the pair is still in flight
+    free_tmem();
   }
 }
 
@@ -456,7 +499,7 @@ struct Few {
   static constexpr int kThreads = 256;  // loader, issuer, two to share the finishing, four that read Tensor Memory
   static constexpr uint32_t kTmem = T < 32 ? 32 : T;
   static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256;
-  static_assert((size_t)kStages * kStage >= (size_t)T * 128 * 4, "the part reuses the ring");
+  static_assert((size_t)kStages * kStage >= (size_t)(T + 7) * 128 * 4, "the parts reuse the ring");
   static_assert(kThreads == 256, "eight warps finish");
 };
 
@@ -570,13 +613,15 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
       umma_commit(done);  // also after a wait that gave up: every MMA issued has ended when it arrives
     }
   }
-  // Every rank leaves its part [row][column] in its own shared memory: all loads have landed and all MMAs read them
-  // when `done` arrives.
-  float* part = reinterpret_cast<float*>(smem);
+  // All loads have landed and all MMAs read them when `done` arrives; then, over the cluster, no ring is in use any more.
+  // Every rank sends row r of its part to rank r % S, which finishes it.
+  float* parts = reinterpret_cast<float*>(smem);  // [split][row / S][column]
+  const int per = (T + S - 1) / S;
   __syncwarp();
   bool ok = mbar_wait_sleep(done, 0, wc, kSiteAccFull);
   ok = __all_sync(0xffffffffu, ok);
   tc_fence_after();
+  if (S > 1) cluster_sync_all();
   if (ok && !*abort_flag) {
     // warp w reads the columns [16, 32, ...) of its half, of the rows of its quarter
     const int q = warp & 3;
@@ -584,40 +629,45 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
     for (int c = (warp >> 2) * 16; c < T && c < P.a.rows; c += 32) {
       uint32_t v[16];
       tmem_load16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+      if (S == 1) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) part[(c + e) * 128 + q * 32 + lane] = __uint_as_float(v[e]);
+        for (int e = 0; e < 16; ++e) parts[(c + e) * 128 + q * 32 + lane] = __uint_as_float(v[e]);
+      } else {
+        int to = c % S, at = rank * per + c / S;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (c + e < P.a.rows) st_cluster(map_to_rank(smem_u32(parts + at * 128 + q * 32 + lane), to), __uint_as_float(v[e]));
+          if (++to == S) to = 0, ++at;
+        }
+      }
     }
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync_all();
-  const int c = nb * 128 + lane * 4;
-  if (c < P.a.n && !*abort_flag) {
-    // a row per warp, every S-th row a rank's
-    const float* at = part + lane * 4;
-    auto remote = [&](int r, int k) { return ld_cluster_f32x4(map_to_rank(smem_u32(at + r * 128), k)); };
-    if (S == 1)
-      finish_rows<1>(P, warp, 8, P.a.rows, 0, c, [&](int r, int) { return *reinterpret_cast<const float4*>(at + r * 128); });
-    else if (S <= 4) finish_rows<4>(P, rank + warp * S, 8 * S, P.a.rows, 0, c, remote);
-    else finish_rows<8>(P, rank + warp * S, 8 * S, P.a.rows, 0, c, remote);
-  }
-  __syncwarp();
-  cluster_sync_all();  // no rank leaves while another reads its part
+  if (S > 1) cluster_sync_all();  // all parts have come
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmem);
+  }
+  const int c = nb * 128 + lane * 4;
+  if (c < P.a.n && !*abort_flag) {
+    // a row per warp, every S-th row a rank's
+    auto part = [&](int r, int k) { return *reinterpret_cast<const float4*>(parts + (k * per + r / S) * 128 + lane * 4); };
+    if (S == 1) finish_rows<1>(P, warp, 8, P.a.rows, 0, c, part);
+    else finish_rows<8>(P, rank + warp * S, 8 * S, P.a.rows, 0, c, part);
   }
 }
 
 // ---- launching -------------------------------------------------------------------------------
 
-bool encode(Params& P, const LinearActArgs& a, uint32_t a_box) {
+bool encode(Params& P, const LinearActArgs& a, uint32_t a_box, uint32_t w_box) {
   memset(&P, 0, sizeof(P));
   P.a = a;
   P.kblocks = (a.k + 63) / 64;
   const uint64_t ad[2] = {(uint64_t)a.k, (uint64_t)a.rows}, wd[2] = {(uint64_t)a.k, (uint64_t)a.n};
   const uint64_t as[1] = {(uint64_t)a.lda * 2}, ws[1] = {(uint64_t)a.ldw * 2};
-  const uint32_t ab[2] = {64, a_box}, wb[2] = {64, 128};
+  const uint32_t ab[2] = {64, a_box}, wb[2] = {64, w_box};
   return encode_tmap_bf16(&P.a_map, a.a, 2, ad, as, ab) && encode_tmap_bf16(&P.w_map, a.w, 2, wd, ws, wb);
 }
 
@@ -645,7 +695,7 @@ cudaLaunchConfig_t config(const Shape& k, unsigned ctas, cudaStream_t s, cudaLau
   return cfg;
 }
 
-constexpr int kKernels = 16;
+constexpr int kKernels = 24;
 
 cudaError_t raise_smem(const Shape& k) {
   static std::atomic<bool> done[16 * kKernels];  // (device, kernel)
@@ -678,17 +728,23 @@ int clusters_at_once(const Shape& k) {
 }
 
 // A split tile is finished by finish4, which looks the activation up.
+template <int BN>
 Shape wide_shape(int act, int splits) {
-  static const Kernel kernels[5] = {linear_act_wide_kernel<0, false>, linear_act_wide_kernel<1, false>,
-                                    linear_act_wide_kernel<2, false>, linear_act_wide_kernel<3, false>,
-                                    linear_act_wide_kernel<4, false>};
-  if (splits > 1) return Shape{linear_act_wide_kernel<0, true>, 5, kWideThreads, 2 * splits, kWideBytes};
-  return Shape{kernels[act], act, kWideThreads, 2, kWideBytes};
+  static const Kernel kernels[5] = {linear_act_wide_kernel<0, false, BN>, linear_act_wide_kernel<1, false, BN>,
+                                    linear_act_wide_kernel<2, false, BN>, linear_act_wide_kernel<3, false, BN>,
+                                    linear_act_wide_kernel<4, false, BN>};
+  constexpr int id = BN == 256 ? 0 : BN == 192 ? 6 : 12;
+  if (splits > 1) return Shape{linear_act_wide_kernel<0, true, BN>, id + 5, kWideThreads, 2 * splits, Wide<BN>::kBytes};
+  return Shape{kernels[act], id + act, kWideThreads, 2, Wide<BN>::kBytes};
+}
+
+Shape wide_shape_of(int bn, int act, int splits) {
+  return bn == 256 ? wide_shape<256>(act, splits) : bn == 192 ? wide_shape<192>(act, splits) : wide_shape<128>(act, splits);
 }
 
 template <int T>
 Shape few_shape(int splits) {
-  return Shape{linear_act_few_kernel<T>, T == 16 ? 6 : T == 32 ? 7 : T == 64 ? 8 : T == 128 ? 9 : 10, Few<T>::kThreads,
+  return Shape{linear_act_few_kernel<T>, T == 16 ? 18 : T == 32 ? 19 : T == 64 ? 20 : T == 128 ? 21 : 22, Few<T>::kThreads,
                splits, Few<T>::kBytes};
 }
 
@@ -711,7 +767,7 @@ int few_splits(int rows, int n, int kblocks) {
 
 cudaError_t launch_few(const LinearActArgs& a, cudaStream_t s) {
   Params P;
-  if (!encode(P, a, a.rows <= 16 ? 16u : a.rows <= 32 ? 32u : a.rows <= 64 ? 64u : a.rows <= 128 ? 128u : 256u))
+  if (!encode(P, a, a.rows <= 16 ? 16u : a.rows <= 32 ? 32u : a.rows <= 64 ? 64u : a.rows <= 128 ? 128u : 256u, 128))
     return cudaErrorInvalidValue;
   P.splits = few_splits(a.rows, a.n, P.kblocks);
   const Shape k = few_shape_of(a.rows, P.splits);
@@ -723,21 +779,38 @@ cudaError_t launch_few(const LinearActArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k.kernel, P);
 }
 
-// Splits only where all tiles' splits run at once, of eight blocks at least.
-int wide_splits(int tiles, int kblocks) {
-  const int most = kblocks / 8;
-  for (int S = most < 4 ? most : 4; S > 1; --S)
-    if (tiles <= clusters_at_once(wide_shape(0, S))) return S;
-  return 1;
+// Columns of a tile and splits of the depth, by the time that a pair's longest way takes: rounds of tiles, blocks of depth
+// in each at what a block of 256, 192 or 128 columns costs, and what comes on top of a split. Splits only where all of
+// them run at once, of eight blocks at least.
+struct WidePlan {
+  int bn, splits;
+};
+WidePlan wide_plan(int rows, int n, int kblocks) {
+  // a block's MMAs take 0.27, 0.20 and 0.13 us, its operands' way through shared memory as long or longer
+  static const int bns[3] = {256, 192, 128};
+  static const float block_us[3] = {0.31f, 0.26f, 0.22f};
+  WidePlan best{256, 1};
+  float least = 1e30f;
+  for (int i = 0; i < 3; ++i) {
+    const long long tiles = (long long)((rows + 255) / 256) * ((n + bns[i] - 1) / bns[i]);
+    const int pairs = sm_count() / 2;
+    for (int S = 1; S <= 4; ++S) {
+      if (S > 1 && (kblocks / S < 8 || tiles > clusters_at_once(wide_shape_of(bns[i], 0, S)))) break;
+      const float us = (float)((tiles + pairs - 1) / pairs) * (float)((kblocks + S - 1) / S) * block_us[i] + (S > 1 ? 2.0f : 0.0f);
+      if (us < least) least = us, best = WidePlan{bns[i], S};
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
   Params P;
-  if (!encode(P, a, 128)) return cudaErrorInvalidValue;
+  const WidePlan plan = wide_plan(a.rows, a.n, (a.k + 63) / 64);
+  if (!encode(P, a, 128, (uint32_t)plan.bn / 2)) return cudaErrorInvalidValue;
   P.m_tiles = (a.rows + 255) / 256;
-  P.tiles = P.m_tiles * ((a.n + 255) / 256);
-  P.splits = wide_splits(P.tiles, P.kblocks);
-  const Shape k = wide_shape(a.act, P.splits);
+  P.tiles = P.m_tiles * ((a.n + plan.bn - 1) / plan.bn);
+  P.splits = plan.splits;
+  const Shape k = wide_shape_of(plan.bn, a.act, P.splits);
   const cudaError_t e = raise_smem(k);
   if (e != cudaSuccess) return e;
   const int most = sm_count() / 2, pairs = P.splits > 1 ? P.tiles * P.splits : P.tiles < most ? P.tiles : most;
@@ -751,8 +824,12 @@ cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
 
 size_t linear_act_parts_bytes(int, int, int) { return 0; }
 
+// Up to 128 rows a cluster per 128 columns of the output; up to 256 where clusters of four all run at once and the depth is
+// worth it: 129 x 4096 x 4096 14.7 us so, 18.4 in wide tiles, 256 x 4096 x 1024 11.4 and 9.7, 250 x 8192 x 1024 (two waves of
+// clusters) 16.1 and 11.0; 65 x 4096 x 4096 11.4 and 17.1.
 cudaError_t launch_linear_act(const LinearActArgs& a, cudaStream_t s) {
-  if (a.rows <= 128 || (a.rows <= 256 && few_splits(a.rows, a.n, (a.k + 63) / 64) >= 4)) return launch_few(a, s);
+  const int kblocks = (a.k + 63) / 64;
+  if (a.rows <= 128 || (a.rows <= 256 && kblocks >= 24 && few_splits(a.rows, a.n, kblocks) >= 4)) return launch_few(a, s);
   return launch_wide(a, s);
 }
 
