@@ -824,12 +824,13 @@ cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
 
 size_t linear_act_parts_bytes(int, int, int) { return 0; }
 
-// Up to 128 rows a cluster per 128 columns of the output; up to 256 where clusters of four all run at once and the depth is
-// worth it: 129 x 4096 x 4096 14.7 us so, 18.4 in wide tiles, 256 x 4096 x 1024 11.4 and 9.7, 250 x 8192 x 1024 (two waves of
-// clusters) 16.1 and 11.0; 65 x 4096 x 4096 11.4 and 17.1.
+// Up to 128 rows a cluster per 128 columns of the output; up to 256 where clusters of four all run at once, or of six
+// for depths under 1536: 129 x 4096 x 4096 14.7 us so, 18.4 in wide tiles, 256 x 4096 x 1024 11.4 and 9.7, 250 x 8192 x 1024 (two waves of
+// clusters) 16.1 and 11.0; 200 x 2048 x 1024 8.8 and 9.0, 65 x 4096 x 4096 11.4 and 17.1.
 cudaError_t launch_linear_act(const LinearActArgs& a, cudaStream_t s) {
   const int kblocks = (a.k + 63) / 64;
-  if (a.rows <= 128 || (a.rows <= 256 && kblocks >= 24 && few_splits(a.rows, a.n, kblocks) >= 4)) return launch_few(a, s);
+  if (a.rows <= 128 || (a.rows <= 256 && few_splits(a.rows, a.n, kblocks) >= (kblocks >= 24 ? 4 : 6)))
+    return launch_few(a, s);
   return launch_wide(a, s);
 }
 

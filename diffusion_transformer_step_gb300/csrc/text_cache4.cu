@@ -9,6 +9,7 @@
 
 #include <atomic>
 
+#include "cta_pair.cuh"
 #include "runtime.h"
 #include "text_join.cuh"
 
@@ -213,11 +214,12 @@ enum : uint32_t { kSiteCache4Full = 0x811, kSiteCache4Empty };
 struct Plan {
   int rows, tile, tiles, walk;  // query rows per key head, of a CTA, tiles, tiles side by side
   int chunk, splits;            // keys per CTA, CTAs per sequence, head and tile
+  bool cluster;                 // the splits are a cluster
 };
 
 struct Params {
   Cache4AttnArgs a;
-  int group, rows, tiles, walk, chunk, splits;
+  int group, rows, tiles, walk, chunk, splits, cluster;
   float scale_log2;
   float2* ml;
   float* o;
@@ -247,6 +249,14 @@ Plan make_plan(const Cache4AttnArgs& a) {
   p.chunk = (int)((chunk + kKeys - 1) / kKeys * kKeys);
   p.splits = (a.max_k + p.chunk - 1) / p.chunk;
   if (p.splits < 1) p.splits = 1;
+  // A cluster joins its runs without a second kernel: one token over 1000 keys 7.1 -> 5.9 us, over 4000 in eight runs instead
+  // of 32 9.4 -> 8.0 (over 8000 in eight it would be 11.3 instead of 10.8). Only while all of them run at once: clusters
+  // wait for places side by side and for their longest run (8 x 4096 tokens 16.0 -> 21 us, 48 ragged ones 187 -> 325).
+  if (p.splits > 8 && a.max_k <= 4096 && items * 8 <= 2 * 152) {
+    p.chunk = ((a.max_k + 7) / 8 + kKeys - 1) / kKeys * kKeys;
+    p.splits = (a.max_k + p.chunk - 1) / p.chunk;
+  }
+  p.cluster = p.splits > 1 && p.splits <= 8 && items * p.splits <= 2 * 152;
   const long long most = (1ll << 30) / (heads * p.splits);
   p.walk = p.tiles < most ? p.tiles : (int)(most < 1 ? 1 : most);
   return p;
@@ -256,7 +266,7 @@ struct Parts {
   size_t ml, o, total;
 };
 Parts parts_of(const Plan& p, const Cache4AttnArgs& a) {
-  const size_t n = p.splits > 1 ? (size_t)a.seqs * a.c.heads * p.splits * p.rows : 0;
+  const size_t n = p.splits > 1 && !p.cluster ? (size_t)a.seqs * a.c.heads * p.splits * p.rows : 0;
   Parts l;
   l.ml = 0;
   l.o = (n * 8 + 255) & ~size_t(255);
@@ -308,6 +318,12 @@ __device__ __forceinline__ void mma_bf16_new(float (&d)[4], const uint32_t (&a)[
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+
+__device__ __forceinline__ float2 ld_cluster(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -556,13 +572,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ uint32_t live[kStages];  // the tiles of 16 tokens that a stage holds
-  __shared__ float2 ml[4][R];
+  __shared__ float2 ml[4][R], sums[R];
   __shared__ int abort_flag;
   const Cache4AttnArgs& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = P.group;
-  // the tiles of the same keys run side by side
-  const int run = blockIdx.x / P.walk, tile0 = blockIdx.x - run * P.walk;
-  const int split = run % P.splits, hk = (run / P.splits) % a.c.heads, seq = run / P.splits / a.c.heads;
+  // the splits of a cluster side by side, or the tiles of the same keys
+  const int side = P.cluster ? P.splits : P.walk, at = blockIdx.x / side, in = blockIdx.x - at * side;
+  const int over = at / (P.cluster ? P.walk : P.splits), under = at - over * (P.cluster ? P.walk : P.splits);
+  const int split = P.cluster ? in : under, tile0 = P.cluster ? under : in;
+  const int hk = over % a.c.heads, seq = over / a.c.heads;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -581,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
   }
   const WaitCtx wc{a.status, &abort_flag, kWaitLimitNs};
   const int first = split * P.chunk;
-  const bool direct = sp.nk <= P.chunk;  // this CTA has all the keys of its rows
+  const bool direct = !P.cluster && sp.nk <= P.chunk;  // this CTA has all the keys of its rows
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // fragment row, and first of two columns
   int used = 0;  // stages filled (or emptied) so far
 
@@ -589,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
     const int base = tile * R, rows = min(R, sp.nq * group - base);  // this tile's query rows
     if (rows <= 0) break;
     const int last = min(keys_seen(a, sp, group, base, rows), first + P.chunk);
-    if (first >= last && split > 0) continue;
+    if (first >= last && split > 0 && !P.cluster) continue;
     const int blocks = first < last ? (last - first + kKeys - 1) / kKeys : 0;
 
     if (warp == 4) {
@@ -775,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
     // The four warps' rows through shared memory: all stages have been read.
     __syncthreads();
     float* parts = reinterpret_cast<float*>(smem);  // [warp][row][dim]
+    float* mine = parts + 4 * R * D;                 // a cluster's: this run's rows
     if (warp < 4) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -815,8 +834,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
 #pragma unroll
           for (int e = 0; e < V; e += 2)
             *reinterpret_cast<uint32_t*>(dst + e) = lr == 0.f ? 0u : pack_bf16x2(out[e] * inv, out[e + 1] * inv);
+        } else if (P.cluster) {
+          if (lane == 0) sums[r] = make_float2(mr, lr);
+#pragma unroll
+          for (int e = 0; e < V; e += 2) *reinterpret_cast<float2*>(mine + r * D + lane * V + e) = make_float2(out[e], out[e + 1]);
         } else {
-          const long long to = (long long)run * P.rows + base + r;
+          const long long to = ((long long)over * P.splits + split) * P.rows + base + r;
           if (lane == 0) P.ml[to] = make_float2(mr, lr);
 #pragma unroll
           for (int e = 0; e < V; e += 2)
@@ -824,9 +847,53 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
         }
       }
     }
+    if (P.cluster) {
+      // Every rank adds every splits-th row up over all runs, in order, one row per warp.
+      cluster_sync_all();
+      for (int r = split + warp * P.splits; warp < 4 && r < rows; r += 4 * P.splits) {
+        float2 y[8];
+        float mr = -INFINITY, lr = 0.f, out[V];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          y[k] = make_float2(-INFINITY, 0.f);
+          if (k < P.splits) y[k] = ld_cluster(map_to_rank(smem_u32(&sums[r]), k));
+          mr = fmaxf(mr, y[k].x);
+        }
+        const float ref = mr == -INFINITY ? 0.f : mr;
+        float v[8][V];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const float2 t = k < P.splits ? ld_cluster(map_to_rank(smem_u32(mine + r * D + lane * V + e), k)) : make_float2(0.f, 0.f);
+            v[k][e] = t.x;
+            v[k][e + 1] = t.y;
+          }
+#pragma unroll
+        for (int e = 0; e < V; ++e) out[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (y[k].y == 0.f) continue;  // no key that the row sees
+          const float f = ex2_approx((y[k].x == -INFINITY ? 0.f : y[k].x) - ref);
+          lr += f * y[k].y;
+#pragma unroll
+          for (int e = 0; e < V; ++e) out[e] += f * v[k][e];
+        }
+        const int token = (base + r) / group, g = base + r - token * group;
+        const float inv = lr == 0.f ? 0.f : 1.0f / lr;
+        bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * group + g) * D + lane * V;
+        if (!abort_flag) {
+#pragma unroll
+          for (int e = 0; e < V; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) = lr == 0.f ? 0u : pack_bf16x2(out[e] * inv, out[e + 1] * inv);
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();  // no rank goes on while another reads its rows
+    }
     if (P.walk < P.tiles) fence_proxy_async_smem();  // before the next tile's copies
     __syncthreads();
-    if (abort_flag) return;
+    if (!P.cluster && abort_flag) return;
   }
 }
 
@@ -865,11 +932,12 @@ cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStre
   P.walk = p.walk;
   P.chunk = p.chunk;
   P.splits = p.splits;
+  P.cluster = p.cluster;
   P.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
   P.ml = reinterpret_cast<float2*>(ws + l.ml);
   P.o = reinterpret_cast<float*>(ws + l.o);
   constexpr size_t smem = kStages * Stage<D>::kBytes;
-  static_assert(smem >= 4 * 8 * NT * D * 4, "the parts reuse the stages");
+  static_assert(smem >= 5 * 8 * NT * D * 4, "the parts reuse the stages");
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 16 || !raised[dev].load(std::memory_order_acquire)) {
@@ -880,12 +948,30 @@ cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStre
   }
   const long long heads = (long long)a.seqs * a.c.heads;
   {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(heads * p.splits * p.walk));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl_enabled()) {
+      attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (p.cluster) {
+      attr[n].id = cudaLaunchAttributeClusterDimension;
+      attr[n].val.clusterDim.x = (unsigned)p.splits;
+      attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+      ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
     LaunchScope scope(kClsCache4Attention, s);
-    const cudaError_t e = launch_k(cache4_attention_kernel<D, NT, kSmall>, dim3((unsigned)(heads * p.splits * p.walk)),
-                                   dim3(kThreads), smem, s, P);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache4_attention_kernel<D, NT, kSmall>, P);
     if (e != cudaSuccess) return e;
   }
-  if (p.splits > 1) {
+  if (p.splits > 1 && !p.cluster) {
     const int fours = (p.rows + 3) / 4;
     LaunchScope scope(kClsCache4Join, s);
     return launch_k(cache4_join_kernel<D>, dim3((unsigned)heads, (unsigned)(fours < 65535 ? fours : 65535)), dim3(128), 0, s, P);
