@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "cta_pair.cuh"
 #include "runtime.h"
@@ -207,7 +208,15 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 // The unit that sums a step's sixteen products lines them up by the exponents of their operands, and a subnormal has that of
 // 2^-14: of each product what lies below 2^-24 2^-14 of the largest other operand is cut off, 2^-14 of that operand per code
 // (measured: one step of random codes is within 2^-20.5 of the sum of magnitudes, eight steps 2^-24.4).
-constexpr int kKeys = 128, kStages = 3, kThreads = 160;
+constexpr int kKeys = 128, kStages = 3, kAhead = 2;
+// Whether the warps that compute send for the stages themselves, in turns, or a fifth warp does. A scheduler's 16384
+// registers hold four warps of 128, three of 168 or two of 255: with sixteen rows of 128-wide heads two CTAs of four warps
+// that do not spill are faster than two of five that do (12 rows over 32 x 8192 tokens 117 us, 142); the others have
+// room for the fifth (8 rows over 64 x 8192: 128 us, 141 to 162 with four CTAs of four; 15 of 64-wide heads 17.3, 20.0).
+template <int D, int NT>
+constexpr bool kOwn = D == 128 && NT == 2;
+template <int D, int NT>
+constexpr int kThreads = kOwn<D, NT> ? 128 : 160;
 
 enum : uint32_t { kSiteCache4Full = 0x811, kSiteCache4Empty };
 
@@ -236,7 +245,7 @@ Plan make_plan(const Cache4AttnArgs& a) {
   // kernel (16 tokens over up to 300 keys 9.0 us in two runs, 6.5 in one; over 1000 9.7 in one, 7.1 in eight), and runs of
   // at most 4096, so that ragged lengths even out (1024 cost 13 % more at 64 x 8192: a run takes ~3 us besides its keys).
   const long long items = heads * p.tiles < (1ll << 30) ? heads * p.tiles : (1ll << 30);
-  long long chunk = (long long)a.max_k * items / (3 * 152);
+  long long chunk = (long long)a.max_k * items / ((p.tile == 8 || a.c.head_dim == 64 ? 3 : 2) * 152);
   if (chunk > 4096) chunk = 4096;
   if (chunk < kKeys) chunk = kKeys;
   if (a.max_k <= 512) chunk = a.max_k;
@@ -565,8 +574,80 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* stage, con
   }
 }
 
+// Brings a run's stages of 128 tokens in. Pages of up to 64 tokens come whole, lane i the i-th of a stage; of larger ones lane
+// `part` brings a part (codes or scales, of the keys or the values). Copies this large matter: a page of 16 tokens in
+// four of them kept the copy unit busy for as long as the arithmetic.
+template <int D>
+struct Sender {
+  static constexpr int G = D / 32;
+  const uint8_t* heads;  // this head of page 0
+  const int32_t* table;
+  uint8_t* smem;
+  uint64_t *full, *empty;
+  uint32_t* live;
+  const WaitCtx* wc;
+  long long page_bytes;
+  int pages, shift, first, last, blocks, used, lane, width, slab, part, t0, each, src0, dst0, sent;
+  bool whole;
+
+  Sender() = default;
+  __device__ __forceinline__ Sender(const Params& P, const WaitCtx& w, uint8_t* smem_, uint64_t* full_, uint64_t* empty_,
+                                    uint32_t* live_, int seq, int hk, int first_, int last_, int blocks_, int used_, int lane_)
+      : smem(smem_), full(full_), empty(empty_), live(live_), wc(&w), first(first_), last(last_), blocks(blocks_), used(used_),
+        lane(lane_) {
+    const Cache4& c = P.a.c;
+    pages = c.pages, shift = c.page_shift, slab = c.slab(), sent = -1;
+    const int ps = 1 << shift;
+    width = min(ps, kKeys), whole = ps <= 64;
+    part = whole ? 0 : lane, t0 = whole ? lane * ps : lane < 4 ? 0 : kKeys;
+    each = part & 1 ? G * 2 : D / 2;  // bytes of a token in a part
+    src0 = (part & 2 ? slab / 2 : 0) + (part & 1 ? c.code_bytes() : 0);
+    dst0 = whole ? lane * slab : (part & 2 ? (int)Stage<D>::kBytes / 2 : 0) + (part & 1 ? kKeys * D / 2 : 0);
+    heads = P.a.cache + (long long)hk * slab, page_bytes = (long long)c.heads * slab;
+    table = P.a.table + (long long)seq * c.max_pages;
+  }
+  __device__ __forceinline__ int page_of(int j) const {
+    const int t = first + j * kKeys + t0;
+    return j < blocks && t0 < kKeys && t < last ? table[t >> shift] : -2;
+  }
+  // Block j, whose page of this lane is `page`, once its stage is free; false if that wait gave up.
+  __device__ __forceinline__ bool send(int j, int page) {
+    const int n = used + j, st = n % kStages, t = first + j * kKeys;
+    const bool wanted = t0 < kKeys && t + t0 < last, ok = wanted && (uint32_t)page < (uint32_t)pages;
+    uint32_t all = 0xffu, total = Stage<D>::kBytes, bytes = whole ? slab : kKeys * each;
+    if (t + kKeys > last || __any_sync(0xffffffffu, wanted && !ok)) {  // not all of the stage
+      if (wanted && !ok && part == 0) report_bad_entry(wc->status, kSiteCache4Page);
+      const int tiles = ok ? (min(width, last - t - t0) + 15) / 16 : 0;  // of 16 tokens
+      bytes = whole ? slab : tiles * 16 * each;
+      all = __reduce_or_sync(0xffffffffu, part == 0 && ok ? ((1u << tiles) - 1u) << (t0 / 16) : 0u);
+      total = __reduce_add_sync(0xffffffffu, ok ? bytes : 0u);
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait_sleep(&empty[st], ((uint32_t)(n / kStages) & 1u) ^ 1u, *wc, kSiteCache4Empty))) return false;
+    if (lane == 0) {
+      live[st] = all;
+      mbar_arrive_expect_tx(&full[st], total);
+    }
+    __syncwarp();
+    if (ok)
+      bulk_load(smem + st * Stage<D>::kBytes + dst0,
+                heads + page * page_bytes + src0 + (whole ? 0 : ((t + t0) & ((1 << shift) - 1)) * each), bytes, &full[st]);
+    sent = n;
+    return true;
+  }
+  // After a wait that gave up: nothing leaves before this warp's copies on their way have landed (bounded).
+  __device__ __forceinline__ void land() const {
+    if (*wc->abort_flag && lane == 0 && sent >= 0) {
+      const uint64_t t = global_timer_ns();
+      for (int n = max(0, sent - kStages + 1); n <= sent; ++n)
+        while (!mbar_try(&full[n % kStages], (uint32_t)(n / kStages) & 1u) && global_timer_ns() - t < 200000000ull) {
+        }
+    }
+    __syncwarp();
+  }
+};
+
 template <int D, int NT, bool kSmall>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
   using L = Stage<D>;
   constexpr int G = L::G, R = 8 * NT, V = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -610,52 +691,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
     if (first >= last && split > 0 && !P.cluster) continue;
     const int blocks = first < last ? (last - first + kKeys - 1) / kKeys : 0;
 
-    if (warp == 4) {
-      // Pages of up to 64 tokens come whole, lane i the i-th of a stage; of larger ones lane `part` brings a part (codes or
-      // scales, of the keys or the values). Copies this large matter: a page of 16 tokens in four of them kept the copy
-      // unit busy for as long as the arithmetic.
-      const int ps = 1 << a.c.page_shift, width = min(ps, kKeys), slab = a.c.slab();
-      const bool whole = ps <= 64;
-      const int part = whole ? 0 : lane, t0 = whole ? lane * ps : lane < 4 ? 0 : kKeys;
-      const int each = part & 1 ? G * 2 : D / 2;  // bytes of a token in a part
-      const int src0 = (part & 2 ? slab / 2 : 0) + (part & 1 ? a.c.code_bytes() : 0);
-      const int dst0 = whole ? lane * slab : (part & 2 ? (int)L::kBytes / 2 : 0) + (part & 1 ? kKeys * D / 2 : 0);
-      const int32_t* table = a.table + (long long)seq * a.c.max_pages;
-      auto page_of = [&](int j) {
-        const int t = first + j * kKeys + t0;
-        return t0 < kKeys && t < last ? table[t >> a.c.page_shift] : -2;
-      };
-      int page = page_of(0), issued = 0;
+    [[maybe_unused]] typename std::conditional<kOwn<D, NT>, Sender<D>, int>::type sender;
+    [[maybe_unused]] int page = 0;
+    if constexpr (kOwn<D, NT>) {
+      sender = Sender<D>(P, wc, smem, full, empty, live, seq, hk, first, last, blocks, used, lane);
+      if (warp < kAhead && warp < blocks) sender.send(warp, sender.page_of(warp));
+      page = sender.page_of(warp + kAhead);  // of this warp's next turn: the blocks warp + kAhead, + 4, + 8, ...
+    } else if (warp == 4) {
+      Sender<D> only(P, wc, smem, full, empty, live, seq, hk, first, last, blocks, used, lane);
+      page = only.page_of(0);
       for (int j = 0; j < blocks; ++j) {
-        const int n = used + j, st = n % kStages, at = first + j * kKeys + t0;
-        const int next = j + 1 < blocks ? page_of(j + 1) : -2;
-        const bool wanted = t0 < kKeys && at < last, ok = wanted && page >= 0 && page < a.c.pages;
-        if (wanted && !ok && part == 0) report_bad_entry(a.status, kSiteCache4Page);
-        const int tiles = ok ? (min(width, last - at) + 15) / 16 : 0;  // of 16 tokens
-        const uint32_t bytes = !ok ? 0u : (uint32_t)(whole ? slab : tiles * 16 * each);
-        const uint32_t mask = part == 0 && ok ? ((1u << tiles) - 1u) << (t0 / 16) : 0u;
-        const uint32_t all = __reduce_or_sync(0xffffffffu, mask), total = __reduce_add_sync(0xffffffffu, bytes);
-        if (!mbar_wait_sleep(&empty[st], ((uint32_t)(n / kStages) & 1u) ^ 1u, wc, kSiteCache4Empty)) break;
-        if (lane == 0) {
-          live[st] = all;
-          mbar_arrive_expect_tx(&full[st], total);
-        }
-        __syncwarp();
-        if (bytes)
-          bulk_load(smem + st * L::kBytes + dst0,
-                    a.cache + ((long long)page * a.c.heads + hk) * slab + src0 + (whole ? 0 : (at & (ps - 1)) * each), bytes,
-                    &full[st]);
+        const int next = only.page_of(j + 1);
+        if (!only.send(j, page)) break;
         page = next;
-        issued = j + 1;
       }
-      // A wait that gave up: nothing leaves before the copies on their way have landed (bounded).
-      if (*(volatile int*)&abort_flag && lane == 0) {
-        const uint64_t t = global_timer_ns();
-        for (int n = max(0, used + issued - kStages); n < used + issued; ++n)
-          while (!mbar_try(&full[n % kStages], (uint32_t)(n / kStages) & 1u) && global_timer_ns() - t < 200000000ull) {
-          }
-      }
-      __syncwarp();
+      only.land();
     }
 
     Rows<D, NT> Q;
@@ -749,20 +799,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
         at.value_codes = page + held * (D * 9 / 16) + (in + c0 + (lane & 2 ? 1 : 0)) * (D / 2) + r0 * (G * 2);
         at.value_scales = at.key_scales + held * (D * 9 / 16);
       }
-      int st = used % kStages, t0 = first + warp * 32;
+      int st = used % kStages, from = first + warp * 32;
       uint32_t phase = (uint32_t)(used / kStages) & 1u;
       const uint8_t* stage = smem + st * L::kBytes;
 #pragma unroll 1
       for (int j = 0; j < blocks; ++j) {
+        if constexpr (kOwn<D, NT>) {
+          if ((j & 3) == warp && j + kAhead < blocks) {
+            sender.send(j + kAhead, page);
+            page = sender.page_of(j + kAhead + 4);
+          }
+        }
         bool ok = mbar_wait(&full[st], phase, wc, kSiteCache4Full);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t here = (live[st] >> (2 * warp)) & 3u;
-        if (here == 3u && t0 + 32 <= open) attend<D, NT, false, kSmall>(Q, stage, at, t0, here, last, lane);
-        else if (here) attend<D, NT, true, kSmall>(Q, stage, at, t0, here, last, lane);
+        if (here == 3u && from + 32 <= open) attend<D, NT, false, kSmall>(Q, stage, at, from, here, last, lane);
+        else if (here) attend<D, NT, true, kSmall>(Q, stage, at, from, here, last, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
-        t0 += kKeys;
+        from += kKeys;
         stage += L::kBytes;
         if (++st == kStages) {
           st = 0;
@@ -788,6 +844,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) cache4_attention_ke
           }
         }
     }
+    if constexpr (kOwn<D, NT>) sender.land();
     used += blocks;
 
     // The four warps' rows through shared memory: all stages have been read.
@@ -950,7 +1007,7 @@ cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStre
   {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(heads * p.splits * p.walk));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads<D, NT>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
