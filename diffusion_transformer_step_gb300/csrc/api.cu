@@ -43,8 +43,8 @@ const char* kernel_class_name(int cls) {
       "rope_table",     "pack_mlp_in",           "gemm_dual_out_proj",  "gemm_dual_mlp_out",
       "gemm_single_out_proj", "quantize_act",    "text_rope_table",     "qk_norm_rope",
       "text_attention", "text_attention_join",   "quantize_blocks_fp8", "linear_fp8_blocks",
-      "linear_fp8_join", "add_rms_norm",         "linear_act",          "linear_act_join",
-      "text_cache4_append", "text_cache4_read",  "text_cache4_attention", "text_cache4_join"};
+      "linear_fp8_join", "add_rms_norm",         "linear_act",          "text_cache4_append",
+      "text_cache4_read", "text_cache4_attention", "text_cache4_join"};
   return (cls >= 0 && cls < kClsCount) ? names[cls] : "?";
 }
 
@@ -1305,7 +1305,7 @@ dit_status dit_add_rms_norm(int rows, int cols, const void* x_dev, long long ldx
 
 dit_status dit_linear_act_workspace(int rows, int n_out, int k, size_t* bytes) {
   if (!linear_act_sizes_ok(rows, n_out, k) || !bytes) return DIT_ERR_INVALID_ARG;
-  *bytes = sizeof(DeviceStatus) + linear_act_parts_bytes(rows, n_out, k);
+  *bytes = sizeof(DeviceStatus);
   return DIT_OK;
 }
 
@@ -1318,7 +1318,7 @@ dit_status dit_linear_act(int rows, int n_out, int k, const void* a_dev, long lo
   if (bad_ld(lda, k) || bad_ld(ldw, k) || bad_ld(ld_out, n_out) || (res_dev && bad_ld(ld_res, n_out)))
     return DIT_ERR_INVALID_ARG;
   if (!aligned16(ws)) return DIT_ERR_INVALID_ARG;
-  if (ws_bytes < sizeof(DeviceStatus) + linear_act_parts_bytes(rows, n_out, k)) return DIT_ERR_WORKSPACE;
+  if (ws_bytes < sizeof(DeviceStatus)) return DIT_ERR_WORKSPACE;
   if (rows == 0) return DIT_OK;
   if (!aligned16(a_dev) || !aligned16(w_dev) || !aligned16(out_dev) || (bias_dev && !aligned16(bias_dev)) ||
       (res_dev && !aligned16(res_dev)))
@@ -1339,7 +1339,6 @@ dit_status dit_linear_act(int rows, int n_out, int k, const void* a_dev, long lo
   p.a = (const bf16*)a_dev; p.w = (const bf16*)w_dev; p.bias = (const bf16*)bias_dev; p.res = (const bf16*)res_dev;
   p.out = out_dev; p.lda = lda; p.ldw = ldw; p.ld_res = ld_res; p.ld_out = ld_out;
   p.status = status_of(ws);
-  p.parts = reinterpret_cast<float*>(at(ws, sizeof(DeviceStatus)));
   return cuda_status(launch_linear_act(p, (cudaStream_t)stream));
 }
 

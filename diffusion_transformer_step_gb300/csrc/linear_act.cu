@@ -9,20 +9,26 @@
 //                            MMA's row side and the activation rows its column side, the depth split over
 //                            a cluster of up to eight CTAs.
 //
-// Splits add up through distributed shared memory, in rank order: each CTA writes its part of a row to the CTA that will
+// Splits add up through distributed shared memory, in rank order: each CTA sends its part of a row to the CTA that will
 // finish it (whose ring has been read), and finishes its own share of the rows from the parts that have come. (Left where
 // they were made and fetched by the one that finishes them, every row waited for another SM's memory: 777 x 1544 x 5160 with
-// all three 33.9 us, so 27.8.)
+// all three 33.9 us, so 28.0.) Wide tiles go by one bulk copy per receiver, 24 KB to 64 KB (stores of 16 bytes: 300 x 1000 x
+// 9000 22.3 us, so 21.6).
 //
-// Measured (bursts of twenty calls on different weights): 8192 x 12288 x 4096 445 to 454 us, 1820 to 1854 TFLOP/s (0.94 to 0.96
+// Loads and MMAs are issued by a thread that elect.sync chose: chosen by its lane number, the compiler guards every such
+// instruction against more than one, and a block of depth takes 0.28 us whatever its tile's columns (elected: 0.27, 0.20 and
+// 0.14 us for 256, 192 and 128).  Then loads bound the narrow tiles, and all where rows do not start on lines of 128 bytes:
+// 777 x 1544 x 5120 16.6 us, 5152 19.0, 5136 20.1, 5160 25.1.
+//
+// Measured (bursts of twenty calls on different weights): 8192 x 12288 x 4096 437 to 450 us, 1830 to 1887 TFLOP/s (0.94 to 0.97
 // of the measured burst); call after call 520 to 540, at the clocks that power leaves, with any epilogue (0.93 of the
-// measured sustained rate). 4096 x 4096 x 4096 82 us; 1 x 12288 x 4096 19.4 (5.2 TB/s of weights), 1 x 2560 x 4096 7.5,
-// 64 x 4096 x 4096 11.8, 777 x 1544 x 5160 25.5 without epilogue. A call has about 3.5 us besides its loads: launch, first
-// load, the cluster's two barriers, the last rows.
+// measured sustained rate). 4096 x 4096 x 4096 82 us, 512 x 4096 x 4096 15.6; 1 x 12288 x 4096 18.7 (5.4 TB/s of weights),
+// 1 x 2560 x 4096 7.2, 64 x 4096 x 4096 11.4, 777 x 1544 x 5160 25.1 without epilogue. A call has about 3.5 us besides its
+// loads (launch, first load, last rows), and a split of wide tiles 5.5 more.
 // Measured and left: accumulators through shared memory to whole lines of the output, at six stages instead of seven (8192 x
 // 12288 x 4096 455 -> 476 us: the MMAs and the loads take all of shared memory's cycles); the first weights sent to L2 before the
 // kernel before has ended (1 x 2560 x 4096 7.3 -> 7.9: every line crosses the copy unit twice); two CTAs of three stages per
-// SM for 128 rows (11.8 -> 13.8).
+// SM for 128 rows (11.8 -> 13.8); a first pass through the finishing code while the loads are on their way (no change).
 #include <math.h>
 
 #include <atomic>
@@ -34,7 +40,7 @@ namespace dit {
 
 namespace {
 
-enum : uint32_t { kSiteEmpty = 0xa01, kSiteFull, kSiteAccEmpty, kSiteAccFull };
+enum : uint32_t { kSiteEmpty = 0xa01, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteParts };
 
 struct alignas(64) Params {
   CUtensorMap a_map, w_map;
@@ -195,44 +201,52 @@ __device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, in
   }
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// The rows r0, r0 + step, ... below `rows` (of the output: m0 further), four columns from c on per thread; part(r, k) is what
-// split k has sent of them, added in split order. Two rows go side by side, the residual of the next two ahead. Not
-// unrolled further: a loop that runs a few times waits for its code as much as for its data (128 rows of one
-// block of depth, eight rows at once: 8.8 us, two 6.4).
+// Of the rows first, first + stride, ... below `rows` (of the output: m0 further) every step-th from number i0 on, four
+// columns from c on per thread; part(i, k) is what split k has sent of row number i, added in split order. Two rows go
+// side by side, the residual of the next two ahead. Not unrolled further: a loop that runs a few times waits for its code
+// as much as for its data (128 rows of one block of depth, eight rows at once: 8.8 us, two 6.4).
 template <int K, typename Part>
-__device__ __forceinline__ void finish_rows(const Params& P, int r0, int step, int rows, int m0, int c, Part part) {
+__device__ __forceinline__ void finish_rows(const Params& P, int i0, int step, int first, int stride, int rows, int m0, int c,
+                                            Part part) {
   const LinearActArgs& p = P.a;
   const uint2 none = make_uint2(0, 0), bias = p.bias ? load4(p.bias, c, p.n) : none;
   auto residual = [&](int r) { return r < rows && p.res ? load4(p.res + (long long)(m0 + r) * p.ld_res, c, p.n) : none; };
-  auto sum = [&](int r) {
-    float4 x = part(min(r, rows - 1), 0);
+  auto sum = [&](int i) {
+    float4 x = part(i, 0);
 #pragma unroll
     for (int k = 1; k < K; ++k)
       if (k < P.splits) {
-        const float4 v = part(min(r, rows - 1), k);
+        const float4 v = part(i, k);
         x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
       }
     return x;
   };
-  uint2 res[2] = {residual(r0), residual(r0 + step)};
+  const int r0 = first + i0 * stride, by = step * stride;
+  uint2 res[2] = {residual(r0), residual(r0 + by)};
 #pragma unroll 1
-  for (int r = r0; r < rows; r += 2 * step) {
-    const int both[2] = {r, r + step};
-    const float4 v[2] = {sum(r), sum(r + step)};
+  for (int r = r0, i = i0; r < rows; r += 2 * by, i += 2 * step) {
+    const int both[2] = {r, r + by};
+    const float4 v[2] = {sum(i), sum(r + by < rows ? i + step : i)};
     const uint2 now[2] = {res[0], res[1]};
-    res[0] = residual(r + 2 * step), res[1] = residual(r + 3 * step);
+    res[0] = residual(r + 2 * by), res[1] = residual(r + 3 * by);
     finish4<kAnyAct>(p, both, rows, m0, c, v, bias, now);
   }
 }
 
 // ---- many rows -------------------------------------------------------------------------------
+
+// One thread of a converged warp, so chosen that the compiler knows that it is one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 
 constexpr int kWideThreads = 320;
 template <int BN>  // columns of a pair's tile: 128, 192 or 256
@@ -240,7 +254,7 @@ struct Wide {
   static constexpr uint32_t kA = 128 * 128, kW = BN / 2 * 128, kStage = kA + kW;
   static constexpr int kStages = 229376 / (int)kStage;
   static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256;
-  static_assert(kStages * kStage >= 131 * BN * 4, "the splits' parts reuse the ring");
+  static_assert(kStages * kStage >= (128 + 96) * BN * 4, "the splits' parts, at most of four, reuse the ring");
 };
 
 // Pair `pair` of a cluster (rank = 2 pair + half) takes the depth blocks [K pair / S, K (pair + 1) / S) of its cluster's
@@ -258,7 +272,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
   uint64_t* acc_full = empty + L::kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* come = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(come + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -267,7 +282,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
   const int first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
   const int kb0 = kSplit ? (int)((long long)P.kblocks * split / S) : 0;
   const int kb1 = kSplit ? (int)((long long)P.kblocks * (split + 1) / S) : P.kblocks;
-  [[maybe_unused]] const int per = (127 + S) / S;  // rows of a half that a split finishes, at most
+  // Splits: split s finishes the rows s, s + S, ... of each half, their number, and room for it.
+  [[maybe_unused]] const int per = (127 + S) / S, m0 = first % P.m_tiles * 256 + (int)half * 128;
+  [[maybe_unused]] auto share = [&](int s) { return (max(min(128, P.a.rows - m0), 0) + S - 1 - s) / S; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -278,8 +295,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
       mbar_init(&acc_empty[i], 16);
     }
     mbar_init(drain, 1);
+    mbar_init(come, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (kSplit) mbar_arrive_expect_tx(come, (uint32_t)((S - 1) * share(split) * BN * 4));
     tma_prefetch_desc(&P.a_map);
     tma_prefetch_desc(&P.w_map);
   }
@@ -298,7 +317,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
   allow_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       long long issued = 0;
       bool ok = true;
@@ -338,7 +357,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && half == 0) {
+    if (half == 0 && elect_one()) {
       const uint32_t idesc = make_idesc_bf16(256, BN, false);
       const uint16_t both = (uint16_t)(3u << leader);
       auto commit = [&](uint64_t* bar) {
@@ -388,21 +407,29 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
       bool ok = mbar_wait_sleep(&acc_full[0], 0, wc, kSiteAccFull);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      cluster_sync_all();  // every CTA's ring has been read
-      // Row r to the pair that finishes it, 16-byte pieces turned by its place there, so that eight rows lie in different banks.
-      const uint32_t owner = map_to_rank(smem_u32(smem), (uint32_t)(2 * (r % S)) + half);
-      const int place = split * per + r / S;
-      if (ok) {
+      cluster_arrive();  // this CTA's ring has been read
+      // Rows by the split that finishes them, 16-byte pieces turned by the row, so that eight rows lie in different banks.
+      float4* mine = reinterpret_cast<float4*>(smem) + ((r % S) * per + r / S) * (BN / 4);
 #pragma unroll 1
-        for (int c = 0; c < BN / 64; ++c) {
-          uint32_t v[32];
-          tmem_load32(tmem + (uint32_t)(eh * (BN / 2) + c * 32) + ((uint32_t)(q * 32) << 16), v);
+      for (int c = 0; c < BN / 64 && ok; ++c) {
+        uint32_t v[32];
+        tmem_load32(tmem + (uint32_t)(eh * (BN / 2) + c * 32) + ((uint32_t)(q * 32) << 16), v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            st_cluster(owner + (uint32_t)(place * (BN / 4) + ((eh * (BN / 8) + c * 8 + i) ^ (r / S & 7))) * 16,
-                       make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                                   __uint_as_float(v[4 * i + 3])));
-        }
+        for (int i = 0; i < 8; ++i)
+          mine[(eh * (BN / 8) + c * 8 + i) ^ (r & 7)] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                                   __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+      }
+      fence_proxy_async_smem();
+      cluster_wait();  // every CTA's ring has been read
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int to = warp - 2;
+      if (to < S && to != split && lane == 0 && share(to) > 0) {
+        const uint32_t dst = smem_u32(smem) + (uint32_t)(S * per + (split < to ? split : split - 1) * per) * (BN * 4);
+        asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         map_to_rank(dst, (uint32_t)(2 * to) + half)),
+                     "r"(smem_u32(smem) + (uint32_t)(to * per) * (BN * 4)), "r"((uint32_t)(share(to) * BN * 4)),
+                     "r"(map_to_rank(smem_u32(come), (uint32_t)(2 * to) + half))
+                     : "memory");
       }
     } else {
       const uint32_t free0 = map_to_rank(smem_u32(acc_empty), leader);
@@ -468,20 +495,31 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
     }
   };
   if constexpr (kSplit) {
-    if (warp < 2) cluster_sync_all();  // the one that the finishing warps went through above
-    tc_fence_before();
-    cluster_sync_all();  // all parts have come, no MMA, load or remote access is still in flight
-    free_tmem();
-    const int nt = first / P.m_tiles, mt = first - nt * P.m_tiles;
-    if (warp >= 2 && !*abort_flag) {
-      // this pair's share of its half's rows, every S-th: half the columns of one row per warp
-      const int m0 = mt * 256 + (int)half * 128, piece = (warp & 1) * (BN / 8) + lane, c = nt * BN + piece * 4;
-      const float4* parts = reinterpret_cast<const float4*>(smem);
-      if (lane < BN / 8 && c < P.a.n)
-        finish_rows<4>(P, split + ((warp - 2) >> 1) * S, 4 * S, min(128, P.a.rows - m0), m0, c, [&](int r, int k) {
-          return parts[(k * per + r / S) * (BN / 4) + (piece ^ (r / S & 7))];
-        });
+    if (warp < 2) {
+      cluster_arrive();
+      cluster_wait();
     }
+    const int nt = first / P.m_tiles;
+    if (warp >= 2) {
+      bool ok = mbar_wait_sleep(come, 0, wc, kSiteParts);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_before();
+      cluster_arrive();  // what was sent here has come; no load or remote arrive is still in flight, with the others'
+      // this pair's share of its half's rows: half the columns of one row per warp
+      const int piece = (warp & 1) * (BN / 8) + lane, c = nt * BN + piece * 4;
+      const float4* parts = reinterpret_cast<const float4*>(smem);
+      if (ok && !*abort_flag && lane < BN / 8 && c < P.a.n && P.a.rows > m0 + split)
+        finish_rows<4>(P, (warp - 2) >> 1, 4, split, S, min(128, P.a.rows - m0), m0, c, [&](int i, int k) {
+          const int slot = (k == split ? split : S + (k < split ? k : k - 1)) * per + i;
+          return parts[slot * (BN / 4) + (piece ^ ((split + i * S) & 7))];
+        });
+      __syncwarp();
+    } else {
+      tc_fence_before();
+      cluster_arrive();
+    }
+    cluster_wait();
+    free_tmem();
   } else {
     tc_fence_before();
     cluster_sync_all();  // no MMA, load or remote arrive of the pair is still in flight
@@ -574,7 +612,7 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
   allow_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int issued = 0;
       bool ok = true;
       for (int i = 0; i < n; ++i) {
@@ -597,7 +635,7 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = make_idesc_bf16(128, T, false);
       const uint64_t w0 = make_sdesc_sw128(smem_u32(sW), 16, 1024), a0 = make_sdesc_sw128(smem_u32(sA), 16, 1024);
       for (int i = 0; i < n; ++i) {
@@ -653,9 +691,9 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
   const int c = nb * 128 + lane * 4;
   if (c < P.a.n && !*abort_flag) {
     // a row per warp, every S-th row a rank's
-    auto part = [&](int r, int k) { return *reinterpret_cast<const float4*>(parts + (k * per + r / S) * 128 + lane * 4); };
-    if (S == 1) finish_rows<1>(P, warp, 8, P.a.rows, 0, c, part);
-    else finish_rows<8>(P, rank + warp * S, 8 * S, P.a.rows, 0, c, part);
+    auto part = [&](int i, int k) { return *reinterpret_cast<const float4*>(parts + (k * per + i) * 128 + lane * 4); };
+    if (S == 1) finish_rows<1>(P, warp, 8, 0, 1, P.a.rows, 0, c, part);
+    else finish_rows<8>(P, warp, 8, rank, S, P.a.rows, 0, c, part);
   }
 }
 
@@ -695,7 +733,7 @@ cudaLaunchConfig_t config(const Shape& k, unsigned ctas, cudaStream_t s, cudaLau
   return cfg;
 }
 
-constexpr int kKernels = 24;
+constexpr int kKernels = 22;
 
 cudaError_t raise_smem(const Shape& k) {
   static std::atomic<bool> done[16 * kKernels];  // (device, kernel)
@@ -744,13 +782,13 @@ Shape wide_shape_of(int bn, int act, int splits) {
 
 template <int T>
 Shape few_shape(int splits) {
-  return Shape{linear_act_few_kernel<T>, T == 16 ? 18 : T == 32 ? 19 : T == 64 ? 20 : T == 128 ? 21 : 22, Few<T>::kThreads,
-               splits, Few<T>::kBytes};
+  return Shape{linear_act_few_kernel<T>, T == 16 ? 18 : T == 32 ? 19 : T == 64 ? 20 : 21, Few<T>::kThreads, splits,
+               Few<T>::kBytes};
 }
 
 Shape few_shape_of(int rows, int splits) {
   return rows <= 16 ? few_shape<16>(splits) : rows <= 32 ? few_shape<32>(splits) : rows <= 64 ? few_shape<64>(splits)
-       : rows <= 128 ? few_shape<128>(splits) : few_shape<256>(splits);
+                                                                                   : few_shape<128>(splits);
 }
 
 // Splits of the depth: as many as still run at once, of two blocks at least.  (The clusters that the runtime says run
@@ -767,7 +805,7 @@ int few_splits(int rows, int n, int kblocks) {
 
 cudaError_t launch_few(const LinearActArgs& a, cudaStream_t s) {
   Params P;
-  if (!encode(P, a, a.rows <= 16 ? 16u : a.rows <= 32 ? 32u : a.rows <= 64 ? 64u : a.rows <= 128 ? 128u : 256u, 128))
+  if (!encode(P, a, a.rows <= 16 ? 16u : a.rows <= 32 ? 32u : a.rows <= 64 ? 64u : 128u, 128))
     return cudaErrorInvalidValue;
   P.splits = few_splits(a.rows, a.n, P.kblocks);
   const Shape k = few_shape_of(a.rows, P.splits);
@@ -780,23 +818,26 @@ cudaError_t launch_few(const LinearActArgs& a, cudaStream_t s) {
 }
 
 // Columns of a tile and splits of the depth, by the time that a pair's longest way takes: rounds of tiles, blocks of depth
-// in each at what a block of 256, 192 or 128 columns costs, and what comes on top of a split. Splits only where all of
-// them run at once, of eight blocks at least.
+// in each at what a block of 256, 192 or 128 columns costs, and what a split adds. Splits only where all of them run at
+// once, of eight blocks at least.
 struct WidePlan {
   int bn, splits;
 };
-WidePlan wide_plan(int rows, int n, int kblocks) {
-  // a block's MMAs take 0.27, 0.20 and 0.13 us, its operands' way through shared memory as long or longer
+WidePlan wide_plan(const LinearActArgs& a, int kblocks) {
+  // A block's MMAs take 0.27, 0.20 and 0.14 us, a little more where many SMs load. Rows of operands that do not start on
+  // 128-byte lines are two lines each to load, which takes longer than that.
   static const int bns[3] = {256, 192, 128};
-  static const float block_us[3] = {0.31f, 0.26f, 0.22f};
+  static const float block_us[2][3] = {{0.30f, 0.24f, 0.175f}, {0.46f, 0.39f, 0.32f}};
+  const bool lines = (a.lda | a.ldw) % 64 == 0 && ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.w)) & 127) == 0;
   WidePlan best{256, 1};
   float least = 1e30f;
   for (int i = 0; i < 3; ++i) {
-    const long long tiles = (long long)((rows + 255) / 256) * ((n + bns[i] - 1) / bns[i]);
+    const long long tiles = (long long)((a.rows + 255) / 256) * ((a.n + bns[i] - 1) / bns[i]);
     const int pairs = sm_count() / 2;
     for (int S = 1; S <= 4; ++S) {
       if (S > 1 && (kblocks / S < 8 || tiles > clusters_at_once(wide_shape_of(bns[i], 0, S)))) break;
-      const float us = (float)((tiles + pairs - 1) / pairs) * (float)((kblocks + S - 1) / S) * block_us[i] + (S > 1 ? 2.0f : 0.0f);
+      const float us = (float)((tiles + pairs - 1) / pairs) * (float)((kblocks + S - 1) / S) * block_us[lines ? 0 : 1][i] +
+                       (S > 1 ? 5.5f : 0.0f);
       if (us < least) least = us, best = WidePlan{bns[i], S};
     }
   }
@@ -805,7 +846,7 @@ WidePlan wide_plan(int rows, int n, int kblocks) {
 
 cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
   Params P;
-  const WidePlan plan = wide_plan(a.rows, a.n, (a.k + 63) / 64);
+  const WidePlan plan = wide_plan(a, (a.k + 63) / 64);
   if (!encode(P, a, 128, (uint32_t)plan.bn / 2)) return cudaErrorInvalidValue;
   P.m_tiles = (a.rows + 255) / 256;
   P.tiles = P.m_tiles * ((a.n + plan.bn - 1) / plan.bn);
@@ -822,15 +863,11 @@ cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t linear_act_parts_bytes(int, int, int) { return 0; }
-
-// Up to 128 rows a cluster per 128 columns of the output; up to 256 where clusters of four all run at once, or of six
-// for depths under 1536: 129 x 4096 x 4096 14.7 us so, 18.4 in wide tiles, 256 x 4096 x 1024 11.4 and 9.7, 250 x 8192 x 1024 (two waves of
-// clusters) 16.1 and 11.0; 200 x 2048 x 1024 8.8 and 9.0, 65 x 4096 x 4096 11.4 and 17.1.
+// Up to 128 rows a cluster per 128 columns of the output (65 x 4096 x 4096 10.7 us so, 13.8 in wide tiles, 128 x 12288 x 4096 23.7
+// and 24.7; 100 x 8192 x 1024, two waves of clusters, 9.7 and 8.8). The same with up to 256 rows: 129 x 4096 x 4096 14.2 and
+// 16.2, 256 x 4096 x 4096 16.6 and 16.6, 200 x 2048 x 1024 8.4 and 6.8, 250 x 8192 x 4096 25.6 and 18.2; left.
 cudaError_t launch_linear_act(const LinearActArgs& a, cudaStream_t s) {
-  const int kblocks = (a.k + 63) / 64;
-  if (a.rows <= 128 || (a.rows <= 256 && few_splits(a.rows, a.n, kblocks) >= (kblocks >= 24 ? 4 : 6)))
-    return launch_few(a, s);
+  if (a.rows <= 128) return launch_few(a, s);
   return launch_wide(a, s);
 }
 

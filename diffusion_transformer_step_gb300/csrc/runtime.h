@@ -35,12 +35,11 @@ enum KernelClass : int {
   kClsLinearFp8Join = 20,  // joining its depth splits
   kClsAddRmsNorm = 21,     // residual addition + RMSNorm (+ e4m3 blocks)
   kClsLinearAct = 22,      // product with bias, activation and residual
-  kClsLinearActJoin = 23,  // joining its depth splits
-  kClsCache4Append = 24,   // new tokens into the 4-bit cache
-  kClsCache4Read = 25,     // tokens back out of it
-  kClsCache4Attention = 26,  // attention over it
-  kClsCache4Join = 27,     // joining its key splits
-  kClsCount = 28
+  kClsCache4Append = 23,   // new tokens into the 4-bit cache
+  kClsCache4Read = 24,     // tokens back out of it
+  kClsCache4Attention = 25,  // attention over it
+  kClsCache4Join = 26,     // joining its key splits
+  kClsCount = 27
 };
 
 const char* kernel_class_name(int cls);
@@ -280,9 +279,7 @@ struct LinearActArgs {
   void* out;
   long long lda, ldw, ld_res, ld_out;
   DeviceStatus* status;
-  float* parts;  // workspace of the depth splits
 };
-size_t linear_act_parts_bytes(int rows, int n, int k);
 cudaError_t launch_linear_act(const LinearActArgs& a, cudaStream_t s);
 
 constexpr uint32_t kSiteCache4Lengths = 0x801, kSiteCache4Page = 0x802;

@@ -524,8 +524,8 @@ typedef enum {
   DIT_ACT_SILU = 4
 } dit_activation;
 
-/* Bytes of workspace that dit_linear_act needs (at least the 256 of the status word; more where the
- * depth of few tiles is split over the GPU, at most 48 MB). */
+/* Bytes of workspace that dit_linear_act needs: the 256 of the status word (sums over a split depth are joined
+ * on the chip). */
 dit_status dit_linear_act_workspace(int rows, int n_out, int k, size_t* bytes);
 
 /* Linear layer with bias, activation and residual in its epilogue:
@@ -535,7 +535,8 @@ dit_status dit_linear_act_workspace(int rows, int n_out, int k, size_t* bytes);
  * (% 8 == 0, at least the row, <= 2^24); bias_dev [n_out] bf16.  bias_dev and res_dev may be NULL.  res_dev may be
  * out_dev itself (same stride, bf16); any other overlap of out_dev with an operand is DIT_ERR_INVALID_ARG.
  * Columns of out_dev from n_out on are not written.  k % 8 == 0, 8 <= k <= 2^20, 1 <= n_out <= 2^20, any n_out,
- * 0 <= rows <= 2^20.  The order of sums depends only on the sizes: equal calls give equal bits. */
+ * 0 <= rows <= 2^20.  The order of sums depends only on the sizes, the row strides and
+ * whether operands start on 128-byte lines: equal calls give equal bits. */
 dit_status dit_linear_act(int rows, int n_out, int k, const void* a_dev, long long lda, const void* w_dev,
                           long long ldw, const void* bias_dev, dit_activation act, const void* res_dev,
                           long long ld_res, void* out_dev, long long ld_out, int out_f32, void* ws, size_t ws_bytes,

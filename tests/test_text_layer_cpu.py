@@ -172,7 +172,7 @@ def test_cache_attention_workspace_over_the_range(dit):
 
 def test_kernel_classes_have_names(dit):
     names = [dit.dit_kernel_class_name(i) for i in range(40)]
-    for n in ("add_rms_norm", "linear_act", "linear_act_join", "text_cache4_append", "text_cache4_read", "text_cache4_attention",
+    for n in ("add_rms_norm", "linear_act", "text_cache4_append", "text_cache4_read", "text_cache4_attention",
               "text_cache4_join"):
         assert names.count(n) == 1
 
