@@ -602,7 +602,8 @@ dit_status dit_text_cache4_attention_workspace(const dit_text_cache4* c, const d
  * sequence's keys.  Scores from exact products of the queries and the cache's integers (what of a query row is below 2^-28 of
  * its largest value is rounded), scaled and summed in fp32; scale times a row's largest magnitude stays below 2^100.
  * Probabilities times the values' scales are rounded to fp16 for the product with V, those below 2^-20 of a row's largest
- * to 2^-31 of it.  A key on a page outside
+ * to 2^-31 of it; so where the largest scale of the values that a row sees is 2^-64 to 2^98 (values of 7 times that). Below
+ * 2^-64 steps stay those of 2^-64, and above 2^98 the sum of the probabilities loses its small terms.  A key on a page outside
  * [0, pages) is left out of the sums, and recorded (0x802); a sequence whose lengths are out of range is skipped, and
  * recorded (0x801).  Meant for few queries per sequence: every 16 rows (tokens x heads_q / heads_k) of a key head read its
  * cache once.  out_dev must not overlap q_dev or the cache; page_table is not read behind a sequence's last token. */
