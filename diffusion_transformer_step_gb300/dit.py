@@ -173,18 +173,24 @@ def _check(fn, st):
 
 def _ptr(t):
     """Device or host pointer of a tensor (or None / int passthrough)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
+_current = None  # the handle of torch's current stream on its current device
+
+
 def _stream(stream):
+    global _current
     if stream is None:
-        import torch
-        # the handle alone: a torch.cuda.Stream object around it costs more than the call it is for
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _current is None:
+            import torch
+            torch.cuda.current_device()  # brings torch's side up where nothing has yet
+            handle, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            # the handle alone: a torch.cuda.Stream object around it costs more than the call it is for
+            _current = lambda: handle(device())  # noqa: E731
+        return _current()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
