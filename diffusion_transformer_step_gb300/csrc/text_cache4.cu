@@ -42,9 +42,10 @@ __device__ __forceinline__ Run load_run(const Cache4MoveArgs& a, int s) {
 // lie side by side in the cache (a word each of the keys' codes, two half-words of the values') and in whole sectors of
 // the rows. A CTA has `tokens` tokens (a power of two), and where those do not fill it several heads side by side; each
 // thread goes through U of them with its loads ahead of its stores. The table is read once per token.
-// Memory bounds it: 512 new tokens of 16 sequences in and 700 to 8192 of each out (429 MB) take 75.7 us for both calls, 5.66
-// TB/s; with eight values a thread, and so many small CTAs, 214. A decoding step's append and read of eight short
-// sequences: 6.5 us, two launches.
+// Memory bounds it: 512 new tokens of 16 sequences in and 700 to 8192 of each out (429 MB) take 73.7 us for both calls, 5.8
+// TB/s (reading alone 6.7); with eight values a thread, and so many small CTAs, 214. Appending alone, 3.6 TB/s, is as much
+// arithmetic as traffic: 8192 tokens of 8 heads 11.9 us, with all divisions in all four threads, conversions and clamps
+// 14.3. A decoding step's append and read of eight short sequences: 5.9 us, two launches.
 template <int D, bool kAppend, int U>
 __global__ void __launch_bounds__(256) cache4_move_kernel(const Cache4MoveArgs a, int tokens, int side, int parts) {
   constexpr int G = D / 32;
@@ -90,27 +91,39 @@ __global__ void __launch_bounds__(256) cache4_move_kernel(const Cache4MoveArgs a
       bool value;
       int head;
       if (!place(u, value, head)) continue;  // the same for a token's four threads
-      uint32_t code[G], sc[G];
+      uint32_t top[G], code[G], sc[G];  // magnitudes of bf16 compare as integers, NaN above infinity
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         const uint32_t w[4] = {in[u][j].x, in[u][j].y, in[u][j].z, in[u][j].w};
-        uint32_t top = 0;  // magnitudes of bf16 compare as integers, NaN above infinity
+        top[j] = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-        top = max(top, __shfl_xor_sync(four, top, 1));
-        top = max(top, __shfl_xor_sync(four, top, 2));
-        const bool bad = top >= 0x7f80u;
-        const bf16 scale = __float2bfloat16(fmaxf(__uint_as_float(top << 16), 7.0f * 0x1p-118f) / 7.0f);
-        const float inv = 1.0f / __bfloat162float(scale);
+        for (int e = 0; e < 4; ++e) top[j] = max(top[j], max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        top[j] = max(top[j], __shfl_xor_sync(four, top[j], 1));
+        top[j] = max(top[j], __shfl_xor_sync(four, top[j], 2));
+      }
+      // each thread divides for one group (two of four do it for the same one where there are two)
+      uint32_t most = top[G - 1];
+#pragma unroll
+      for (int j = 0; j < G - 1; ++j)
+        if ((t & (G - 1)) == j) most = top[j];
+      const bf16 scale = __float2bfloat16(fmaxf(__uint_as_float(most << 16), 7.0f * 0x1p-118f) / 7.0f);
+      const float own = 1.0f / __bfloat162float(scale);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t w[4] = {in[u][j].x, in[u][j].y, in[u][j].z, in[u][j].w};
+        const bool bad = top[j] >= 0x7f80u;
+        const float inv = __shfl_sync(four, own, j, 4);
+        sc[j] = __shfl_sync(four, (uint32_t)__bfloat16_as_ushort(scale), j, 4);
+        // Added to 2^23 + 2^22 + 8 a product is rounded to an integer, ties to even, and its code left in the lowest four bits;
+        // no product reaches 7.5, since the scale is within 2^-8 of max / 7.
         code[j] = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = unpack_bf16x2(w[e]);
-          code[j] |= (uint32_t)(max(-7, min(7, __float2int_rn(f.x * inv))) + 8) << (8 * e);
-          code[j] |= (uint32_t)(max(-7, min(7, __float2int_rn(f.y * inv))) + 8) << (8 * e + 4);
+          code[j] |= (__float_as_uint(__fadd_rn(__fmul_rn(f.x, inv), 12582920.0f)) & 15u) << (8 * e);
+          code[j] |= (__float_as_uint(__fadd_rn(__fmul_rn(f.y, inv), 12582920.0f)) & 15u) << (8 * e + 4);
         }
-        if (bad) code[j] = 0x88888888u;
-        sc[j] = bad ? 0x7fffu : (uint32_t)__bfloat16_as_ushort(scale);
+        if (bad) code[j] = 0x88888888u, sc[j] = 0x7fffu;
       }
       uint32_t out[G];
 #pragma unroll

@@ -17,6 +17,15 @@ and rotation of 40000 rows of 40 heads of 128.
     python -m diffusion_transformer_step_gb300.profile_case --text linear --reps 2
     python -m diffusion_transformer_step_gb300.profile_case --text qk --reps 2
 
+The norm of 16384 rows of 4096 with residual and both outputs, the product 4096 x 4096 x 4096 with bias, SiLU
+and residual, 512 new tokens into the 4-bit cache of each of 16 sequences of 8192 and all of them read back, 16 new tokens
+over that cache (one each).
+
+    python -m diffusion_transformer_step_gb300.profile_case --text norm --reps 2
+    python -m diffusion_transformer_step_gb300.profile_case --text linear_act --reps 2
+    python -m diffusion_transformer_step_gb300.profile_case --text cache4 --reps 2
+    python -m diffusion_transformer_step_gb300.profile_case --text decode4 --reps 2
+
 `--fp8` runs the block with every projection in e4m3 (per-row activation and per-output-channel
 weight scales, the library's low-precision variant).
 """
@@ -52,6 +61,40 @@ def text_case(kind, reps):
         def run():
             dit.dit_quantize_blocks_fp8(x, k, m, k, 1, aq, a_s)
             dit.dit_linear_fp8_blocks(m, n, k, aq, a_s, wq, w_s, out, n, ws, ws.numel())
+    elif kind == "norm":
+        rows, cols = 16384, 4096
+        x, res = (synth.normal((rows, cols), 1.0, g, dev) for _ in range(2))
+        w = torch.ones(cols, dtype=torch.bfloat16, device=dev)
+        s, y = torch.empty_like(x), torch.empty_like(x)
+        q, sc = torch.empty((rows, cols), dtype=torch.uint8, device=dev), torch.empty((rows, cols // 128), device=dev)
+        run = lambda: dit.dit_add_rms_norm(rows, cols, x, cols, res, cols, w, 0.0, 1e-6, s, cols, y, cols, q, sc)  # noqa: E731
+    elif kind == "linear_act":
+        m = n = k = 4096
+        x, w, res = synth.normal((m, k), 1.0, g, dev), synth.normal((n, k), 0.02, g, dev), synth.normal((m, n), 1.0, g, dev)
+        b, out = synth.normal((n,), 1.0, g, dev), torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        run = lambda: dit.dit_linear_act(m, n, k, x, k, w, k, b, dit.DIT_ACT_SILU, res, n, out, n, False, ws, ws.numel())  # noqa: E731
+    elif kind in ("cache4", "decode4"):
+        seqs, nk, page, nq = 16, 8192, 64, 512 if kind == "cache4" else 1
+        c = dit.make_text_cache4(hk, d, seqs * nk // page, page, nk // page)
+        cache = torch.empty(dit.dit_text_cache4_bytes(c), dtype=torch.uint8, device=dev)
+        pages = torch.randperm(c.pages, generator=g, device=dev).to(torch.int32)
+        kv = synth.normal((seqs * nk, 2 * hk * d), 1.0, g, dev)
+        v, wide = kv[:, hk * d:], 2 * hk * d
+        full, kl, qo = i32([i * nk for i in range(seqs + 1)]), i32([nk] * seqs), i32([i * nq for i in range(seqs + 1)])
+        dit.dit_text_cache4_append(c, seqs, seqs * nk, nk, full, None, kl, pages, kv, wide, v, wide, cache, ws, ws.numel())
+        if kind == "cache4":
+            out = torch.empty_like(kv)
+
+            def run():
+                dit.dit_text_cache4_append(c, seqs, seqs * nq, nq, qo, None, kl, pages, kv, wide, v, wide, cache, ws, ws.numel())
+                dit.dit_text_cache4_read(c, seqs, seqs * nk, nk, full, None, pages, cache, out, wide, out[:, hk * d:], wide, ws,
+                                         ws.numel())
+        else:
+            q = synth.normal((seqs, hq * d), 1.0, g, dev)
+            out = torch.empty_like(q)
+            a = dit.make_text_attn(seqs, hq, hk, d, seqs, 0, 1, nk)
+            run = lambda: dit.dit_text_cache4_attention(c, a, qo, None, kl, pages, q, hq * d, cache, out, hq * d, ws,  # noqa: E731
+                                                        ws.numel())
     else:
         rows, wide = 40000, (hq + hk) * d
         x = synth.normal((rows, wide), 1.0, g, dev)
@@ -73,7 +116,7 @@ def main():
     ap.add_argument("--block", choices=["single", "dual", "modulation"], default="single")
     ap.add_argument("--reps", type=int, default=2)
     ap.add_argument("--fp8", action="store_true", help="every block projection in e4m3")
-    ap.add_argument("--text", choices=["attention", "decode", "linear", "qk"])
+    ap.add_argument("--text", choices=["attention", "decode", "linear", "qk", "norm", "linear_act", "cache4", "decode4"])
     args = ap.parse_args()
     build_lib.build()
     if args.text:
