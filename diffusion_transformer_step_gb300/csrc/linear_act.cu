@@ -20,15 +20,16 @@
 // 0.14 us for 256, 192 and 128).  Then loads bound the narrow tiles, and all where rows do not start on lines of 128 bytes:
 // 777 x 1544 x 5120 16.6 us, 5152 19.0, 5136 20.1, 5160 25.1.
 //
-// Measured (bursts of twenty calls on different weights): 8192 x 12288 x 4096 437 to 450 us, 1830 to 1887 TFLOP/s (0.94 to 0.97
-// of the measured burst); call after call 520 to 540, at the clocks that power leaves, with any epilogue (0.93 of the
-// measured sustained rate). 4096 x 4096 x 4096 82 us, 512 x 4096 x 4096 15.6; 1 x 12288 x 4096 18.7 (5.4 TB/s of weights),
+// Measured (bursts of twenty calls on different weights): 8192 x 12288 x 4096 432 to 438 us, 1880 to 1905 TFLOP/s (0.97 to 0.98
+// of the measured burst); call after call 515 to 530, at the clocks that power leaves, with any epilogue (0.93 of the
+// measured sustained rate). 4096 x 4096 x 4096 76 us, 512 x 4096 x 4096 15.3; 1 x 12288 x 4096 18.7 (5.4 TB/s of weights),
 // 1 x 2560 x 4096 7.2, 64 x 4096 x 4096 11.4, 777 x 1544 x 5160 25.1 without epilogue. A call has about 3.5 us besides its
 // loads (launch, first load, last rows), and a split of wide tiles 5.5 more.
 // Measured and left: accumulators through shared memory to whole lines of the output, at six stages instead of seven (8192 x
 // 12288 x 4096 455 -> 476 us: the MMAs and the loads take all of shared memory's cycles); the first weights sent to L2 before the
 // kernel before has ended (1 x 2560 x 4096 7.3 -> 7.9: every line crosses the copy unit twice); two CTAs of three stages per
-// SM for 128 rows (11.8 -> 13.8); a first pass through the finishing code while the loads are on their way (no change).
+// SM for 128 rows (11.8 -> 13.8); a first pass through the finishing code while the loads are on their way (no change); a
+// tile's residual sent to L2 while it is worked on, or fetched two pieces ahead (4096 x 4096 x 1024 31.4 -> 33.4 and 32.7).
 #include <math.h>
 
 #include <atomic>
@@ -160,10 +161,34 @@ __device__ __forceinline__ void finish4(const LinearActArgs& p, const int (&r)[N
   }
 }
 
-// 32 columns [c, c + 32) of one row, all below n; res: that piece of the residual.
+// Four lanes that hold four pieces of a row each, to each holding one piece of all four rows, and back.
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+#pragma unroll
+  for (int by = 1; by < 4; by *= 2) {
+    const bool up = lane & by;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & by) continue;
+      uint4 &lo = x[i], &hi = x[i + by];
+      const uint4 give = up ? lo : hi;
+      uint4 take;
+      take.x = __shfl_xor_sync(0xffffffffu, give.x, by);
+      take.y = __shfl_xor_sync(0xffffffffu, give.y, by);
+      take.z = __shfl_xor_sync(0xffffffffu, give.z, by);
+      take.w = __shfl_xor_sync(0xffffffffu, give.w, by);
+      if (up) lo = take;
+      else hi = take;
+    }
+  }
+}
+
+// 32 columns [c, c + 32) of the warp's rows, row `row` of this lane's, all below n. Memory is read and written with four
+// lanes to a row's 64 bytes, eight rows at once, which takes as many lines of an instruction as rows: 4096 x 4096 x 1024
+// 30.4 -> 25.0 us, with bias, GELU and residual 47.4 -> 40.0, to fp32 48.7 -> 36.7 (each lane its own row before). res[i] is
+// piece lane % 4 of the residual of the i-th of the four rows, bias what the columns add.
 template <int kAct>
-__device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, int c, const uint32_t (&v)[32],
-                                         const uint4 (&res)[4]) {
+__device__ __forceinline__ void finish32(const LinearActArgs& p, int row, int c, const uint32_t (&v)[32], const uint4 (&bias)[4],
+                                         uint4 (&res)[4], int lane) {
   auto eight = [](const uint4& u, float2 (&f)[4]) {
     f[0] = unpack_bf16x2(u.x), f[1] = unpack_bf16x2(u.y), f[2] = unpack_bf16x2(u.z), f[3] = unpack_bf16x2(u.w);
   };
@@ -171,7 +196,7 @@ __device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, in
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float2 b[4];
-    if (p.bias) eight(__ldg(reinterpret_cast<const uint4*>(p.bias + c + g * 8)), b);
+    if (p.bias) eight(bias[g], b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 z = make_float2(__uint_as_float(v[g * 8 + 2 * i]), __uint_as_float(v[g * 8 + 2 * i + 1]));
@@ -180,6 +205,7 @@ __device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, in
     }
   }
   if (p.res) {
+    transpose4(res, lane);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       float2 x[4];
@@ -188,16 +214,32 @@ __device__ __forceinline__ void finish32(const LinearActArgs& p, long long r, in
       for (int i = 0; i < 4; ++i) o[g * 4 + i] = __fadd2_rn(o[g * 4 + i], x[i]);
     }
   }
+  const int r0 = row - (lane & 3);
   if (p.out_f32) {
-    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + r * p.ld_out + c);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
+    for (int h = 0; h < 2; ++h) {
+      uint4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = make_uint4(__float_as_uint(o[8 * h + 2 * i].x), __float_as_uint(o[8 * h + 2 * i].y),
+                          __float_as_uint(o[8 * h + 2 * i + 1].x), __float_as_uint(o[8 * h + 2 * i + 1].y));
+      transpose4(x, lane);
+      float* dst = reinterpret_cast<float*>(p.out) + r0 * p.ld_out + c + h * 16 + (lane & 3) * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r0 + i < p.rows) *reinterpret_cast<uint4*>(dst + i * p.ld_out) = x[i];
+    }
   } else {
-    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(p.out) + r * p.ld_out + c);
+    uint4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      dst[i] = make_uint4(pack_bf16x2(o[4 * i].x, o[4 * i].y), pack_bf16x2(o[4 * i + 1].x, o[4 * i + 1].y),
-                          pack_bf16x2(o[4 * i + 2].x, o[4 * i + 2].y), pack_bf16x2(o[4 * i + 3].x, o[4 * i + 3].y));
+      x[i] = make_uint4(pack_bf16x2(o[4 * i].x, o[4 * i].y), pack_bf16x2(o[4 * i + 1].x, o[4 * i + 1].y),
+                        pack_bf16x2(o[4 * i + 2].x, o[4 * i + 2].y), pack_bf16x2(o[4 * i + 3].x, o[4 * i + 3].y));
+    transpose4(x, lane);
+    bf16* dst = reinterpret_cast<bf16*>(p.out) + r0 * p.ld_out + c + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r0 + i < p.rows) *reinterpret_cast<uint4*>(dst + i * p.ld_out) = x[i];
   }
 }
 
@@ -441,10 +483,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
         // the residual's pieces one ahead, the first before the accumulator is waited for
         uint4 ahead[4];
         auto fetch = [&](int c) {
-          if (!P.a.res || row >= P.a.rows || c + 32 > P.a.n) return;
-          const uint4* src = reinterpret_cast<const uint4*>(P.a.res + row * P.a.ld_res + c);
+          if (!P.a.res || c + 32 > P.a.n) return;
+          const int r0 = row - (lane & 3);
+          const bf16* src = P.a.res + r0 * P.a.ld_res + c + (lane & 3) * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ahead[i] = src[i];
+          for (int i = 0; i < 4; ++i)
+            ahead[i] = r0 + i < P.a.rows ? *reinterpret_cast<const uint4*>(src + i * P.a.ld_res) : make_uint4(0u, 0u, 0u, 0u);
         };
         fetch(col);
         bool ok = mbar_wait_sleep(&acc_full[acc], (uint32_t)(local >> 1) & 1u, wc, kSiteAccFull);
@@ -460,12 +504,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
 #pragma unroll
           for (int i = 0; i < 4; ++i) res[i] = ahead[i];
           if (c + 1 < BN / 64) fetch(cc + 32);
+          uint4 bias[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (P.a.bias && cc + 32 <= P.a.n) bias[i] = __ldg(reinterpret_cast<const uint4*>(P.a.bias + cc + i * 8));
           uint32_t v[32];
           tmem_load32(tb + c * 32, v);
-          if (row >= P.a.rows) continue;
           if (cc + 32 <= P.a.n) {
-            finish32<kAct>(P.a, row, cc, v, res);
-          } else {
+            finish32<kAct>(P.a, row, cc, v, bias, res, lane);
+          } else if (row < P.a.rows) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (cc + 4 * i < P.a.n) {
