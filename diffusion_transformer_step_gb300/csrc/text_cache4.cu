@@ -203,8 +203,9 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 // several CTAs are joined by a second kernel.
 //
 // The tokens are the rows of both products, the few queries their columns: S^T = K Q^T and O^T = V^T P^T. What bounds
-// this kernel is not the MMA but the integer pipe, which has to spread 4-bit codes over 16-bit operands, half a
-// warp per cycle: so a code is left where one AND leaves it. As the bits of an fp16 number, a code c in the lowest four
+// this kernel is issue: 311 instructions per 16 tokens (8 rows, 128 dims), 144 of them on the integer pipe, which takes half a warp
+// per cycle, to spread 4-bit codes over 16-bit operands, and 21 MMAs, with three warps per scheduler to choose from (a fourth,
+// with two CTAs of seven and a sender, gains its scheduler 5 %; from L2 the same calls take 2 % less). So a code is left where one AND leaves it. As the bits of an fp16 number, a code c in the lowest four
 // bits is the subnormal c 2^-24, in the next four c 2^-20: both exact operands, five operations per eight codes of the keys
 // and six of the values. (As bf16 128 + c, with an OR and more shifts, and an exact subtraction of 136 for the values: 458
 // instructions per 16 tokens instead of 355, 64 tokens over 8192 each 172 us instead of 140, all else equal.)
@@ -216,8 +217,9 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 // Values: the scales, one per token and 32 values, belong to the index that the product sums over, so they go into the
 // probabilities. f = p s is rounded to fp16 (2^-11): the reference that a row's exponents are taken from is that of its largest
 // p s, 2^6 below it, so that f stays under 2^15, and what is rounded coarser (subnormal) is below 2^-20 of the row's
-// largest weight, within 2^-31 of it. The 8 is taken off at the end: -8 sum(f) of the rounded f, which one more product
-// with ones gives.
+// largest weight, within 2^-31 of it. The 8 is taken off at the end: -8 sum(f) of the rounded f, by one more product with ones, or
+// by additions (kAdds): four products of the 21 that a tile takes, or sixteen additions and half of the registers (64 x 8192 tokens
+// 124.4 -> 121.6 us, 12 rows 104.9 -> 102; eight short sequences 8.8 -> 9.5, for their code has to come first).
 // The unit that sums a step's sixteen products lines them up by the exponents of their operands, and a subnormal has that of
 // 2^-14: of each product what lies below 2^-24 2^-14 of the largest other operand is cut off, 2^-14 of that operand per code
 // (measured: one step of random codes is within 2^-20.5 of the sum of magnitudes, eight steps 2^-24.4).
@@ -237,15 +239,26 @@ struct Plan {
   int rows, tile, tiles, walk;  // query rows per key head, of a CTA, tiles, tiles side by side
   int chunk, splits;            // keys per CTA, CTAs per sequence, head and tile
   bool cluster;                 // the splits are a cluster
+  int even;                     // CTAs that share all blocks of keys out evenly, or 0
+};
+
+// Even shares: the parts that the last piece of a CTA's share, the first of its sequence and head, is joined from.
+struct Cut {
+  int head, q0, nq, parts;  // parts 0: there is none
 };
 
 struct Params {
   Cache4AttnArgs a;
-  int group, rows, tiles, walk, chunk, splits, cluster;
+  int group, rows, tiles, walk, chunk, splits, cluster, even;
   float scale_log2;
   float2* ml;
   float* o;
+  Cut* cuts;
 };
+
+// What a piece of an even share costs besides its keys, in blocks of them (48 tokens over up to 32768 keys of 128-wide heads with
+// 0, 2, 3, 4, 6: 163, 153, 151, 152, 153 us; 45 over up to 5001 of 64-wide ones with 2, 3, 4, 6: 22.9, 21.6, 19.9, 15.9).
+constexpr int piece_cost(int head_dim) { return head_dim == 64 ? 6 : 3; }
 
 Plan make_plan(const Cache4AttnArgs& a) {
   Plan p;
@@ -258,7 +271,8 @@ Plan make_plan(const Cache4AttnArgs& a) {
   // kernel (16 tokens over up to 300 keys 9.0 us in two runs, 6.5 in one; over 1000 9.7 in one, 7.1 in eight), and runs of
   // at most 4096, so that ragged lengths even out (1024 cost 13 % more at 64 x 8192: a run takes ~3 us besides its keys).
   const long long items = heads * p.tiles < (1ll << 30) ? heads * p.tiles : (1ll << 30);
-  long long chunk = (long long)a.max_k * items / ((p.tile == 8 || a.c.head_dim == 64 ? 3 : 2) * 152);
+  const int resident = p.tile == 8 || a.c.head_dim == 64 ? 3 : 2;
+  long long chunk = (long long)a.max_k * items / (resident * 152);
   if (chunk > 4096) chunk = 4096;
   if (chunk < kKeys) chunk = kKeys;
   if (a.max_k <= 512) chunk = a.max_k;
@@ -279,20 +293,29 @@ Plan make_plan(const Cache4AttnArgs& a) {
     p.splits = (a.max_k + p.chunk - 1) / p.chunk;
   }
   p.cluster = p.splits > 1 && p.splits <= 8 && items * p.splits <= 2 * 152;
+  // Longer calls of few rows share all keys out evenly over the CTAs that run at once, from 512 keys each on and for sequences
+  // that may be longer than 2048 (48 tokens over up to 32768 keys 186 -> 151 us, 32 over up to 8192 57.9 -> 40.8, 64 over 8192
+  // each 127.8 -> 120; 8 over 4096 each, 574 keys per CTA, 16.4 and 15.9; many short sequences are better off with a CTA each,
+  // whose starts overlap: 200 of up to 2000 70.8 and 75.4, 1000 of up to 400 129 and 148).
+  const long long blocks = heads * ((a.max_k + kKeys - 1) / kKeys + 1 + piece_cost(a.c.head_dim)), slots = resident * 152;
+  p.even = p.tiles == 1 && !p.cluster && a.seqs <= 1024 && a.max_k > 2048 && a.max_k * heads >= 512 * slots && blocks < (1 << 30)
+               ? (int)slots : 0;
   const long long most = (1ll << 30) / (heads * p.splits);
   p.walk = p.tiles < most ? p.tiles : (int)(most < 1 ? 1 : most);
   return p;
 }
 
 struct Parts {
-  size_t ml, o, total;
+  size_t ml, o, cuts, total;
 };
 Parts parts_of(const Plan& p, const Cache4AttnArgs& a) {
-  const size_t n = p.splits > 1 && !p.cluster ? (size_t)a.seqs * a.c.heads * p.splits * p.rows : 0;
+  const size_t n = p.even ? (size_t)2 * p.even * p.rows
+                          : p.splits > 1 && !p.cluster ? (size_t)a.seqs * a.c.heads * p.splits * p.rows : 0;
   Parts l;
   l.ml = 0;
   l.o = (n * 8 + 255) & ~size_t(255);
-  l.total = l.o + n * (size_t)a.c.head_dim * 4;
+  l.cuts = l.o + n * (size_t)a.c.head_dim * 4;
+  l.total = l.cuts + (size_t)p.even * sizeof(Cut);
   return l;
 }
 
@@ -315,6 +338,97 @@ __device__ __forceinline__ int keys_seen(const Cache4AttnArgs& a, const Span& sp
   if (!a.causal) return sp.nk;
   return min(sp.nk, max(0, (base + rows - 1) / G + sp.nk - sp.nq + 1));
 }
+
+// ---- even shares: all blocks of 128 keys of all sequences and key heads in a row, as much of them to each CTA ---------
+
+// Of a head of sequence s: its blocks and what comes on top, or zero. Queries without keys have one.
+template <int D>
+__device__ __forceinline__ int cost_of(const Cache4AttnArgs& a, int s) {
+  if (s >= a.seqs) return 0;
+  const Span sp = load_span(a, s);
+  return sp.nq == 0 ? 0 : max(1, (sp.nk + kKeys - 1) / kKeys) + piece_cost(D);
+}
+
+struct Share {
+  int per;     // what a CTA has of it
+  int before;  // of a head of the sequences before `seq`
+  int seq, n;  // a sequence and its own
+};
+
+// The share's size, and the sequence that holds the first block of the CTA's (a.seqs: there is none). One warp, all lanes the
+// same; the lengths of 128 sequences are fetched at once.
+template <int D>
+__device__ __forceinline__ Share find_share(const Cache4AttnArgs& a, int ctas, int cta, int lane) {
+  int all = 0, n[4];
+  for (int s0 = 0; s0 < a.seqs; s0 += 128) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = cost_of<D>(a, s0 + 32 * i + lane);
+    all += n[0] + n[1] + n[2] + n[3];
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  Share r;
+  r.per = max(piece_cost(D) + 1, (int)((unsigned)(all * a.c.heads + ctas - 1) / (unsigned)ctas));
+  r.before = 0;
+  r.seq = a.seqs, r.n = 0;
+  for (int s0 = 0; s0 < a.seqs; s0 += 128) {
+    if (a.seqs > 128) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n[i] = cost_of<D>(a, s0 + 32 * i + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int upto = n[i];
+#pragma unroll
+      for (int w = 1; w < 32; w <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, upto, w);
+        if (lane >= w) upto += t;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, (unsigned)((r.before + upto) * a.c.heads) > (unsigned)(cta * r.per));
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        r.seq = s0 + 32 * i + l;
+        r.n = __shfl_sync(0xffffffffu, n[i], l);
+        r.before += __shfl_sync(0xffffffffu, upto - n[i], l);
+        return r;
+      }
+      r.before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  return r;
+}
+
+// What a CTA does at a time: of a sequence and key head the keys from block `block` on.
+struct Piece {
+  int seq, head, q0, nq, nk;
+  int block, keys;           // keys < 0: nothing is left
+  int whole;                 // these are all keys
+  int n, left, per;          // even shares: blocks of the sequence, what is left of the share at its first block, a share
+  long long row;             // of the parts
+  __device__ __forceinline__ void of(const Cache4AttnArgs& a, int s) {
+    const Span sp = load_span(a, s);
+    seq = s, q0 = sp.q0, nq = sp.nq, nk = sp.nk;
+  }
+  __device__ __forceinline__ void cut(const Params& P) {
+    const int count = min(n - block, left);
+    keys = count > 0 ? count * kKeys : -1;
+    whole = count == n;
+    row = (long long)(2 * blockIdx.x + (block + count == n ? 0 : 1)) * P.rows;
+  }
+  template <int D>
+  __device__ __forceinline__ void next(const Params& P) {
+    left -= keys / kKeys + piece_cost(D);
+    block = 0;
+    if (left > 0 && ++head == P.a.c.heads) {
+      head = 0;
+      int cost;
+      do cost = cost_of<D>(P.a, ++seq);
+      while (cost == 0 && seq < P.a.seqs);
+      n = cost == 0 ? 0 : cost - piece_cost(D);
+      if (n > 0) of(P.a, seq);
+    }
+    cut(P);
+  }
+};
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
@@ -358,6 +472,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Both halves of an fp16 pair added in fp32.
+template <int N>
+__device__ __forceinline__ void add_f16x2(float (&s)[N], uint32_t v) {
+  asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %1, hi, %1;\n\t}"
+      : "+f"(s[0]), "+f"(s[1])
+      : "r"(v));
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -406,14 +528,16 @@ __device__ __forceinline__ void scales(float (&s)[2 * N], const uint32_t (&w)[N]
 }
 
 // What a warp keeps of its query rows: columns 8 n + c0 + {0, 1} of the scores and the output, c0 = 2 (lane % 4).
-template <int D, int NT>
+template <int D, int NT, bool kLong>
 struct Rows {
   static constexpr int G = D / 32;
+  static constexpr bool kAdds = kLong || NT == 2;  // how sums of f are taken
+  static constexpr int kF = kAdds ? 2 : 4;
   uint32_t q[NT][2 * G][2];  // the queries as the scores' column operand
   uint32_t eight[NT][2];     // -8 sums of their groups, in three bf16 parts
   float scale[NT][2];        // from sums of products to exponents of two
   int limit[NT][2];          // keys that the columns see
-  float o[NT][2 * G][4], f[NT][G][4];  // sums of c f, times 2^-24 (the codes' odd places: 2^-20), and of f
+  float o[NT][2 * G][4], f[NT][G][kF];  // sums of c f, times 2^-24 (the codes' odd places: 2^-20), and of f
   float m[NT][2], l[NT][2];            // what exponents are taken from, sums of probabilities
 };
 
@@ -421,8 +545,8 @@ constexpr float kRoom = 6.0f;  // a row's largest weight lies 2^6 above its refe
 
 // A warp's 32 tokens of a stage, from token t0 of the sequence on. kMasked: some column does not see some of them. kSmall: the
 // two tiles are pages of 16 tokens each, not neighbours in one.
-template <int D, int NT, bool kMasked, bool kSmall>
-__device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* stage, const Places& at, int t0, uint32_t here, int last,
+template <int D, int NT, bool kMasked, bool kSmall, bool kLong>
+__device__ __forceinline__ void attend(Rows<D, NT, kLong>& R, const uint8_t* stage, const Places& at, int t0, uint32_t here, int last,
                                        int lane) {
   constexpr int G = Stage<D>::G;
   constexpr int kCodesOn = kSmall ? 16 * D * 9 / 8 : 16 * D / 2, kScalesOn = kSmall ? 16 * D * 9 / 8 : 16 * G * 2;
@@ -522,7 +646,7 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* stage, con
       for (int g = 0; g < G; ++g) {
         R.f[n][g][0] *= alpha[0];
         R.f[n][g][1] *= alpha[1];
-        R.f[n][g][2] = R.f[n][g][3] = 0.f;  // rows 8 to 15, the same again, are not read
+        if constexpr (!R.kAdds) R.f[n][g][2] = R.f[n][g][3] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 2 * G; ++i) {
@@ -569,10 +693,17 @@ __device__ __forceinline__ void attend(Rows<D, NT>& R, const uint8_t* stage, con
           for (int e = 0; e < 4; ++e)
             if (!sees(i, n, e >> 1, e & 1)) f[e] = 0.f;
         }
-        b[n][0] = transpose8x8(pack_f16x2(f[0], f[1]));
-        b[n][1] = transpose8x8(pack_f16x2(f[2], f[3]));
-        const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-        mma_f16(R.f[n][g], one, b[n]);
+        const uint32_t lo = pack_f16x2(f[0], f[1]), hi = pack_f16x2(f[2], f[3]);
+        if constexpr (R.kAdds) {
+          add_f16x2(R.f[n][g], lo);
+          add_f16x2(R.f[n][g], hi);
+        }
+        b[n][0] = transpose8x8(lo);
+        b[n][1] = transpose8x8(hi);
+        if constexpr (!R.kAdds) {
+          const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+          mma_f16(R.f[n][g], one, b[n]);  // rows 8 to 15 are the same again
+        }
       }
       // the codes' low bytes of the group's half-words, then the high ones
 #pragma unroll
@@ -659,7 +790,7 @@ struct Sender {
   }
 };
 
-template <int D, int NT, bool kSmall>
+template <int D, int NT, bool kSmall, bool kEven>
 __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
   using L = Stage<D>;
   constexpr int G = L::G, R = 8 * NT, V = D / 32;
@@ -668,13 +799,13 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
   __shared__ uint32_t live[kStages];  // the tiles of 16 tokens that a stage holds
   __shared__ float2 ml[4][R], sums[R];
   __shared__ int abort_flag;
+  __shared__ Piece piece;
   const Cache4AttnArgs& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = P.group;
   // the splits of a cluster side by side, or the tiles of the same keys
-  const int side = P.cluster ? P.splits : P.walk, at = blockIdx.x / side, in = blockIdx.x - at * side;
-  const int over = at / (P.cluster ? P.walk : P.splits), under = at - over * (P.cluster ? P.walk : P.splits);
-  const int split = P.cluster ? in : under, tile0 = P.cluster ? under : in;
-  const int hk = over % a.c.heads, seq = over / a.c.heads;
+  const int side = !kEven && P.cluster ? P.splits : P.walk, at = blockIdx.x / side, in = blockIdx.x - at * side;
+  const int over = at / (!kEven && P.cluster ? P.walk : P.splits), under = at - over * (!kEven && P.cluster ? P.walk : P.splits);
+  const int split = !kEven && P.cluster ? in : under, tile0 = !kEven && P.cluster ? under : in;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -686,22 +817,51 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
   __syncthreads();
   grid_dependency_wait();
   allow_dependents();
-  const Span sp = load_span(a, seq);
-  if (!sp.ok) {
-    if (split == 0 && hk == 0 && tile0 == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteCache4Lengths);
-    return;
+  Span sp;
+  int hk = over % a.c.heads, seq = over / a.c.heads, first = split * P.chunk, keys = P.chunk;
+  if constexpr (kEven) {
+    if (warp == 0) {
+      const int c = blockIdx.x;
+      if (c == 0)
+        for (int i = lane; i < a.seqs; i += 32)
+          if (!load_span(a, i).ok) report_bad_entry(a.status, kSiteCache4Lengths);
+      const Share h = find_share<D>(a, P.even, c, lane);
+      if (lane == 0) {
+        P.cuts[c].parts = 0;
+        piece.keys = -1;
+        piece.per = h.per;
+        if (h.seq < a.seqs) {
+          const int in = c * h.per - h.before * a.c.heads;
+          piece.of(a, h.seq);
+          piece.head = in / h.n, piece.n = h.n - piece_cost(D);
+          const int at_cost = in % h.n - piece_cost(D);  // a share that begins in what comes on top begins with the first block
+          piece.block = max(0, at_cost), piece.left = h.per + min(0, at_cost);
+          piece.cut(P);
+        }
+      }
+    }
+    __syncthreads();
+  } else {
+    sp = load_span(a, seq);
+    if (!sp.ok) {
+      if (split == 0 && hk == 0 && tile0 == 0 && threadIdx.x == 0) report_bad_entry(a.status, kSiteCache4Lengths);
+      return;
+    }
   }
   const WaitCtx wc{a.status, &abort_flag, kWaitLimitNs};
-  const int first = split * P.chunk;
-  const bool direct = !P.cluster && sp.nk <= P.chunk;  // this CTA has all the keys of its rows
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;  // fragment row, and first of two columns
   int used = 0;  // stages filled (or emptied) so far
 
-  for (int tile = tile0; tile < P.tiles; tile += P.walk) {
+  for (int tile = kEven ? 0 : tile0; kEven || tile < P.tiles; tile += kEven ? 0 : P.walk) {
+    if constexpr (kEven) {
+      if (piece.keys < 0) break;
+      seq = piece.seq, hk = piece.head, first = piece.block * kKeys, keys = piece.keys;
+      sp = Span{piece.q0, piece.nq, piece.nk, true};
+    }
     const int base = tile * R, rows = min(R, sp.nq * group - base);  // this tile's query rows
     if (rows <= 0) break;
-    const int last = min(keys_seen(a, sp, group, base, rows), first + P.chunk);
-    if (first >= last && split > 0 && !P.cluster) continue;
+    const int last = min(keys_seen(a, sp, group, base, rows), first + keys);
+    if (!kEven && first >= last && split > 0 && !P.cluster) continue;
     const int blocks = first < last ? (last - first + kKeys - 1) / kKeys : 0;
 
     [[maybe_unused]] typename std::conditional<kOwn<D, NT>, Sender<D>, int>::type sender;
@@ -721,7 +881,7 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
       only.land();
     }
 
-    Rows<D, NT> Q;
+    Rows<D, NT, kEven> Q;
     if (warp < 4) {
       int open = last;  // keys below it are seen by all rows
 #pragma unroll
@@ -795,7 +955,9 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
           Q.m[n][e] = -INFINITY;
           Q.l[n][e] = 0.f;
 #pragma unroll
-          for (int g = 0; g < G; ++g) Q.f[n][g][e] = Q.f[n][g][e + 2] = 0.f;
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = e; i < Q.kF; i += 2) Q.f[n][g][i] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) Q.o[n][i][0] = Q.o[n][i][1] = Q.o[n][i][2] = Q.o[n][i][3] = 0.f;
@@ -827,8 +989,8 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t here = (live[st] >> (2 * warp)) & 3u;
-        if (here == 3u && from + 32 <= open) attend<D, NT, false, kSmall>(Q, stage, at, from, here, last, lane);
-        else if (here) attend<D, NT, true, kSmall>(Q, stage, at, from, here, last, lane);
+        if (here == 3u && from + 32 <= open) attend<D, NT, false, kSmall, kEven>(Q, stage, at, from, here, last, lane);
+        else if (here) attend<D, NT, true, kSmall, kEven>(Q, stage, at, from, here, last, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
         from += kKeys;
@@ -848,7 +1010,9 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
           for (int w = 4; w < 32; w <<= 1) Q.l[n][e] += __shfl_xor_sync(0xffffffffu, Q.l[n][e], w);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            const float f = Q.f[n][g][e];
+            float f = Q.f[n][g][e];
+#pragma unroll
+            for (int w = 4; w < 32 && Q.kAdds; w <<= 1) f += __shfl_xor_sync(0xffffffffu, f, w);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               Q.o[n][2 * g + h][e] = fmaf(Q.o[n][2 * g + h][e], 0x1p24f, -8.0f * f);
@@ -862,6 +1026,12 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
 
     // The four warps' rows through shared memory: all stages have been read.
     __syncthreads();
+    // even shares: read again, since the loop has no registers for them
+    const int at0 = kEven ? 0 : base, many = kEven ? min(R, piece.nq * group) : rows;
+    const int head = kEven ? piece.head : hk, q0 = kEven ? piece.q0 : sp.q0;
+    // this CTA has all the keys of its rows; the first row of its parts
+    const bool whole = kEven ? piece.whole : !P.cluster && sp.nk <= P.chunk;
+    const long long row0 = kEven ? piece.row : ((long long)over * P.splits + split) * P.rows;
     float* parts = reinterpret_cast<float*>(smem);  // [warp][row][dim]
     float* mine = parts + 4 * R * D;                 // a cluster's: this run's rows
     if (warp < 4) {
@@ -871,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
         for (int e = 0; e < 2; ++e) {
           const int r = n * 8 + c0 + e;
           if (r0 == 0) ml[warp][r] = make_float2(Q.m[n][e], Q.l[n][e]);
-          if (r < rows) {
+          if (r < many) {
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i)
               *reinterpret_cast<float2*>(parts + (warp * R + r) * D + (i >> 1) * 32 + 4 * r0 + 2 * (i & 1)) =
@@ -881,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
     }
     __syncthreads();
     if (warp < 4 && !abort_flag) {
-      for (int r = warp; r < rows; r += 4) {
+      for (int r = warp; r < many; r += 4) {
         float mr = -INFINITY, lr = 0.f, out[V];
 #pragma unroll
         for (int w = 0; w < 4; ++w) mr = fmaxf(mr, ml[w][r].x);
@@ -897,19 +1067,19 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
 #pragma unroll
           for (int e = 0; e < V; ++e) out[e] += f * parts[(w * R + r) * D + lane * V + e];
         }
-        if (direct) {
-          const int token = (base + r) / group, g = base + r - token * group;
+        if (whole) {
+          const int token = (at0 + r) / group, g = at0 + r - token * group;
           const float inv = lr == 0.f ? 0.f : 1.0f / lr;
-          bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * group + g) * D + lane * V;
+          bf16* dst = a.out + (long long)(q0 + token) * a.ldo + (head * group + g) * D + lane * V;
 #pragma unroll
           for (int e = 0; e < V; e += 2)
             *reinterpret_cast<uint32_t*>(dst + e) = lr == 0.f ? 0u : pack_bf16x2(out[e] * inv, out[e + 1] * inv);
-        } else if (P.cluster) {
+        } else if (!kEven && P.cluster) {
           if (lane == 0) sums[r] = make_float2(mr, lr);
 #pragma unroll
           for (int e = 0; e < V; e += 2) *reinterpret_cast<float2*>(mine + r * D + lane * V + e) = make_float2(out[e], out[e + 1]);
         } else {
-          const long long to = ((long long)over * P.splits + split) * P.rows + base + r;
+          const long long to = row0 + at0 + r;
           if (lane == 0) P.ml[to] = make_float2(mr, lr);
 #pragma unroll
           for (int e = 0; e < V; e += 2)
@@ -917,10 +1087,10 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
         }
       }
     }
-    if (P.cluster) {
+    if (!kEven && P.cluster) {
       // Every rank adds every splits-th row up over all runs, in order, one row per warp.
       cluster_sync_all();
-      for (int r = split + warp * P.splits; warp < 4 && r < rows; r += 4 * P.splits) {
+      for (int r = split + warp * P.splits; warp < 4 && r < many; r += 4 * P.splits) {
         float2 y[8];
         float mr = -INFINITY, lr = 0.f, out[V];
 #pragma unroll
@@ -949,9 +1119,9 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
 #pragma unroll
           for (int e = 0; e < V; ++e) out[e] += f * v[k][e];
         }
-        const int token = (base + r) / group, g = base + r - token * group;
+        const int token = (at0 + r) / group, g = at0 + r - token * group;
         const float inv = lr == 0.f ? 0.f : 1.0f / lr;
-        bf16* dst = a.out + (long long)(sp.q0 + token) * a.ldo + (hk * group + g) * D + lane * V;
+        bf16* dst = a.out + (long long)(q0 + token) * a.ldo + (head * group + g) * D + lane * V;
         if (!abort_flag) {
 #pragma unroll
           for (int e = 0; e < V; e += 2)
@@ -961,34 +1131,52 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
       __syncwarp();
       cluster_sync_all();  // no rank goes on while another reads its rows
     }
-    if (P.walk < P.tiles) fence_proxy_async_smem();  // before the next tile's copies
+    if (kEven || P.walk < P.tiles) fence_proxy_async_smem();  // before the next tile's copies
+    if (kEven && threadIdx.x == 0) {
+      const int done = piece.keys / kKeys;
+      if (piece.block == 0 && done < piece.n && !abort_flag)
+        P.cuts[blockIdx.x] = Cut{piece.head, piece.q0, piece.nq, 1 + (piece.n - done + piece.per - 1) / piece.per};
+      piece.template next<D>(P);
+    }
     __syncthreads();
-    if (!P.cluster && abort_flag) return;
+    if ((kEven || !P.cluster) && abort_flag) return;
   }
 }
 
-// Adds up the runs of the sequences that took several, in order: one warp per row, grid (sequence and key head,
-// four rows).
+// Adds up the runs of the sequences that took several, in order: one warp per row, grid (sequence and key head, or the share
+// where they begin, four rows).
 template <int D>
 __global__ void __launch_bounds__(128) cache4_join_kernel(const __grid_constant__ Params P) {
   grid_dependency_wait();
   allow_dependents();
   const Cache4AttnArgs& a = P.a;
-  const int G = P.group, hk = blockIdx.x % a.c.heads, seq = blockIdx.x / a.c.heads;
+  const int G = P.group, lane = threadIdx.x & 31;
+  if (P.even) {
+    const Cut cut = P.cuts[blockIdx.x];
+    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), token = r / G, first = blockIdx.x, end = first + cut.parts - 1;
+    if (cut.parts == 0 || r >= cut.nq * G) return;
+    // the last part is the first piece of its CTA, the others the last ones of theirs
+    join_row<D>(P.ml + r, P.o + (long long)r * D,
+                [&](int i) { return (long long)(2 * (first + i) + (first + i < end ? 1 : 0)) * P.rows; }, cut.parts, lane,
+                a.out + (long long)(cut.q0 + token) * a.ldo + (cut.head * G + r - token * G) * D);
+    return;
+  }
+  const int hk = blockIdx.x % a.c.heads, seq = blockIdx.x / a.c.heads;
   const Span sp = load_span(a, seq);
-  if (!sp.ok || sp.nk <= P.chunk) return;
+  if (!sp.ok) return;
+  if (sp.nk <= P.chunk) return;
   const int tile = P.rows <= 8 ? 8 : 16;
   for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < sp.nq * G; r += gridDim.y * 4) {
     const int base = r / tile * tile;
     const int seen = keys_seen(a, sp, G, base, min(tile, sp.nq * G - base)), runs = (seen + P.chunk - 1) / P.chunk;
     const long long at = (long long)blockIdx.x * P.splits * P.rows + r;
     const int token = r / G;
-    join_row<D>(P.ml + at, P.o + at * D, P.rows, max(1, runs), threadIdx.x & 31,
+    join_row<D>(P.ml + at, P.o + at * D, P.rows, max(1, runs), lane,
                 a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + r - token * G) * D);
   }
 }
 
-template <int D, int NT, bool kSmall>
+template <int D, int NT, bool kSmall, bool kEven>
 cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStream_t s) {
   static std::atomic<bool> raised[16];  // per device
   Params P;
@@ -1003,23 +1191,25 @@ cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStre
   P.chunk = p.chunk;
   P.splits = p.splits;
   P.cluster = p.cluster;
+  P.even = p.even;
   P.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
   P.ml = reinterpret_cast<float2*>(ws + l.ml);
   P.o = reinterpret_cast<float*>(ws + l.o);
+  P.cuts = reinterpret_cast<Cut*>(ws + l.cuts);
   constexpr size_t smem = kStages * Stage<D>::kBytes;
   static_assert(smem >= 5 * 8 * NT * D * 4, "the parts reuse the stages");
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 16 || !raised[dev].load(std::memory_order_acquire)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(cache4_attention_kernel<D, NT, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(cache4_attention_kernel<D, NT, kSmall, kEven>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev < 16) raised[dev].store(true, std::memory_order_release);
   }
   const long long heads = (long long)a.seqs * a.c.heads;
   {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(heads * p.splits * p.walk));
+    cfg.gridDim = dim3(p.even ? (unsigned)p.even : (unsigned)(heads * p.splits * p.walk));
     cfg.blockDim = dim3(kThreads<D, NT>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -1038,13 +1228,13 @@ cudaError_t launch_attention_as(const Cache4AttnArgs& a, const Plan& p, cudaStre
     cfg.attrs = attr;
     cfg.numAttrs = n;
     LaunchScope scope(kClsCache4Attention, s);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache4_attention_kernel<D, NT, kSmall>, P);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache4_attention_kernel<D, NT, kSmall, kEven>, P);
     if (e != cudaSuccess) return e;
   }
-  if (p.splits > 1 && !p.cluster) {
+  if (p.even || (p.splits > 1 && !p.cluster)) {
     const int fours = (p.rows + 3) / 4;
     LaunchScope scope(kClsCache4Join, s);
-    return launch_k(cache4_join_kernel<D>, dim3((unsigned)heads, (unsigned)(fours < 65535 ? fours : 65535)), dim3(128), 0, s, P);
+    return launch_k(cache4_join_kernel<D>, dim3(p.even ? (unsigned)p.even : (unsigned)heads, (unsigned)(fours < 65535 ? fours : 65535)), dim3(128), 0, s, P);
   }
   return cudaSuccess;
 }
@@ -1067,11 +1257,16 @@ size_t cache4_attention_parts_bytes(const Cache4AttnArgs& a) {
 cudaError_t launch_cache4_attention(const Cache4AttnArgs& a, cudaStream_t s) {
   const Plan p = make_plan(a);
   const bool small = a.c.page_shift == 4, eight = p.tile == 8;
-  if (a.c.head_dim == 64)
-    return small ? (eight ? launch_attention_as<64, 1, true>(a, p, s) : launch_attention_as<64, 2, true>(a, p, s))
-                 : (eight ? launch_attention_as<64, 1, false>(a, p, s) : launch_attention_as<64, 2, false>(a, p, s));
-  return small ? (eight ? launch_attention_as<128, 1, true>(a, p, s) : launch_attention_as<128, 2, true>(a, p, s))
-               : (eight ? launch_attention_as<128, 1, false>(a, p, s) : launch_attention_as<128, 2, false>(a, p, s));
+  auto of = [&](auto d, auto small_page) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool kSmall = decltype(small_page)::value;
+    if (p.even) return eight ? launch_attention_as<D, 1, kSmall, true>(a, p, s) : launch_attention_as<D, 2, kSmall, true>(a, p, s);
+    return eight ? launch_attention_as<D, 1, kSmall, false>(a, p, s) : launch_attention_as<D, 2, kSmall, false>(a, p, s);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (a.c.head_dim == 64) return small ? of(D64{}, std::true_type{}) : of(D64{}, std::false_type{});
+  return small ? of(D128{}, std::true_type{}) : of(D128{}, std::false_type{});
 }
 
 }  // namespace dit

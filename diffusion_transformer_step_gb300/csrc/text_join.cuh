@@ -5,14 +5,14 @@
 
 namespace dit {
 
-// One output row from its n parts, in order: part i has (max, sum) at ml[i step] and the unnormalised
-// row at o[i step D].  One warp; the parts' rows are fetched eight at a time, since what a join costs
+// One output row from its n parts, in order: part i has (max, sum) at ml[at(i)] and the unnormalised
+// row at o[at(i) D].  One warp; the parts' rows are fetched eight at a time, since what a join costs
 // is the latency of its loads.
-template <int D>
-__device__ __forceinline__ void join_row(const float2* ml, const float* o, int step, int n, int lane, bf16* out) {
+template <int D, typename At>
+__device__ __forceinline__ void join_row(const float2* ml, const float* o, At at, int n, int lane, bf16* out) {
   constexpr int V = D / 32;
   float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[(long long)s * step].x);
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[at(s)].x);
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
   const float ref = m == -INFINITY ? 0.f : m;
@@ -21,7 +21,7 @@ __device__ __forceinline__ void join_row(const float2* ml, const float* o, int s
   for (int e = 0; e < V; ++e) sum[e] = 0.f;
   for (int s0 = 0; s0 < n; s0 += 32) {
     float2 x = make_float2(0.f, 0.f);
-    if (s0 + lane < n) x = ml[(long long)(s0 + lane) * step];
+    if (s0 + lane < n) x = ml[at(s0 + lane)];
     // a part that held no key the row sees adds nothing, whatever its row holds
     const float f = x.y == 0.f ? -1.f : ex2_approx(x.x - ref);
     l += f < 0.f ? 0.f : f * x.y;
@@ -29,7 +29,7 @@ __device__ __forceinline__ void join_row(const float2* ml, const float* o, int s
       float v[8][V];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float* p = o + (long long)min(s0 + i + u, n - 1) * step * D + lane * V;
+        const float* p = o + at(min(s0 + i + u, n - 1)) * D + lane * V;
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           const float2 t = *reinterpret_cast<const float2*>(p + e);
@@ -51,6 +51,12 @@ __device__ __forceinline__ void join_row(const float2* ml, const float* o, int s
 #pragma unroll
   for (int e = 0; e < V; e += 2)
     *reinterpret_cast<uint32_t*>(out + lane * V + e) = pack_bf16x2(sum[e] * inv, sum[e + 1] * inv);
+}
+
+// The same of parts `step` rows from one another.
+template <int D>
+__device__ __forceinline__ void join_row(const float2* ml, const float* o, int step, int n, int lane, bf16* out) {
+  join_row<D>(ml, o, [=](int i) { return (long long)i * step; }, n, lane, out);
 }
 
 }  // namespace dit
