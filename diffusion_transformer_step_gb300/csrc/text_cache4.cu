@@ -200,7 +200,9 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 // One CTA takes a run of keys of one sequence and key head for up to 8 NT query rows (tokens x heads of the
 // group): warp 4 brings stages of 128 tokens in by bulk copies, page by page, and warps 0 to 3 take 32 tokens of a
 // stage each through mma.sync with a running maximum and sum of their own, which add up at the end in order. Runs of
-// several CTAs are joined by a second kernel.
+// several CTAs are joined in shared memory where they are a cluster, by a second kernel otherwise. The runs are cut by the
+// bounds that the host knows, or, for longer calls, evenly by the lengths on the device (kEven): then a CTA has pieces of
+// several sequences and heads, one after another.
 //
 // The tokens are the rows of both products, the few queries their columns: S^T = K Q^T and O^T = V^T P^T. What bounds
 // this kernel is issue: 311 instructions per 16 tokens (8 rows, 128 dims), 144 of them on the integer pipe, which takes half a warp
@@ -227,7 +229,8 @@ constexpr int kKeys = 128, kStages = 3, kAhead = 2;
 // Whether the warps that compute send for the stages themselves, in turns, or a fifth warp does. A scheduler's 16384
 // registers hold four warps of 128, three of 168 or two of 255: with sixteen rows of 128-wide heads two CTAs of four warps
 // that do not spill are faster than two of five that do (12 rows over 32 x 8192 tokens 117 us, 142); the others have
-// room for the fifth (8 rows over 64 x 8192: 128 us, 141 to 162 with four CTAs of four; 15 of 64-wide heads 17.3, 20.0).
+// room for the fifth (8 rows over 64 x 8192: 121 us, 126 with three CTAs of four warps of 168, 137 with four of 128; 15 rows of
+// 64-wide heads 17.3, 20.0).
 template <int D, int NT>
 constexpr bool kOwn = D == 128 && NT == 2;
 template <int D, int NT>
