@@ -170,6 +170,19 @@ def test_cache_attention_workspace_over_the_range(dit):
                         assert 256 <= dit.dit_text_cache4_attention_workspace(c, a) < 1 << 34
 
 
+def test_cache_attention_workspace_stays_small(dit):
+    """At most 2^17 rows of parts, whichever way the keys are cut: by bounds, into clusters, in even shares."""
+    for d in (64, 128):
+        for seqs in (1, 9, 48, 456, 1024, 1025, 16384):
+            for hq, hk in ((1, 1), (32, 8), (96, 8), (1024, 1024)):
+                for max_q in (1, 2, 5, 500):
+                    for max_k in (1, 128, 512, 513, 2048, 2049, 5001, 32768, 1 << 20, 1 << 24):
+                        c = dit.make_text_cache4(hk, d, 1 << 20, 64, (1 << 24) // 64)
+                        a = dit.make_text_attn(seqs, hq, hk, d, 1 << 20, 0, max_q, max_k)
+                        need = dit.dit_text_cache4_attention_workspace(c, a)
+                        assert 256 <= need <= 1024 + (1 << 17) * (8 + 4 * d) + 456 * 16, (d, seqs, hq, hk, max_q, max_k, need)
+
+
 def test_kernel_classes_have_names(dit):
     names = [dit.dit_kernel_class_name(i) for i in range(40)]
     for n in ("add_rms_norm", "linear_act", "text_cache4_append", "text_cache4_read", "text_cache4_attention",
