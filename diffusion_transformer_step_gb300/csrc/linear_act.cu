@@ -250,10 +250,11 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 }
 
 // Of the rows first, first + stride, ... below `rows` (of the output: m0 further) every step-th from number i0 on, four
-// columns from c on per thread; part(i, k) is what split k has sent of row number i, added in split order. Two rows go
-// side by side, the residual of the next two ahead. Not unrolled further: a loop that runs a few times waits for its code
-// as much as for its data (128 rows of one block of depth, eight rows at once: 8.8 us, two 6.4).
-template <int K, typename Part>
+// columns from c on per thread; part(i, k) is what split k has sent of row number i, added in split order. R rows go
+// side by side, the residual of the next R ahead. A loop that runs a few times waits for its code as much as for its data: 1
+// x 2560 x 64 with one, two, four rows at once 2.3, 2.5, 2.7 us, 64 x 4096 x 4096 with everything 12.5, 12.1, 12.8, 777 x 1544 x
+// 5160 with everything 30.9, 28.0, 27.3.
+template <int K, int R, typename Part>
 __device__ __forceinline__ void finish_rows(const Params& P, int i0, int step, int first, int stride, int rows, int m0, int c,
                                             Part part) {
   const LinearActArgs& p = P.a;
@@ -270,14 +271,22 @@ __device__ __forceinline__ void finish_rows(const Params& P, int i0, int step, i
     return x;
   };
   const int r0 = first + i0 * stride, by = step * stride;
-  uint2 res[2] = {residual(r0), residual(r0 + by)};
+  uint2 res[R];
+#pragma unroll
+  for (int u = 0; u < R; ++u) res[u] = residual(r0 + u * by);
 #pragma unroll 1
-  for (int r = r0, i = i0; r < rows; r += 2 * by, i += 2 * step) {
-    const int both[2] = {r, r + by};
-    const float4 v[2] = {sum(i), sum(r + by < rows ? i + step : i)};
-    const uint2 now[2] = {res[0], res[1]};
-    res[0] = residual(r + 2 * by), res[1] = residual(r + 3 * by);
-    finish4<kAnyAct>(p, both, rows, m0, c, v, bias, now);
+  for (int r = r0, i = i0; r < rows; r += R * by, i += R * step) {
+    int all[R];
+    float4 v[R];
+    uint2 now[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      all[u] = r + u * by;
+      v[u] = sum(r + u * by < rows ? i + u * step : i);
+      now[u] = res[u];
+      res[u] = residual(r + (R + u) * by);
+    }
+    finish4<kAnyAct>(p, all, rows, m0, c, v, bias, now);
   }
 }
 
@@ -556,7 +565,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) linear_act_wide_kernel(const 
       const int piece = (warp & 1) * (BN / 8) + lane, c = nt * BN + piece * 4;
       const float4* parts = reinterpret_cast<const float4*>(smem);
       if (ok && !*abort_flag && lane < BN / 8 && c < P.a.n && P.a.rows > m0 + split)
-        finish_rows<4>(P, (warp - 2) >> 1, 4, split, S, min(128, P.a.rows - m0), m0, c, [&](int i, int k) {
+        finish_rows<4, 4>(P, (warp - 2) >> 1, 4, split, S, min(128, P.a.rows - m0), m0, c, [&](int i, int k) {
           const int slot = (k == split ? split : S + (k < split ? k : k - 1)) * per + i;
           return parts[slot * (BN / 4) + (piece ^ ((split + i * S) & 7))];
         });
@@ -739,8 +748,9 @@ __global__ void __launch_bounds__(Few<T>::kThreads, Few<T>::kResident)
   if (c < P.a.n && !*abort_flag) {
     // a row per warp, every S-th row a rank's
     auto part = [&](int i, int k) { return *reinterpret_cast<const float4*>(parts + (k * per + i) * 128 + lane * 4); };
-    if (S == 1) finish_rows<1>(P, warp, 8, 0, 1, P.a.rows, 0, c, part);
-    else finish_rows<8>(P, warp, 8, rank, S, P.a.rows, 0, c, part);
+    constexpr int R = T <= 16 ? 1 : 2;
+    if (S == 1) finish_rows<1, R>(P, warp, 8, 0, 1, P.a.rows, 0, c, part);
+    else finish_rows<8, R>(P, warp, 8, rank, S, P.a.rows, 0, c, part);
   }
 }
 
