@@ -12,7 +12,7 @@
 // Splits add up through distributed shared memory, in rank order: each CTA sends its part of a row to the CTA that will
 // finish it (whose ring has been read), and finishes its own share of the rows from the parts that have come. (Left where
 // they were made and fetched by the one that finishes them, every row waited for another SM's memory: 777 x 1544 x 5160 with
-// all three 33.9 us, so 28.0.) Wide tiles go by one bulk copy per receiver, 24 KB to 64 KB (stores of 16 bytes: 300 x 1000 x
+// all three 33.9 us, so 26.9.) Wide tiles go by one bulk copy per receiver, 24 KB to 64 KB (stores of 16 bytes: 300 x 1000 x
 // 9000 22.3 us, so 21.6).
 //
 // Loads and MMAs are issued by a thread that elect.sync chose: chosen by its lane number, the compiler guards every such
@@ -23,7 +23,7 @@
 // Measured (bursts of twenty calls on different weights): 8192 x 12288 x 4096 432 to 438 us, 1880 to 1905 TFLOP/s (0.97 to 0.98
 // of the measured burst); call after call 515 to 530, at the clocks that power leaves, with any epilogue (0.93 of the
 // measured sustained rate). 4096 x 4096 x 4096 76 us, 512 x 4096 x 4096 15.3; 1 x 12288 x 4096 18.7 (5.4 TB/s of weights),
-// 1 x 2560 x 4096 7.2, 64 x 4096 x 4096 11.4, 777 x 1544 x 5160 25.1 without epilogue. A call has about 3.5 us besides its
+// 1 x 2560 x 4096 7.1, 64 x 4096 x 4096 11.4, 777 x 1544 x 5160 25.1 without epilogue. A call has about 3.5 us besides its
 // loads (launch, first load, last rows), and a split of wide tiles 5.5 more.
 // Measured and left: accumulators through shared memory to whole lines of the output, at six stages instead of seven (8192 x
 // 12288 x 4096 455 -> 476 us: the MMAs and the loads take all of shared memory's cycles); the first weights sent to L2 before the
