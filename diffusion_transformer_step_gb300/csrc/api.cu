@@ -1269,6 +1269,7 @@ dit_status dit_add_rms_norm(int rows, int cols, const void* x_dev, long long ldx
   if (cols < 8 || cols > 32768 || cols % 8 != 0 || (q_dev && cols % 16 != 0)) return DIT_ERR_UNSUPPORTED;
   if (rows < 0 || rows > kMaxTextRows || !(eps >= 0.f && eps <= 3.0e38f) || !(fabsf(gain_offset) <= 3.0e38f))
     return DIT_ERR_INVALID_ARG;
+  if (rows == 0) return DIT_OK;  // whose buffers need not be there
   if ((!y_dev && !q_dev) || (q_dev == nullptr) != (scale_dev == nullptr)) return DIT_ERR_INVALID_ARG;
   if (bad_ld(ldx, cols) || (res_dev && bad_ld(ld_res, cols)) || (sum_out_dev && bad_ld(ld_sum, cols)) ||
       (y_dev && bad_ld(ldy, cols)))
@@ -1277,7 +1278,6 @@ dit_status dit_add_rms_norm(int rows, int cols, const void* x_dev, long long ldx
   if (!aligned16(x_dev) || bad_ptr(res_dev) || bad_ptr(w_dev) || bad_ptr(sum_out_dev) || bad_ptr(y_dev) ||
       bad_ptr(q_dev) || bad_ptr(scale_dev))
     return DIT_ERR_INVALID_ARG;
-  if (rows == 0) return DIT_OK;
   // a thread reads its values before it writes any: exactly in place is the one overlap allowed
   struct Mat { const void* p; long long ld; };
   const Mat in[2] = {{x_dev, ldx}, {res_dev, ld_res}}, out[2] = {{sum_out_dev, ld_sum}, {y_dev, ldy}};

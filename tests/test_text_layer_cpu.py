@@ -50,7 +50,10 @@ def test_add_rms_norm_refusals(dit, change, st):
 def test_nothing_to_do_is_no_launch(dit):
     before = dit.dit_launch_count()
     dit.dit_add_rms_norm(*{**NORM, "rows": 0}.values(), stream=0)
+    none = dict.fromkeys(("x", "res", "sum_out", "y", "q", "scale"))  # as the pointers of tensors without elements
+    dit.dit_add_rms_norm(*{**NORM, **none, "rows": 0}.values(), stream=0)
     dit.dit_linear_act(*{**LIN, "rows": 0, "a": None}.values(), stream=0)
+    dit.dit_linear_act(*{**LIN, "rows": 0, "a": 0, "res": 0, "out": 0}.values(), stream=0)
     c = dit.make_text_cache4(**CACHE)
     for change in ({"seqs": 0}, {"rows": 0}, {"max_q": 0}):
         dit.dit_text_cache4_append(c, *{**APPEND, **change, "q_off": None}.values(), stream=0)

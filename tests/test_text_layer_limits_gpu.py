@@ -230,6 +230,17 @@ def test_graphs_that_share_a_workspace(dit, ws):
     _ok(dit, ws)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_no_keys_at_all(dit, ws, d):
+    """Queries of a cache without tokens are zeros, also where the bound says that there are none."""
+    for max_k in (0, 1, 700):
+        st = Setup(dit, 2, d, 16, [0, 0, 0], seed=1)
+        st.max_pages = 64
+        st.c = dit.make_text_cache4(2, d, st.ref.pages, 16, 64)
+        out = _check_attention(dit, ws, st, 4, [1, 3, 0], seed=2, max_k=max_k)
+        assert (out[[1, 3, 4, 5]] == 0).all()
+
+
 def test_many_short_sequences(dit, ws):
     """As many sequences as a call takes, most without tokens, the last with some."""
     seqs, d, page = 16384, 64, 16
