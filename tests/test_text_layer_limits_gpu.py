@@ -305,3 +305,45 @@ def test_operands_that_start_off_their_lines(dit, ws):
         dit.dit_linear_act(m, n, k, av, k, wv, k, None, 0, None, 0, out, n, False, ws, ws.numel())
         _ok(dit, ws)
         _within(out, want, R.linear_act_tolerance(want, size, z, k, None, False))
+
+
+@pytest.mark.parametrize("m,n,k", [(1 << 20, 8, 8), (1, 1 << 20, 8), (130, 1 << 18, 16), (8, 8, 1 << 20), (300, 9, 1 << 19)])
+def test_linear_act_longest_sides(dit, ws, m, n, k):
+    """As many rows, columns and as much depth as a call takes."""
+    a, w = _randn(m, k, seed=1), _randn(n, k, seed=2, std=k ** -0.5)
+    out = torch.zeros(m, n + -n % 8, device=DEV)
+    dit.dit_linear_act(m, n, k, a.to(DEV), k, w.to(DEV), k, None, 0, None, 0, out, out.stride(0), True, ws, ws.numel())
+    _ok(dit, ws)
+    pick = [0, 1, m // 2, m - 1] if m > 4 else list(range(m))
+    want, size, z = R.linear_act(a[pick], w, None, "none", None)
+    _within(out[pick, :n], want, R.linear_act_tolerance(want, size, z, k, None, True))
+
+
+def test_add_rms_norm_many_rows(dit):
+    """Four million rows of eight columns: several rows of a CTA at once, each CTA many."""
+    rows = 1 << 22
+    x = _randn(1024, 8, seed=1).repeat(rows // 1024, 1).to(DEV)
+    y = torch.zeros_like(x)
+    dit.dit_add_rms_norm(rows, 8, x, 8, None, 0, None, 0.0, 1e-6, None, 0, y, 8, None, None)
+    torch.cuda.synchronize()
+    _, want = R.add_rms_norm(x[:1024].cpu(), None, None, 0.0, float(np.float32(1e-6)))
+    _within(y[:1024], want, 2.0 ** -8 * want.abs() + _norm_tolerance(want, 8) * 1.01)
+    assert bool((y.view(-1, 1024, 8) == y[:1024]).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_cache_of_as_many_heads_as_there_may_be(dit, ws, d):
+    heads, lens = 1024, [3, 17]
+    st = Setup(dit, heads, d, 16, lens, seed=d)
+    kv = _randn(20, 2 * heads * d, seed=1)
+    kvd = kv.to(DEV)
+    st.append(ws, 20, _i32([0, 3, 20]), None, _i32(lens), kvd, kvd[:, heads * d:])
+    _ok(dit, ws)
+    row = 0
+    for s, n in enumerate(lens):
+        for i in range(n):
+            st.ref.put(st.table[s][i // 16], i % 16, kv[row, :heads * d].view(heads, d), kv[row, heads * d:].view(heads, d))
+            row += 1
+    assert st.same()
+    _check_attention(dit, ws, st, heads, [1, 2], seed=3)
+    _check_attention(dit, ws, st, heads, [1, 2], seed=3, max_k=1 << 20)
