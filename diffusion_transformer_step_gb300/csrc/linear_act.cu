@@ -35,6 +35,7 @@
 #include <atomic>
 
 #include "cta_pair.cuh"
+#include "linear_act_plan.h"
 #include "runtime.h"
 
 namespace dit {
@@ -802,26 +803,6 @@ cudaError_t raise_smem(const Shape& k) {
   return e;
 }
 
-// Clusters that the current device runs at once; it depends on which SMs each of its processing clusters
-// has.  Asked once per (device, kernel, cluster size).
-int clusters_at_once(const Shape& k) {
-  static std::atomic<int> known[16 * kKernels * 9];
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  std::atomic<int>* slot = dev < 16 ? &known[(dev * kKernels + k.id) * 9 + k.cluster] : nullptr;
-  if (slot) n = slot->load(std::memory_order_relaxed);
-  if (n > 0) return n;
-  cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = config(k, (unsigned)k.cluster, nullptr, attr);
-  cfg.numAttrs = 1;
-  if (raise_smem(k) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, (const void*)k.kernel, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return sm_count() / k.cluster / 2 > 0 ? sm_count() / k.cluster / 2 : 1;
-  }
-  if (slot) slot->store(n, std::memory_order_relaxed);
-  return n;
-}
-
 // A split tile is finished by finish4, which looks the activation up.
 template <int BN>
 Shape wide_shape(int act, int splits) {
@@ -848,23 +829,11 @@ Shape few_shape_of(int rows, int splits) {
                                                                                    : few_shape<128>(splits);
 }
 
-// Splits of the depth: as many as still run at once, of two blocks at least.  (The clusters that the runtime says run
-// at once count one CTA per SM; two are placed where they fit.)
-int few_splits(int rows, int n, int kblocks) {
-  const int blocks = (n + 127) / 128, most = kblocks / 2;
-  int S = most < 8 ? most : 8;
-  const int start = S;
-  while (S > 1 && blocks > clusters_at_once(few_shape_of(rows, S))) --S;
-  if (S < 3 && rows <= 64)  // two CTAs per SM
-    for (S = start; S > 1 && blocks > 2 * clusters_at_once(few_shape_of(rows, S));) --S;
-  return S > 1 ? S : 1;
-}
-
-cudaError_t launch_few(const LinearActArgs& a, cudaStream_t s) {
+cudaError_t launch_few(const LinearActArgs& a, LinearActPlan plan, cudaStream_t s) {
   Params P;
   if (!encode(P, a, a.rows <= 16 ? 16u : a.rows <= 32 ? 32u : a.rows <= 64 ? 64u : 128u, 128))
     return cudaErrorInvalidValue;
-  P.splits = few_splits(a.rows, a.n, P.kblocks);
+  P.splits = plan.splits;
   const Shape k = few_shape_of(a.rows, P.splits);
   const cudaError_t e = raise_smem(k);
   if (e != cudaSuccess) return e;
@@ -874,36 +843,8 @@ cudaError_t launch_few(const LinearActArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k.kernel, P);
 }
 
-// Columns of a tile and splits of the depth, by the time that a pair's longest way takes: rounds of tiles, blocks of depth
-// in each at what a block of 256, 192 or 128 columns costs, and what a split adds. Splits only where all of them run at
-// once, of eight blocks at least.
-struct WidePlan {
-  int bn, splits;
-};
-WidePlan wide_plan(const LinearActArgs& a, int kblocks) {
-  // A block's MMAs take 0.27, 0.20 and 0.14 us, a little more where many SMs load. Rows of operands that do not start on
-  // 128-byte lines are two lines each to load, which takes longer than that.
-  static const int bns[3] = {256, 192, 128};
-  static const float block_us[2][3] = {{0.30f, 0.24f, 0.175f}, {0.46f, 0.39f, 0.32f}};
-  const bool lines = (a.lda | a.ldw) % 64 == 0 && ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.w)) & 127) == 0;
-  WidePlan best{256, 1};
-  float least = 1e30f;
-  for (int i = 0; i < 3; ++i) {
-    const long long tiles = (long long)((a.rows + 255) / 256) * ((a.n + bns[i] - 1) / bns[i]);
-    const int pairs = sm_count() / 2;
-    for (int S = 1; S <= 4; ++S) {
-      if (S > 1 && (kblocks / S < 8 || tiles > clusters_at_once(wide_shape_of(bns[i], 0, S)))) break;
-      const float us = (float)((tiles + pairs - 1) / pairs) * (float)((kblocks + S - 1) / S) * block_us[lines ? 0 : 1][i] +
-                       (S > 1 ? 5.5f : 0.0f);
-      if (us < least) least = us, best = WidePlan{bns[i], S};
-    }
-  }
-  return best;
-}
-
-cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
+cudaError_t launch_wide(const LinearActArgs& a, LinearActPlan plan, cudaStream_t s) {
   Params P;
-  const WidePlan plan = wide_plan(a, (a.k + 63) / 64);
   if (!encode(P, a, 128, (uint32_t)plan.bn / 2)) return cudaErrorInvalidValue;
   P.m_tiles = (a.rows + 255) / 256;
   P.tiles = P.m_tiles * ((a.n + plan.bn - 1) / plan.bn);
@@ -920,12 +861,10 @@ cudaError_t launch_wide(const LinearActArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Up to 128 rows a cluster per 128 columns of the output (65 x 4096 x 4096 10.7 us so, 13.8 in wide tiles, 128 x 12288 x 4096 23.7
-// and 24.7; 100 x 8192 x 1024, two waves of clusters, 9.7 and 8.8). The same with up to 256 rows: 129 x 4096 x 4096 14.2 and
-// 16.2, 256 x 4096 x 4096 16.6 and 16.6, 200 x 2048 x 1024 8.4 and 6.8, 250 x 8192 x 4096 25.6 and 18.2; left.
 cudaError_t launch_linear_act(const LinearActArgs& a, cudaStream_t s) {
-  if (a.rows <= 128) return launch_few(a, s);
-  return launch_wide(a, s);
+  const bool lines = (a.lda | a.ldw) % 64 == 0 && ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.w)) & 127) == 0;
+  const LinearActPlan plan = linear_act_plan(a.rows, a.n, (a.k + 63) / 64, lines);
+  return plan.bn == 0 ? launch_few(a, plan, s) : launch_wide(a, plan, s);
 }
 
 }  // namespace dit
