@@ -39,7 +39,6 @@ namespace dit {
 namespace {
 
 constexpr float kAmaxFloor = 448.0f * 0x1p-118f;  // keeps 448 / max finite
-constexpr int kSMs = 152;
 
 // ---- quantisation ------------------------------------------------------------------------
 

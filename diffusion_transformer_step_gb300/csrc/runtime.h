@@ -62,6 +62,9 @@ class LaunchScope {
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// SMs of a GB300, for plans that decide the order of sums: those follow from sizes alone.
+constexpr int kSMs = 152;
+
 // Launch a step kernel with programmatic stream serialisation (its prologue may overlap the
 // previous kernel's tail; the kernel itself calls grid_dependency_wait() before touching
 // dependent memory).  DIT_NO_PDL=1 in the environment turns the attribute off.

@@ -69,7 +69,6 @@ constexpr uint32_t kHalfBytes = 128 * 64 * 2;  // 64 dims of a 128-row tile
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPsumLimit = 4096.0f;  // row sum of P that sends a key block down the slow path
 constexpr int kInlineSeqs = 64;        // up to here one warp finds its item itself
-constexpr int kSMs = 152;
 constexpr int kLevels = 1024;          // tile-index levels of the listing kernel
 
 struct Span {

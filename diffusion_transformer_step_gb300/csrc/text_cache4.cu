@@ -259,9 +259,25 @@ struct Params {
   Cut* cuts;
 };
 
-// What a piece of an even share costs besides its keys, in blocks of them (48 tokens over up to 32768 keys of 128-wide heads with
-// 0, 2, 3, 4, 6: 163, 153, 151, 152, 153 us; 45 over up to 5001 of 64-wide ones with 2, 3, 4, 6: 22.9, 21.6, 19.9, 15.9).
-constexpr int piece_cost(int head_dim) { return head_dim == 64 ? 6 : 3; }
+// CTAs per SM, of `rows` query rows (8 or 16) each. For eight rows 128 registers and three CTAs of five warps; for sixteen three
+// warps of 168 registers (64-wide heads) or two of 255 fit a scheduler, which is two CTAs of five or four. The plan cuts the keys
+// for as many CTAs as run at once, so it takes this number from here, and the kernel's launch bounds do too. (Cut for three CTAs of sixteen rows
+// of 64-wide heads, a third of the shares began in a second round: 12 rows over 32 x 8192 tokens 82 us instead of 62, 15 over 4
+// sequences of up to 32768 44 instead of 32; where runs are cut by bounds 17 tokens of 4 heads over 20000 21 instead of 15.)
+__host__ __device__ constexpr int ctas_per_sm(int rows) { return rows == 8 ? 3 : 2; }
+
+// What a piece of an even share costs besides its keys, in blocks of them: more of the 64-wide ones, which are shorter,
+// and more again where two CTAs per SM instead of three hide it. Microseconds with 2, 3, 4, 6 and 8, 4 or 12 query rows
+// per key head, lengths drawn from a tenth of the longest on:
+//   rows x width   64 of up to 4096 keys     200 of up to 3000     48 of up to 32768     9 of up to 5001
+//    8 x 128       47.5 45.9 46.4 48.5 49.5  101  97  99 101 104   195 193 194 197 199   17.2 16.7 16.8 19.1 22.1
+//   16 x 128       75.0 71.8 70.2 70.9 73.6  170 161 155 159 162   306 302 303 304 307   23.4 23.4 23.3 23.4 23.5
+//    8 x 64        31.8 30.5 30.6 31.2 32.4   70  65  65  66  67   121 119 119 120 122   13.3 12.6 12.6 14.2 15.5
+//   16 x 64        52.0 50.6 47.5 45.2 46.6  117 110 105 101 102   186 181 180 177 179   15.3 15.2 15.3 15.2 15.2
+// Calls of equal lengths take the same within 4 % with 2 to 4.
+__host__ __device__ constexpr int piece_cost(int head_dim, int rows) {
+  return head_dim == 128 ? 3 : rows == 8 ? 4 : 6;
+}
 
 Plan make_plan(const Cache4AttnArgs& a) {
   Plan p;
@@ -269,13 +285,13 @@ Plan make_plan(const Cache4AttnArgs& a) {
   p.rows = (int)(rows < (1ll << 30) ? rows : (1ll << 30));
   p.tile = rows <= 8 ? 8 : 16;
   p.tiles = (p.rows + p.tile - 1) / p.tile;
-  // Runs that give every SM three CTAs where the keys allow it, of 128 keys at least: a fourth CTA waits for a second
+  // Runs that give every SM as many CTAs as it holds where the keys allow it, of 128 keys at least: one more waits for a second
   // round (one token over 32768 keys 25.3 us in six per SM, 19.0 in three). Up to 512 keys one run, without the second
   // kernel (16 tokens over up to 300 keys 9.0 us in two runs, 6.5 in one; over 1000 9.7 in one, 7.1 in eight), and runs of
   // at most 4096, so that ragged lengths even out (1024 cost 13 % more at 64 x 8192: a run takes ~3 us besides its keys).
   const long long items = heads * p.tiles < (1ll << 30) ? heads * p.tiles : (1ll << 30);
-  const int resident = p.tile == 8 || a.c.head_dim == 64 ? 3 : 2;
-  long long chunk = (long long)a.max_k * items / (resident * 152);
+  const int slots = ctas_per_sm(p.tile) * kSMs;
+  long long chunk = (long long)a.max_k * items / slots;
   if (chunk > 4096) chunk = 4096;
   if (chunk < kKeys) chunk = kKeys;
   if (a.max_k <= 512) chunk = a.max_k;
@@ -291,18 +307,18 @@ Plan make_plan(const Cache4AttnArgs& a) {
   // A cluster joins its runs without a second kernel: one token over 1000 keys 7.1 -> 5.9 us, over 4000 in eight runs instead
   // of 32 9.4 -> 8.0 (over 8000 in eight it would be 11.3 instead of 10.8). Only while all of them run at once: clusters
   // wait for places side by side and for their longest run (8 x 4096 tokens 16.0 -> 21 us, 48 ragged ones 187 -> 325).
-  if (p.splits > 8 && a.max_k <= 4096 && items * 8 <= 2 * 152) {
+  if (p.splits > 8 && a.max_k <= 4096 && items * 8 <= 2 * kSMs) {
     p.chunk = ((a.max_k + 7) / 8 + kKeys - 1) / kKeys * kKeys;
     p.splits = (a.max_k + p.chunk - 1) / p.chunk;
   }
-  p.cluster = p.splits > 1 && p.splits <= 8 && items * p.splits <= 2 * 152;
+  p.cluster = p.splits > 1 && p.splits <= 8 && items * p.splits <= 2 * kSMs;
   // Longer calls of few rows share all keys out evenly over the CTAs that run at once, from 512 keys each on and for sequences
   // that may be longer than 2048 (48 tokens over up to 32768 keys 186 -> 151 us, 32 over up to 8192 57.9 -> 40.8, 64 over 8192
   // each 127.8 -> 120; 8 over 4096 each, 574 keys per CTA, 16.4 and 15.9; many short sequences are better off with a CTA each,
   // whose starts overlap: 200 of up to 2000 70.8 and 75.4, 1000 of up to 400 129 and 148).
-  const long long blocks = heads * ((a.max_k + kKeys - 1) / kKeys + 1 + piece_cost(a.c.head_dim)), slots = resident * 152;
+  const long long blocks = heads * ((a.max_k + kKeys - 1) / kKeys + 1 + piece_cost(a.c.head_dim, p.tile));
   p.even = p.tiles == 1 && !p.cluster && a.seqs <= 1024 && a.max_k > 2048 && a.max_k * heads >= 512 * slots && blocks < (1 << 30)
-               ? (int)slots : 0;
+               ? slots : 0;
   const long long most = (1ll << 30) / (heads * p.splits);
   p.walk = p.tiles < most ? p.tiles : (int)(most < 1 ? 1 : most);
   return p;
@@ -345,11 +361,11 @@ __device__ __forceinline__ int keys_seen(const Cache4AttnArgs& a, const Span& sp
 // ---- even shares: all blocks of 128 keys of all sequences and key heads in a row, as much of them to each CTA ---------
 
 // Of a head of sequence s: its blocks and what comes on top, or zero. Queries without keys have one.
-template <int D>
+template <int kCost>
 __device__ __forceinline__ int cost_of(const Cache4AttnArgs& a, int s) {
   if (s >= a.seqs) return 0;
   const Span sp = load_span(a, s);
-  return sp.nq == 0 ? 0 : max(1, (sp.nk + kKeys - 1) / kKeys) + piece_cost(D);
+  return sp.nq == 0 ? 0 : max(1, (sp.nk + kKeys - 1) / kKeys) + kCost;
 }
 
 struct Share {
@@ -360,23 +376,25 @@ struct Share {
 
 // The share's size, and the sequence that holds the first block of the CTA's (a.seqs: there is none). One warp, all lanes the
 // same; the lengths of 128 sequences are fetched at once.
-template <int D>
+template <int kCost>
 __device__ __forceinline__ Share find_share(const Cache4AttnArgs& a, int ctas, int cta, int lane) {
   int all = 0, n[4];
   for (int s0 = 0; s0 < a.seqs; s0 += 128) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n[i] = cost_of<D>(a, s0 + 32 * i + lane);
+    for (int i = 0; i < 4; ++i) n[i] = cost_of<kCost>(a, s0 + 32 * i + lane);
     all += n[0] + n[1] + n[2] + n[3];
   }
   all = __reduce_add_sync(0xffffffffu, all);
   Share r;
-  r.per = max(piece_cost(D) + 1, (int)((unsigned)(all * a.c.heads + ctas - 1) / (unsigned)ctas));
+  // at least what comes on top and one block, so that a share which begins with a head has some of its keys (shares of seven or
+  // ten blocks at least: 9 tokens over up to 5001 of 128-wide heads 16.7 us -> 19.4 and 22.5, of 64-wide ones 12.6 -> 13.9, 15.7)
+  r.per = max(kCost + 1, (int)((unsigned)(all * a.c.heads + ctas - 1) / (unsigned)ctas));
   r.before = 0;
   r.seq = a.seqs, r.n = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += 128) {
     if (a.seqs > 128) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = cost_of<D>(a, s0 + 32 * i + lane);
+      for (int i = 0; i < 4; ++i) n[i] = cost_of<kCost>(a, s0 + 32 * i + lane);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -417,16 +435,16 @@ struct Piece {
     whole = count == n;
     row = (long long)(2 * blockIdx.x + (block + count == n ? 0 : 1)) * P.rows;
   }
-  template <int D>
+  template <int kCost>
   __device__ __forceinline__ void next(const Params& P) {
-    left -= keys / kKeys + piece_cost(D);
+    left -= keys / kKeys + kCost;
     block = 0;
     if (left > 0 && ++head == P.a.c.heads) {
       head = 0;
       int cost;
-      do cost = cost_of<D>(P.a, ++seq);
+      do cost = cost_of<kCost>(P.a, ++seq);
       while (cost == 0 && seq < P.a.seqs);
-      n = cost == 0 ? 0 : cost - piece_cost(D);
+      n = cost == 0 ? 0 : cost - kCost;
       if (n > 0) of(P.a, seq);
     }
     cut(P);
@@ -794,9 +812,9 @@ struct Sender {
 };
 
 template <int D, int NT, bool kSmall, bool kEven>
-__global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_attention_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads<D, NT>, ctas_per_sm(8 * NT)) cache4_attention_kernel(const __grid_constant__ Params P) {
   using L = Stage<D>;
-  constexpr int G = L::G, R = 8 * NT, V = D / 32;
+  constexpr int G = L::G, R = 8 * NT, V = D / 32, kCost = piece_cost(D, R);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ uint32_t live[kStages];  // the tiles of 16 tokens that a stage holds
@@ -828,7 +846,7 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
       if (c == 0)
         for (int i = lane; i < a.seqs; i += 32)
           if (!load_span(a, i).ok) report_bad_entry(a.status, kSiteCache4Lengths);
-      const Share h = find_share<D>(a, P.even, c, lane);
+      const Share h = find_share<kCost>(a, P.even, c, lane);
       if (lane == 0) {
         P.cuts[c].parts = 0;
         piece.keys = -1;
@@ -836,8 +854,8 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
         if (h.seq < a.seqs) {
           const int in = c * h.per - h.before * a.c.heads;
           piece.of(a, h.seq);
-          piece.head = in / h.n, piece.n = h.n - piece_cost(D);
-          const int at_cost = in % h.n - piece_cost(D);  // a share that begins in what comes on top begins with the first block
+          piece.head = in / h.n, piece.n = h.n - kCost;
+          const int at_cost = in % h.n - kCost;  // a share that begins in what comes on top begins with the first block
           piece.block = max(0, at_cost), piece.left = h.per + min(0, at_cost);
           piece.cut(P);
         }
@@ -1139,7 +1157,7 @@ __global__ void __launch_bounds__(kThreads<D, NT>, NT == 1 ? 3 : 2) cache4_atten
       const int done = piece.keys / kKeys;
       if (piece.block == 0 && done < piece.n && !abort_flag)
         P.cuts[blockIdx.x] = Cut{piece.head, piece.q0, piece.nq, 1 + (piece.n - done + piece.per - 1) / piece.per};
-      piece.template next<D>(P);
+      piece.template next<kCost>(P);
     }
     __syncthreads();
     if ((kEven || !P.cluster) && abort_flag) return;
