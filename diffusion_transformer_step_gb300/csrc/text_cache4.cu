@@ -970,7 +970,9 @@ __global__ void __launch_bounds__(kThreads<D, NT>, ctas_per_sm(8 * NT)) cache4_a
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = n * 8 + c0 + e;
-          Q.scale[n][e] = ldexpf(P.scale_log2, 24 - __shfl_sync(0xffffffffu, up, (c0 + e) * 4));
+          // never zero, whose product with the minus infinity of a key that is not seen would be NaN; what it adds to a factor below
+          // fp32's smallest number is at most 2^-21 of an exponent
+          Q.scale[n][e] = fmaxf(ldexpf(P.scale_log2, 24 - __shfl_sync(0xffffffffu, up, (c0 + e) * 4)), 0x1p-149f);
           Q.limit[n][e] = i < rows && a.causal ? min(sp.nk, (base + i) / group + sp.nk - sp.nq + 1) : sp.nk;
           open = min(open, Q.limit[n][e]);
           Q.m[n][e] = -INFINITY;
