@@ -659,9 +659,10 @@ __device__ __forceinline__ void attend(Rows<D, NT, kLong>& R, const uint8_t* sta
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
         const float mn = fmaxf(R.m[n][e], top - kRoom);
-        alpha[e] = ex2_approx(R.m[n][e] - (mn == -INFINITY ? 0.f : mn));
+        const float by = R.m[n][e] - (mn == -INFINITY ? 0.f : mn);
+        alpha[e] = ex2_approx(by);
         R.m[n][e] = mn;
-        R.l[n][e] *= alpha[e];
+        R.l[n][e] = rescaled(R.l[n][e], by);
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -1085,8 +1086,8 @@ __global__ void __launch_bounds__(kThreads<D, NT>, ctas_per_sm(8 * NT)) cache4_a
         for (int w = 0; w < 4; ++w) {
           const float2 y = ml[w][r];
           if (y.y == 0.f) continue;  // no key that the row sees
-          const float f = ex2_approx((y.x == -INFINITY ? 0.f : y.x) - ref);
-          lr += f * y.y;
+          const float by = (y.x == -INFINITY ? 0.f : y.x) - ref, f = ex2_approx(by);
+          lr += rescaled(y.y, by);
 #pragma unroll
           for (int e = 0; e < V; ++e) out[e] += f * parts[(w * R + r) * D + lane * V + e];
         }
@@ -1137,8 +1138,8 @@ __global__ void __launch_bounds__(kThreads<D, NT>, ctas_per_sm(8 * NT)) cache4_a
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (y[k].y == 0.f) continue;  // no key that the row sees
-          const float f = ex2_approx((y[k].x == -INFINITY ? 0.f : y[k].x) - ref);
-          lr += f * y[k].y;
+          const float by = (y[k].x == -INFINITY ? 0.f : y[k].x) - ref, f = ex2_approx(by);
+          lr += rescaled(y[k].y, by);
 #pragma unroll
           for (int e = 0; e < V; ++e) out[e] += f * v[k][e];
         }
@@ -1179,7 +1180,7 @@ __global__ void __launch_bounds__(128) cache4_join_kernel(const __grid_constant_
     const int r = blockIdx.y * 4 + (threadIdx.x >> 5), token = r / G, first = blockIdx.x, end = first + cut.parts - 1;
     if (cut.parts == 0 || r >= cut.nq * G) return;
     // the last part is the first piece of its CTA, the others the last ones of theirs
-    join_row<D>(P.ml + r, P.o + (long long)r * D,
+    join_row<D, true>(P.ml + r, P.o + (long long)r * D,
                 [&](int i) { return (long long)(2 * (first + i) + (first + i < end ? 1 : 0)) * P.rows; }, cut.parts, lane,
                 a.out + (long long)(cut.q0 + token) * a.ldo + (cut.head * G + r - token * G) * D);
     return;
@@ -1194,7 +1195,7 @@ __global__ void __launch_bounds__(128) cache4_join_kernel(const __grid_constant_
     const int seen = keys_seen(a, sp, G, base, min(tile, sp.nq * G - base)), runs = (seen + P.chunk - 1) / P.chunk;
     const long long at = (long long)blockIdx.x * P.splits * P.rows + r;
     const int token = r / G;
-    join_row<D>(P.ml + at, P.o + at * D, P.rows, max(1, runs), lane,
+    join_row<D, true>(P.ml + at, P.o + at * D, P.rows, max(1, runs), lane,
                 a.out + (long long)(sp.q0 + token) * a.ldo + (hk * G + r - token * G) * D);
   }
 }

@@ -5,10 +5,17 @@
 
 namespace dit {
 
+// A sum of probabilities times 2^by, by <= 0, in two steps: where references follow the products of probability and value scale,
+// `by` holds the logarithm of the scales' ratio as well, down to -162, and 2^by alone is below fp32's range.
+__device__ __forceinline__ float rescaled(float l, float by) {
+  const float half = ex2_approx(0.5f * by);
+  return l * half * half;
+}
+
 // One output row from its n parts, in order: part i has (max, sum) at ml[at(i)] and the unnormalised
 // row at o[at(i) D].  One warp; the parts' rows are fetched eight at a time, since what a join costs
-// is the latency of its loads.
-template <int D, typename At>
+// is the latency of its loads. kScaled: references that hold scales.
+template <int D, bool kScaled, typename At>
 __device__ __forceinline__ void join_row(const float2* ml, const float* o, At at, int n, int lane, bf16* out) {
   constexpr int V = D / 32;
   float m = -INFINITY;
@@ -24,7 +31,7 @@ __device__ __forceinline__ void join_row(const float2* ml, const float* o, At at
     if (s0 + lane < n) x = ml[at(s0 + lane)];
     // a part that held no key the row sees adds nothing, whatever its row holds
     const float f = x.y == 0.f ? -1.f : ex2_approx(x.x - ref);
-    l += f < 0.f ? 0.f : f * x.y;
+    l += f < 0.f ? 0.f : kScaled ? rescaled(x.y, x.x - ref) : f * x.y;
     for (int i = 0; i < 32 && s0 + i < n; i += 8) {
       float v[8][V];
 #pragma unroll
@@ -54,9 +61,9 @@ __device__ __forceinline__ void join_row(const float2* ml, const float* o, At at
 }
 
 // The same of parts `step` rows from one another.
-template <int D>
+template <int D, bool kScaled = false>
 __device__ __forceinline__ void join_row(const float2* ml, const float* o, int step, int n, int lane, bf16* out) {
-  join_row<D>(ml, o, [=](int i) { return (long long)i * step; }, n, lane, out);
+  join_row<D, kScaled>(ml, o, [=](int i) { return (long long)i * step; }, n, lane, out);
 }
 
 }  // namespace dit
