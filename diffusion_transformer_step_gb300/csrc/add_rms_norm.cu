@@ -7,8 +7,9 @@
 // per thread, for the least time from load to store.
 //
 // Memory bounds all but the e4m3 output alone: 16384 rows of 4096 with residual 93.5 us to both outputs (6.5 TB/s), 81 to bf16
-// (6.6); without residual to e4m3 alone 54 (3.8 TB/s), where 158 instructions per eight values do. Seven rows of 2560: 2.0
-// us. With one row per CTA and no loads ahead the three took 96, 82 and 71 us, 16384 rows of 256 17.1 (now 7.1).
+// (6.6); without residual 48 to bf16 (5.6 TB/s) and 54 to e4m3 alone (3.8), where 158 instructions per eight values do.
+// Seven rows of 2560: 2.0 us. With one row per CTA and no loads ahead both outputs, bf16 and e4m3 alone took 96, 82 and 71 us, 16384
+// rows of 256 17.1 (now 5.8).
 #include <cuda_fp8.h>
 
 #include "runtime.h"

@@ -12,18 +12,18 @@
 // Splits add up through distributed shared memory, in rank order: each CTA sends its part of a row to the CTA that will
 // finish it (whose ring has been read), and finishes its own share of the rows from the parts that have come. (Left where
 // they were made and fetched by the one that finishes them, every row waited for another SM's memory: 777 x 1544 x 5160 with
-// all three 33.9 us, so 26.9.) Wide tiles go by one bulk copy per receiver, 24 KB to 64 KB (stores of 16 bytes: 300 x 1000 x
+// all three 33.9 us, so 26.6.) Wide tiles go by one bulk copy per receiver, 24 KB to 64 KB (stores of 16 bytes: 300 x 1000 x
 // 9000 22.3 us, so 21.6).
 //
 // Loads and MMAs are issued by a thread that elect.sync chose: chosen by its lane number, the compiler guards every such
 // instruction against more than one, and a block of depth takes 0.28 us whatever its tile's columns (elected: 0.27, 0.20 and
 // 0.14 us for 256, 192 and 128).  Then loads bound the narrow tiles, and all where rows do not start on lines of 128 bytes:
-// 777 x 1544 x 5120 16.6 us, 5152 19.0, 5136 20.1, 5160 25.1.
+// 777 x 1544 x 5120 16.5 us, 5152 19.0, 5136 20.1, 5160 24.6.
 //
 // Measured (bursts of twenty calls on different weights): 8192 x 12288 x 4096 432 to 438 us, 1880 to 1905 TFLOP/s (0.97 to 0.98
-// of the measured burst); call after call 515 to 530, at the clocks that power leaves, with any epilogue (0.93 of the
-// measured sustained rate). 4096 x 4096 x 4096 76 us, 512 x 4096 x 4096 15.3; 1 x 12288 x 4096 18.7 (5.4 TB/s of weights),
-// 1 x 2560 x 4096 7.1, 64 x 4096 x 4096 11.4, 777 x 1544 x 5160 25.1 without epilogue. A call has about 3.5 us besides its
+// of the measured burst); call after call 505 to 530, at the clocks that power leaves, with any epilogue (0.93 of the
+// measured sustained rate). 4096 x 4096 x 4096 76 to 78 us, 512 x 4096 x 4096 15.4; 1 x 12288 x 4096 18.7 (5.4 TB/s of weights),
+// 1 x 2560 x 4096 7.1, 64 x 4096 x 4096 11.4, 777 x 1544 x 5160 24.6 without epilogue. A call has about 3.5 us besides its
 // loads (launch, first load, last rows), and a split of wide tiles 5.5 more.
 // Measured and left: accumulators through shared memory to whole lines of the output, at six stages instead of seven (8192 x
 // 12288 x 4096 455 -> 476 us: the MMAs and the loads take all of shared memory's cycles); the first weights sent to L2 before the
@@ -58,7 +58,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// Two values at a time: packed fp32 arithmetic, exponentials and reciprocals of the special unit.
+// Two values at a time: packed fp32 arithmetic, exponentials and reciprocals of the special unit. Where the reciprocal is below fp32's
+// normal numbers (z below -87) an output is zero instead of under 2^-119.
 template <int kAct>
 __device__ __forceinline__ float2 activate(float2 z) {
   auto f2 = [](float v) { return make_float2(v, v); };
@@ -254,7 +255,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 // columns from c on per thread; part(i, k) is what split k has sent of row number i, added in split order. R rows go
 // side by side, the residual of the next R ahead. A loop that runs a few times waits for its code as much as for its data: 1
 // x 2560 x 64 with one, two, four rows at once 2.3, 2.5, 2.7 us, 64 x 4096 x 4096 with everything 12.5, 12.1, 12.8, 777 x 1544 x
-// 5160 with everything 30.9, 28.0, 27.3.
+// 5160 with everything 30.9, 28.0, 27.3 (26.6 with the steps after this one).
 template <int K, int R, typename Part>
 __device__ __forceinline__ void finish_rows(const Params& P, int i0, int step, int first, int stride, int rows, int m0, int c,
                                             Part part) {

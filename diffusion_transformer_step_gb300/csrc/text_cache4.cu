@@ -206,13 +206,13 @@ cudaError_t launch_move(const Cache4MoveArgs& a, int cls, cudaStream_t s) {
 //
 // The tokens are the rows of both products, the few queries their columns: S^T = K Q^T and O^T = V^T P^T. What bounds
 // this kernel is issue: 311 instructions per 16 tokens (8 rows, 128 dims), 144 of them on the integer pipe, which takes half a warp
-// per cycle, to spread 4-bit codes over 16-bit operands, and 21 MMAs, with three warps per scheduler to choose from (a fourth,
+// per cycle, to spread 4-bit codes over 16-bit operands, and 21 MMAs (17 in even shares, see kAdds), with three warps per scheduler to choose from (a fourth,
 // with two CTAs of seven and a sender, gains its scheduler 5 %; from L2 the same calls take 2 % less). So a code is left where one AND leaves it. As the bits of an fp16 number, a code c in the lowest four
 // bits is the subnormal c 2^-24, in the next four c 2^-20: both exact operands, five operations per eight codes of the keys
 // and six of the values. (As bf16 128 + c, with an OR and more shifts, and an exact subtraction of 136 for the values: 458
 // instructions per 16 tokens instead of 355, 64 tokens over 8192 each 172 us instead of 140, all else equal.)
 //
-// Keys: the queries become fp16 times a power of two per row (largest magnitude in [2^13, 2^14)), exact down to 2^-28 of the
+// Keys: the queries become fp16 times a power of two per row (largest magnitude in [2^13, 2^14)), exact down to 2^-26 of the
 // row's largest; those that meet the higher codes are divided by 16. The 8 that every code is too large is taken off
 // by -8 sum(q) per group: scales times those sums is one more small product (they go in as three bf16 parts, 24 bits), and
 // the accumulators of the groups are added to it, times the key's scale, in fp32.

@@ -504,7 +504,8 @@ dit_status dit_linear_fp8_blocks(int rows, int n_out, int k, const void* a_q_dev
  * bf16; y_dev, y rounded to bf16; q_dev and scale_dev (both or neither), y in e4m3 with a scale per 128 values
  * of a row, as dit_quantize_blocks_fp8 with block_rows 1 takes them from a matrix: q_dev [rows, cols]
  * contiguous, scale_dev [rows, ceil(cols / 128)], the operand of dit_linear_fp8_blocks; the codes are of
- * the unrounded y.  Squares are summed in fp32: rows whose values stay below 2^56 cannot overflow them.
+ * the unrounded y.  Squares are summed in fp32: rows whose values stay below 2^56 cannot overflow them; with eps 0, rows whose
+ * largest value is below 2^-55 lose digits of them.
  * x, res, sum and y have row strides ld*, % 8 == 0, >= cols, <= 2^24; w_dev [cols] bf16.  sum_out_dev and y_dev may
  * each be x_dev or res_dev itself (same pointer and stride); any other overlap of outputs with inputs or with
  * one another is DIT_ERR_INVALID_ARG.  cols % 8 == 0 (q_dev: % 16), 8 <= cols <= 32768, 0 <= rows <= 2^26;
@@ -583,7 +584,9 @@ dit_status dit_text_cache4_append(const dit_text_cache4* c, int seqs, int rows, 
 /* The tokens of whole sequences back in bf16 (n * scale, rounded): token i of sequence s, i < nk = k_len[s] (or
  * k_off[s + 1] - k_off[s] where k_len is NULL), to row k_off[s] + i of k_out_dev and v_out_dev, which have `rows` rows;
  * max_k is an upper bound of nk (0 .. 2^24).  For many query rows over a cache (a further chunk of a long prompt)
- * this and dit_text_attention on its output are faster than dit_text_cache4_attention.  Lengths out of
+ * this and dit_text_attention on its output are faster than dit_text_cache4_attention: from about 64 rows per key head on
+ * (new tokens of a sequence times heads_q / heads_k; 16 sequences of 4096 keys, 32 heads of 128 on 8: 32 rows 80 us and 112,
+ * 64 rows 110 and 112, 128 rows 219 and 112).  Lengths out of
  * range and pages outside the cache as in dit_text_cache4_append: their rows are left as they were, and recorded.  Sequences' rows
  * must not overlap.  Other limits as dit_text_cache4_append. */
 dit_status dit_text_cache4_read(const dit_text_cache4* c, int seqs, int rows, int max_k, const int32_t* k_off,
@@ -599,8 +602,8 @@ dit_status dit_text_cache4_attention_workspace(const dit_text_cache4* c, const d
  * the nk = k_len[s] tokens of its page table as keys, and the queries [q_off[s], q_off[s] + nq).  What `a` says holds as
  * there (heads_k and head_dim as in `c`; rows_k is not used; causal: the last query sees the last key), and so does
  * what is said there of queries without keys, of rows that belong to no sequence, and of values behind a
- * sequence's keys.  Scores from exact products of the queries and the cache's integers (what of a query row is below 2^-28 of
- * its largest value is rounded), scaled and summed in fp32; scale times a row's largest magnitude stays below 2^100.
+ * sequence's keys.  Scores from exact products of the queries and the cache's integers (what of a query row is below 2^-26 of
+ * its largest value may be rounded, by 2^-34 of that at most), scaled and summed in fp32; scale times a row's largest magnitude stays below 2^100.
  * Probabilities times the values' scales are rounded to fp16 for the product with V, those below 2^-20 of a row's largest
  * to 2^-31 of it; so where the largest scale of the values that a row sees is 2^-64 to 2^98 (values of 7 times that). Below
  * 2^-64 steps stay those of 2^-64, and above 2^98 the sum of the probabilities loses its small terms.  A key on a page outside
